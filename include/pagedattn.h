@@ -294,6 +294,122 @@ int pa_copy_blocks(void* key_cache, void* value_cache,
                    pa_dtype dtype, cudaStream_t stream);
 
 /*
+ * The 8-bit cache. A pool holds, for K and for V, e4m3 codes
+ *   key_cache, value_cache  [NB, B, Hkv, d]     one byte an element
+ * and the rows' exponent bytes
+ *   cache_scales            [NB, Hkv, 2, B]     uint8; K's at index 0, V's at 1
+ * Element i of the row of (slot, kv head) is code_i * 2^(e - 127), e the row's
+ * exponent byte (1 .. 254; 0 reads as a factor of zero in K and in read-back,
+ * which a zero-filled pool holds). e4m3 is the format with 4 exponent and 3
+ * fraction bits, largest value 448, no infinity. A pool takes d + 1 bytes a
+ * row where a 16-bit cache takes 2 d. Tables, slots and lengths are those of
+ * the 16-bit caches, and so is the block manager.
+ *
+ * Quantising cache write: what pa_reshape_and_cache does, into an 8-bit pool.
+ * A row's e is the smallest with max |x_i| <= 448 * 2^(e - 127), the maximum
+ * taken over its finite elements (at least 1); code_i is x_i * 2^(127 - e) at
+ * the nearest e4m3 value, ties to even. NaN and infinities become NaN codes. A
+ * row's values depend on that row alone. A slot must not occur twice among the
+ * non-negative slots: such a row would be left as a mix of the tokens' bytes.
+ * dtype: of key and value. Sizes, skipped and counted slots and errors as for
+ * pa_reshape_and_cache; num_kv_heads * head_dim at most 2^24.
+ */
+int pa_reshape_and_cache_fp8(const void* key, const void* value,
+                             void* key_cache, void* value_cache, uint8_t* cache_scales,
+                             const int64_t* slot_mapping, int num_tokens,
+                             int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                             pa_dtype dtype, cudaStream_t stream);
+
+/* pa_copy_blocks for an 8-bit pool: codes and exponent bytes of whole blocks. */
+int pa_copy_blocks_fp8(void* key_cache, void* value_cache, uint8_t* cache_scales,
+                       const int32_t* src, const int32_t* dst, int num_copies,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       cudaStream_t stream);
+
+/*
+ * Read-back: for every sequence s and token t < seq_lens[s], the K and V rows
+ * of the token as 16-bit values (each rounded once, nearest even; exact unless
+ * out of the type's range) at row out_start[s] + t of key_out and value_out
+ * [num_out_rows, Hkv, d]. Rows that no token maps to are left as they were.
+ * With out_start[s] a multiple of B the outputs are also 16-bit pools of
+ * consecutive blocks, ready for pa_prefill with a table of the block numbers
+ * out_start[s] / B, out_start[s] / B + 1, ...
+ * out_start: DEVICE int64 [num_seqs]. A token whose row is outside
+ * [0, num_out_rows) is skipped and counted; two tokens with one row race.
+ * Lengths above the table and block ids outside the pool as for pa_decode.
+ * num_seqs at most 65535; num_seqs or num_out_rows of 0 is a no-op.
+ * Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA.
+ */
+int pa_gather_cache_fp8(void* key_out, void* value_out,
+                        const void* key_cache, const void* value_cache,
+                        const uint8_t* cache_scales, const int32_t* block_tables,
+                        const int32_t* seq_lens, const int64_t* out_start, int64_t num_out_rows,
+                        int num_seqs, int num_kv_heads, int head_dim, int block_size,
+                        int max_blocks_per_seq, int num_blocks, pa_dtype dtype,
+                        cudaStream_t stream);
+
+/*
+ * pa_decode over an 8-bit pool, without a 16-bit copy of it: the same
+ * definition with K_t and V_t the pool's values. dtype is the type of query
+ * (and of out, unless that is fp32). Arithmetic is fp32 around fp16 products of
+ * the exact codes: the query enters as its fp16 value (bf16: scaled by a power
+ * of two for each head, so that its bits are kept), softmax weights, times V's
+ * factors, as the sum of two fp16 parts. Other arguments, sizes, the workspace
+ * (pa_decode_workspace_bytes) and errors as for pa_decode.
+ */
+int pa_decode_fp8(void* out, const void* query,
+                  const void* key_cache, const void* value_cache, const uint8_t* cache_scales,
+                  const int32_t* block_tables, const int32_t* seq_lens,
+                  int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                  int block_size, float scale,
+                  int max_blocks_per_seq, int num_blocks, int partition_tokens,
+                  pa_dtype dtype, pa_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/*
+ * pa_decode for batches in which groups of sequences begin with the same
+ * tokens: one system prompt before every request, or several candidates of one
+ * prompt (pa_bm_fork). The K/V of a group's prefix are read once for all its
+ * members and multiplied on the tensor cores; the rest of each sequence is
+ * read as in pa_decode, and the parts are joined by log-sum-exp.
+ *
+ * Group g holds the sequences group_start[g] .. group_start[g+1] - 1
+ * (group_start: DEVICE int32 [num_groups + 1], non-decreasing, from 0 to
+ * num_seqs; a group may be empty), and their first prefix_lens[g] tokens
+ * (DEVICE int32 [num_groups], any number, also one inside a block) are taken
+ * to be those of its first sequence: tokens t < prefix_lens[g] of every member
+ * are read through block_tables[group_start[g]], the others through the
+ * member's own table. Where the tables agree this is pa_decode.
+ * max_prefix_len and max_group_size (HOST) bound prefix_lens and the groups'
+ * sizes; they size the grid and the workspace. Longer prefixes are used up to
+ * max_prefix_len, members beyond max_group_size are computed alone, and both
+ * are counted by pa_bad_index_count, as are lengths or starts out of range. A
+ * sequence shorter than its group's prefix is computed alone, from its own
+ * table. If group_start decreases, outputs are unspecified (nothing outside
+ * the arrays is touched).
+ * num_groups in [1, 65535] (unless num_seqs is 0), num_blocks * block_size
+ * below 2^31. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
+ * with the zeroing and sharing rules of pa_decode_workspace_bytes. Arithmetic,
+ * other arguments and errors as for pa_decode.
+ */
+int pa_decode_shared_prefix(void* out, const void* query,
+                            const void* key_cache, const void* value_cache,
+                            const int32_t* block_tables, const int32_t* seq_lens,
+                            const int32_t* group_start, const int32_t* prefix_lens,
+                            int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                            int head_dim, int block_size, float scale,
+                            int max_blocks_per_seq, int num_blocks,
+                            int max_prefix_len, int max_group_size,
+                            pa_dtype dtype, pa_dtype out_dtype,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of pa_decode_shared_prefix; 0 for invalid sizes. */
+size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,
+                                               int num_kv_heads, int head_dim,
+                                               int max_blocks_per_seq, int block_size,
+                                               int max_prefix_len, int max_group_size);
+
+/*
  * Block manager: host-side bookkeeping of the pool ("PagedAttention by hand",
  * What is PagedAttention: free blocks are a stack of interchangeable ids, a
  * block table maps each sequence's logical blocks to physical ones; Why divide

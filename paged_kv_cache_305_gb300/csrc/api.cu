@@ -192,6 +192,23 @@ size_t prefill_v16_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_b
   return round_up(static_cast<size_t>(slots) * num_kv_heads * head_dim * 2, 256);
 }
 
+// How the prefix pass cuts the prefix: a CTA takes one chunk of tokens for 128
+// rows (members x query heads) of a group and a kv head. Chunks are whole
+// 64-token tiles, as long as they may be while the grid still has about
+// kPrefixCtas CTAs: each chunk leaves one fp32 piece per row behind.
+void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
+                 int max_prefix_len, int max_group_size) {
+  x->max_prefix_len = std::min(max_prefix_len, lmax);
+  x->max_group_size = max_group_size;
+  const int members = std::max(kPrefixRows / std::max(group, 1), 1);
+  const long long tiles = (static_cast<long long>(max_group_size) + members - 1) / members;
+  const long long per_chunk = std::max(tiles * num_groups * num_kv_heads, 1ll);
+  const long long want = std::max((kPrefixCtas + per_chunk - 1) / per_chunk, 1ll);
+  const long long t = std::max((x->max_prefix_len + want - 1) / want, static_cast<long long>(kPrefixMinChunk));
+  x->chunk_tokens = static_cast<int>(std::min((t + 63) / 64 * 64, 1ll << 30));
+  x->max_chunks = max_group_size > 0 ? (x->max_prefix_len + x->chunk_tokens - 1) / x->chunk_tokens : 0;
+}
+
 WorkspaceLayout workspace_layout(int num_seqs, int num_q_heads, int head_dim, int max_partitions) {
   WorkspaceLayout w{};
   const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
@@ -276,6 +293,128 @@ int pa_copy_blocks(void* key_cache, void* value_cache, const int32_t* src, const
   cudaError_t e = pa::launch_copy_blocks(key_cache, value_cache, src, dst, num_copies, block_bytes,
                                          num_blocks, bad, stream);
   if (e != cudaSuccess) return cuda_fail(e, "copy_blocks launch");
+  return PA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The checks that every entry point on an 8-bit pool shares; fills *p.
+int check_fp8_pool(const void* key_cache, const void* value_cache, const uint8_t* cache_scales,
+                   int num_kv_heads, int head_dim, int block_size, int num_blocks, bool pointers,
+                   pa::Fp8Pool* p) {
+  if (num_kv_heads < 1) return fail(PA_ERR_INVALID, "num_kv_heads %d < 1", num_kv_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PA_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
+  if (log2_pow2(block_size) < 0)
+    return fail(PA_ERR_UNSUPPORTED, "block_size %d (supported: powers of two up to 64)", block_size);
+  if (num_blocks < 1) return fail(PA_ERR_INVALID, "num_blocks %d < 1", num_blocks);
+  if (static_cast<long long>(num_kv_heads) * head_dim > (1ll << 24))
+    return fail(PA_ERR_UNSUPPORTED, "num_kv_heads * head_dim above 2^24");
+  if (pointers) {
+    if (!key_cache || !value_cache || !cache_scales)
+      return fail(PA_ERR_INVALID, "a pointer argument is NULL");
+    if (!aligned16(key_cache) || !aligned16(value_cache) || !aligned16(cache_scales))
+      return fail(PA_ERR_INVALID, "the caches and cache_scales must be 16-byte aligned");
+  }
+  p->key_cache = static_cast<uint8_t*>(const_cast<void*>(key_cache));
+  p->value_cache = static_cast<uint8_t*>(const_cast<void*>(value_cache));
+  p->scales = const_cast<uint8_t*>(cache_scales);
+  p->num_kv_heads = num_kv_heads;
+  p->head_dim = head_dim;
+  p->block_shift = log2_pow2(block_size);
+  p->num_blocks = num_blocks;
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_reshape_and_cache_fp8(const void* key, const void* value, void* key_cache,
+                             void* value_cache, uint8_t* cache_scales, const int64_t* slot_mapping,
+                             int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, pa_dtype dtype, cudaStream_t stream) {
+  g_error.clear();
+  int rc = check_dtype(dtype);
+  if (rc != PA_OK) return rc;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID, "num_tokens %d < 0", num_tokens);
+  pa::Fp8Pool p{};
+  rc = check_fp8_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
+                      num_blocks, num_tokens > 0, &p);
+  if (rc != PA_OK || num_tokens == 0) return rc;
+  if (!key || !value || !slot_mapping) return fail(PA_ERR_INVALID, "a pointer argument is NULL");
+  if (!aligned16(key) || !aligned16(value))
+    return fail(PA_ERR_INVALID, "key and value must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
+    return fail(PA_ERR_INVALID, "slot_mapping must be 8-byte aligned");
+  unsigned long long* bad = nullptr;
+  rc = bad_counter(&bad);
+  if (rc != PA_OK) return rc;
+  cudaError_t e = pa::launch_write_fp8(p, dtype == PA_BFLOAT16, key, value, slot_mapping,
+                                       num_tokens, bad, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "reshape_and_cache_fp8 launch");
+  return PA_OK;
+}
+
+int pa_copy_blocks_fp8(void* key_cache, void* value_cache, uint8_t* cache_scales,
+                       const int32_t* src, const int32_t* dst, int num_copies, int num_kv_heads,
+                       int head_dim, int block_size, int num_blocks, cudaStream_t stream) {
+  g_error.clear();
+  if (num_copies < 0) return fail(PA_ERR_INVALID, "num_copies %d < 0", num_copies);
+  pa::Fp8Pool p{};
+  int rc = check_fp8_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
+                          num_blocks, num_copies > 0, &p);
+  if (rc != PA_OK || num_copies == 0) return rc;
+  if (!src || !dst) return fail(PA_ERR_INVALID, "a pointer argument is NULL");
+  if (!aligned4(src) || !aligned4(dst)) return fail(PA_ERR_INVALID, "src and dst must be 4-byte aligned");
+  unsigned long long* bad = nullptr;
+  rc = bad_counter(&bad);
+  if (rc != PA_OK) return rc;
+  cudaError_t e = pa::launch_copy_blocks_fp8(p, src, dst, num_copies, bad, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "copy_blocks_fp8 launch");
+  return PA_OK;
+}
+
+int pa_gather_cache_fp8(void* key_out, void* value_out, const void* key_cache,
+                        const void* value_cache, const uint8_t* cache_scales,
+                        const int32_t* block_tables, const int32_t* seq_lens,
+                        const int64_t* out_start, int64_t num_out_rows, int num_seqs,
+                        int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                        int num_blocks, pa_dtype dtype, cudaStream_t stream) {
+  g_error.clear();
+  int rc = check_dtype(dtype);
+  if (rc != PA_OK) return rc;
+  if (num_seqs < 0) return fail(PA_ERR_INVALID, "num_seqs %d < 0", num_seqs);
+  if (num_seqs > 65535) return fail(PA_ERR_UNSUPPORTED, "num_seqs %d above 65535", num_seqs);
+  if (num_out_rows < 0)
+    return fail(PA_ERR_INVALID, "num_out_rows %lld < 0", static_cast<long long>(num_out_rows));
+  const bool work = num_seqs > 0 && num_out_rows > 0;
+  pa::Fp8Pool p{};
+  rc = check_fp8_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
+                      num_blocks, work, &p);
+  if (rc != PA_OK) return rc;
+  if (max_blocks_per_seq < 1)
+    return fail(PA_ERR_INVALID, "max_blocks_per_seq %d < 1", max_blocks_per_seq);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffll)
+    return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size overflows int");
+  if (!work) return PA_OK;
+  if (!key_out || !value_out || !block_tables || !seq_lens || !out_start)
+    return fail(PA_ERR_INVALID, "a pointer argument is NULL");
+  if (!aligned16(key_out) || !aligned16(value_out))
+    return fail(PA_ERR_INVALID, "key_out and value_out must be 16-byte aligned");
+  if (!aligned4(block_tables) || !aligned4(seq_lens))
+    return fail(PA_ERR_INVALID, "block_tables and seq_lens must be 4-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(out_start) & 7u) != 0)
+    return fail(PA_ERR_INVALID, "out_start must be 8-byte aligned");
+  unsigned long long* bad = nullptr;
+  rc = bad_counter(&bad);
+  if (rc != PA_OK) return rc;
+  cudaError_t e = pa::launch_gather_fp8(p, dtype == PA_BFLOAT16, key_out, value_out, num_out_rows,
+                                        block_tables, seq_lens, out_start, num_seqs,
+                                        max_blocks_per_seq, bad, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "gather_cache_fp8 launch");
   return PA_OK;
 }
 
@@ -432,12 +571,22 @@ size_t pa_decode_workspace_bytes(int num_seqs, int num_q_heads, int head_dim,
 
 namespace {
 
+// What the entry points beside pa_decode add to the call.
+struct DecodeExtra {
+  const void* new_key = nullptr;    // pa_decode_append
+  const void* new_value = nullptr;
+  const uint8_t* scales = nullptr;  // pa_decode_fp8: the caches hold e4m3 codes
+  bool fp8 = false;
+  bool prefix = false;              // pa_decode_shared_prefix
+  pa::PrefixArgs groups{};
+};
+
 int decode_impl(void* out, const void* query, const void* key_cache, const void* value_cache,
                 const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
                 int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale,
                 int max_blocks_per_seq, int num_blocks, int partition_tokens, pa_dtype dtype,
                 pa_dtype out_dtype, void* workspace, size_t workspace_bytes,
-                const void* new_key, const void* new_value, cudaStream_t stream) {
+                const DecodeExtra& extra, cudaStream_t stream) {
   g_error.clear();
   int rc = check_dtype(dtype);
   if (rc != PA_OK) return rc;
@@ -481,9 +630,16 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
     return fail(PA_ERR_INVALID, "out, query and the caches must be 16-byte aligned");
   if (!aligned4(block_tables) || !aligned4(seq_lens))
     return fail(PA_ERR_INVALID, "block_tables and seq_lens must be 4-byte aligned");
+  if (extra.fp8) {
+    if (!extra.scales) return fail(PA_ERR_INVALID, "a pointer argument is NULL");
+    if (!aligned16(extra.scales)) return fail(PA_ERR_INVALID, "cache_scales must be 16-byte aligned");
+  }
 
+  // a shared prefix adds the pieces of its chunks to every row
   const int parts = static_cast<int>((lmax + pt - 1) / pt);
-  const pa::WorkspaceLayout wl = pa::workspace_layout(num_seqs, num_q_heads, head_dim, parts);
+  const int pieces = parts + (extra.prefix ? extra.groups.max_chunks : 0);
+  const pa::WorkspaceLayout wl =
+      pa::workspace_layout(num_seqs, num_q_heads, head_dim, extra.prefix ? std::max(pieces, 2) : pieces);
   if (wl.total > 0) {
     if (workspace == nullptr || workspace_bytes < wl.total)
       return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", wl.total,
@@ -530,11 +686,12 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = num_blocks;
   a.partition_tokens = pt;
-  a.max_partitions = parts;
+  a.max_partitions = pieces;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.out_f32 = out_dtype == PA_FLOAT32 ? 1 : 0;
-  a.new_key = new_key;
-  a.new_value = new_value;
+  a.new_key = extra.new_key;
+  a.new_value = extra.new_value;
+  a.scales = extra.scales;
   char* ws = static_cast<char*>(workspace);
   a.ws_count = wl.total ? reinterpret_cast<int*>(ws + wl.count_off) : nullptr;
   // the trailing partitions of rows are handed out at run time only with a
@@ -546,7 +703,9 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   a.ws_lse = wl.total ? reinterpret_cast<float*>(ws + wl.lse_off) : nullptr;
   a.ws_out = wl.total ? reinterpret_cast<float*>(ws + wl.out_off) : nullptr;
   a.bad = bad;
-  cudaError_t e = pa::launch_decode(a, head_dim, dtype == PA_BFLOAT16, sms, stream);
+  cudaError_t e = extra.fp8 || extra.prefix
+                      ? pa::launch_decode_rows(a, extra.groups, head_dim, dtype == PA_BFLOAT16, stream)
+                      : pa::launch_decode(a, head_dim, dtype == PA_BFLOAT16, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
   return PA_OK;
 }
@@ -563,7 +722,7 @@ int pa_decode(void* out, const void* query, const void* key_cache, const void* v
   return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
                      num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes,
-                     nullptr, nullptr, stream);
+                     DecodeExtra{}, stream);
 }
 
 int pa_decode_append(void* out, const void* query, const void* new_key, const void* new_value,
@@ -578,10 +737,94 @@ int pa_decode_append(void* out, const void* query, const void* new_key, const vo
     if (!aligned16(new_key) || !aligned16(new_value))
       return fail(PA_ERR_INVALID, "new_key and new_value must be 16-byte aligned");
   }
+  DecodeExtra extra;
+  extra.new_key = new_key;
+  extra.new_value = new_value;
   return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
                      num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes,
-                     new_key, new_value, stream);
+                     extra, stream);
+}
+
+int pa_decode_fp8(void* out, const void* query, const void* key_cache, const void* value_cache,
+                  const uint8_t* cache_scales, const int32_t* block_tables,
+                  const int32_t* seq_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                  int head_dim, int block_size, float scale, int max_blocks_per_seq,
+                  int num_blocks, int partition_tokens, pa_dtype dtype, pa_dtype out_dtype,
+                  void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  DecodeExtra extra;
+  extra.fp8 = true;
+  extra.scales = cache_scales;
+  return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
+                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes,
+                     extra, stream);
+}
+
+size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,
+                                               int num_kv_heads, int head_dim,
+                                               int max_blocks_per_seq, int block_size,
+                                               int max_prefix_len, int max_group_size) {
+  if (num_seqs < 0 || num_groups < 1 || num_q_heads < 1 || num_kv_heads < 1 ||
+      num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > pa::kMaxGroup ||
+      (head_dim != 64 && head_dim != 128) || max_blocks_per_seq < 1 || log2_pow2(block_size) < 0 ||
+      max_prefix_len < 0 || max_group_size < 0 ||
+      static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffll)
+    return 0;
+  std::string saved = g_error;
+  int pt = 0;
+  const int rc = resolve_partition(0, block_size, max_blocks_per_seq, &pt);
+  g_error = saved;
+  if (rc != PA_OK) return 0;
+  pa::PrefixArgs x{};
+  pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads,
+                  max_blocks_per_seq * block_size, max_prefix_len, max_group_size);
+  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
+  const long long pieces = (lmax + pt - 1) / pt + x.max_chunks;
+  return pa::workspace_layout(num_seqs, num_q_heads, head_dim,
+                              static_cast<int>(std::max(pieces, 2ll)))
+      .total;
+}
+
+int pa_decode_shared_prefix(void* out, const void* query, const void* key_cache,
+                            const void* value_cache, const int32_t* block_tables,
+                            const int32_t* seq_lens, const int32_t* group_start,
+                            const int32_t* prefix_lens, int num_seqs, int num_groups,
+                            int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                            float scale, int max_blocks_per_seq, int num_blocks,
+                            int max_prefix_len, int max_group_size, pa_dtype dtype,
+                            pa_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  g_error.clear();
+  if (num_seqs > 0) {
+    if (num_groups < 1) return fail(PA_ERR_INVALID, "num_groups %d < 1", num_groups);
+    if (num_groups > 65535) return fail(PA_ERR_UNSUPPORTED, "num_groups %d above 65535", num_groups);
+    if (max_prefix_len < 0) return fail(PA_ERR_INVALID, "max_prefix_len %d < 0", max_prefix_len);
+    if (max_group_size < 0) return fail(PA_ERR_INVALID, "max_group_size %d < 0", max_group_size);
+    if (!group_start || !prefix_lens)
+      return fail(PA_ERR_INVALID, "group_start / prefix_lens is NULL");
+    if (!aligned4(group_start) || !aligned4(prefix_lens))
+      return fail(PA_ERR_INVALID, "group_start and prefix_lens must be 4-byte aligned");
+    if (log2_pow2(block_size) >= 0 &&
+        !pa::prefill_tc_supported(block_size, static_cast<long long>(num_blocks) * block_size))
+      return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size is 2^31 slots or more");
+  }
+  DecodeExtra extra;
+  extra.prefix = true;
+  if (num_seqs > 0 && num_kv_heads >= 1 && num_q_heads >= num_kv_heads && max_blocks_per_seq >= 1 &&
+      log2_pow2(block_size) >= 0) {  // other sizes are rejected before the plan is used
+    pa::PrefixArgs& x = extra.groups;
+    const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
+    x.group_start = group_start;
+    x.prefix_lens = prefix_lens;
+    x.num_groups = num_groups;
+    x.num_seqs = num_seqs;
+    pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads,
+                    static_cast<int>(std::min(lmax, 0x7fffffffll)), max_prefix_len, max_group_size);
+  }
+  return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
+                     num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, extra, stream);
 }
 
 }  // extern "C"

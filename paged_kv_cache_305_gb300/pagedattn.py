@@ -25,7 +25,9 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_bytes", "pa_decode",
             "pa_bm_append", "pa_bm_block_tables", "pa_bm_num_free_blocks", "pa_bm_ref_count",
             "pa_decode_append", "pa_prefill", "pa_wait_timeout_count",
             "pa_testing_prefill_stalled", "pa_prefill_workspace_bytes",
-            "pa_decode_partition_tokens")
+            "pa_decode_partition_tokens", "pa_reshape_and_cache_fp8", "pa_copy_blocks_fp8",
+            "pa_gather_cache_fp8", "pa_decode_fp8", "pa_decode_shared_prefix",
+            "pa_decode_shared_prefix_workspace_bytes")
 PA_ERR_CAPACITY = -5
 
 _lib = None
@@ -80,6 +82,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.pa_testing_prefill_stalled.restype = i32
     L.pa_copy_blocks.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]
     L.pa_copy_blocks.restype = i32
+    L.pa_reshape_and_cache_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]
+    L.pa_reshape_and_cache_fp8.restype = i32
+    L.pa_copy_blocks_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]
+    L.pa_copy_blocks_fp8.restype = i32
+    L.pa_gather_cache_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, i32, i32, i32,
+                                      i32, i32, i32, i32, vp]
+    L.pa_gather_cache_fp8.restype = i32
+    L.pa_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float,
+                                i32, i32, i32, i32, i32, vp, sz, vp]
+    L.pa_decode_fp8.restype = i32
+    L.pa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                          i32, ctypes.c_float, i32, i32, i32, i32, i32, i32, vp, sz,
+                                          vp]
+    L.pa_decode_shared_prefix.restype = i32
+    L.pa_decode_shared_prefix_workspace_bytes.argtypes = [i32] * 9
+    L.pa_decode_shared_prefix_workspace_bytes.restype = sz
     ip = ctypes.POINTER(ctypes.c_int)
     L.pa_bm_create.argtypes = [i32, i32, i32, ctypes.POINTER(vp)]
     L.pa_bm_create.restype = i32
@@ -400,6 +418,205 @@ def copy_blocks(key_cache: torch.Tensor, value_cache: torch.Tensor, src: torch.T
         _check(L.pa_copy_blocks(key_cache.data_ptr(), value_cache.data_ptr(), src.data_ptr(),
                                 dst.data_ptr(), src.numel(), Hkv, d, B, NB, _dtype_code(key_cache),
                                 _stream(key_cache, stream)))
+
+
+def _need_fp8_pool(key_cache: torch.Tensor, value_cache: torch.Tensor,
+                   cache_scales: torch.Tensor) -> None:
+    _need(key_cache.dim() == 4 and value_cache.shape == key_cache.shape, "cache shape mismatch")
+    _need(key_cache.dtype == value_cache.dtype == torch.float8_e4m3fn, "the caches must be float8_e4m3fn")
+    NB, B, Hkv, _ = key_cache.shape
+    _need(cache_scales.dtype == torch.uint8 and cache_scales.shape == (NB, Hkv, 2, B),
+          "cache_scales must be uint8 [num_blocks, num_kv_heads, 2, block_size]")
+
+
+def _need_same_device(first: torch.Tensor, *rest: torch.Tensor) -> None:
+    for t in (first,) + rest:
+        _need(t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors")
+        _need(t.device == first.device, "tensors must be on one device")
+
+
+def alloc_fp8_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """Zero-filled 8-bit pool: (key_cache, value_cache, cache_scales)."""
+    shape = (num_blocks, block_size, num_kv_heads, head_dim)
+    codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    scales = torch.zeros((num_blocks, num_kv_heads, 2, block_size), dtype=torch.uint8, device=device)
+    return codes[0], codes[1], scales
+
+
+def reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor,
+                          value_cache: torch.Tensor, cache_scales: torch.Tensor,
+                          slot_mapping: torch.Tensor, stream=None) -> None:
+    """Quantise key/value [T, Hkv, d] rows into the 8-bit pool at slot_mapping [T] (int64).
+
+    Caches float8_e4m3fn [NB, B, Hkv, d]; ``cache_scales`` uint8 [NB, Hkv, 2,
+    B] receives each row's biased power-of-two exponent (K at index 0, V at 1):
+    an element is its code times 2**(byte - 127). Non-negative slots must be
+    distinct.
+    """
+    _need_fp8_pool(key_cache, value_cache, cache_scales)
+    _need_same_device(key, value, key_cache, value_cache, cache_scales, slot_mapping)
+    NB, B, Hkv, d = key_cache.shape
+    T = key.shape[0]
+    _need(key.shape == (T, Hkv, d) and value.shape == (T, Hkv, d), "key/value shape mismatch")
+    _need(key.dtype == value.dtype, "dtype mismatch")
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,),
+          "slot_mapping must be int64 [num_tokens]")
+    code = _dtype_code(key)
+    L = load_library()
+    with torch.cuda.device(key.device):
+        _check(L.pa_reshape_and_cache_fp8(key.data_ptr(), value.data_ptr(), key_cache.data_ptr(),
+                                          value_cache.data_ptr(), cache_scales.data_ptr(),
+                                          slot_mapping.data_ptr(), T, Hkv, d, B, NB, code,
+                                          _stream(key, stream)))
+
+
+def copy_blocks_fp8(key_cache: torch.Tensor, value_cache: torch.Tensor, cache_scales: torch.Tensor,
+                    src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """:func:`copy_blocks` for an 8-bit pool (codes and exponent bytes)."""
+    _need_fp8_pool(key_cache, value_cache, cache_scales)
+    _need_same_device(key_cache, value_cache, cache_scales, src, dst)
+    _need(src.dtype == torch.int32 and dst.dtype == torch.int32 and src.shape == dst.shape
+          and src.dim() == 1, "src/dst must be 1-D int32 tensors")
+    NB, B, Hkv, d = key_cache.shape
+    L = load_library()
+    with torch.cuda.device(key_cache.device):
+        _check(L.pa_copy_blocks_fp8(key_cache.data_ptr(), value_cache.data_ptr(),
+                                    cache_scales.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                                    src.numel(), Hkv, d, B, NB, _stream(key_cache, stream)))
+
+
+def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: torch.Tensor,
+                     value_cache: torch.Tensor, cache_scales: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, out_start: torch.Tensor,
+                     stream=None) -> None:
+    """Read sequences of an 8-bit pool back as 16-bit rows.
+
+    Token t of sequence s goes to row ``out_start[s] + t`` (int64 [S]) of
+    ``key_out`` / ``value_out`` [rows, Hkv, d] (float16 or bfloat16); other
+    rows stay as they are. With starts that are multiples of B the outputs,
+    viewed as [rows / B, B, Hkv, d], are pools for :func:`prefill`.
+    """
+    _need_fp8_pool(key_cache, value_cache, cache_scales)
+    _need_same_device(key_out, value_out, key_cache, value_cache, cache_scales, block_tables,
+                      seq_lens, out_start)
+    NB, B, Hkv, d = key_cache.shape
+    _need(key_out.dim() == 3 and key_out.shape[1:] == (Hkv, d) and value_out.shape == key_out.shape
+          and key_out.dtype == value_out.dtype, "key_out/value_out dtype or shape mismatch")
+    S = seq_lens.shape[0]
+    _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32,
+          "block_tables and seq_lens must be int32")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
+          "block_tables/seq_lens shape mismatch")
+    _need(out_start.dtype == torch.int64 and out_start.shape == (S,), "out_start must be int64 [num_seqs]")
+    code = _dtype_code(key_out)
+    L = load_library()
+    with torch.cuda.device(key_cache.device):
+        _check(L.pa_gather_cache_fp8(key_out.data_ptr(), value_out.data_ptr(), key_cache.data_ptr(),
+                                     value_cache.data_ptr(), cache_scales.data_ptr(),
+                                     block_tables.data_ptr(), seq_lens.data_ptr(),
+                                     out_start.data_ptr(), key_out.shape[0], S, Hkv, d, B,
+                                     block_tables.shape[1], NB, code, _stream(key_cache, stream)))
+
+
+def _need_decode(out: torch.Tensor, query: torch.Tensor, head_dim: int, block_tables: torch.Tensor,
+                 seq_lens: torch.Tensor, workspace: Optional[torch.Tensor]):
+    """The checks of decode calls; returns (out dtype code, workspace pointer, workspace bytes)."""
+    _need(query.dim() == 3 and query.shape[2] == head_dim, "cache shape mismatch")
+    _need(out.shape == query.shape and out.dtype in (query.dtype, torch.float32),
+          "out dtype or shape mismatch")
+    S = query.shape[0]
+    _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32,
+          "block_tables and seq_lens must be int32")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
+          "block_tables/seq_lens shape mismatch")
+    code = PA_FLOAT32 if out.dtype == torch.float32 else _dtype_code(query)
+    if workspace is None:
+        return code, 0, 0
+    _need_same_device(query, workspace)
+    return code, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+               value_cache: torch.Tensor, cache_scales: torch.Tensor, block_tables: torch.Tensor,
+               seq_lens: torch.Tensor, scale: float, partition_tokens: int = 0,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """:func:`decode` over an 8-bit pool (see :func:`reshape_and_cache_fp8`).
+
+    ``query`` is float16 or bfloat16; the workspace comes from
+    :func:`alloc_workspace` with the 8-bit ``key_cache``.
+    """
+    _need_fp8_pool(key_cache, value_cache, cache_scales)
+    NB, B, Hkv, d = key_cache.shape
+    odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace)
+    _need_same_device(out, query, key_cache, value_cache, cache_scales, block_tables, seq_lens)
+    S, Hq, _ = query.shape
+    L = load_library()
+    with torch.cuda.device(query.device):
+        _check(L.pa_decode_fp8(out.data_ptr(), query.data_ptr(), key_cache.data_ptr(),
+                               value_cache.data_ptr(), cache_scales.data_ptr(),
+                               block_tables.data_ptr(), seq_lens.data_ptr(), S, Hq, Hkv, d, B,
+                               float(scale), block_tables.shape[1], NB, partition_tokens,
+                               _dtype_code(query), odt, ws_ptr, ws_bytes, _stream(query, stream)))
+    return out
+
+
+def decode_shared_prefix_workspace_bytes(num_seqs: int, num_groups: int, num_q_heads: int,
+                                         num_kv_heads: int, head_dim: int, max_blocks_per_seq: int,
+                                         block_size: int, max_prefix_len: int,
+                                         max_group_size: int) -> int:
+    return int(load_library().pa_decode_shared_prefix_workspace_bytes(
+        num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+        max_prefix_len, max_group_size))
+
+
+def alloc_shared_prefix_workspace(query: torch.Tensor, key_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, group_start: torch.Tensor,
+                                  max_prefix_len: int, max_group_size: int) -> torch.Tensor:
+    """Zero-filled workspace for :func:`decode_shared_prefix` with these shapes."""
+    S, Hq, d = query.shape
+    n = decode_shared_prefix_workspace_bytes(S, group_start.shape[0] - 1, Hq, key_cache.shape[2], d,
+                                             block_tables.shape[1], key_cache.shape[1],
+                                             max_prefix_len, max_group_size)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=query.device)
+
+
+def decode_shared_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                         value_cache: torch.Tensor, block_tables: torch.Tensor,
+                         seq_lens: torch.Tensor, group_start: torch.Tensor,
+                         prefix_lens: torch.Tensor, max_prefix_len: int, max_group_size: int,
+                         scale: float, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """:func:`decode` for groups of sequences that begin with the same tokens.
+
+    Sequences ``group_start[g] .. group_start[g+1] - 1`` (int32 [groups + 1])
+    share their first ``prefix_lens[g]`` tokens (int32 [groups]), which are read
+    once, through the first one's table row. ``max_prefix_len`` and
+    ``max_group_size`` bound both on the host. The workspace comes from
+    :func:`alloc_shared_prefix_workspace`.
+    """
+    NB, B, Hkv, d = key_cache.shape
+    _need(value_cache.shape == key_cache.shape, "cache shape mismatch")
+    _need(query.dtype == key_cache.dtype == value_cache.dtype, "query/cache dtype mismatch")
+    odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace)
+    _need(group_start.dtype == torch.int32 and prefix_lens.dtype == torch.int32,
+          "group_start and prefix_lens must be int32")
+    _need(prefix_lens.dim() == 1 and group_start.shape == (prefix_lens.shape[0] + 1,),
+          "group_start/prefix_lens shape mismatch")
+    _need_same_device(out, query, key_cache, value_cache, block_tables, seq_lens, group_start,
+                      prefix_lens)
+    S, Hq, _ = query.shape
+    L = load_library()
+    with torch.cuda.device(query.device):
+        _check(L.pa_decode_shared_prefix(out.data_ptr(), query.data_ptr(), key_cache.data_ptr(),
+                                         value_cache.data_ptr(), block_tables.data_ptr(),
+                                         seq_lens.data_ptr(), group_start.data_ptr(),
+                                         prefix_lens.data_ptr(), S, prefix_lens.shape[0], Hq, Hkv, d,
+                                         B, float(scale), block_tables.shape[1], NB,
+                                         int(max_prefix_len), int(max_group_size),
+                                         _dtype_code(query), odt, ws_ptr, ws_bytes,
+                                         _stream(query, stream)))
+    return out
 
 
 class BlockManager:
