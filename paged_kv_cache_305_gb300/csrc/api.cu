@@ -703,9 +703,34 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   a.ws_lse = wl.total ? reinterpret_cast<float*>(ws + wl.lse_off) : nullptr;
   a.ws_out = wl.total ? reinterpret_cast<float*>(ws + wl.out_off) : nullptr;
   a.bad = bad;
-  cudaError_t e = extra.fp8 || extra.prefix
-                      ? pa::launch_decode_rows(a, extra.groups, head_dim, dtype == PA_BFLOAT16, stream)
-                      : pa::launch_decode(a, head_dim, dtype == PA_BFLOAT16, sms, stream);
+  const bool bf16 = dtype == PA_BFLOAT16;
+  a.groups = extra.groups;
+  if (extra.prefix) {
+    pa::PrefillArgs x{};
+    x.query = query;
+    x.key_cache = key_cache;
+    x.value_cache = value_cache;
+    x.block_tables = block_tables;
+    x.num_q_heads = num_q_heads;
+    x.num_kv_heads = num_kv_heads;
+    x.group = group;
+    x.block_shift = shift;
+    x.max_blocks_per_seq = max_blocks_per_seq;
+    x.num_blocks = num_blocks;
+    x.scale_log2 = a.scale_log2;
+    x.bad = bad;
+    rc = counter(true, &x.timeouts);
+    if (rc != PA_OK) return rc;
+    x.groups = extra.groups;
+    x.max_pieces = pieces;
+    x.ws_lse = a.ws_lse;
+    x.ws_out = a.ws_out;
+    cudaError_t pe = pa::launch_prefix_pass(x, head_dim, bf16, stream);
+    if (pe != cudaSuccess) return cuda_fail(pe, "shared prefix launch");
+  }
+  cudaError_t e = extra.prefix ? pa::launch_decode_prefix(a, head_dim, bf16, sms, stream)
+                  : extra.fp8  ? pa::launch_decode_fp8(a, head_dim, bf16, sms, stream)
+                               : pa::launch_decode(a, head_dim, bf16, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
   return PA_OK;
 }

@@ -1,0 +1,12 @@
+// The second half of pa_decode_shared_prefix: every sequence's tokens behind its
+// group's prefix, and the merge with the pieces of the prefix pass.
+#include "decode_kernel.cuh"
+
+namespace pa {
+
+cudaError_t launch_decode_prefix(const DecodeArgs& a, int head_dim, bool bf16, int num_sms,
+                                 cudaStream_t stream) {
+  return launch_mode<kPrefix>(a, head_dim, bf16, num_sms, stream);
+}
+
+}  // namespace pa

@@ -16,6 +16,18 @@ constexpr long long kLongContextTokens = 4096;
 constexpr int kMaxPartitionTokens = 1 << 20;
 constexpr int kMaxGroup = 16;  // query heads per kv head (rows of one mma tile)
 
+// Groups of sequences that share a prefix (pa_decode_shared_prefix).
+struct PrefixArgs {
+  const int32_t* group_start;  // [num_groups + 1]
+  const int32_t* prefix_lens;  // [num_groups]
+  int num_groups;              // 0: no sharing
+  int num_seqs;
+  int max_prefix_len;
+  int max_group_size;
+  int chunk_tokens;  // tokens of the prefix that one CTA of the prefix pass takes
+  int max_chunks;    // ceil(max_prefix_len / chunk_tokens)
+};
+
 struct DecodeArgs {
   void* out;
   const void* query;
@@ -45,18 +57,7 @@ struct DecodeArgs {
   int dyn_percent;     // share (%) of each row's partitions handed out at run time
   unsigned long long* bad;  // device counter of rejected indices
   const uint8_t* scales;    // 8-bit caches: exponent bytes [NB, Hkv, 2, B], else null
-};
-
-// Groups of sequences that share a prefix (pa_decode_shared_prefix).
-struct PrefixArgs {
-  const int32_t* group_start;  // [num_groups + 1]
-  const int32_t* prefix_lens;  // [num_groups]
-  int num_groups;              // 0: no sharing
-  int num_seqs;
-  int max_prefix_len;
-  int max_group_size;
-  int chunk_tokens;  // tokens of the prefix that one CTA of the prefix pass takes
-  int max_chunks;    // ceil(max_prefix_len / chunk_tokens)
+  PrefixArgs groups;        // shared prefixes (num_groups 0: none)
 };
 
 // An 8-bit pool: e4m3 codes [NB, B, Hkv, d] and exponent bytes [NB, Hkv, 2, B].
@@ -91,6 +92,11 @@ struct PrefillArgs {
   unsigned long long* timeouts;  // bounded waits that gave up (tensor-core kernel)
   int stall_for_test;  // 1: the product thread waits on a barrier nothing signals
   void* v16;           // bf16 caches: fp16 copy of the value rows [S * MB * B, Hkv, d], or null
+  PrefixArgs groups;   // the prefix pass: its groups, query tiles a group (set by the
+  int prefix_tiles;    // launcher), and the pieces it leaves
+  int max_pieces;      // pieces a row has room for in ws_lse and ws_out
+  float* ws_lse;
+  float* ws_out;
 };
 
 // Bytes of the fp16 copy of the value rows the bf16 prefill can use (0 when
@@ -101,6 +107,7 @@ size_t prefill_v16_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_b
 // Tensor-core (tcgen05) prefill: block sizes 1..64 (TMA block copies from 8
 // up, 16-byte row copies below), fewer than 2^31 slots.
 bool prefill_tc_supported(int block_size, long long num_slots);
+cudaError_t launch_prefix_pass(PrefillArgs a, int head_dim, bool bf16, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, int head_dim, bool bf16, int max_query_len,
                               cudaStream_t stream);
 
@@ -139,8 +146,10 @@ constexpr int kMaxSegments = 64;
 cudaError_t launch_decode(const DecodeArgs& a, int head_dim, bool bf16, int num_sms,
                           cudaStream_t stream);
 
-cudaError_t launch_decode_rows(const DecodeArgs& a, const PrefixArgs& x, int head_dim, bool bf16,
-                               cudaStream_t stream);
+cudaError_t launch_decode_fp8(const DecodeArgs& a, int head_dim, bool bf16, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_decode_prefix(const DecodeArgs& a, int head_dim, bool bf16, int num_sms,
+                                 cudaStream_t stream);
 
 cudaError_t launch_write_fp8(const Fp8Pool& p, bool bf16, const void* key, const void* value,
                              const int64_t* slot_mapping, int num_tokens, unsigned long long* bad,

@@ -34,16 +34,25 @@
 // Tensor memory (256 columns): S at 0, P at 64, O at 128, so the product of
 // the next S overlaps the whole softmax of the current tile. All waits are
 // bounded; a wait that gives up is counted and the CTA winds down.
+//
+// The prefix pass of pa_decode_shared_prefix is the same kernel with PREFIX:
+// the sequences of a group take the place of a chunk's positions (a row is a
+// member and a head), every row attends to all tokens of the CTA's chunk of
+// the prefix, read through the table of the group's first member, and the
+// result is left as a piece (normalised fp32 row and base-2 log-sum-exp) for
+// the merge of the decode kernel.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
 #include "internal.h"
+#include "prefix.cuh"
 #include "ptx.cuh"
 #include "tc.cuh"
 
@@ -172,8 +181,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
 
 // SINGLE: fp16 weights in one P V product with fp16 V (fp16 caches, or bf16
 // caches whose value rows were first converted to an fp16 copy, v16);
-// otherwise bf16 weights as a head plus the rounding of the remainder.
-template <typename Ty, int D, bool SINGLE>
+// otherwise weights of the input type as a head plus the rounding of the
+// remainder (bf16 prefill without the copy, and both types in the prefix pass).
+template <typename Ty, int D, bool SINGLE, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const PrefillArgs a) {
@@ -182,28 +192,42 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
   constexpr int kChunks = D / 8;  // 16-byte chunks per row
   constexpr int kKSteps = D / 16;
 
-  const int qt = gridDim.x - 1 - blockIdx.x;  // longest tiles first
+  // longest tiles first; PREFIX: the tiles of one chunk next to each other
+  const int qt = PREFIX ? blockIdx.x % a.prefix_tiles : gridDim.x - 1 - blockIdx.x;
   const int h = blockIdx.y;
-  const int s = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group;
   const int P = kRows / G;  // query positions per tile
   const int shift = a.block_shift;
   const int Lmax = a.max_blocks_per_seq << shift;
 
-  int L = a.seq_lens[s];
-  const int q0 = a.query_start[s];
-  int Q = a.query_start[s + 1] - q0;
-  if (L < 0 || L > Lmax || Q < 0 || Q > L) {
-    if (qt == 0 && h == 0 && tid == 0) atomicAdd(a.bad, 1ull);
-    L = min(max(L, 0), Lmax);
-    Q = min(max(Q, 0), L);
+  // s: row of the block table; L: tokens before it are read, from key tile
+  // tile0 on; q0, Q: first query row and number of positions (or members)
+  int s = blockIdx.z, L, q0, Q, tile0 = 0;
+  if constexpr (PREFIX) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    q0 = s = group_begin(a.groups, blockIdx.z);
+    Q = min(group_begin(a.groups, blockIdx.z + 1) - q0, a.groups.max_group_size);
+    const int c0 = static_cast<int>(blockIdx.x / a.prefix_tiles) * a.groups.chunk_tokens;
+    const int n = group_prefix(a.groups, blockIdx.z, Lmax);
+    if (c0 >= n) return;
+    L = min(n - c0, a.groups.chunk_tokens) + c0;
+    tile0 = c0 / kKeys;
+  } else {
+    L = a.seq_lens[s];
+    q0 = a.query_start[s];
+    Q = a.query_start[s + 1] - q0;
+    if (L < 0 || L > Lmax || Q < 0 || Q > L) {
+      if (qt == 0 && h == 0 && tid == 0) atomicAdd(a.bad, 1ull);
+      L = min(max(L, 0), Lmax);
+      Q = min(max(Q, 0), L);
+    }
   }
   const int j0 = qt * P;
   if (j0 >= Q) return;
   const int jn = min(P, Q - j0);
-  const int last_pos = L - Q + j0 + jn - 1;
-  const int ntiles = last_pos / kKeys + 1;
+  const int last_pos = PREFIX ? L - 1 : L - Q + j0 + jn - 1;
+  const int ntiles = last_pos / kKeys + 1 - tile0;
 
   extern __shared__ unsigned char raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
@@ -270,7 +294,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     // ---------------- softmax: thread tid owns query row tid (TMEM lane tid)
     const int r = tid;
     const bool row_valid = r < P * G && r / G < jn;
-    const int qp = row_valid ? L - Q + j0 + r / G : last_pos;  // causal limit
+    // causal limit; PREFIX: the chunk's end, for every row
+    const int qp = (row_valid && !PREFIX ? L - Q + j0 + r / G : last_pos) - tile0 * kKeys;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float sl2 = fabsf(a.scale_log2);  // the query tile carries the sign
     float m = -INFINITY, l = 0.f;  // running max (base-2 units) and sum of weights
@@ -355,10 +380,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
           if constexpr (!SINGLE) {
             rs[i & 3] += p0;
             rs[i & 3] += p1;
-            const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
-            ph[i] = __byte_perm(b0, b1, 0x7632);
-            pl[i] = Ty::pack(p0 - __uint_as_float(b0 & 0xffff0000u),
-                             p1 - __uint_as_float(b1 & 0xffff0000u));
+            if constexpr (Ty::kIsBf16) {
+              const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+              ph[i] = __byte_perm(b0, b1, 0x7632);
+              pl[i] = Ty::pack(p0 - __uint_as_float(b0 & 0xffff0000u),
+                               p1 - __uint_as_float(b1 & 0xffff0000u));
+            } else {
+              ph[i] = Ty::pack(p0, p1);
+              const float2 hv = Ty::unpack(ph[i]);
+              pl[i] = Ty::pack(p0 - hv.x, p1 - hv.y);
+            }
           } else {
             ph[i] = F16::pack(p0, p1);
             rs[i & 3] = add_f16x2(rs[i & 3], ph[i]);
@@ -409,16 +440,21 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     if (ok) {
       tc::tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const size_t row = static_cast<size_t>(q0 + j0 + r / G) * a.num_q_heads +
-                         static_cast<size_t>(h) * G + r % G;
+      size_t row = static_cast<size_t>(q0 + j0 + r / G) * a.num_q_heads +
+                   static_cast<size_t>(h) * G + r % G;
+      if constexpr (PREFIX) {  // the chunk's piece of the row
+        row = row * a.max_pieces + blockIdx.x / a.prefix_tiles;
+        if (row_valid) a.ws_lse[row] = l > 0.f ? m + __log2f(l) : -INFINITY;
+      }
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         uint32_t x[16];
         tc::tmem_ld16(lane_addr + kColO + 16 * c, x);
         tc::tmem_ld_wait16(x);
         if (!row_valid) continue;
-        if (a.out_f32) {
-          float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + 16 * c);
+        if (PREFIX || a.out_f32) {
+          float4* o = reinterpret_cast<float4*>((PREFIX ? a.ws_out : static_cast<float*>(a.out)) +
+                                                row * D + 16 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             o[i] = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
@@ -467,7 +503,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
       id = -1;
       valid = 0;
       if (lane < nb && jt < ntiles) {
-        const int blk = jt * nb + lane;
+        const int blk = (tile0 + jt) * nb + lane;
         valid = min(max(L - (blk << shift), 0), B);
         if (valid > 0) {
           if (from_v16) {
@@ -538,7 +574,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
       auto row_slots = [&](int jt, int (&sr)[2]) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int t = jt * kKeys + lane + 32 * u;
+          const int t = (tile0 + jt) * kKeys + lane + 32 * u;
           sr[u] = -1;
           if (jt < ntiles && t < L) {
             if (from_v16) {
@@ -767,15 +803,15 @@ bool encode_cache_map(CUtensorMap* map, const void* cache, bool bf16, long long 
 
 // after_convert: launched right behind the conversion pass as a programmatic
 // dependent launch (its CTAs may start while the pass is finishing).
-template <typename Ty, int D, bool SINGLE>
+template <typename Ty, int D, bool SINGLE, bool PREFIX>
 cudaError_t launch_kernel(const CUtensorMap& km, const CUtensorMap& vm, const PrefillArgs& a,
-                          int tiles, bool after_convert, cudaStream_t stream) {
-  auto kern = paged_prefill_tc_kernel<Ty, D, SINGLE>;
+                          dim3 grid, bool after_convert, cudaStream_t stream) {
+  auto kern = paged_prefill_tc_kernel<Ty, D, SINGLE, PREFIX>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcGeo<D>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles, a.num_kv_heads, a.num_seqs);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = TcGeo<D>::kSmem;
   cfg.stream = stream;
@@ -792,6 +828,7 @@ cudaError_t launch_tc(const PrefillArgs& a, int max_query_len, cudaStream_t stre
   const int P = kRows / a.group;
   const int tiles = (max_query_len + P - 1) / P;
   if (tiles < 1) return cudaSuccess;
+  const dim3 grid(tiles, a.num_kv_heads, a.num_seqs);
   const int B = 1 << a.block_shift;
   const long long slots = static_cast<long long>(a.num_blocks) << a.block_shift;
   CUtensorMap km, vm;
@@ -806,11 +843,25 @@ cudaError_t launch_tc(const PrefillArgs& a, int max_query_len, cudaStream_t stre
     v16_convert_kernel<D><<<dim3(a.max_blocks_per_seq, a.num_seqs), 256, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_kernel<Ty, D, true>(km, vm, a, tiles, true, stream);
+    return launch_kernel<Ty, D, true, false>(km, vm, a, grid, true, stream);
   }
   if (!encode_cache_map(&vm, a.value_cache, Ty::kIsBf16, slots, a.num_kv_heads, D, B))
     return cudaErrorInvalidValue;
-  return launch_kernel<Ty, D, !Ty::kIsBf16>(km, vm, a, tiles, false, stream);
+  return launch_kernel<Ty, D, !Ty::kIsBf16, false>(km, vm, a, grid, false, stream);
+}
+
+template <typename Ty, int D>
+cudaError_t launch_prefix(const PrefillArgs& a, cudaStream_t stream) {
+  const int B = 1 << a.block_shift;
+  const long long slots = static_cast<long long>(a.num_blocks) << a.block_shift;
+  CUtensorMap km, vm;
+  if (!encode_cache_map(&km, a.key_cache, Ty::kIsBf16, slots, a.num_kv_heads, D, B) ||
+      !encode_cache_map(&vm, a.value_cache, Ty::kIsBf16, slots, a.num_kv_heads, D, B))
+    return cudaErrorInvalidValue;
+  const long long x = static_cast<long long>(a.prefix_tiles) * a.groups.max_chunks;
+  if (x > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  return launch_kernel<Ty, D, false, true>(
+      km, vm, a, dim3(static_cast<unsigned>(x), a.num_kv_heads, a.groups.num_groups), false, stream);
 }
 
 }  // namespace
@@ -827,6 +878,15 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, int head_dim, bool bf16, int
   }
   return head_dim == 64 ? launch_tc<F16, 64>(a, max_query_len, stream)
                         : launch_tc<F16, 128>(a, max_query_len, stream);
+}
+
+cudaError_t launch_prefix_pass(PrefillArgs a, int head_dim, bool bf16, cudaStream_t stream) {
+  const int P = kRows / a.group;
+  a.prefix_tiles = (std::min(a.groups.max_group_size, a.groups.num_seqs) + P - 1) / P;
+  if (a.prefix_tiles < 1 || a.groups.max_chunks < 1) return cudaSuccess;
+  if (bf16)
+    return head_dim == 64 ? launch_prefix<BF16, 64>(a, stream) : launch_prefix<BF16, 128>(a, stream);
+  return head_dim == 64 ? launch_prefix<F16, 64>(a, stream) : launch_prefix<F16, 128>(a, stream);
 }
 
 }  // namespace pa

@@ -27,6 +27,11 @@ __device__ __forceinline__ int group_of(const PrefixArgs& x, int s) {
   return lo;
 }
 
+// Pieces that the prefix pass leaves for a sequence of which it computed `shared` tokens.
+__device__ __forceinline__ int prefix_pieces(const PrefixArgs& x, int shared) {
+  return (shared + x.chunk_tokens - 1) / x.chunk_tokens;
+}
+
 // Counts the groups whose start, size or prefix is out of range (one thread a
 // group; called by one CTA).
 __device__ __forceinline__ void count_bad_groups(const PrefixArgs& x, int tid, int threads,
