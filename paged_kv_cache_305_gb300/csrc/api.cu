@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -193,19 +194,30 @@ size_t prefill_v16_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_b
 }
 
 // How the prefix pass cuts the prefix: a CTA takes one chunk of tokens for 128
-// rows (members x query heads) of a group and a kv head. Chunks are whole
-// 64-token tiles, as long as they may be while the grid still has about
-// kPrefixCtas CTAs: each chunk leaves one fp32 piece per row behind.
+// rows (members x query heads) of a group and a kv head. Every chunk leaves an
+// fp32 piece of each row behind, so the fewest chunks are taken whose CTAs
+// (two on each of the 152 SMs at a time) fill nine tenths of their waves, or
+// three waves. Chunks are whole 64-token tiles, at least kPrefixMinChunk long.
 void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
                  int max_prefix_len, int max_group_size) {
   x->max_prefix_len = std::min(max_prefix_len, lmax);
   x->max_group_size = max_group_size;
   const int members = std::max(kPrefixRows / std::max(group, 1), 1);
   const long long tiles = (static_cast<long long>(max_group_size) + members - 1) / members;
-  const long long per_chunk = std::max(tiles * num_groups * num_kv_heads, 1ll);
-  const long long want = std::max((kPrefixCtas + per_chunk - 1) / per_chunk, 1ll);
-  const long long t = std::max((x->max_prefix_len + want - 1) / want, static_cast<long long>(kPrefixMinChunk));
-  x->chunk_tokens = static_cast<int>(std::min((t + 63) / 64 * 64, 1ll << 30));
+  const double waves = static_cast<double>(tiles) * num_groups * num_kv_heads / kPrefixCtas;  // a chunk's
+  const long long most = std::max(x->max_prefix_len / kPrefixMinChunk, 1);
+  long long chunks = 1, best = 1;
+  double best_fill = 0.0;
+  for (; chunks <= most && waves > 0.0; ++chunks) {
+    const double w = waves * chunks, fill = w / std::ceil(w);
+    if (fill > best_fill) {
+      best_fill = fill;
+      best = chunks;
+    }
+    if (fill >= 0.9 || w >= 3.0) break;
+  }
+  const long long t = (x->max_prefix_len + best - 1) / best;
+  x->chunk_tokens = static_cast<int>(std::min(std::max((t + 63) / 64 * 64, 64ll), 1ll << 30));
   x->max_chunks = max_group_size > 0 ? (x->max_prefix_len + x->chunk_tokens - 1) / x->chunk_tokens : 0;
 }
 

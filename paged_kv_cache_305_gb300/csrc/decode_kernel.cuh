@@ -71,9 +71,9 @@ enum Mode {
             // stores it into its cache slot
   kFp8,     // the caches hold e4m3 codes (pa_decode_fp8): tiles of 32 tokens,
             // decode_fp8.cuh
-  kPrefix,  // the tokens that a group of sequences shares were computed by the
+  kPrefix,  // the tokens that a group of sequences shares are computed by the
             // prefix pass (pa_decode_shared_prefix): a row begins behind them,
-            // and the pass's pieces take part in its merge
+            // and its pieces and the pass's are left to the merge kernel
 };
 
 constexpr int kWarps = 4;
@@ -143,6 +143,7 @@ paged_decode_kernel(const DecodeArgs a) {
   constexpr int kCopies = kTileTokens / kRowsPerCopy;  // copies per lane per tensor per tile
   constexpr int kOS = Geo::kOStride;
 
+  if constexpr (PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int cta = blockIdx.x;
   const int NC = gridDim.x;
   const int tid = threadIdx.x;
@@ -831,6 +832,13 @@ paged_decode_kernel(const DecodeArgs a) {
                       lrun[nt][c] > 0.f ? mrun[nt][c] + __log2f(lrun[nt][c]) : -INFINITY;
               }
           }
+          if constexpr (PREFIX) {
+            // the merge kernel finds the number of this kernel's pieces here
+            if (lane == 0) a.ws_count[static_cast<size_t>(g.s) * Hkv + h] = g.npieces;
+            reset_state();
+            if (sg + 1 < nseg) load_q(sSeg[sg + 1]);
+            continue;
+          }
           __syncwarp();
           int* counter = a.ws_count + static_cast<size_t>(g.s) * Hkv + h;
           int last = 0;
@@ -842,13 +850,7 @@ paged_decode_kernel(const DecodeArgs a) {
           last = __shfl_sync(kFull, last, 0);
           if (last) {
             // merge the head's pieces: lane handles 4 consecutive columns of a row
-            int n = g.npieces;
-            if constexpr (PREFIX) {
-              // the prefix pass may still be running (programmatic dependent
-              // launch): its pieces come first
-              asm volatile("griddepcontrol.wait;" ::: "memory");
-              n += g.aux;
-            }
+            const int n = g.npieces;
             constexpr int kC4 = D / 4;
             for (int e = lane; e < G * kC4; e += 32) {
               const int gr = e / kC4, c4 = e % kC4;
@@ -908,8 +910,8 @@ paged_decode_kernel(const DecodeArgs a) {
     cp_async_wait<0>();
     __syncthreads();  // the segment records are rewritten for the next batch
   }
-  // no CTA ends before the prefix pass does: what comes after this kernel in
-  // the stream may then rely on both
+  // no CTA ends before the prefix pass does: the merge kernel behind this one
+  // then waits for both
   if constexpr (PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (a.ws_claim != nullptr && tid == 0) {
     // the last CTA to finish (every claim made) leaves the counters at zero
@@ -948,7 +950,7 @@ template <typename Ty, int D, int STAGES, int NT, Mode MODE>
 cudaError_t launch_typed(const DecodeArgs& a, long long grid, size_t smem, cudaStream_t stream) {
   if constexpr (MODE == kPrefix) {
     // a programmatic dependent launch behind the prefix pass: its CTAs may
-    // start as the pass's finish, and only merges wait for the whole pass
+    // start as the pass's finish
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
