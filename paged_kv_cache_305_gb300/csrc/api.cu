@@ -134,6 +134,14 @@ int resolve_partition(int partition_tokens, int block_size, int max_blocks_per_s
   return PA_OK;
 }
 
+// Partition length behind a shared prefix. What is left of a sequence is short
+// next to its table, so partitions are shorter than pa_decode's: rows of a few
+// hundred tokens then still divide evenly among the CTAs.
+int prefix_partition(int block_size, int max_blocks_per_seq) {
+  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
+  return lmax <= 16384 ? 256 : lmax <= 32768 ? 512 : 1024;
+}
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Split-K workspaces: how many leading bytes of each are known to be zero.
@@ -194,27 +202,34 @@ size_t prefill_v16_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_b
 }
 
 // How the prefix pass cuts the prefix: a CTA takes one chunk of tokens for 128
-// rows (members x query heads) of a group and a kv head. Every chunk leaves an
-// fp32 piece of each row behind, so the fewest chunks are taken whose CTAs
-// (two on each of the 152 SMs at a time) fill nine tenths of their waves, or
-// three waves. Chunks are whole 64-token tiles, at least kPrefixMinChunk long.
+// rows (members x query heads) of a group and a kv head, and leaves an fp32
+// piece of each row behind. Chunks are whole 64-token tiles, at least
+// kPrefixMinChunk long.
 void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
                  int max_prefix_len, int max_group_size) {
   x->max_prefix_len = std::min(max_prefix_len, lmax);
   x->max_group_size = max_group_size;
   const int members = std::max(kPrefixRows / std::max(group, 1), 1);
   const long long tiles = (static_cast<long long>(max_group_size) + members - 1) / members;
-  const double waves = static_cast<double>(tiles) * num_groups * num_kv_heads / kPrefixCtas;  // a chunk's
+  const long long per_chunk = tiles * num_groups * num_kv_heads;
   const long long most = std::max(x->max_prefix_len / kPrefixMinChunk, 1);
-  long long chunks = 1, best = 1;
-  double best_fill = 0.0;
-  for (; chunks <= most && waves > 0.0; ++chunks) {
-    const double w = waves * chunks, fill = w / std::ceil(w);
-    if (fill > best_fill) {
-      best_fill = fill;
-      best = chunks;
+  x->beside_decode = per_chunk <= kPrefixSms ? 1 : 0;
+  long long best = 1;
+  if (x->beside_decode) {
+    best = std::min(most, kPrefixSms / std::max(per_chunk, 1ll));
+  } else {
+    // more CTAs than SMs whatever the chunk: two on each SM at a time, in the
+    // fewest chunks whose CTAs fill nine tenths of their waves, or three waves
+    const double waves = static_cast<double>(per_chunk) / (2 * kPrefixSms);
+    double best_fill = 0.0;
+    for (long long chunks = 1; chunks <= most; ++chunks) {
+      const double w = waves * chunks, fill = w / std::ceil(w);
+      if (fill > best_fill) {
+        best_fill = fill;
+        best = chunks;
+      }
+      if (fill >= 0.9 || w >= 3.0) break;
     }
-    if (fill >= 0.9 || w >= 3.0) break;
   }
   const long long t = (x->max_prefix_len + best - 1) / best;
   x->chunk_tokens = static_cast<int>(std::min(std::max((t + 63) / 64 * 64, 64ll), 1ll << 30));
@@ -808,11 +823,7 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
       max_prefix_len < 0 || max_group_size < 0 ||
       static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffll)
     return 0;
-  std::string saved = g_error;
-  int pt = 0;
-  const int rc = resolve_partition(0, block_size, max_blocks_per_seq, &pt);
-  g_error = saved;
-  if (rc != PA_OK) return 0;
+  const int pt = prefix_partition(block_size, max_blocks_per_seq);
   pa::PrefixArgs x{};
   pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads,
                   max_blocks_per_seq * block_size, max_prefix_len, max_group_size);
@@ -861,7 +872,9 @@ int pa_decode_shared_prefix(void* out, const void* query, const void* key_cache,
   }
   return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
-                     num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, extra, stream);
+                     num_blocks,
+                     log2_pow2(block_size) >= 0 ? prefix_partition(block_size, max_blocks_per_seq) : 0,
+                     dtype, out_dtype, workspace, workspace_bytes, extra, stream);
 }
 
 }  // extern "C"

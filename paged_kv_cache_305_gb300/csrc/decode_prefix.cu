@@ -20,15 +20,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const De
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long head = blockIdx.x;  // sequence * Hkv + kv head
   const int s = static_cast<int>(head / a.num_kv_heads);
+  const int Lmax = a.max_blocks_per_seq << a.block_shift;
+  int lead;
+  const int before = prefix_pieces(
+      a.groups, prefix_of(a.groups, s, min(max(a.seq_lens[s], 0), Lmax), Lmax, &lead));
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int mine = a.ws_count[head];
+  const int mine = __ldcg(a.ws_count + head);
   __syncthreads();
   if (mine == 0) return;
   if (threadIdx.x == 0) a.ws_count[head] = 0;
-  const int Lmax = a.max_blocks_per_seq << a.block_shift;
-  int lead;
-  const int n = mine + prefix_pieces(a.groups, prefix_of(a.groups, s, min(max(a.seq_lens[s], 0), Lmax),
-                                                         Lmax, &lead));
+  const int n = mine + before;
   for (int g = warp; g < a.group; g += kMergeWarps) {
     const size_t row = static_cast<size_t>(head) * a.group + g;
     const float* lse = a.ws_lse + row * a.max_partitions;

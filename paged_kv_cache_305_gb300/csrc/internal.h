@@ -26,6 +26,7 @@ struct PrefixArgs {
   int max_group_size;
   int chunk_tokens;  // tokens of the prefix that one CTA of the prefix pass takes
   int max_chunks;    // ceil(max_prefix_len / chunk_tokens)
+  int beside_decode;  // one CTA of the pass per SM, leaving room for the decode kernel's
 };
 
 struct DecodeArgs {
@@ -127,9 +128,9 @@ constexpr size_t kWorkspaceHeader = 256;
 // Percentage of each row's partitions the decode kernel hands out at run time.
 constexpr int kDynamicPercent = 8;
 // The prefix pass of pa_decode_shared_prefix: 128 rows per CTA, chunks sized
-// for about kPrefixCtas CTAs (two on each of the 152 SMs).
+// for the 152 SMs.
 constexpr int kPrefixRows = 128;
-constexpr long long kPrefixCtas = 304;
+constexpr long long kPrefixSms = 152;
 constexpr int kPrefixMinChunk = 256;
 void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
                  int max_prefix_len, int max_group_size);

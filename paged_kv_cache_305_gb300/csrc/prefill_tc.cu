@@ -94,6 +94,9 @@ struct TcGeo {
   // (2 x 256 tensor-memory columns) share an SM
   static constexpr int kSmem = kBarOff + 128 + 1024 > 80 * 1024 ? kBarOff + 128 + 1024 : 80 * 1024;
 };
+// Prefix pass beside the decode kernel: more than half of an SM's 228 KB, so
+// that one CTA of the pass and one of the decode kernel (under 104 KB) share it.
+constexpr int kBesideSmem = 118 * 1024;
 static_assert(kStages == 2, "stage and S buffer of tile j are both j & 1");
 
 // barrier slots (8 bytes each) after the tiles
@@ -807,13 +810,16 @@ template <typename Ty, int D, bool SINGLE, bool PREFIX>
 cudaError_t launch_kernel(const CUtensorMap& km, const CUtensorMap& vm, const PrefillArgs& a,
                           dim3 grid, bool after_convert, cudaStream_t stream) {
   auto kern = paged_prefill_tc_kernel<Ty, D, SINGLE, PREFIX>;
+  const int smem = PREFIX && a.groups.beside_decode ? std::max(TcGeo<D>::kSmem, kBesideSmem)
+                                                    : TcGeo<D>::kSmem;
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcGeo<D>::kSmem);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           PREFIX ? std::max(TcGeo<D>::kSmem, kBesideSmem) : TcGeo<D>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = TcGeo<D>::kSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
