@@ -131,6 +131,11 @@ template <typename Ty, int D, int STAGES, int NT, Mode MODE>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 paged_decode_kernel(const DecodeArgs a) {
   constexpr bool APPEND = MODE == kAppend, FP8 = MODE == kFp8, PREFIX = MODE == kPrefix;
+  // The newer modes end a segment jointly and leave the merge of a row's pieces
+  // to a kernel behind this one (decode_merge.cuh): a piece is then stored and
+  // forgotten, where the last one to arrive would fence, count, and read the
+  // others back while its CTA waits. They take one kv head per CTA.
+  constexpr bool JOINT = FP8 || PREFIX;
   using Geo = Geometry<D, STAGES, FP8, NT>;
   using T = typename Ty::T;
   using C = std::conditional_t<FP8, uint8_t, T>;  // a cache element
@@ -143,7 +148,7 @@ paged_decode_kernel(const DecodeArgs a) {
   constexpr int kCopies = kTileTokens / kRowsPerCopy;  // copies per lane per tensor per tile
   constexpr int kOS = Geo::kOStride;
 
-  if constexpr (PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (JOINT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int cta = blockIdx.x;
   const int NC = gridDim.x;
   const int tid = threadIdx.x;
@@ -707,6 +712,84 @@ paged_decode_kernel(const DecodeArgs a) {
           lrun[nt][c] += __shfl_xor_sync(kFull, lrun[nt][c], 8);
           lrun[nt][c] += __shfl_xor_sync(kFull, lrun[nt][c], 16);
         }
+      if constexpr (JOINT) {
+        // all warps (they share the head) leave their states in shared memory,
+        // and all threads join them: four dims of a query head each
+        __syncthreads();  // the area was last read at the previous segment's end
+        float* sMw = sMerge + warp * G * kOS;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int head = nt * 8 + tq + c;
+              if (head >= G) continue;
+              if constexpr (FP8) {  // two neighbouring dims
+                *reinterpret_cast<float2*>(sMw + head * kOS + dim_of(mt, 0)) =
+                    make_float2(o[mt][nt][c], o[mt][nt][c + 2]);
+              } else {
+                sMw[head * kOS + dim_of(mt, 0)] = o[mt][nt][c];
+                sMw[head * kOS + dim_of(mt, 2)] = o[mt][nt][c + 2];
+              }
+            }
+        if (r8 == 0) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              sML[(warp * kMLRows + 0) * kHeads + nt * 8 + tq + c] = mrun[nt][c];
+              sML[(warp * kMLRows + 1) * kHeads + nt * 8 + tq + c] = lrun[nt][c];
+              if constexpr (FP8) sML[(warp * kMLRows + 2) * kHeads + nt * 8 + tq + c] = rrun[nt][c];
+            }
+        }
+        reset_state();
+        if (sg + 1 < nseg) load_q(sSeg[sg + 1]);
+        __syncthreads();
+        const size_t row0 = static_cast<size_t>(g.s) * a.num_q_heads + static_cast<size_t>(g.hg) * G;
+        for (int i = tid; i < G * (D / 4); i += kThreads) {
+          const int head = i / (D / 4), c4 = i % (D / 4) * 4;
+          float m[kWarps], r[kWarps], M = -INFINITY, U = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            m[w] = sML[(w * kMLRows) * kHeads + head];
+            r[w] = FP8 ? sML[(w * kMLRows + 2) * kHeads + head] : 0.f;
+            M = fmaxf(M, m[w]);
+            if constexpr (FP8) U = fmaxf(U, m[w] + r[w]);
+          }
+          // kFp8: a warp's O is relative to 2^(m + r) (decode_fp8.cuh)
+          const float R = FP8 && M != -INFINITY ? ceilf(U - M) : 0.f;
+          float l = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float f = M == -INFINITY ? 0.f : ex2(m[w] - M);
+            const float fo = FP8 ? (M == -INFINITY ? 0.f : ex2((m[w] - M) + (r[w] - R))) : f;
+            const float4 v = *reinterpret_cast<const float4*>(sMerge + (w * G + head) * kOS + c4);
+            l += f * sML[(w * kMLRows + 1) * kHeads + head];
+            acc.x += fo * v.x;
+            acc.y += fo * v.y;
+            acc.z += fo * v.z;
+            acc.w += fo * v.w;
+          }
+          float iv = l > 0.f ? 1.f / l : 0.f;
+          if constexpr (FP8) iv *= ex2(R);
+          acc = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+          const size_t row = row0 + head;
+          if (g.piece >= 0) {
+            *reinterpret_cast<float4*>(a.ws_out + (row * P + g.piece) * D + c4) = acc;
+            if (c4 == 0) a.ws_lse[row * P + g.piece] = l > 0.f ? M + __log2f(l) : -INFINITY;
+          } else if (a.out_f32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + c4) = acc;
+          } else {
+            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + c4) =
+                make_uint2(Ty::pack(acc.x, acc.y), Ty::pack(acc.z, acc.w));
+          }
+        }
+        // the merge kernel finds the number of this kernel's pieces here
+        if (g.piece >= 0 && tid == 0) a.ws_count[static_cast<size_t>(g.s) * Hkv + g.hg] = g.npieces;
+        continue;
+      }
       if (Wh > 1) {
         // warps sharing a head: the others hand their state to the head's first warp
         if (ws != 0) {
@@ -727,7 +810,6 @@ paged_decode_kernel(const DecodeArgs a) {
               for (int c = 0; c < 2; ++c) {
                 sML[(warp * kMLRows + 0) * kHeads + nt * 8 + tq + c] = mrun[nt][c];
                 sML[(warp * kMLRows + 1) * kHeads + nt * 8 + tq + c] = lrun[nt][c];
-                if constexpr (FP8) sML[(warp * kMLRows + 2) * kHeads + nt * 8 + tq + c] = rrun[nt][c];
               }
           }
         }
@@ -740,41 +822,26 @@ paged_decode_kernel(const DecodeArgs a) {
               const int head = nt * 8 + tq + c;
               float M = mrun[nt][c];
               for (int w = warp + 1; w < warp + Wh; ++w) M = fmaxf(M, sML[(w * kMLRows) * kHeads + head]);
-              // kFp8: V's weighted rows are kept relative to 2^(m + r)
-              float R = 0.f;
-              if constexpr (FP8) {
-                float U = mrun[nt][c] + rrun[nt][c];
-                for (int w = warp + 1; w < warp + Wh; ++w)
-                  U = fmaxf(U, sML[(w * kMLRows) * kHeads + head] + sML[(w * kMLRows + 2) * kHeads + head]);
-                R = M == -INFINITY ? 0.f : ceilf(U - M);
-              }
-              auto factor = [&](float m, float r) {
-                return M == -INFINITY ? 0.f : ex2(FP8 ? (m - M) + (r - R) : m - M);
-              };
               const float f = M == -INFINITY ? 0.f : ex2(mrun[nt][c] - M);
               lrun[nt][c] *= f;
-              const float fo = FP8 ? factor(mrun[nt][c], rrun[nt][c]) : f;
 #pragma unroll
               for (int mt = 0; mt < kMT; ++mt) {
-                o[mt][nt][c] *= fo;
-                o[mt][nt][c + 2] *= fo;
+                o[mt][nt][c] *= f;
+                o[mt][nt][c + 2] *= f;
               }
               for (int w = warp + 1; w < warp + Wh; ++w) {
-                const float mw = sML[(w * kMLRows) * kHeads + head];
-                const float gw = M == -INFINITY ? 0.f : ex2(mw - M);
+                const float gw = M == -INFINITY ? 0.f : ex2(sML[(w * kMLRows) * kHeads + head] - M);
                 lrun[nt][c] += gw * sML[(w * kMLRows + 1) * kHeads + head];
-                const float go = FP8 ? factor(mw, sML[(w * kMLRows + 2) * kHeads + head]) : gw;
                 if (head < G) {
                   const float* sMw = sMerge + w * G * kOS + head * kOS;
 #pragma unroll
                   for (int mt = 0; mt < kMT; ++mt) {
-                    o[mt][nt][c] += go * sMw[dim_of(mt, 0)];
-                    o[mt][nt][c + 2] += go * sMw[dim_of(mt, 2)];
+                    o[mt][nt][c] += gw * sMw[dim_of(mt, 0)];
+                    o[mt][nt][c + 2] += gw * sMw[dim_of(mt, 2)];
                   }
                 }
               }
               mrun[nt][c] = M;
-              if constexpr (FP8) rrun[nt][c] = R;
             }
         }
         __syncthreads();  // the merge area is reused at the next segment end
@@ -788,10 +855,7 @@ paged_decode_kernel(const DecodeArgs a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            inv[nt][c] = lrun[nt][c] > 0.f ? 1.f / lrun[nt][c] : 0.f;
-            if constexpr (FP8) inv[nt][c] *= ex2(rrun[nt][c]);
-          }
+          for (int c = 0; c < 2; ++c) inv[nt][c] = lrun[nt][c] > 0.f ? 1.f / lrun[nt][c] : 0.f;
         if (g.piece < 0) {
 #pragma unroll
           for (int mt = 0; mt < kMT; ++mt)
@@ -831,13 +895,6 @@ paged_decode_kernel(const DecodeArgs a) {
                   a.ws_lse[(row0 + head) * P + g.piece] =
                       lrun[nt][c] > 0.f ? mrun[nt][c] + __log2f(lrun[nt][c]) : -INFINITY;
               }
-          }
-          if constexpr (PREFIX) {
-            // the merge kernel finds the number of this kernel's pieces here
-            if (lane == 0) a.ws_count[static_cast<size_t>(g.s) * Hkv + h] = g.npieces;
-            reset_state();
-            if (sg + 1 < nseg) load_q(sSeg[sg + 1]);
-            continue;
           }
           __syncwarp();
           int* counter = a.ws_count + static_cast<size_t>(g.s) * Hkv + h;
