@@ -60,7 +60,7 @@ def _peaks():
 def _decode_source_sha() -> str:
     """SHA-256 over the decode kernel's source and the header of its constants."""
     h = hashlib.sha256()
-    for name in ("decode_kernel.cuh", "internal.h"):
+    for name in ("decode.cu", "internal.h"):
         h.update(open(os.path.join(ROOT, "paged_kv_cache_305_gb300", "csrc", name), "rb").read())
     return h.hexdigest()
 

@@ -354,8 +354,14 @@ int pa_gather_cache_fp8(void* key_out, void* value_out,
  * (and of out, unless that is fp32). Arithmetic is fp32 around fp16 products of
  * the exact codes: the query enters as its fp16 value (bf16: scaled by a power
  * of two for each head, so that its bits are kept), softmax weights, times V's
- * factors, as the sum of two fp16 parts. Other arguments, sizes, the workspace
- * (pa_decode_workspace_bytes) and errors as for pa_decode.
+ * factors, as the sum of two fp16 parts.
+ * Rows are cut into pieces of about partition_tokens tokens or more (0 = the
+ * default, see pa_decode_fp8_workspace_bytes), wherever equal shares of the
+ * work end; the pieces are joined in order by a second kernel, and the result
+ * does not depend on which CTA computed which. workspace:
+ * pa_decode_fp8_workspace_bytes(...) bytes, with the zeroing and sharing rules
+ * of pa_decode_workspace_bytes. Other arguments, sizes and errors as for
+ * pa_decode.
  */
 int pa_decode_fp8(void* out, const void* query,
                   const void* key_cache, const void* value_cache, const uint8_t* cache_scales,
@@ -365,6 +371,17 @@ int pa_decode_fp8(void* out, const void* query,
                   int max_blocks_per_seq, int num_blocks, int partition_tokens,
                   pa_dtype dtype, pa_dtype out_dtype, void* workspace, size_t workspace_bytes,
                   cudaStream_t stream);
+
+/*
+ * Workspace bytes of pa_decode_fp8. With partition_tokens = 0 a row has room
+ * for 16 pieces, for more where num_seqs * num_kv_heads rows are few (at most
+ * 128, none under 256 tokens), and for one where max_blocks_per_seq *
+ * block_size is at most 512; otherwise this is pa_decode_workspace_bytes.
+ * 0 for invalid sizes, and where rows are not cut.
+ */
+size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq, int block_size,
+                                     int partition_tokens);
 
 /*
  * pa_decode for batches in which groups of sequences begin with the same

@@ -20,6 +20,7 @@ from .pagedattn import (  # noqa: F401
     decode,
     decode_append,
     decode_fp8,
+    decode_fp8_workspace_bytes,
     decode_no_alloc,
     decode_partition_tokens,
     decode_shared_prefix,

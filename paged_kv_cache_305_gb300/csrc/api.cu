@@ -16,6 +16,7 @@
 #include "internal.h"
 #include "pagedattn.h"
 #include "pagedattn_testing.h"
+#include "stream.h"
 
 // Share (%) of every row's partitions that the decode kernel hands out at run
 // time, for 512-token partitions, scaled with the partition length (0: the
@@ -134,9 +135,20 @@ int resolve_partition(int partition_tokens, int block_size, int max_blocks_per_s
   return PA_OK;
 }
 
+// Partition length of decode over an 8-bit cache, where the caller names none:
+// the workspace's room for pieces, and with it how finely rows may be cut. 16
+// pieces of the longest row, more where the rows are few (eight units for each
+// of the 456 CTAs); rows of up to 512 tokens are not cut.
+int fp8_partition(int num_seqs, int num_kv_heads, long long lmax) {
+  if (lmax <= 512) return 512;
+  const long long rows = std::max(static_cast<long long>(num_seqs) * num_kv_heads, 1ll);
+  const long long pieces = std::min(std::max((8 * 456 + rows - 1) / rows, 16ll), 128ll);
+  const long long pt = std::max((lmax + pieces - 1) / pieces, 256ll);
+  return static_cast<int>(std::min((pt + 63) / 64 * 64, static_cast<long long>(pa::kMaxPartitionTokens)));
+}
+
 // Partition length behind a shared prefix. What is left of a sequence is short
-// next to its table, so partitions are shorter than pa_decode's: rows of a few
-// hundred tokens then still divide evenly among the CTAs.
+// next to its table, so rows of a few hundred tokens may still be cut.
 int prefix_partition(int block_size, int max_blocks_per_seq) {
   const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
   return lmax <= 16384 ? 256 : lmax <= 32768 ? 512 : 1024;
@@ -641,10 +653,12 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   if ((static_cast<long long>(num_blocks) << shift) > 0xfffffffeLL)
     return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size is 2^32 - 1 slots or more");
   if (!isfinite(scale)) return fail(PA_ERR_INVALID, "scale is not finite");
+  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
+  if (extra.fp8 && partition_tokens == 0)
+    partition_tokens = fp8_partition(num_seqs, num_kv_heads, lmax);
   int pt = 0;
   rc = resolve_partition(partition_tokens, block_size, max_blocks_per_seq, &pt);
   if (rc != PA_OK) return rc;
-  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
   if (lmax > 0x7fffffffll)
     return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size = %lld overflows int", lmax);
   if (num_seqs > 65535 || num_kv_heads > 65535)
@@ -657,6 +671,13 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
     return fail(PA_ERR_INVALID, "out, query and the caches must be 16-byte aligned");
   if (!aligned4(block_tables) || !aligned4(seq_lens))
     return fail(PA_ERR_INVALID, "block_tables and seq_lens must be 4-byte aligned");
+  if (extra.fp8 || extra.prefix) {
+    // the streaming kernel's positions (tiles of 16 tokens or more) are 32-bit
+    const double tiles = static_cast<double>(num_seqs) * num_kv_heads *
+                         (static_cast<double>(lmax) / (extra.fp8 ? 32 : 16) + 2.0);
+    if (tiles >= 2147483648.0)
+      return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_kv_heads * max sequence length too large");
+  }
   if (extra.fp8) {
     if (!extra.scales) return fail(PA_ERR_INVALID, "a pointer argument is NULL");
     if (!aligned16(extra.scales)) return fail(PA_ERR_INVALID, "cache_scales must be 16-byte aligned");
@@ -718,7 +739,6 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   a.out_f32 = out_dtype == PA_FLOAT32 ? 1 : 0;
   a.new_key = extra.new_key;
   a.new_value = extra.new_value;
-  a.scales = extra.scales;
   char* ws = static_cast<char*>(workspace);
   a.ws_count = wl.total ? reinterpret_cast<int*>(ws + wl.count_off) : nullptr;
   // the trailing partitions of rows are handed out at run time only with a
@@ -731,33 +751,42 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   a.ws_out = wl.total ? reinterpret_cast<float*>(ws + wl.out_off) : nullptr;
   a.bad = bad;
   const bool bf16 = dtype == PA_BFLOAT16;
-  a.groups = extra.groups;
-  if (extra.prefix) {
-    pa::PrefillArgs x{};
-    x.query = query;
-    x.key_cache = key_cache;
-    x.value_cache = value_cache;
-    x.block_tables = block_tables;
-    x.num_q_heads = num_q_heads;
-    x.num_kv_heads = num_kv_heads;
-    x.group = group;
-    x.block_shift = shift;
-    x.max_blocks_per_seq = max_blocks_per_seq;
-    x.num_blocks = num_blocks;
-    x.scale_log2 = a.scale_log2;
-    x.bad = bad;
+  cudaError_t e = cudaSuccess;
+  if (extra.fp8 || extra.prefix) {
+    pa::StreamArgs x{};
+    static_cast<pa::DecodeArgs&>(x) = a;
+    x.scales = extra.scales;
+    x.groups = extra.groups;
     rc = counter(true, &x.timeouts);
     if (rc != PA_OK) return rc;
-    x.groups = extra.groups;
-    x.max_pieces = pieces;
-    x.ws_lse = a.ws_lse;
-    x.ws_out = a.ws_out;
-    cudaError_t pe = pa::launch_prefix_pass(x, head_dim, bf16, stream);
-    if (pe != cudaSuccess) return cuda_fail(pe, "shared prefix launch");
+    if (extra.prefix) {
+      pa::PrefixPassArgs p{};
+      p.query = query;
+      p.key_cache = key_cache;
+      p.value_cache = value_cache;
+      p.block_tables = block_tables;
+      p.num_q_heads = num_q_heads;
+      p.num_kv_heads = num_kv_heads;
+      p.group = group;
+      p.block_shift = shift;
+      p.max_blocks_per_seq = max_blocks_per_seq;
+      p.num_blocks = num_blocks;
+      p.scale_log2 = a.scale_log2;
+      p.bad = bad;
+      p.timeouts = x.timeouts;
+      p.groups = extra.groups;
+      p.max_pieces = pieces;
+      p.ws_lse = a.ws_lse;
+      p.ws_out = a.ws_out;
+      e = pa::launch_prefix_pass(p, head_dim, bf16, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+      e = pa::launch_decode_prefix(x, head_dim, bf16, sms, stream);
+    } else {
+      e = pa::launch_decode_fp8(x, head_dim, bf16, sms, stream);
+    }
+  } else {
+    e = pa::launch_decode(a, head_dim, bf16, sms, stream);
   }
-  cudaError_t e = extra.prefix ? pa::launch_decode_prefix(a, head_dim, bf16, sms, stream)
-                  : extra.fp8  ? pa::launch_decode_fp8(a, head_dim, bf16, sms, stream)
-                               : pa::launch_decode(a, head_dim, bf16, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
   return PA_OK;
 }
@@ -811,6 +840,16 @@ int pa_decode_fp8(void* out, const void* query, const void* key_cache, const voi
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
                      num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes,
                      extra, stream);
+}
+
+size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq, int block_size, int partition_tokens) {
+  if (num_seqs < 0 || num_kv_heads < 1 || max_blocks_per_seq < 1) return 0;
+  if (partition_tokens == 0)
+    partition_tokens =
+        fp8_partition(num_seqs, num_kv_heads, static_cast<long long>(max_blocks_per_seq) * block_size);
+  return pa_decode_workspace_bytes(num_seqs, num_q_heads, head_dim, max_blocks_per_seq, block_size,
+                                   partition_tokens);
 }
 
 size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,

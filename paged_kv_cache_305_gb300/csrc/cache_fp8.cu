@@ -12,8 +12,8 @@
 #include <type_traits>
 
 #include "fp8.cuh"
-#include "internal.h"
 #include "ptx.cuh"
+#include "stream.h"
 
 namespace pa {
 namespace {

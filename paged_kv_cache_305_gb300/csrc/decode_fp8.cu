@@ -1,11 +1,11 @@
 // Decode over 8-bit caches: pa_decode_fp8.
-#include "decode_merge.cuh"
+#include "decode_stream.cuh"
 
 namespace pa {
 
-cudaError_t launch_decode_fp8(const DecodeArgs& a, int head_dim, bool bf16, int num_sms,
+cudaError_t launch_decode_fp8(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
                               cudaStream_t stream) {
-  return launch_mode_and_merge<kFp8>(a, head_dim, bf16, num_sms, stream);
+  return launch_all<true>(a, head_dim, bf16, num_sms, stream);
 }
 
 }  // namespace pa

@@ -16,19 +16,6 @@ constexpr long long kLongContextTokens = 4096;
 constexpr int kMaxPartitionTokens = 1 << 20;
 constexpr int kMaxGroup = 16;  // query heads per kv head (rows of one mma tile)
 
-// Groups of sequences that share a prefix (pa_decode_shared_prefix).
-struct PrefixArgs {
-  const int32_t* group_start;  // [num_groups + 1]
-  const int32_t* prefix_lens;  // [num_groups]
-  int num_groups;              // 0: no sharing
-  int num_seqs;
-  int max_prefix_len;
-  int max_group_size;
-  int chunk_tokens;  // tokens of the prefix that one CTA of the prefix pass takes
-  int max_chunks;    // ceil(max_prefix_len / chunk_tokens)
-  int beside_decode;  // one CTA of the pass per SM, leaving room for the decode kernel's
-};
-
 struct DecodeArgs {
   void* out;
   const void* query;
@@ -57,19 +44,6 @@ struct DecodeArgs {
   unsigned* ws_done;             // CTAs finished (zero between calls)
   int dyn_percent;     // share (%) of each row's partitions handed out at run time
   unsigned long long* bad;  // device counter of rejected indices
-  const uint8_t* scales;    // 8-bit caches: exponent bytes [NB, Hkv, 2, B], else null
-  PrefixArgs groups;        // shared prefixes (num_groups 0: none)
-};
-
-// An 8-bit pool: e4m3 codes [NB, B, Hkv, d] and exponent bytes [NB, Hkv, 2, B].
-struct Fp8Pool {
-  uint8_t* key_cache;
-  uint8_t* value_cache;
-  uint8_t* scales;
-  int num_kv_heads;
-  int head_dim;
-  int block_shift;
-  int num_blocks;
 };
 
 struct PrefillArgs {
@@ -93,11 +67,6 @@ struct PrefillArgs {
   unsigned long long* timeouts;  // bounded waits that gave up (tensor-core kernel)
   int stall_for_test;  // 1: the product thread waits on a barrier nothing signals
   void* v16;           // bf16 caches: fp16 copy of the value rows [S * MB * B, Hkv, d], or null
-  PrefixArgs groups;   // the prefix pass: its groups, query tiles a group (set by the
-  int prefix_tiles;    // launcher), and the pieces it leaves
-  int max_pieces;      // pieces a row has room for in ws_lse and ws_out
-  float* ws_lse;
-  float* ws_out;
 };
 
 // Bytes of the fp16 copy of the value rows the bf16 prefill can use (0 when
@@ -108,7 +77,6 @@ size_t prefill_v16_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_b
 // Tensor-core (tcgen05) prefill: block sizes 1..64 (TMA block copies from 8
 // up, 16-byte row copies below), fewer than 2^31 slots.
 bool prefill_tc_supported(int block_size, long long num_slots);
-cudaError_t launch_prefix_pass(PrefillArgs a, int head_dim, bool bf16, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, int head_dim, bool bf16, int max_query_len,
                               cudaStream_t stream);
 
@@ -127,13 +95,6 @@ struct WorkspaceLayout {
 constexpr size_t kWorkspaceHeader = 256;
 // Percentage of each row's partitions the decode kernel hands out at run time.
 constexpr int kDynamicPercent = 8;
-// The prefix pass of pa_decode_shared_prefix: 128 rows per CTA, chunks sized
-// for the 152 SMs.
-constexpr int kPrefixRows = 128;
-constexpr long long kPrefixSms = 152;
-constexpr int kPrefixMinChunk = 256;
-void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
-                 int max_prefix_len, int max_group_size);
 WorkspaceLayout workspace_layout(int num_seqs, int num_q_heads, int head_dim, int max_partitions);
 
 // Scheduling of the persistent decode kernel: a partition weighs its tokens
@@ -146,21 +107,6 @@ constexpr int kMaxSegments = 64;
 // multiple of it).
 cudaError_t launch_decode(const DecodeArgs& a, int head_dim, bool bf16, int num_sms,
                           cudaStream_t stream);
-
-cudaError_t launch_decode_fp8(const DecodeArgs& a, int head_dim, bool bf16, int num_sms,
-                              cudaStream_t stream);
-cudaError_t launch_decode_prefix(const DecodeArgs& a, int head_dim, bool bf16, int num_sms,
-                                 cudaStream_t stream);
-
-cudaError_t launch_write_fp8(const Fp8Pool& p, bool bf16, const void* key, const void* value,
-                             const int64_t* slot_mapping, int num_tokens, unsigned long long* bad,
-                             cudaStream_t stream);
-cudaError_t launch_copy_blocks_fp8(const Fp8Pool& p, const int32_t* src, const int32_t* dst,
-                                   int num_copies, unsigned long long* bad, cudaStream_t stream);
-cudaError_t launch_gather_fp8(const Fp8Pool& p, bool bf16, void* key_out, void* value_out,
-                              long long num_out_rows, const int32_t* block_tables,
-                              const int32_t* seq_lens, const int64_t* out_start, int num_seqs,
-                              int max_blocks_per_seq, unsigned long long* bad, cudaStream_t stream);
 
 cudaError_t launch_copy_blocks(void* key_cache, void* value_cache, const int32_t* src,
                                const int32_t* dst, int num_copies, long long block_bytes,

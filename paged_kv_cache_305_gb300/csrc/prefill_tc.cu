@@ -41,20 +41,19 @@
 // the prefix, read through the table of the group's first member, and the
 // result is left as a piece (normalised fp32 row and base-2 log-sum-exp) for
 // the merge of the decode kernel.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
 #include "prefix.cuh"
 #include "ptx.cuh"
+#include "stream.h"
 #include "tc.cuh"
+#include "tensor_map.h"
 
 namespace pa {
 namespace {
@@ -189,14 +188,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
 template <typename Ty, int D, bool SINGLE, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap, const PrefillArgs a) {
+                        const __grid_constant__ CUtensorMap vmap,
+                        const std::conditional_t<PREFIX, PrefixPassArgs, PrefillArgs> a) {
   using Geo = TcGeo<D>;
   using T = typename Ty::T;
   constexpr int kChunks = D / 8;  // 16-byte chunks per row
   constexpr int kKSteps = D / 16;
 
   // longest tiles first; PREFIX: the tiles of one chunk next to each other
-  const int qt = PREFIX ? blockIdx.x % a.prefix_tiles : gridDim.x - 1 - blockIdx.x;
+  int qt = gridDim.x - 1 - blockIdx.x;
+  if constexpr (PREFIX) qt = blockIdx.x % a.prefix_tiles;
   const int h = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group;
@@ -445,7 +446,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
       const float inv = l > 0.f ? 1.f / l : 0.f;
       size_t row = static_cast<size_t>(q0 + j0 + r / G) * a.num_q_heads +
                    static_cast<size_t>(h) * G + r % G;
+      void* out = a.out;
       if constexpr (PREFIX) {  // the chunk's piece of the row
+        out = a.ws_out;
         row = row * a.max_pieces + blockIdx.x / a.prefix_tiles;
         if (row_valid) a.ws_lse[row] = l > 0.f ? m + __log2f(l) : -INFINITY;
       }
@@ -456,8 +459,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         tc::tmem_ld_wait16(x);
         if (!row_valid) continue;
         if (PREFIX || a.out_f32) {
-          float4* o = reinterpret_cast<float4*>((PREFIX ? a.ws_out : static_cast<float*>(a.out)) +
-                                                row * D + 16 * c);
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * D + 16 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             o[i] = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
@@ -761,22 +763,6 @@ __global__ void __launch_bounds__(256) v16_convert_kernel(const PrefillArgs a) {
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
-  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
-  if (f == nullptr) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess && p != nullptr) {
-      f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-      fn.store(f, std::memory_order_release);
-    }
-  }
-  return f;
-}
-
 // One cache [num_blocks * B slots, Hkv, d] viewed, innermost first, as
 // (64 elements of a head-dim slice, 8 slots of a group, d / 64 slices,
 // slot groups, kv head); a box is one block of one kv head: (64, 8, d / 64,
@@ -807,14 +793,16 @@ bool encode_cache_map(CUtensorMap* map, const void* cache, bool bf16, long long 
 // after_convert: launched right behind the conversion pass as a programmatic
 // dependent launch (its CTAs may start while the pass is finishing).
 template <typename Ty, int D, bool SINGLE, bool PREFIX>
-cudaError_t launch_kernel(const CUtensorMap& km, const CUtensorMap& vm, const PrefillArgs& a,
-                          dim3 grid, bool after_convert, cudaStream_t stream) {
+cudaError_t launch_kernel(const CUtensorMap& km, const CUtensorMap& vm,
+                          const std::conditional_t<PREFIX, PrefixPassArgs, PrefillArgs>& a, dim3 grid,
+                          bool after_convert, cudaStream_t stream) {
   auto kern = paged_prefill_tc_kernel<Ty, D, SINGLE, PREFIX>;
-  const int smem = PREFIX && a.groups.beside_decode ? std::max(TcGeo<D>::kSmem, kBesideSmem)
-                                                    : TcGeo<D>::kSmem;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           PREFIX ? std::max(TcGeo<D>::kSmem, kBesideSmem) : TcGeo<D>::kSmem);
+  int smem = TcGeo<D>::kSmem, most = smem;
+  if constexpr (PREFIX) {
+    most = std::max(smem, kBesideSmem);
+    if (a.groups.beside_decode) smem = most;
+  }
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -857,7 +845,7 @@ cudaError_t launch_tc(const PrefillArgs& a, int max_query_len, cudaStream_t stre
 }
 
 template <typename Ty, int D>
-cudaError_t launch_prefix(const PrefillArgs& a, cudaStream_t stream) {
+cudaError_t launch_prefix(const PrefixPassArgs& a, cudaStream_t stream) {
   const int B = 1 << a.block_shift;
   const long long slots = static_cast<long long>(a.num_blocks) << a.block_shift;
   CUtensorMap km, vm;
@@ -886,7 +874,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, int head_dim, bool bf16, int
                         : launch_tc<F16, 128>(a, max_query_len, stream);
 }
 
-cudaError_t launch_prefix_pass(PrefillArgs a, int head_dim, bool bf16, cudaStream_t stream) {
+cudaError_t launch_prefix_pass(PrefixPassArgs a, int head_dim, bool bf16, cudaStream_t stream) {
   const int P = kRows / a.group;
   a.prefix_tiles = (std::min(a.groups.max_group_size, a.groups.num_seqs) + P - 1) / P;
   if (a.prefix_tiles < 1 || a.groups.max_chunks < 1) return cudaSuccess;

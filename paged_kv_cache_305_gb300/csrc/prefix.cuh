@@ -1,7 +1,7 @@
 // Which tokens of a sequence its group's shared prefix covers.
 #pragma once
 
-#include "internal.h"
+#include "stream.h"
 
 namespace pa {
 

@@ -1,0 +1,80 @@
+// Internal interface of the 8-bit cache and of decode over a shared prefix,
+// between the C-ABI layer (api.cu) and the kernel files.
+#pragma once
+
+#include "internal.h"
+
+namespace pa {
+
+// Groups of sequences that share a prefix (pa_decode_shared_prefix).
+struct PrefixArgs {
+  const int32_t* group_start;  // [num_groups + 1]
+  const int32_t* prefix_lens;  // [num_groups]
+  int num_groups;              // 0: no sharing
+  int num_seqs;
+  int max_prefix_len;
+  int max_group_size;
+  int chunk_tokens;   // tokens of the prefix that one CTA of the prefix pass takes
+  int max_chunks;     // ceil(max_prefix_len / chunk_tokens)
+  int beside_decode;  // one CTA of the pass per SM, leaving room for the decode kernel's
+};
+
+// The streaming decode kernel (decode_stream.cuh). max_partitions is the number
+// of pieces a row has room for; group_start and the partition fields that only
+// the 16-bit decode kernel uses stay unset.
+struct StreamArgs : DecodeArgs {
+  const uint8_t* scales;  // 8-bit caches: exponent bytes [NB, Hkv, 2, B]
+  PrefixArgs groups;      // shared prefixes (num_groups 0: none)
+  int least_tiles;        // shortest unit of work, in tiles (0: rows are not cut)
+  unsigned long long* timeouts;  // bounded waits that gave up
+};
+
+// The prefix pass: a prefill whose positions are the sequences of a group.
+struct PrefixPassArgs : PrefillArgs {
+  PrefixArgs groups;
+  int prefix_tiles;  // query tiles of a group (set by the launcher)
+  int max_pieces;    // pieces a row has room for in ws_lse and ws_out
+  float* ws_lse;
+  float* ws_out;
+};
+
+// An 8-bit pool: e4m3 codes [NB, B, Hkv, d] and exponent bytes [NB, Hkv, 2, B].
+struct Fp8Pool {
+  uint8_t* key_cache;
+  uint8_t* value_cache;
+  uint8_t* scales;
+  int num_kv_heads;
+  int head_dim;
+  int block_shift;
+  int num_blocks;
+};
+
+// The prefix pass: 128 rows per CTA, chunks sized for the 152 SMs.
+constexpr int kPrefixRows = 128;
+constexpr long long kPrefixSms = 152;
+constexpr int kPrefixMinChunk = 256;
+void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
+                 int max_prefix_len, int max_group_size);
+
+// Schedule of the streaming decode kernel: the share (%) of the work that is
+// dealt out to the CTAs beforehand, and about how many units each claims of the rest.
+constexpr int kStaticShare = 80;
+constexpr int kClaims = 4;
+
+cudaError_t launch_decode_fp8(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_decode_prefix(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
+                                 cudaStream_t stream);
+cudaError_t launch_prefix_pass(PrefixPassArgs a, int head_dim, bool bf16, cudaStream_t stream);
+
+cudaError_t launch_write_fp8(const Fp8Pool& p, bool bf16, const void* key, const void* value,
+                             const int64_t* slot_mapping, int num_tokens, unsigned long long* bad,
+                             cudaStream_t stream);
+cudaError_t launch_copy_blocks_fp8(const Fp8Pool& p, const int32_t* src, const int32_t* dst,
+                                   int num_copies, unsigned long long* bad, cudaStream_t stream);
+cudaError_t launch_gather_fp8(const Fp8Pool& p, bool bf16, void* key_out, void* value_out,
+                              long long num_out_rows, const int32_t* block_tables,
+                              const int32_t* seq_lens, const int64_t* out_start, int num_seqs,
+                              int max_blocks_per_seq, unsigned long long* bad, cudaStream_t stream);
+
+}  // namespace pa

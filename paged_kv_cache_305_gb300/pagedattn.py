@@ -27,6 +27,7 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_bytes", "pa_decode",
             "pa_testing_prefill_stalled", "pa_prefill_workspace_bytes",
             "pa_decode_partition_tokens", "pa_reshape_and_cache_fp8", "pa_copy_blocks_fp8",
             "pa_gather_cache_fp8", "pa_decode_fp8", "pa_decode_shared_prefix",
+            "pa_decode_fp8_workspace_bytes",
             "pa_decode_shared_prefix_workspace_bytes")
 PA_ERR_CAPACITY = -5
 
@@ -92,6 +93,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.pa_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float,
                                 i32, i32, i32, i32, i32, vp, sz, vp]
     L.pa_decode_fp8.restype = i32
+    L.pa_decode_fp8_workspace_bytes.argtypes = [i32] * 7
+    L.pa_decode_fp8_workspace_bytes.restype = sz
     L.pa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                           i32, ctypes.c_float, i32, i32, i32, i32, i32, i32, vp, sz,
                                           vp]
@@ -175,6 +178,14 @@ def decode_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int,
                                                         partition_tokens))
 
 
+def decode_fp8_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                               max_blocks_per_seq: int, block_size: int,
+                               partition_tokens: int = 0) -> int:
+    return int(load_library().pa_decode_fp8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                            max_blocks_per_seq, block_size,
+                                                            partition_tokens))
+
+
 def decode_partition_tokens(partition_tokens: int, block_size: int,
                             max_blocks_per_seq: int) -> int:
     """The split-K partition length pa_decode resolves these arguments to."""
@@ -187,9 +198,14 @@ def decode_partition_tokens(partition_tokens: int, block_size: int,
 
 def alloc_workspace(query: torch.Tensor, key_cache: torch.Tensor, block_tables: torch.Tensor,
                     partition_tokens: int = 0) -> Optional[torch.Tensor]:
-    """Zero-filled workspace for :func:`decode` with these shapes (None if none is needed)."""
+    """Zero-filled workspace for :func:`decode` (or :func:`decode_fp8`, for a float8
+    ``key_cache``) with these shapes (None if none is needed)."""
     S, Hq, d = query.shape
-    n = decode_workspace_bytes(S, Hq, d, block_tables.shape[1], key_cache.shape[1], partition_tokens)
+    if key_cache.dtype == torch.float8_e4m3fn:
+        n = decode_fp8_workspace_bytes(S, Hq, key_cache.shape[2], d, block_tables.shape[1],
+                                       key_cache.shape[1], partition_tokens)
+    else:
+        n = decode_workspace_bytes(S, Hq, d, block_tables.shape[1], key_cache.shape[1], partition_tokens)
     if n == 0:
         return None
     return torch.zeros(n, dtype=torch.uint8, device=query.device)
