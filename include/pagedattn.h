@@ -355,13 +355,13 @@ int pa_gather_cache_fp8(void* key_out, void* value_out,
  * the exact codes: the query enters as its fp16 value (bf16: scaled by a power
  * of two for each head, so that its bits are kept), softmax weights, times V's
  * factors, as the sum of two fp16 parts.
- * Rows are cut into pieces of about partition_tokens tokens or more (0 = the
- * default, see pa_decode_fp8_workspace_bytes), wherever equal shares of the
- * work end; the pieces are joined in order by a second kernel, and the result
- * does not depend on which CTA computed which. workspace:
- * pa_decode_fp8_workspace_bytes(...) bytes, with the zeroing and sharing rules
- * of pa_decode_workspace_bytes. Other arguments, sizes and errors as for
- * pa_decode.
+ * Work is cut into equal shares, inside rows as it comes (shares are not under
+ * partition_tokens tokens where that is given; 0 = the default); a second kernel
+ * joins a row's pieces in order, and the result does not depend on which CTA
+ * computed which. workspace: pa_decode_fp8_workspace_bytes(...) bytes, with the
+ * zeroing and sharing rules of pa_decode_workspace_bytes. num_seqs *
+ * num_kv_heads * max_blocks_per_seq * block_size / 32 must be below 2^31.
+ * Other arguments, sizes and errors as for pa_decode.
  */
 int pa_decode_fp8(void* out, const void* query,
                   const void* key_cache, const void* value_cache, const uint8_t* cache_scales,
@@ -373,15 +373,12 @@ int pa_decode_fp8(void* out, const void* query,
                   cudaStream_t stream);
 
 /*
- * Workspace bytes of pa_decode_fp8. With partition_tokens = 0 a row has room
- * for 16 pieces, for more where num_seqs * num_kv_heads rows are few (at most
- * 128, none under 256 tokens), and for one where max_blocks_per_seq *
- * block_size is at most 512; otherwise this is pa_decode_workspace_bytes.
- * 0 for invalid sizes, and where rows are not cut.
+ * Workspace bytes of pa_decode_fp8 (any partition_tokens): 0 where
+ * max_blocks_per_seq * block_size is at most 512 (rows are not cut then), and
+ * for invalid sizes.
  */
 size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                                     int max_blocks_per_seq, int block_size,
-                                     int partition_tokens);
+                                     int max_blocks_per_seq, int block_size);
 
 /*
  * pa_decode for batches in which groups of sequences begin with the same
@@ -405,7 +402,7 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
  * table. If group_start decreases, outputs are unspecified (nothing outside
  * the arrays is touched).
  * num_groups in [1, 65535] (unless num_seqs is 0), num_blocks * block_size
- * below 2^31. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
+ * and num_seqs * num_kv_heads * max_blocks_per_seq * block_size / 16 below 2^31. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
  * with the zeroing and sharing rules of pa_decode_workspace_bytes. Arithmetic,
  * other arguments and errors as for pa_decode.
  */

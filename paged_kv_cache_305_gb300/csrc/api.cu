@@ -135,25 +135,6 @@ int resolve_partition(int partition_tokens, int block_size, int max_blocks_per_s
   return PA_OK;
 }
 
-// Partition length of decode over an 8-bit cache, where the caller names none:
-// the workspace's room for pieces, and with it how finely rows may be cut. 16
-// pieces of the longest row, more where the rows are few (eight units for each
-// of the 456 CTAs); rows of up to 512 tokens are not cut.
-int fp8_partition(int num_seqs, int num_kv_heads, long long lmax) {
-  if (lmax <= 512) return 512;
-  const long long rows = std::max(static_cast<long long>(num_seqs) * num_kv_heads, 1ll);
-  const long long pieces = std::min(std::max((8 * 456 + rows - 1) / rows, 16ll), 128ll);
-  const long long pt = std::max((lmax + pieces - 1) / pieces, 256ll);
-  return static_cast<int>(std::min((pt + 63) / 64 * 64, static_cast<long long>(pa::kMaxPartitionTokens)));
-}
-
-// Partition length behind a shared prefix. What is left of a sequence is short
-// next to its table, so rows of a few hundred tokens may still be cut.
-int prefix_partition(int block_size, int max_blocks_per_seq) {
-  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
-  return lmax <= 16384 ? 256 : lmax <= 32768 ? 512 : 1024;
-}
-
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Split-K workspaces: how many leading bytes of each are known to be zero.
@@ -246,6 +227,39 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   const long long t = (x->max_prefix_len + best - 1) / best;
   x->chunk_tokens = static_cast<int>(std::min(std::max((t + 63) / 64 * 64, 64ll), 1ll << 30));
   x->max_chunks = max_group_size > 0 ? (x->max_prefix_len + x->chunk_tokens - 1) / x->chunk_tokens : 0;
+}
+
+// Kv heads that a CTA of the streaming kernel takes at a time. 16-bit rows of one
+// head (256 bytes at d = 128) are long enough by themselves; 8-bit ones are read
+// with their neighbours while that leaves every CTA kGroupTiles tiles of the
+// longest lengths to share.
+int stream_heads(bool fp8, int num_seqs, int num_kv_heads, long long lmax) {
+  for (int hc = 4; fp8 && hc > 1; hc /= 2)
+    if (num_kv_heads % hc == 0 &&
+        static_cast<double>(num_seqs) * (num_kv_heads / hc) * (static_cast<double>(lmax) / 32) >=
+            static_cast<double>(kMaxCtas) * kGroupTiles)
+      return hc;
+  return 1;
+}
+
+StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                           long long lmax, int max_chunks) {
+  StreamLayout w{};
+  w.heads = stream_heads(fp8, num_seqs, num_kv_heads, lmax);
+  w.cut = lmax > kUncutTokens;
+  if (!w.cut && max_chunks == 0) return w;
+  const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
+  const size_t group = static_cast<size_t>(w.heads) * (num_q_heads / num_kv_heads);
+  // one slot for each (row, unit) boundary on the line of tiles
+  const size_t slots = static_cast<size_t>(num_seqs) * (num_kv_heads / w.heads) +
+                       (w.cut ? static_cast<size_t>(kMaxCtas) * (1 + kClaims) : kMaxCtas);
+  w.row_off = kWorkspaceHeader;
+  w.pre_lse = round_up(w.row_off + static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(int2), 256);
+  w.seg_lse = w.pre_lse + round_up(rows * max_chunks * sizeof(float), 256);
+  w.pre_out = w.seg_lse + round_up(slots * group * sizeof(float), 256);
+  w.seg_out = w.pre_out + rows * max_chunks * head_dim * sizeof(float);
+  w.total = w.seg_out + slots * group * head_dim * sizeof(float);
+  return w;
 }
 
 WorkspaceLayout workspace_layout(int num_seqs, int num_q_heads, int head_dim, int max_partitions) {
@@ -610,22 +624,12 @@ size_t pa_decode_workspace_bytes(int num_seqs, int num_q_heads, int head_dim,
 
 namespace {
 
-// What the entry points beside pa_decode add to the call.
-struct DecodeExtra {
-  const void* new_key = nullptr;    // pa_decode_append
-  const void* new_value = nullptr;
-  const uint8_t* scales = nullptr;  // pa_decode_fp8: the caches hold e4m3 codes
-  bool fp8 = false;
-  bool prefix = false;              // pa_decode_shared_prefix
-  pa::PrefixArgs groups{};
-};
-
 int decode_impl(void* out, const void* query, const void* key_cache, const void* value_cache,
                 const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
                 int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale,
                 int max_blocks_per_seq, int num_blocks, int partition_tokens, pa_dtype dtype,
                 pa_dtype out_dtype, void* workspace, size_t workspace_bytes,
-                const DecodeExtra& extra, cudaStream_t stream) {
+                const void* new_key, const void* new_value, cudaStream_t stream) {
   g_error.clear();
   int rc = check_dtype(dtype);
   if (rc != PA_OK) return rc;
@@ -653,12 +657,10 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   if ((static_cast<long long>(num_blocks) << shift) > 0xfffffffeLL)
     return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size is 2^32 - 1 slots or more");
   if (!isfinite(scale)) return fail(PA_ERR_INVALID, "scale is not finite");
-  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
-  if (extra.fp8 && partition_tokens == 0)
-    partition_tokens = fp8_partition(num_seqs, num_kv_heads, lmax);
   int pt = 0;
   rc = resolve_partition(partition_tokens, block_size, max_blocks_per_seq, &pt);
   if (rc != PA_OK) return rc;
+  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
   if (lmax > 0x7fffffffll)
     return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size = %lld overflows int", lmax);
   if (num_seqs > 65535 || num_kv_heads > 65535)
@@ -671,23 +673,9 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
     return fail(PA_ERR_INVALID, "out, query and the caches must be 16-byte aligned");
   if (!aligned4(block_tables) || !aligned4(seq_lens))
     return fail(PA_ERR_INVALID, "block_tables and seq_lens must be 4-byte aligned");
-  if (extra.fp8 || extra.prefix) {
-    // the streaming kernel's positions (tiles of 16 tokens or more) are 32-bit
-    const double tiles = static_cast<double>(num_seqs) * num_kv_heads *
-                         (static_cast<double>(lmax) / (extra.fp8 ? 32 : 16) + 2.0);
-    if (tiles >= 2147483648.0)
-      return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_kv_heads * max sequence length too large");
-  }
-  if (extra.fp8) {
-    if (!extra.scales) return fail(PA_ERR_INVALID, "a pointer argument is NULL");
-    if (!aligned16(extra.scales)) return fail(PA_ERR_INVALID, "cache_scales must be 16-byte aligned");
-  }
 
-  // a shared prefix adds the pieces of its chunks to every row
   const int parts = static_cast<int>((lmax + pt - 1) / pt);
-  const int pieces = parts + (extra.prefix ? extra.groups.max_chunks : 0);
-  const pa::WorkspaceLayout wl =
-      pa::workspace_layout(num_seqs, num_q_heads, head_dim, extra.prefix ? std::max(pieces, 2) : pieces);
+  const pa::WorkspaceLayout wl = pa::workspace_layout(num_seqs, num_q_heads, head_dim, parts);
   if (wl.total > 0) {
     if (workspace == nullptr || workspace_bytes < wl.total)
       return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", wl.total,
@@ -734,11 +722,11 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = num_blocks;
   a.partition_tokens = pt;
-  a.max_partitions = pieces;
+  a.max_partitions = parts;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.out_f32 = out_dtype == PA_FLOAT32 ? 1 : 0;
-  a.new_key = extra.new_key;
-  a.new_value = extra.new_value;
+  a.new_key = new_key;
+  a.new_value = new_value;
   char* ws = static_cast<char*>(workspace);
   a.ws_count = wl.total ? reinterpret_cast<int*>(ws + wl.count_off) : nullptr;
   // the trailing partitions of rows are handed out at run time only with a
@@ -750,43 +738,7 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
   a.ws_lse = wl.total ? reinterpret_cast<float*>(ws + wl.lse_off) : nullptr;
   a.ws_out = wl.total ? reinterpret_cast<float*>(ws + wl.out_off) : nullptr;
   a.bad = bad;
-  const bool bf16 = dtype == PA_BFLOAT16;
-  cudaError_t e = cudaSuccess;
-  if (extra.fp8 || extra.prefix) {
-    pa::StreamArgs x{};
-    static_cast<pa::DecodeArgs&>(x) = a;
-    x.scales = extra.scales;
-    x.groups = extra.groups;
-    rc = counter(true, &x.timeouts);
-    if (rc != PA_OK) return rc;
-    if (extra.prefix) {
-      pa::PrefixPassArgs p{};
-      p.query = query;
-      p.key_cache = key_cache;
-      p.value_cache = value_cache;
-      p.block_tables = block_tables;
-      p.num_q_heads = num_q_heads;
-      p.num_kv_heads = num_kv_heads;
-      p.group = group;
-      p.block_shift = shift;
-      p.max_blocks_per_seq = max_blocks_per_seq;
-      p.num_blocks = num_blocks;
-      p.scale_log2 = a.scale_log2;
-      p.bad = bad;
-      p.timeouts = x.timeouts;
-      p.groups = extra.groups;
-      p.max_pieces = pieces;
-      p.ws_lse = a.ws_lse;
-      p.ws_out = a.ws_out;
-      e = pa::launch_prefix_pass(p, head_dim, bf16, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
-      e = pa::launch_decode_prefix(x, head_dim, bf16, sms, stream);
-    } else {
-      e = pa::launch_decode_fp8(x, head_dim, bf16, sms, stream);
-    }
-  } else {
-    e = pa::launch_decode(a, head_dim, bf16, sms, stream);
-  }
+  cudaError_t e = pa::launch_decode(a, head_dim, dtype == PA_BFLOAT16, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
   return PA_OK;
 }
@@ -803,7 +755,7 @@ int pa_decode(void* out, const void* query, const void* key_cache, const void* v
   return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
                      num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes,
-                     DecodeExtra{}, stream);
+                     nullptr, nullptr, stream);
 }
 
 int pa_decode_append(void* out, const void* query, const void* new_key, const void* new_value,
@@ -818,14 +770,178 @@ int pa_decode_append(void* out, const void* query, const void* new_key, const vo
     if (!aligned16(new_key) || !aligned16(new_value))
       return fail(PA_ERR_INVALID, "new_key and new_value must be 16-byte aligned");
   }
-  DecodeExtra extra;
-  extra.new_key = new_key;
-  extra.new_value = new_value;
   return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
                      num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes,
-                     extra, stream);
+                     new_key, new_value, stream);
 }
+
+}  // extern "C"
+
+namespace {
+
+// pa_decode_fp8 (scales) and pa_decode_shared_prefix (groups).
+int stream_impl(void* out, const void* query, const void* key_cache, const void* value_cache,
+                const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale,
+                int max_blocks_per_seq, int num_blocks, int partition_tokens, pa_dtype dtype,
+                pa_dtype out_dtype, void* workspace, size_t workspace_bytes, bool fp8,
+                const uint8_t* scales, const int32_t* group_start, const int32_t* prefix_lens,
+                int num_groups, int max_prefix_len, int max_group_size, cudaStream_t stream) {
+  g_error.clear();
+  int rc = check_dtype(dtype);
+  if (rc != PA_OK) return rc;
+  if (out_dtype != dtype && out_dtype != PA_FLOAT32)
+    return fail(PA_ERR_INVALID, "out_dtype %d must equal dtype %d or be PA_FLOAT32", (int)out_dtype,
+                (int)dtype);
+  if (num_seqs < 0) return fail(PA_ERR_INVALID, "num_seqs %d < 0", num_seqs);
+  if (num_q_heads < 1 || num_kv_heads < 1)
+    return fail(PA_ERR_INVALID, "num_q_heads %d / num_kv_heads %d must be >= 1", num_q_heads,
+                num_kv_heads);
+  if (num_q_heads % num_kv_heads != 0)
+    return fail(PA_ERR_INVALID, "num_q_heads %d is not a multiple of num_kv_heads %d", num_q_heads,
+                num_kv_heads);
+  const int group = num_q_heads / num_kv_heads;
+  if (group > pa::kMaxGroup)
+    return fail(PA_ERR_UNSUPPORTED, "%d query heads per kv head (> %d)", group, pa::kMaxGroup);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PA_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
+  const int shift = log2_pow2(block_size);
+  if (shift < 0)
+    return fail(PA_ERR_UNSUPPORTED, "block_size %d (supported: powers of two up to 64)", block_size);
+  if (max_blocks_per_seq < 1) return fail(PA_ERR_INVALID, "max_blocks_per_seq %d < 1", max_blocks_per_seq);
+  if (num_blocks < 1) return fail(PA_ERR_INVALID, "num_blocks %d < 1", num_blocks);
+  if ((static_cast<long long>(num_blocks) << shift) > 0xfffffffeLL)
+    return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size is 2^32 - 1 slots or more");
+  if (!fp8 && !pa::prefill_tc_supported(block_size, static_cast<long long>(num_blocks) << shift))
+    return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size is 2^31 slots or more");
+  if (!isfinite(scale)) return fail(PA_ERR_INVALID, "scale is not finite");
+  if (partition_tokens < 0 || partition_tokens % 16 != 0 || partition_tokens % block_size != 0)
+    return fail(PA_ERR_INVALID, "partition_tokens %d must be a multiple of 16 and of block_size %d",
+                partition_tokens, block_size);
+  if (partition_tokens > pa::kMaxPartitionTokens)
+    return fail(PA_ERR_UNSUPPORTED, "partition_tokens %d > %d", partition_tokens, pa::kMaxPartitionTokens);
+  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
+  if (lmax > 0x7fffffffll)
+    return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size = %lld overflows int", lmax);
+  if (num_seqs > 65535 || num_kv_heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "num_seqs %d / num_kv_heads %d above 65535", num_seqs, num_kv_heads);
+  // positions on the line of tiles (of 16 or 32 tokens) are 32-bit in the kernel
+  if (static_cast<double>(num_seqs) * num_kv_heads * (static_cast<double>(lmax) / (fp8 ? 32 : 16) + 2.0) >=
+      2147483648.0)
+    return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_kv_heads * max sequence length too large");
+  pa::PrefixArgs groups{};
+  if (!fp8 && num_seqs > 0) {
+    if (num_groups < 1) return fail(PA_ERR_INVALID, "num_groups %d < 1", num_groups);
+    if (num_groups > 65535) return fail(PA_ERR_UNSUPPORTED, "num_groups %d above 65535", num_groups);
+    if (max_prefix_len < 0) return fail(PA_ERR_INVALID, "max_prefix_len %d < 0", max_prefix_len);
+    if (max_group_size < 0) return fail(PA_ERR_INVALID, "max_group_size %d < 0", max_group_size);
+    if (!group_start || !prefix_lens)
+      return fail(PA_ERR_INVALID, "group_start / prefix_lens is NULL");
+    if (!aligned4(group_start) || !aligned4(prefix_lens))
+      return fail(PA_ERR_INVALID, "group_start and prefix_lens must be 4-byte aligned");
+    groups.group_start = group_start;
+    groups.prefix_lens = prefix_lens;
+    groups.num_groups = num_groups;
+    groups.num_seqs = num_seqs;
+    pa::plan_prefix(&groups, num_groups, group, num_kv_heads, static_cast<int>(lmax), max_prefix_len,
+                    max_group_size);
+  }
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !query || !key_cache || !value_cache || !block_tables || !seq_lens || (fp8 && !scales))
+    return fail(PA_ERR_INVALID, "a pointer argument is NULL");
+  if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache))
+    return fail(PA_ERR_INVALID, "out, query and the caches must be 16-byte aligned");
+  if (!aligned4(block_tables) || !aligned4(seq_lens))
+    return fail(PA_ERR_INVALID, "block_tables and seq_lens must be 4-byte aligned");
+  if (!aligned16(scales)) return fail(PA_ERR_INVALID, "cache_scales must be 16-byte aligned");
+  const pa::StreamLayout wl = pa::stream_layout(fp8, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                lmax, groups.max_chunks);
+  if (wl.total > 0) {
+    if (workspace == nullptr || workspace_bytes < wl.total)
+      return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", wl.total,
+                  workspace == nullptr ? (size_t)0 : workspace_bytes);
+    if (!aligned16(workspace)) return fail(PA_ERR_INVALID, "workspace must be 16-byte aligned");
+  }
+  int sms = 0;
+  rc = num_sms(&sms);
+  if (rc != PA_OK) return rc;
+  unsigned long long *bad = nullptr, *timeouts = nullptr;
+  rc = bad_counter(&bad);
+  if (rc != PA_OK) return rc;
+  rc = counter(true, &timeouts);
+  if (rc != PA_OK) return rc;
+  if (wl.total > 0) {
+    // only the header has to be zero, and is left so
+    cudaError_t e = prepare_workspace(workspace, pa::kWorkspaceHeader, pa::kWorkspaceHeader, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace counters)");
+  }
+
+  char* ws = static_cast<char*>(workspace);
+  pa::StreamArgs a{};
+  a.out = out;
+  a.query = query;
+  a.key_cache = key_cache;
+  a.value_cache = value_cache;
+  a.scales = scales;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = group;
+  a.heads_at_a_time = wl.heads;
+  a.block_shift = shift;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.out_f32 = out_dtype == PA_FLOAT32 ? 1 : 0;
+  a.groups = groups;
+  a.cut = wl.cut ? 1 : 0;
+  a.least_tiles = std::max(partition_tokens / (fp8 ? 32 : 16), pa::kLeastTiles);
+  if (wl.total > 0) {
+    a.ws_claim = reinterpret_cast<unsigned long long*>(ws);
+    a.ws_done = reinterpret_cast<unsigned*>(ws + 8);
+    a.ws_rows = reinterpret_cast<int2*>(ws + wl.row_off);
+    a.pre_lse = reinterpret_cast<float*>(ws + wl.pre_lse);
+    a.pre_out = reinterpret_cast<float*>(ws + wl.pre_out);
+    a.seg_lse = reinterpret_cast<float*>(ws + wl.seg_lse);
+    a.seg_out = reinterpret_cast<float*>(ws + wl.seg_out);
+  }
+  a.bad = bad;
+  a.timeouts = timeouts;
+  const bool bf16 = dtype == PA_BFLOAT16;
+  cudaError_t e = cudaSuccess;
+  if (groups.max_chunks > 0) {
+    pa::PrefixPassArgs p{};
+    p.query = query;
+    p.key_cache = key_cache;
+    p.value_cache = value_cache;
+    p.block_tables = block_tables;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = group;
+    p.block_shift = shift;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.scale_log2 = a.scale_log2;
+    p.bad = bad;
+    p.timeouts = timeouts;
+    p.groups = groups;
+    p.pre_lse = a.pre_lse;
+    p.pre_out = a.pre_out;
+    e = pa::launch_prefix_pass(p, head_dim, bf16, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+  }
+  e = fp8 ? pa::launch_decode_fp8(a, head_dim, bf16, sms, stream)
+          : pa::launch_decode_prefix(a, head_dim, bf16, sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "streaming decode launch");
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
 
 int pa_decode_fp8(void* out, const void* query, const void* key_cache, const void* value_cache,
                   const uint8_t* cache_scales, const int32_t* block_tables,
@@ -833,44 +949,10 @@ int pa_decode_fp8(void* out, const void* query, const void* key_cache, const voi
                   int head_dim, int block_size, float scale, int max_blocks_per_seq,
                   int num_blocks, int partition_tokens, pa_dtype dtype, pa_dtype out_dtype,
                   void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  DecodeExtra extra;
-  extra.fp8 = true;
-  extra.scales = cache_scales;
-  return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+  return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
-                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes,
-                     extra, stream);
-}
-
-size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                                     int max_blocks_per_seq, int block_size, int partition_tokens) {
-  if (num_seqs < 0 || num_kv_heads < 1 || max_blocks_per_seq < 1) return 0;
-  if (partition_tokens == 0)
-    partition_tokens =
-        fp8_partition(num_seqs, num_kv_heads, static_cast<long long>(max_blocks_per_seq) * block_size);
-  return pa_decode_workspace_bytes(num_seqs, num_q_heads, head_dim, max_blocks_per_seq, block_size,
-                                   partition_tokens);
-}
-
-size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,
-                                               int num_kv_heads, int head_dim,
-                                               int max_blocks_per_seq, int block_size,
-                                               int max_prefix_len, int max_group_size) {
-  if (num_seqs < 0 || num_groups < 1 || num_q_heads < 1 || num_kv_heads < 1 ||
-      num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > pa::kMaxGroup ||
-      (head_dim != 64 && head_dim != 128) || max_blocks_per_seq < 1 || log2_pow2(block_size) < 0 ||
-      max_prefix_len < 0 || max_group_size < 0 ||
-      static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffll)
-    return 0;
-  const int pt = prefix_partition(block_size, max_blocks_per_seq);
-  pa::PrefixArgs x{};
-  pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads,
-                  max_blocks_per_seq * block_size, max_prefix_len, max_group_size);
-  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
-  const long long pieces = (lmax + pt - 1) / pt + x.max_chunks;
-  return pa::workspace_layout(num_seqs, num_q_heads, head_dim,
-                              static_cast<int>(std::max(pieces, 2ll)))
-      .total;
+                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, true,
+                     cache_scales, nullptr, nullptr, 0, 0, 0, stream);
 }
 
 int pa_decode_shared_prefix(void* out, const void* query, const void* key_cache,
@@ -882,38 +964,37 @@ int pa_decode_shared_prefix(void* out, const void* query, const void* key_cache,
                             int max_prefix_len, int max_group_size, pa_dtype dtype,
                             pa_dtype out_dtype, void* workspace, size_t workspace_bytes,
                             cudaStream_t stream) {
-  g_error.clear();
-  if (num_seqs > 0) {
-    if (num_groups < 1) return fail(PA_ERR_INVALID, "num_groups %d < 1", num_groups);
-    if (num_groups > 65535) return fail(PA_ERR_UNSUPPORTED, "num_groups %d above 65535", num_groups);
-    if (max_prefix_len < 0) return fail(PA_ERR_INVALID, "max_prefix_len %d < 0", max_prefix_len);
-    if (max_group_size < 0) return fail(PA_ERR_INVALID, "max_group_size %d < 0", max_group_size);
-    if (!group_start || !prefix_lens)
-      return fail(PA_ERR_INVALID, "group_start / prefix_lens is NULL");
-    if (!aligned4(group_start) || !aligned4(prefix_lens))
-      return fail(PA_ERR_INVALID, "group_start and prefix_lens must be 4-byte aligned");
-    if (log2_pow2(block_size) >= 0 &&
-        !pa::prefill_tc_supported(block_size, static_cast<long long>(num_blocks) * block_size))
-      return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size is 2^31 slots or more");
-  }
-  DecodeExtra extra;
-  extra.prefix = true;
-  if (num_seqs > 0 && num_kv_heads >= 1 && num_q_heads >= num_kv_heads && max_blocks_per_seq >= 1 &&
-      log2_pow2(block_size) >= 0) {  // other sizes are rejected before the plan is used
-    pa::PrefixArgs& x = extra.groups;
-    const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
-    x.group_start = group_start;
-    x.prefix_lens = prefix_lens;
-    x.num_groups = num_groups;
-    x.num_seqs = num_seqs;
-    pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads,
-                    static_cast<int>(std::min(lmax, 0x7fffffffll)), max_prefix_len, max_group_size);
-  }
-  return decode_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+  return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
-                     num_blocks,
-                     log2_pow2(block_size) >= 0 ? prefix_partition(block_size, max_blocks_per_seq) : 0,
-                     dtype, out_dtype, workspace, workspace_bytes, extra, stream);
+                     num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, false, nullptr,
+                     group_start, prefix_lens, num_groups, max_prefix_len, max_group_size, stream);
+}
+
+size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq, int block_size) {
+  if (num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 ||
+      (head_dim != 64 && head_dim != 128) || max_blocks_per_seq < 1 || log2_pow2(block_size) < 0)
+    return 0;
+  return pa::stream_layout(true, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                           static_cast<long long>(max_blocks_per_seq) * block_size, 0)
+      .total;
+}
+
+size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,
+                                               int num_kv_heads, int head_dim,
+                                               int max_blocks_per_seq, int block_size,
+                                               int max_prefix_len, int max_group_size) {
+  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
+  if (num_seqs < 0 || num_groups < 1 || num_q_heads < 1 || num_kv_heads < 1 ||
+      num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > pa::kMaxGroup ||
+      (head_dim != 64 && head_dim != 128) || max_blocks_per_seq < 1 || log2_pow2(block_size) < 0 ||
+      max_prefix_len < 0 || max_group_size < 0 || lmax > 0x7fffffffll)
+    return 0;
+  pa::PrefixArgs x{};
+  pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads, static_cast<int>(lmax),
+                  max_prefix_len, max_group_size);
+  return pa::stream_layout(false, num_seqs, num_q_heads, num_kv_heads, head_dim, lmax, x.max_chunks)
+      .total;
 }
 
 }  // extern "C"

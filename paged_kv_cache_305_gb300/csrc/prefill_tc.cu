@@ -448,9 +448,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    static_cast<size_t>(h) * G + r % G;
       void* out = a.out;
       if constexpr (PREFIX) {  // the chunk's piece of the row
-        out = a.ws_out;
-        row = row * a.max_pieces + blockIdx.x / a.prefix_tiles;
-        if (row_valid) a.ws_lse[row] = l > 0.f ? m + __log2f(l) : -INFINITY;
+        out = a.pre_out;
+        row = row * a.groups.max_chunks + blockIdx.x / a.prefix_tiles;
+        if (row_valid) a.pre_lse[row] = l > 0.f ? m + __log2f(l) : -INFINITY;
       }
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {

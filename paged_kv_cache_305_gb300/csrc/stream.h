@@ -19,13 +19,36 @@ struct PrefixArgs {
   int beside_decode;  // one CTA of the pass per SM, leaving room for the decode kernel's
 };
 
-// The streaming decode kernel (decode_stream.cuh). max_partitions is the number
-// of pieces a row has room for; group_start and the partition fields that only
-// the 16-bit decode kernel uses stay unset.
-struct StreamArgs : DecodeArgs {
-  const uint8_t* scales;  // 8-bit caches: exponent bytes [NB, Hkv, 2, B]
-  PrefixArgs groups;      // shared prefixes (num_groups 0: none)
-  int least_tiles;        // shortest unit of work, in tiles (0: rows are not cut)
+// The streaming decode kernel and its merge (decode_stream.cuh).
+struct StreamArgs {
+  void* out;
+  const void* query;
+  const void* key_cache;
+  const void* value_cache;
+  const uint8_t* scales;  // 8-bit caches: exponent bytes [NB, Hkv, 2, B], else null
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  int num_seqs;
+  int num_q_heads;
+  int num_kv_heads;
+  int group;            // num_q_heads / num_kv_heads
+  int heads_at_a_time;  // kv heads a CTA takes together (4, 2 or 1; divides num_kv_heads)
+  int block_shift;
+  int max_blocks_per_seq;
+  int num_blocks;
+  float scale_log2;     // scale * log2(e)
+  int out_f32;
+  PrefixArgs groups;    // shared prefixes (num_groups 0: none)
+  int cut;              // 1: rows may be cut between units
+  int least_tiles;      // shortest unit that cuts rows, in tiles
+  unsigned long long* ws_claim;  // units claimed so far (zero between calls)
+  unsigned* ws_done;             // CTAs finished (zero between calls)
+  int2* ws_rows;        // [S, Hkv] first slot and number of a row's segments (0: the row is finished)
+  float* pre_lse;       // [S, Hq, max_chunks] pieces of the prefix pass: base-2 log-sum-exp
+  float* pre_out;       // and normalised fp32 rows [.., d]
+  float* seg_lse;       // [slots, heads_at_a_time, G] pieces of segments, likewise
+  float* seg_out;
+  unsigned long long* bad;
   unsigned long long* timeouts;  // bounded waits that gave up
 };
 
@@ -33,9 +56,8 @@ struct StreamArgs : DecodeArgs {
 struct PrefixPassArgs : PrefillArgs {
   PrefixArgs groups;
   int prefix_tiles;  // query tiles of a group (set by the launcher)
-  int max_pieces;    // pieces a row has room for in ws_lse and ws_out
-  float* ws_lse;
-  float* ws_out;
+  float* pre_lse;
+  float* pre_out;
 };
 
 // An 8-bit pool: e4m3 codes [NB, B, Hkv, d] and exponent bytes [NB, Hkv, 2, B].
@@ -56,10 +78,26 @@ constexpr int kPrefixMinChunk = 256;
 void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
                  int max_prefix_len, int max_group_size);
 
-// Schedule of the streaming decode kernel: the share (%) of the work that is
-// dealt out to the CTAs beforehand, and about how many units each claims of the rest.
+// Schedule of the streaming decode kernel: three CTAs on each of the 152 SMs;
+// the share (%) of the work that is dealt out to them beforehand, and about how
+// many units each claims of the rest; the shortest unit that may cut a row, in
+// tiles; tables of up to kUncutTokens leave rows whole.
+constexpr int kMaxCtas = 456;
 constexpr int kStaticShare = 80;
 constexpr int kClaims = 4;
+constexpr int kLeastTiles = 4;
+constexpr long long kUncutTokens = 512;
+constexpr int kGroupTiles = 16;  // see stream_heads
+
+// Workspace of the streaming decode kernel: the header (claims, CTAs finished),
+// the rows' segment counts, then the pieces.
+struct StreamLayout {
+  int heads;  // kv heads at a time
+  bool cut;   // rows may be cut
+  size_t row_off, pre_lse, seg_lse, pre_out, seg_out, total;
+};
+StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                           long long lmax, int max_chunks);
 
 cudaError_t launch_decode_fp8(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
                               cudaStream_t stream);

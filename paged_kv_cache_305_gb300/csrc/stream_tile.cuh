@@ -3,22 +3,27 @@
 // for 8-bit caches (tiles of 32 tokens) and 16-bit ones (16 tokens).
 //
 // Both take the tile as S^T = K q^T with the legacy m16n8k16 product (16 tokens
-// x 8 query heads; a group of up to 8 heads costs one product per 16 dims), and
-// O^T = V^T P^T with the same instruction, weights as two 16-bit parts.
+// x 8 columns, a column for a query head), and O^T = V^T P^T with the same
+// instruction, weights as two 16-bit parts. With up to 4 query heads (SPLIT)
+// columns 4-7 repeat the heads of columns 0-3: both halves compute the same
+// scores, columns 0-3 carry the weights' 16-bit roundings and columns 4-7 the
+// remainders, and one product serves both parts where two would leave half of
+// their columns empty (32 instead of 48 products a tile of 32 tokens).
+//
+// Softmax, base 2, in raw scores x = q . k (the sign of the scale is given to
+// q): weights p = 2^(x sl2 - m sl2), sl2 = |scale| log2(e). The reference m is
+// raised, and l and O rescaled, only when a score passes it by more than 8
+// binary orders: weights stay below 2^8, and most tiles take one vote in the
+// place of the reduction of their maxima.
 //
 // 8-bit caches. A token's K row is its codes k8 times 2^(ek - 127), its V row
 // v8 times 2^(ev - 127). Codes become fp16 exactly (one conversion instruction
 // per two), the products run on fp16 with fp32 accumulation, and the factors
-// enter outside of them: K's multiplies the score, V's the softmax weight.
-//
-//   x_t = (q . k8_t) 2^(ek_t - 127) scale log2(e)
-//   m = max x,  l = sum 2^(x_t - m)
-//   O = sum 2^((x_t - m) + (ev_t - 127 - r)) v8_t,   out = O 2^r / l
-//
-// r is a whole number, at least max_t (x_t + ev_t - 127) - m, so every weight
-// of O is at most 1 and the largest is above 1/2, whatever V's factors are: a
-// weight's two fp16 parts then keep 22 bits of the ones that count. Being
-// whole, ev - 127 - r is exact, and no second rounding enters the exponent.
+// enter outside of them: K's multiplies the score, V's the softmax weight:
+//   O = sum p_t 2^(ev_t - r + 7) v8_t,   out = O 2^(r - 127 - 7) / l
+// with r the largest ev so far. A weight of O is below 2^15 and exact up to its
+// two fp16 parts, which reach down to 2^-25: V's rows may differ by 2^20 in
+// size before a row of normal size loses bits next to a huge one.
 //
 // Fragment orders of 8-bit tiles. ldmatrix moves 8x8 tiles of 16-bit units,
 // here pairs of codes. For K a lane gets four neighbouring codes of one token,
@@ -37,26 +42,41 @@
 
 namespace pa {
 
-// The running state of a warp: fragment element e of m-tile mt and head tile nt
-// belongs to query head nt * 8 + 2 (lane % 4) + (e & 1).
+constexpr float kRaiseAt = 8.f;  // binary orders a score may pass the reference by
+constexpr int kWeightShift = 7;  // V's weighted rows: weights below 2^(8 + 7)
+
+// The query heads of a kv head as B operand; sl2: factor of a column's scores.
+template <int D, int NT>
+struct Query {
+  uint32_t b[D / 16][NT][2];
+  float sl2[NT][2];
+};
+
+// The running state of a warp: fragment element e of m-tile mt and column tile
+// nt belongs to column nt * 8 + 2 (lane % 4) + (e & 1).
 template <int D, int NT>
 struct State {
-  float m[NT][2], l[NT][2];   // running max (base 2) and sum
-  float u[NT][2], r[NT][2];   // 8-bit: running max of x + ev - 127, and r
+  float m[NT][2], nm[NT][2];  // reference (raw score), and -m sl2
+  float l[NT][2];             // sum of weights (this lane's tokens)
   float o[D / 16][NT][4];     // O^T
+  int r;                      // 8-bit: the largest exponent byte of V so far
+  bool fresh;                 // no tile yet
   __device__ __forceinline__ void reset() {
+    fresh = true;
+    r = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[nt][c] = u[nt][c] = -INFINITY;
-        l[nt][c] = r[nt][c] = 0.f;
+        m[nt][c] = -INFINITY;
+        nm[nt][c] = l[nt][c] = 0.f;
       }
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
   }
+  // O columns times al.
   __device__ __forceinline__ void scale(const float (&al)[NT][2]) {
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
@@ -68,13 +88,36 @@ struct State {
         o[mt][nt][3] *= al[nt][1];
       }
   }
-};
-
-// The query heads of a kv head as B operand, and the factor of their scores.
-template <int D, int NT>
-struct Query {
-  uint32_t b[D / 16][NT][2];
-  float sl2[NT][2];
+  // Raises the references to the columns' maxima, of which mx are this lane's,
+  // where any has been passed by kRaiseAt. `top`: the largest exponent byte of
+  // the tile's V rows (0 for 16-bit caches).
+  __device__ __forceinline__ void raise(const float (&mx)[NT][2], int top, const Query<D, NT>& q) {
+    bool passed = fresh || top > r;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) passed |= (mx[nt][c] - m[nt][c]) * q.sl2[nt][c] > kRaiseAt;
+    if (!__any_sync(0xffffffffu, passed)) return;
+    const float shrink = exponent_factor(max(127 - max(top - r, 0), 0));
+    r = max(r, top);
+    float al[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float v = mx[nt][c];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+        const float mn = fmaxf(m[nt][c], v);
+        const float f = fresh ? 0.f : ex2((m[nt][c] - mn) * q.sl2[nt][c]);
+        l[nt][c] *= f;
+        al[nt][c] = f * shrink;
+        m[nt][c] = mn;
+        nm[nt][c] = -mn * q.sl2[nt][c];
+      }
+    if (!fresh) scale(al);
+    fresh = false;
+  }
 };
 
 // Tile geometry. off(row, chunk): byte offset of a row's 16-byte chunk, in the
@@ -101,37 +144,41 @@ struct Tile {
   }
 };
 
-// qh: the first of the kv head's G query rows. 8-bit: fp16 in the k order above;
+// qh: the first of the kv head's G query rows; sl2 = scale log2(e). 8-bit: fp16 in the k order above;
 // bf16 queries are scaled for each head by the power of two that brings the
 // largest element to [2^14, 2^15): their 8 bits fit into fp16's 11, and what
 // falls below fp16's range is under 2^-39 of the largest.
-template <typename Ty, int D, int NT, bool FP8>
+template <typename Ty, int D, int NT, bool FP8, bool SPLIT>
 __device__ __forceinline__ void load_query(const typename Ty::T* qh, int G, float sl2, Query<D, NT>& q) {
   const int lane = threadIdx.x & 31, r8 = lane >> 2, t = lane & 3;
+  const uint32_t sign = sl2 < 0.f ? 0x80008000u : 0u;
+  sl2 = fabsf(sl2);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int head = nt * 8 + r8;
+    const int head = SPLIT ? r8 & 3 : nt * 8 + r8;
+    const typename Ty::T* row = qh + head * D;
+    q.sl2[nt][0] = q.sl2[nt][1] = sl2;
     if constexpr (!FP8) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const typename Ty::T* p = qh + head * D + kk * 16 + 2 * t;
-        q.b[kk][nt][0] = head < G ? *reinterpret_cast<const uint32_t*>(p) : 0u;
-        q.b[kk][nt][1] = head < G ? *reinterpret_cast<const uint32_t*>(p + 8) : 0u;
+        const typename Ty::T* p = row + kk * 16 + 2 * t;
+        q.b[kk][nt][0] = head < G ? *reinterpret_cast<const uint32_t*>(p) ^ sign : 0u;
+        q.b[kk][nt][1] = head < G ? *reinterpret_cast<const uint32_t*>(p + 8) ^ sign : 0u;
       }
-      q.sl2[nt][0] = q.sl2[nt][1] = sl2;
     } else {
       uint2 w[D / 16];
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        w[kk] = head < G ? *reinterpret_cast<const uint2*>(qh + head * D + kk * 16 + 4 * t)
-                         : make_uint2(0u, 0u);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        w[kk] = head < G ? *reinterpret_cast<const uint2*>(row + kk * 16 + 4 * t) : make_uint2(0u, 0u);
+        w[kk].x ^= sign;
+        w[kk].y ^= sign;
+      }
       if constexpr (!Ty::kIsBf16) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           q.b[kk][nt][0] = w[kk].x;
           q.b[kk][nt][1] = w[kk].y;
         }
-        q.sl2[nt][0] = q.sl2[nt][1] = sl2;
       } else {
         uint32_t top = 0;  // the largest magnitude's bits, as a bf16 in the upper half
 #pragma unroll
@@ -150,30 +197,56 @@ __device__ __forceinline__ void load_query(const typename Ty::T* qh, int G, floa
           q.b[kk][nt][1] = F16::pack(b.x * f, b.y * f);
         }
         const float back = sl2 * exponent_factor(254 - e);
-        q.sl2[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);      // lane of head 2 t
+        q.sl2[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);      // lane of column 2 t
         q.sl2[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);  // and of the next
       }
     }
   }
 }
 
+// Weights of two columns of a token as B fragments of O^T = V^T P^T. SPLIT: the
+// columns' own part (columns 4-7: the remainder) in hi; otherwise both.
+template <typename Ty, bool SPLIT>
+__device__ __forceinline__ void weight_parts(float w0, float w1, uint32_t rest, uint32_t& hi, uint32_t& lo) {
+  const uint32_t h = Ty::pack(w0, w1);
+  const float2 v = Ty::unpack(SPLIT ? h & rest : h);
+  const uint32_t part = Ty::pack(w0 - v.x, w1 - v.y);
+  hi = movmatrix_trans(SPLIT ? part : h);
+  lo = SPLIT ? 0u : movmatrix_trans(part);
+}
+
 // 8-bit tile. sk, sv: K and V codes in shared memory; ek, ev: the exponent
 // bytes of token `lane`; tokens lo .. hi - 1 count (the others' V rows are zero).
-template <int D, int NT>
-__device__ __forceinline__ void tile_8(uint32_t sk, uint32_t sv, uint32_t ek, uint32_t ev, int lo,
-                                       int hi, const Query<D, NT>& q, State<D, NT>& st) {
+template <int D, int NT, bool SPLIT>
+__device__ __forceinline__ void tile_8(uint32_t sk, uint32_t sv, int ek, int ev, int lo, int hi,
+                                       const Query<D, NT>& q, State<D, NT>& st) {
   using Geo = Tile<D, true>;
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, r8 = lane >> 2;
   const int mi = lane >> 3, rr = lane & 7;
+  const bool edge = lo > 0 || hi < Geo::kTokens;
+  if (edge && (lane < lo || lane >= hi)) ev = 0;
 
-  float sc[2][NT][4];  // S^T of tokens 0-15 and 16-31
+  // factors of this lane's tokens r8 + 8 i, as the upper halves of fp32 numbers
+  const int top = __reduce_max_sync(kAll, ev);
+  uint32_t pair = static_cast<uint32_t>(ek) << 23 |
+                  static_cast<uint32_t>(max(ev - max(top, st.r) + 127 + kWeightShift, 0)) << 7;
+  float fk[4], fv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = __shfl_sync(kAll, pair, r8 + 8 * i);
+    fk[i] = __uint_as_float(b & 0xffff0000u);
+    fv[i] = __uint_as_float(b << 16);
+  }
+
+  // S^T of tokens 0-15 and 16-31, each in two accumulators: short chains
+  float sc[2][2][NT][4];
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[hf][nt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) sc[hf][0][nt][e] = sc[hf][1][nt][e] = 0.f;
 #pragma unroll
   for (int kp = 0; kp < D / 32; ++kp) {
 #pragma unroll
@@ -186,70 +259,47 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t sv, uint32_t ek, ui
                                e4m3x2_to_f16x2(k[2 * c] >> 16), e4m3x2_to_f16x2(k[2 * c + 1] >> 16)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          F16::mma(sc[hf][nt], a, q.b[2 * kp + c][nt][0], q.b[2 * kp + c][nt][1]);
+          F16::mma(sc[hf][c][nt], a, q.b[2 * kp + c][nt][0], q.b[2 * kp + c][nt][1]);
       }
     }
   }
 
-  // factors of this lane's tokens r8 + 8 i
-  const uint32_t both = ek | ev << 8;
-  float fk[4], lv[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t b = __shfl_sync(kAll, both, r8 + 8 * i);
-    fk[i] = exponent_factor(b & 0xff);
-    lv[i] = static_cast<float>(static_cast<int>(b >> 8) - 127);
-  }
-
-  uint32_t ph[2][NT][2], pl[2][NT][2];  // weights as B fragments: fp16 and remainder
-  float al[NT][2];
-  bool rescale = false;
+  uint32_t ph[2][NT][2], pl[2][NT][2];
+  float x[NT][4][2], mx[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float x[4][2], w[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float v = sc[i >> 1][nt][(i & 1) * 2 + c] * fk[i] * q.sl2[nt][c];
-        x[i][c] = r8 + 8 * i >= lo && r8 + 8 * i < hi ? v : -INFINITY;
+        const int e = (i & 1) * 2 + c;
+        x[nt][i][c] = (sc[i >> 1][0][nt][e] + sc[i >> 1][1][nt][e]) * fk[i];
       }
+    if (edge) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float mx = fmaxf(fmaxf(x[0][c], x[1][c]), fmaxf(x[2][c], x[3][c]));
-      float ux = fmaxf(fmaxf(x[0][c] + lv[0], x[1][c] + lv[1]), fmaxf(x[2][c] + lv[2], x[3][c] + lv[3]));
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
-        ux = fmaxf(ux, __shfl_xor_sync(kAll, ux, off));
-      }
-      const float mn = fmaxf(st.m[nt][c], mx);
-      st.u[nt][c] = fmaxf(st.u[nt][c], ux);
-      const float rn = ceilf(st.u[nt][c] - mn);
-      const float dm = st.m[nt][c] - mn;
-      al[nt][c] = ex2(dm + (st.r[nt][c] - rn));
-      st.l[nt][c] *= ex2(dm);
-      st.m[nt][c] = mn;
-      st.r[nt][c] = rn;
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float d = x[i][c] - mn;
-        s += ex2(d);
-        w[i][c] = ex2(d + (lv[i] - rn));
-      }
-      st.l[nt][c] += s;
-      rescale |= al[nt][c] != 1.f;
+      for (int i = 0; i < 4; ++i)
+        if (r8 + 8 * i < lo || r8 + 8 * i >= hi) x[nt][i][0] = x[nt][i][1] = -INFINITY;
     }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      mx[nt][c] = fmaxf(fmaxf(x[nt][0][c], x[nt][1][c]), fmaxf(x[nt][2][c], x[nt][3][c]));
+  }
+  st.raise(mx, top, q);
+  const uint32_t rest = (lane & 2) != 0 ? kAll : 0u;  // SPLIT: columns 4-7
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t h = F16::pack(w[i][0], w[i][1]);
-      const float2 hv = F16::unpack(h);
-      ph[i >> 1][nt][i & 1] = movmatrix_trans(h);
-      pl[i >> 1][nt][i & 1] = movmatrix_trans(F16::pack(w[i][0] - hv.x, w[i][1] - hv.y));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) x[nt][i][c] = ex2(fmaf(x[nt][i][c], q.sl2[nt][c], st.nm[nt][c]));
+      if (edge && (r8 + 8 * i < lo || r8 + 8 * i >= hi)) x[nt][i][0] = x[nt][i][1] = 0.f;  // scale 0
+      weight_parts<F16, SPLIT>(x[nt][i][0] * fv[i], x[nt][i][1] * fv[i], rest, ph[i >> 1][nt][i & 1],
+                               pl[i >> 1][nt][i & 1]);
     }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      st.l[nt][c] += (x[nt][0][c] + x[nt][1][c]) + (x[nt][2][c] + x[nt][3][c]);
   }
-  if (__any_sync(kAll, rescale)) st.scale(al);
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) {
     uint32_t v[4];  // tokens 0-7, 8-15, 16-23, 24-31 of the m-tile's 16 dims
@@ -262,20 +312,20 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t sv, uint32_t ek, ui
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         F16::mma(st.o[mt][nt], a, ph[hf][nt][0], ph[hf][nt][1]);
-        F16::mma(st.o[mt][nt], a, pl[hf][nt][0], pl[hf][nt][1]);
+        if constexpr (!SPLIT) F16::mma(st.o[mt][nt], a, pl[hf][nt][0], pl[hf][nt][1]);
       }
     }
   }
 }
 
 // 16-bit tile.
-template <typename Ty, int D, int NT>
+template <typename Ty, int D, int NT, bool SPLIT>
 __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi,
                                         const Query<D, NT>& q, State<D, NT>& st) {
   using Geo = Tile<D, false>;
-  constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, r8 = lane >> 2;
   const int mi = lane >> 3, rr = lane & 7;
+  const bool edge = lo > 0 || hi < Geo::kTokens;
 
   float sc[NT][2][4];  // two accumulators: half the dependent chain
 #pragma unroll
@@ -290,40 +340,35 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
     for (int nt = 0; nt < NT; ++nt) Ty::mma(sc[nt][kk & 1], k, q.b[kk][nt][0], q.b[kk][nt][1]);
   }
   uint32_t ph[NT][2], pl[NT][2];
-  float al[NT][2];
-  bool rescale = false;
+  float x[NT][2][2], mx[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float x[2][2], w[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float v = (sc[nt][0][2 * i + c] + sc[nt][1][2 * i + c]) * q.sl2[nt][c];
-        x[i][c] = r8 + 8 * i >= lo && r8 + 8 * i < hi ? v : -INFINITY;
-      }
+      for (int c = 0; c < 2; ++c) x[nt][i][c] = sc[nt][0][2 * i + c] + sc[nt][1][2 * i + c];
+    if (edge) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float mx = fmaxf(x[0][c], x[1][c]);
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
-      const float mn = fmaxf(st.m[nt][c], mx);
-      al[nt][c] = ex2(st.m[nt][c] - mn);
-      st.m[nt][c] = mn;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) w[i][c] = ex2(x[i][c] - mn);
-      st.l[nt][c] = st.l[nt][c] * al[nt][c] + (w[0][c] + w[1][c]);
-      rescale |= al[nt][c] != 1.f;
+      for (int i = 0; i < 2; ++i)
+        if (r8 + 8 * i < lo || r8 + 8 * i >= hi) x[nt][i][0] = x[nt][i][1] = -INFINITY;
     }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) mx[nt][c] = fmaxf(x[nt][0][c], x[nt][1][c]);
+  }
+  st.raise(mx, 0, q);
+  const uint32_t rest = (lane & 2) != 0 ? 0xffffffffu : 0u;  // SPLIT: columns 4-7
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t h = Ty::pack(w[i][0], w[i][1]);
-      const float2 hv = Ty::unpack(h);
-      ph[nt][i] = movmatrix_trans(h);
-      pl[nt][i] = movmatrix_trans(Ty::pack(w[i][0] - hv.x, w[i][1] - hv.y));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) x[nt][i][c] = ex2(fmaf(x[nt][i][c], q.sl2[nt][c], st.nm[nt][c]));
+      if (edge && (r8 + 8 * i < lo || r8 + 8 * i >= hi)) x[nt][i][0] = x[nt][i][1] = 0.f;  // scale 0
+      weight_parts<Ty, SPLIT>(x[nt][i][0], x[nt][i][1], rest, ph[nt][i], pl[nt][i]);
     }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) st.l[nt][c] += x[nt][0][c] + x[nt][1][c];
   }
-  if (__any_sync(kAll, rescale)) st.scale(al);
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) {
     uint32_t v[4];
@@ -331,7 +376,7 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       Ty::mma(st.o[mt][nt], v, ph[nt][0], ph[nt][1]);
-      Ty::mma(st.o[mt][nt], v, pl[nt][0], pl[nt][1]);
+      if constexpr (!SPLIT) Ty::mma(st.o[mt][nt], v, pl[nt][0], pl[nt][1]);
     }
   }
 }

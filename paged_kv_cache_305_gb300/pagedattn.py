@@ -93,7 +93,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.pa_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float,
                                 i32, i32, i32, i32, i32, vp, sz, vp]
     L.pa_decode_fp8.restype = i32
-    L.pa_decode_fp8_workspace_bytes.argtypes = [i32] * 7
+    L.pa_decode_fp8_workspace_bytes.argtypes = [i32] * 6
     L.pa_decode_fp8_workspace_bytes.restype = sz
     L.pa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                           i32, ctypes.c_float, i32, i32, i32, i32, i32, i32, vp, sz,
@@ -179,11 +179,9 @@ def decode_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int,
 
 
 def decode_fp8_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
-                               max_blocks_per_seq: int, block_size: int,
-                               partition_tokens: int = 0) -> int:
+                               max_blocks_per_seq: int, block_size: int) -> int:
     return int(load_library().pa_decode_fp8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                                            max_blocks_per_seq, block_size,
-                                                            partition_tokens))
+                                                            max_blocks_per_seq, block_size))
 
 
 def decode_partition_tokens(partition_tokens: int, block_size: int,
@@ -203,7 +201,7 @@ def alloc_workspace(query: torch.Tensor, key_cache: torch.Tensor, block_tables: 
     S, Hq, d = query.shape
     if key_cache.dtype == torch.float8_e4m3fn:
         n = decode_fp8_workspace_bytes(S, Hq, key_cache.shape[2], d, block_tables.shape[1],
-                                       key_cache.shape[1], partition_tokens)
+                                       key_cache.shape[1])
     else:
         n = decode_workspace_bytes(S, Hq, d, block_tables.shape[1], key_cache.shape[1], partition_tokens)
     if n == 0:

@@ -345,7 +345,8 @@ def test_decode_bit_identical_however_placed_and_repeated():
 def test_workspace_shared_with_16_bit_decode_and_other_sizes():
     rng = np.random.default_rng(8)
     B, d, Hkv = 16, 64, 2
-    big = torch.zeros(pa.decode_workspace_bytes(6, 8, d, 64, B, 16), dtype=torch.uint8, device="cuda")
+    n = max(pa.decode_workspace_bytes(6, 8, d, 64, B, 16), pa.decode_fp8_workspace_bytes(6, 8, Hkv, d, 64, B))
+    big = torch.zeros(n, dtype=torch.uint8, device="cuda")
     case = W.random_case(num_seqs=4, num_q_heads=8, num_kv_heads=Hkv, head_dim=d, block_size=B,
                          len_range=(1, 900), dtype="fp16", seed=9)
     ref16 = oracle.paged_decode(case.query, case.key_cache, case.value_cache, case.block_tables,
