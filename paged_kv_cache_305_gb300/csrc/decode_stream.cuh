@@ -28,15 +28,17 @@
 // boundary, so slots rise, those of a row follow each other, and there are as
 // many as rows and units together, however long a row is.
 //
-// Streaming. The warps of a head take its tiles in turn, each through its own
-// ring of kStages tiles in shared memory. A lane issues a tensor copy per block
-// for K and for V, straight from the block table, and one bulk copy for the
-// block's exponent bytes; table entries are read kIdDepth tiles ahead. Blocks
-// under 8 tokens, and pools beyond a tensor map's reach, are copied row by row
-// with cp.async (ROWS). The ring runs on across segments and units: the records
-// of the next segments are made a batch ahead, so that their first tiles are on
-// the way when a unit ends. At a segment's end the states of a head's warps are
-// joined through shared memory.
+// Streaming. Four warps compute, a fifth feeds them: it claims units, finds their
+// rows, reads the block table and fills the stages of a ring in shared memory,
+// 32 KB each at d = 128: one tile for every computing warp, the tiles of the
+// CTA's heads side by side. A lane issues a tensor copy per block for K and for
+// V, straight from the block table and for all heads at once, and a bulk copy
+// for the block's exponent bytes. Blocks under 8 tokens, and pools beyond a
+// tensor map's reach, are copied row by row with cp.async (ROWS). A stage carries
+// a note of what it holds, so the computing warps know of nothing but stages:
+// they load the query at a segment's first one and join their states at its
+// last one, while the copies run on across segments and units. All waits are
+// bounded; one that gives up is counted, and the CTA winds down.
 #pragma once
 
 #include <cuda.h>
@@ -56,58 +58,71 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kBatch = 16;      // segments whose records are made at a time
-constexpr int kJoinHeads = 4;   // query heads joined at a time at a segment's end
-constexpr int kIdDepth = 4;     // tiles whose table entries are in flight
+constexpr int kWarps = 4;                      // computing warps
+constexpr int kThreads = kWarps * 32 + 32;     // and the feeding one
+constexpr int kChunks = 128;                   // runs of sequences with a known position on the line
+constexpr int kJoinHeads = 4;                  // query heads joined at a time at a segment's end
 constexpr unsigned kFull = 0xffffffffu;
 
-struct Seg {
-  int s, hg;          // sequence, head group
-  int tile0, ntiles;  // first tile (in tiles of the sequence) and their number
-  int lo, hi;         // tokens of the row: [lo, hi)
-  int slot;           // of its piece; -1: the row is finished here
-  int turn;           // which of a head's warps takes the first tile
+// What a stage holds.
+struct Note {
+  int s, hg;   // sequence, head group
+  int t0;      // its first token
+  int lo, hi;  // tokens of the row: [lo, hi)
+  int slot;    // of the segment's piece; -1: the row is finished here
+  int flags;
+  int pad;
 };
+enum : int { kFirst = 1, kLast = 2, kEnd = 4 };  // of the segment; of all work
 
 template <int D, bool FP8, int NT>
 struct Ring {
   using T = Tile<D, FP8>;
-  static constexpr int kStageBytes = 2 * T::kBytes;
-  static constexpr int kStages = 16384 / kStageBytes;  // 16 KB for each warp
-  static constexpr int kScaleBytes = 64;               // exponent bytes of a stage: K's, V's by block
+  static constexpr int kHalf = kWarps * T::kBytes;       // K (or V) of a stage
+  static constexpr int kStages = 65536 / (2 * kHalf);
+  static constexpr int kScaleBytes = kWarps * 64;        // exponent bytes of a stage
   static constexpr int kHeads = NT * 8;
   static constexpr int kOStride = D + 4;
   // offsets in shared memory
-  static constexpr int kScales = kWarps * kStages * kStageBytes;
-  static constexpr int kBars = kScales + (FP8 ? kWarps * kStages * kScaleBytes : 0);
-  static constexpr int kStats = kBars + kWarps * kStages * 8;  // [warp][m, l, r][head]
-  static constexpr int kSegs = kStats + kWarps * 3 * kHeads * 4;
-  static constexpr int kMisc = kSegs + 2 * kBatch * static_cast<int>(sizeof(Seg));
-  static constexpr int kJoin = kMisc + 128;                    // [warp][head][kOStride]
+  static constexpr int kScales = kStages * 2 * kHalf;
+  static constexpr int kNotes = kScales + (FP8 ? kStages * kScaleBytes : 0);
+  static constexpr int kBars = kNotes + kStages * static_cast<int>(sizeof(Note));  // full, empty, joins
+  static constexpr int kStats = kBars + (2 * kStages + kWarps) * 8;  // [warp][m, l, r][head]
+  static constexpr int kBase = kStats + kWarps * 3 * kHeads * 4;     // [kChunks]
+  static constexpr int kMisc = kBase + kChunks * 4;
+  static constexpr int kJoin = (kMisc + 64 + 15) / 16 * 16;          // [warp][head][kOStride]
   static constexpr int kBytes = kJoin + kWarps * kJoinHeads * kOStride * 4;
-  static_assert(kStages >= 2, "a tile lands while another is computed");
+  static_assert(kStages >= 2, "a stage lands while another is computed");
+  static_assert(kStats % 8 == 0 && kBars % 8 == 0 && kNotes % 16 == 0, "alignment");
 };
 
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 
-// Shared scratch of the schedule. Positions on the line of tiles are 32-bit: the
-// host refuses sizes that could have 2^31 tiles.
+// Shared scratch. Positions on the line are 32-bit: the host refuses sizes that
+// could have 2^31 of them.
 struct Misc {
   unsigned scan[kWarps];
-  unsigned row_pos;        // position of the cursor's row
-  int hg, s;               // the cursor's row
-  unsigned unit, next;     // the cursor's unit, and the one after it
-  int more;                // the unit goes on behind the records made so far
-  int nseg[2];             // records of the even and the odd batch
-  unsigned Wseq, W;        // tiles of one kv head's rows, and of all
-  unsigned T1, W1, nstat;  // tiles of a static unit, end and number of those
-  unsigned T2, nunits;     // tiles of a claimed unit, number of all units
+  unsigned Wseq, W;        // stages of one head group's rows, and of all
+  unsigned T1, W1, nstat;  // stages of a static unit, end and number of those
+  unsigned T2, nunits;     // stages of a claimed unit, number of all units
+  int abort;               // a wait has given up
 };
-static_assert(sizeof(Misc) <= 128, "room reserved in Ring");
+static_assert(sizeof(Misc) <= 64, "room reserved in Ring");
+
+// ROWS: the entry of token x, held by lane x % 32 at x / 32 (x differs by lane; all
+// lanes of the warp call this together).
+template <int N>
+__device__ __forceinline__ uint32_t row_id(const uint32_t (&v)[N], int x) {
+  uint32_t got = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t t = __shfl_sync(kFull, v[j], x & 31);
+    if (j == x >> 5) got = t;
+  }
+  return got;
+}
 
 // SPLIT: at most 4 query heads a kv head (stream_tile.cuh).
 template <typename Ty, int D, int NT, bool FP8, bool ROWS, bool SPLIT>
@@ -117,7 +132,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   using R = Ring<D, FP8, NT>;
   using Geo = Tile<D, FP8>;
   using T = typename Ty::T;
-  constexpr int kTT = Geo::kTokens, kStages = R::kStages;
+  constexpr int kTT = Geo::kTokens, kStages = R::kStages, kRB = Geo::kRowBytes;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -126,29 +141,45 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   const int G = a.group, S = a.num_seqs, Hkv = a.num_kv_heads, shift = a.block_shift;
   const int Lmax = a.max_blocks_per_seq << shift;
   const int Hc = a.heads_at_a_time, NG = Hkv / Hc;  // heads at a time, head groups
-  const int Wh = kWarps / Hc;                     // warps of a head
-  const int hsub = warp / Wh, wsub = warp % Wh;   // this warp's head, and its place among the head's
-  Seg* sSeg = reinterpret_cast<Seg*>(smem + R::kSegs);
+  const int Wh = kWarps / Hc;                       // warps of a head
+  const int ST = Wh * kTT;                          // tokens of a stage
+  const int lb = ROWS ? ST : min(1 << shift, ST);   // tokens that lie together in a stage
   Misc& misc = *reinterpret_cast<Misc*>(smem + R::kMisc);
-  float* sStats = reinterpret_cast<float*>(smem + R::kStats);
-  float* sJoin = reinterpret_cast<float*>(smem + R::kJoin);
-  const uint32_t ring = smem_u32(smem) + warp * kStages * R::kStageBytes;
-  unsigned char* wscales = smem + R::kScales + warp * kStages * R::kScaleBytes;
-  const uint32_t bars = smem_u32(smem + R::kBars) + warp * kStages * 8;
+  Note* notes = reinterpret_cast<Note*>(smem + R::kNotes);
+  unsigned* sBase = reinterpret_cast<unsigned*>(smem + R::kBase);
+  const uint32_t ring = smem_u32(smem), bars = smem_u32(smem + R::kBars);
+  auto full = [&](uint32_t st) { return bars + 8 * st; };
+  auto empty = [&](uint32_t st) { return bars + 8 * (kStages + st); };
+  auto join_bar = [&](int h) { return bars + 8 * (2 * kStages + h); };
+  // bounded wait of a warp; false once any wait of the CTA has given up
+  volatile int* aborted = &misc.abort;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (__all_sync(kFull, tc::mbar_wait(bar, parity))) return true;
+    if (lane == 0 && *aborted == 0) {
+      *aborted = 1;
+      atomicAdd(a.timeouts, 1ull);
+    }
+    return false;
+  };
 
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) tc::mbar_init(bars + 8 * i, ROWS ? 32 : 1);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(full(i), ROWS ? 64 : 1);
+      tc::mbar_init(empty(i), kWarps);
+    }
+    for (int i = 0; i < kWarps; ++i) tc::mbar_init(join_bar(i), Wh);
     tc::mbar_init_fence();
+    misc.abort = 0;
     if constexpr (!ROWS) {
       tc::prefetch_tensormap(&kmap);
       tc::prefetch_tensormap(&vmap);
     }
   }
 
-  // ---- the line of tiles ---------------------------------------------------
+  // ---- the line of stages ----------------------------------------------------
   struct Row {
     int lo, hi;  // tokens
-    int n;       // tiles; one (without tokens) for an empty row
+    int n;       // stages; one (without tokens) for an empty row
     int before;  // pieces of the prefix pass
   };
   auto row_of = [&](int s) {
@@ -162,41 +193,42 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         r.before = prefix_pieces(a.groups, r.lo);
       }
     }
-    r.n = max((r.hi + kTT - 1) / kTT - r.lo / kTT, 1);
+    r.n = max((r.hi + ST - 1) / ST - r.lo / ST, 1);
     return r;
   };
-  const int per = (S + kThreads - 1) / kThreads;
-  const int s_lo = min(S, tid * per), s_hi = min(S, s_lo + per);
-  unsigned mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) {
-    mine += row_of(s).n;
-    if (blockIdx.x == 0) {
-      const int raw = __ldg(a.seq_lens + s);
-      if (raw < 0 || raw > Lmax) atomicAdd(a.bad, 1ull);
+  const int per = (S + kChunks - 1) / kChunks;
+  if (warp < kWarps) {
+    unsigned mine = 0;
+    for (int s = tid * per; s < min(S, (tid + 1) * per); ++s) {
+      mine += row_of(s).n;
+      if (blockIdx.x == 0) {
+        const int raw = __ldg(a.seq_lens + s);
+        if (raw < 0 || raw > Lmax) atomicAdd(a.bad, 1ull);
+      }
     }
-  }
-  if constexpr (!FP8) {
-    if (blockIdx.x == 0) count_bad_groups(a.groups, tid, kThreads, a.bad);
-  }
-  unsigned base = mine;  // exclusive prefix of the sequences before this thread's
+    if constexpr (!FP8) {
+      if (blockIdx.x == 0) count_bad_groups(a.groups, tid, kChunks, a.bad);
+    }
+    unsigned incl = mine;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const unsigned v = __shfl_up_sync(kFull, base, off);
-    if (lane >= off) base += v;
+    for (int off = 1; off < 32; off <<= 1) {
+      const unsigned v = __shfl_up_sync(kFull, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (lane == 31) misc.scan[warp] = incl;
+    sBase[tid] = incl - mine;
   }
-  if (lane == 31) misc.scan[warp] = base;
-  base -= mine;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (w < warp) base += misc.scan[w];
-
-  // ---- units ---------------------------------------------------------------
-  // T1 tiles for each of the first C, then T2 for each that is claimed. Where
-  // rows are not cut a unit takes the rows that start in it.
   const bool whole = a.cut == 0;
+  if (warp < kWarps) {
+    unsigned before = 0;
+    for (int w = 0; w < warp; ++w) before += misc.scan[w];
+    sBase[tid] += before;
+  }
+  // Units: T1 stages for each of the first C, then T2 for each that is claimed.
+  // Where rows are not cut a unit takes the rows that start in it.
   if (tid == 0) {
-    const unsigned C = gridDim.x, least = a.least_tiles;
+    const unsigned C = gridDim.x, least = (a.least_tiles + Wh - 1) / Wh;
     unsigned Wseq = 0;
     for (int w = 0; w < kWarps; ++w) Wseq += misc.scan[w];
     const unsigned W = Wseq * NG;
@@ -213,344 +245,324 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     misc.nstat = (misc.W1 + T1 - 1) / T1;
     misc.T2 = T2;
     misc.nunits = misc.nstat + (W - misc.W1 + T2 - 1) / T2;
-    misc.more = 0;
-    // static units are dealt out by CTA; a claim c stands for unit nstat + c
-    misc.next = blockIdx.x < misc.nstat ? blockIdx.x
-                : whole                 ? misc.nunits
-                                        : misc.nstat + static_cast<unsigned>(atomicAdd(a.ws_claim, 1ull));
   }
-  unsigned claimed = 0;  // of thread 0: the unit after misc.next, claimed ahead of time
-  if (!whole && tid == 0) claimed = static_cast<unsigned>(atomicAdd(a.ws_claim, 1ull));
   __syncthreads();
-  auto unit_of = [&](unsigned pos) {
-    return pos < misc.W1 ? pos / misc.T1 : misc.nstat + (pos - misc.W1) / misc.T2;
-  };
 
-  State<D, NT> st;
-  Query<D, NT> q;
-  bool gave_up = false;
+  if (warp == kWarps) {
+    // ======================= the feeding warp ==================================
+    auto unit_of = [&](unsigned pos) {
+      return pos < misc.W1 ? pos / misc.T1 : misc.nstat + (pos - misc.W1) / misc.T2;
+    };
+    auto claim = [&]() -> unsigned {  // of lane 0
+      return lane == 0 ? static_cast<unsigned>(atomicAdd(a.ws_claim, 1ull)) : 0u;
+    };
+    const int bt = ROWS ? 1 : lb;  // tokens a lane's table entry stands for
+    constexpr uint32_t kNone = 0xffffffffu, kBad = 0xfffffffeu;
+    constexpr int kPer = ROWS ? 4 : 1;  // entries of a lane: tokens lane, lane + 32, .. (at most 128)
+    uint32_t filled = 0;  // stages
+    bool ok = true;
 
-  auto load_q = [&](const Seg& g) {
-    const T* qh = static_cast<const T*>(a.query) +
-                  (static_cast<size_t>(g.s) * a.num_q_heads + static_cast<size_t>(g.hg * Hc + hsub) * G) * D;
-    load_query<Ty, D, NT, FP8, SPLIT>(qh, G, a.scale_log2, q);
-  };
-  // the warps of this warp's head meet
-  auto meet = [&]() {
-    if (Wh == 1)
-      __syncwarp();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + hsub), "r"(Wh * 32) : "memory");
-  };
-  // this warp's first tile of a segment, and how many it takes
-  auto first_of = [&](const Seg& g) { return (wsub - g.turn) & (Wh - 1); };
-  auto count_of = [&](const Seg& g) { return max(g.ntiles - first_of(g) + Wh - 1, 0) / Wh; };
-
-  // static units are dealt out by CTA; a claim c stands for unit nstat + c
-  // ---- records of the next segments (all threads) ----------------------------
-  auto make_batch = [&](int buf) {
-    bool more = misc.more != 0;
-    const unsigned unit = more ? misc.unit : misc.next;
-    const bool stat = unit < misc.nstat;
-    const unsigned u0 = stat ? unit * misc.T1 : misc.W1 + (unit - misc.nstat) * misc.T2;
-    const unsigned u1 = stat ? min(u0 + misc.T1, misc.W1) : min(u0 + misc.T2, misc.W);
-    const bool any = more || unit < misc.nunits;
-    if (!more && any) {  // a new unit: the row it begins in
-      const int hg = static_cast<int>(u0 / misc.Wseq);
-      const unsigned off = u0 - hg * misc.Wseq;
-      if (mine > 0 && base <= off && off < base + mine) {
-        unsigned p = base;
-        int s = s_lo;
-        for (; s < s_hi - 1; ++s) {
-          const unsigned n = row_of(s).n;
-          if (off < p + n) break;
-          p += n;
-        }
-        misc.hg = hg;
-        misc.s = s;
-        misc.row_pos = hg * misc.Wseq + p;
-      }
-    }
-    __syncthreads();
-    if (warp == 0 && any) {
-      const unsigned at = static_cast<unsigned>(misc.s) + lane;
-      const int hg = misc.hg + static_cast<int>(at / S), s = static_cast<int>(at % S);
-      Row r{0, 0, 0, 0};
-      if (hg < NG && lane < kBatch) r = row_of(s);
-      unsigned end = r.n;
+    // what a lane knows of a stage: the slots of its blocks (ROWS: tokens); kNone:
+    // nothing to copy (outside the row), kBad: a rejected block
+    struct Ids {
+      uint32_t v[kPer];
+    };
+    auto load_ids = [&](const int32_t* row, int t0, int lo, int hi) {
+      Ids ids;
 #pragma unroll
-      for (int off = 1; off < kBatch; off <<= 1) {
-        const unsigned v = __shfl_up_sync(kFull, end, off);
-        if (lane >= off) end += v;
-      }
-      end += misc.row_pos;
-      const unsigned p = end - r.n;
-      // a row without cuts belongs to the unit that it starts in
-      const unsigned from = whole ? p : max(p, u0), to = whole ? end : min(end, u1);
-      const bool in = hg < NG && lane < kBatch && p < u1 && (!whole || p >= u0);
-      Seg g;
-      g.s = s;
-      g.hg = hg;
-      g.tile0 = r.lo / kTT + static_cast<int>(from - p);
-      g.ntiles = r.hi > r.lo ? static_cast<int>(to - from) : 0;
-      g.lo = r.lo;
-      g.hi = r.hi;
-      g.slot = -1;
-      if (in) {
-        const unsigned first = whole ? unit : unit_of(p), last = whole ? unit : unit_of(end - 1);
-        const bool pieces = last > first || r.before > 0;
-        if (pieces) g.slot = hg * S + s + static_cast<int>(unit);
-        // the merge kernel finds the row's pieces here (none: the row is finished)
-        if (unit == first && a.ws_rows != nullptr) {
-          for (int i = 0; i < Hc; ++i)
-            a.ws_rows[static_cast<size_t>(s) * Hkv + hg * Hc + i] =
-                make_int2(g.slot, pieces ? static_cast<int>(last - first) + 1 : 0);
-        }
-      }
-      const unsigned mask = __ballot_sync(kFull, in);
-      const int lead = whole && mask != 0 ? __ffs(mask) - 1 : 0;  // an earlier unit's row may come first
-      int turn = in ? g.ntiles & (kWarps - 1) : 0;
-#pragma unroll
-      for (int off = 1; off < kBatch; off <<= 1) {
-        const int v = __shfl_up_sync(kFull, turn, off);
-        if (lane >= off) turn += v;
-      }
-      g.turn = (turn - (in ? g.ntiles : 0)) & (Wh - 1);
-      if (in) sSeg[buf * kBatch + lane - lead] = g;
-      __syncwarp();  // the cursor has been read by every lane
-      if (lane == kBatch - 1) {
-        misc.nseg[buf] = __popc(mask);
-        misc.more = hg < NG && end < u1;
-        misc.s = static_cast<int>((at + 1) % S);
-        misc.hg = hg + (at % S + 1 == static_cast<unsigned>(S) ? 1 : 0);
-        misc.row_pos = end;
-      }
-      if (tid == 0) {
-        misc.unit = unit;
-        if (!more) {
-          misc.next = whole ? misc.nunits : misc.nstat + claimed;
-          if (!whole && misc.next < misc.nunits) claimed = static_cast<unsigned>(atomicAdd(a.ws_claim, 1ull));
-        }
-      }
-    }
-    if (tid == 0 && !any) misc.nseg[buf] = 0;
-    __syncthreads();
-    // whole rows: an earlier unit's rows may fill a batch
-    return any && (misc.nseg[buf] > 0 || misc.more != 0);
-  };
-
-  // ---- this warp's stream ----------------------------------------------------
-  // Two iterators run ahead of the tile that is computed, over the records made
-  // so far: one over table entries, one over copies. (batch, segment) of each,
-  // and the tiles left there for this warp.
-  int made = -1;  // the last batch made
-  int id_b = 0, id_sg = -1, id_left = 0, id_t = 0, id_lo = 0, id_hi = 0;
-  const int32_t* id_row = nullptr;
-  auto id_next = [&]() {
-    while (id_left == 0) {
-      if (id_sg + 1 < misc.nseg[id_b & 1]) {
-        const Seg& g = sSeg[(id_b & 1) * kBatch + ++id_sg];
-        id_left = count_of(g);
-        id_t = (g.tile0 + first_of(g)) * kTT;
-        id_lo = g.lo;
-        id_hi = g.hi;
-        id_row = a.block_tables + static_cast<size_t>(g.s) * a.max_blocks_per_seq;
-      } else if (id_b < made) {
-        ++id_b;
-        id_sg = -1;
-      } else {
-        return;
-      }
-    }
-  };
-  int is_b = 0, is_sg = -1, is_left = 0, is_h = 0;
-  auto is_next = [&]() {
-    while (is_left == 0) {
-      if (is_sg + 1 < misc.nseg[is_b & 1]) {
-        const Seg& g = sSeg[(is_b & 1) * kBatch + ++is_sg];
-        is_left = count_of(g);
-        is_h = g.hg * Hc + hsub;
-      } else if (is_b < made) {
-        ++is_b;
-        is_sg = -1;
-      } else {
-        return;
-      }
-    }
-  };
-  // What a lane knows of a tile ahead of its copy. Whole blocks: lane i has the
-  // slot at which the i-th block of the tile starts. ROWS: lane i has the slot of
-  // token i. kNone: nothing to copy (outside the row); kBad: a rejected block.
-  const int bt = ROWS ? 1 : min(1 << shift, kTT);  // tokens a lane's entry stands for
-  constexpr uint32_t kNone = 0xffffffffu, kBad = 0xfffffffeu;
-  uint32_t idq[kIdDepth];
-  int idn = 0;  // entries in the queue
-  auto fill_ids = [&]() {
-    while (idn < kIdDepth && id_left > 0) {
-      uint32_t got = kNone;
-      const int t = id_t + lane * bt;
-      if (lane * bt < kTT && t < id_hi && t + bt > id_lo) {
-        const int id = __ldg(id_row + (t >> shift));
-        const int at = t & ((1 << shift) - 1);
-        got = (static_cast<uint32_t>(id) << shift) + static_cast<uint32_t>(at);
-        if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) {
-          if (!ROWS || at == 0 || t == id_lo || lane == 0) atomicAdd(a.bad, 1ull);
-          got = kBad;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kIdDepth; ++k)
-        if (k == idn) idq[k] = got;
-      ++idn;
-      id_t += Wh * kTT;
-      --id_left;
-      id_next();
-    }
-  };
-  uint32_t issued = 0, consumed = 0;
-  // ROWS: exponents of the tile issued last, on their way to shared memory
-  [[maybe_unused]] uint32_t last_ek = 0, last_ev = 0;
-  [[maybe_unused]] bool pending = false;
-  auto store_scales = [&]() {
-    if (FP8 && ROWS && pending) {
-      unsigned char* se = wscales + (issued - 1) % kStages * R::kScaleBytes;
-      se[2 * lane] = static_cast<unsigned char>(last_ek);
-      se[2 * lane + 1] = static_cast<unsigned char>(last_ev);
-      pending = false;
-    }
-  };
-  auto issue = [&]() {
-    const int h = is_h;
-    const int stage = static_cast<int>(issued % kStages);
-    const uint32_t sk = ring + stage * R::kStageBytes, sv = sk + Geo::kBytes;
-    const uint32_t bar = bars + 8 * stage;
-    const uint32_t mine_id = idq[0];
-    const size_t block = mine_id >> shift;
-    const uint8_t* e = FP8 ? a.scales + ((block * Hkv + h) * 2 << shift) + (mine_id & ((1u << shift) - 1)) : nullptr;
-    if constexpr (ROWS) {
-      constexpr int kRowsPerCopy = 32 / Geo::kChunks;
-      const int cc = lane % Geo::kChunks, cr = lane / Geo::kChunks;
-      const size_t stride = static_cast<size_t>(Hkv) * Geo::kRowBytes;
-      const size_t hoff = static_cast<size_t>(h) * Geo::kRowBytes + cc * 16;
-      const char* kb = static_cast<const char*>(a.key_cache) + hoff;
-      const char* vb = static_cast<const char*>(a.value_cache) + hoff;
-#pragma unroll
-      for (int i = 0; i < kTT / kRowsPerCopy; ++i) {
-        const int r = cr + i * kRowsPerCopy;
-        const uint32_t slot = __shfl_sync(kFull, mine_id, r);
-        const bool ok = slot < kBad;
-        const size_t o = (ok ? slot : 0u) * stride;
-        cp_async_16(sk + Geo::off(r, cc), kb + o, ok);
-        cp_async_16(sv + Geo::off(r, cc), vb + o, ok);
-      }
-      tc::cp_async_mbar_arrive_noinc(bar);
-      if constexpr (FP8) {
-        store_scales();  // of the tile before
-        last_ek = mine_id < kBad ? __ldg(e) : 0u;
-        last_ev = mine_id < kBad ? __ldg(e + (1 << shift)) : 0u;
-        pending = true;
-      }
-    } else {
-      const int nb = kTT / bt;  // blocks of the tile: lanes 0 .. nb - 1
-      const unsigned bad = __ballot_sync(kFull, mine_id == kBad);
-      const unsigned live = __ballot_sync(kFull, mine_id < kBad);
-      unsigned char* se = wscales + stage * R::kScaleBytes;
-      if (bad != 0) {  // rejected blocks read as zeros
-        for (int i = 0; i < nb; ++i) {
-          if (!((bad >> i) & 1u)) continue;
-          for (int c = lane; c < bt * Geo::kChunks; c += 32) {
-            const uint32_t o = Geo::off(i * bt + c / Geo::kChunks, c % Geo::kChunks);
-            st_shared_zero16(sk + o);
-            st_shared_zero16(sv + o);
-          }
-          if constexpr (FP8) {
-            for (int c = lane; c < 2 * bt; c += 32) se[i * 2 * bt + c] = 0;
+      for (int k = 0; k < kPer; ++k) {
+        const int x = (lane + 32 * k) * bt, t = t0 + x;
+        ids.v[k] = kNone;
+        if (x < ST && t < hi && t + bt > lo) {
+          const int id = __ldg(row + (t >> shift));
+          const int at = t & ((1 << shift) - 1);
+          ids.v[k] = (static_cast<uint32_t>(id) << shift) + static_cast<uint32_t>(at);
+          if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) {
+            if (!ROWS || at == 0 || t == lo || lane == 0) atomicAdd(a.bad, 1ull);
+            ids.v[k] = kBad;
           }
         }
-        tc::fence_async_smem();
-        __syncwarp();
       }
-      if (lane == 0)
-        tc::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(live)) * bt *
-                                           (2 * Geo::kRowBytes + (FP8 ? 2 : 0)));
-      __syncwarp();
-      if (mine_id < kBad) {
-        const uint32_t dst = static_cast<uint32_t>(lane * bt * Geo::kRowBytes);
-        const int grp = static_cast<int>(mine_id >> 3);
-        tc::tma_load_5d(sk + dst, &kmap, bar, 0, 0, 0, grp, h);
-        tc::tma_load_5d(sv + dst, &vmap, bar, 0, 0, 0, grp, h);
+      return ids;
+    };
+    // the next stage, free to be filled
+    auto next_stage = [&]() {
+      const uint32_t st = filled % kStages;
+      if (filled >= kStages && ok) ok = *aborted == 0 && wait(empty(st), (filled / kStages - 1) & 1);
+      return st;
+    };
+    auto fill = [&](const Note& note, const Ids& ids) {
+      const uint32_t st = next_stage();
+      if (!ok) return;
+      const uint32_t sk = ring + st * 2 * R::kHalf, sv = sk + R::kHalf;
+      unsigned char* se = smem + R::kScales + st * R::kScaleBytes;
+      const int h0 = note.hg * Hc;
+      if (lane == 0) notes[st] = note;
+      if constexpr (ROWS) {
+        // the CTA's heads of a token are neighbours: Hc rows are one run
+        const int run = Hc * Geo::kChunks;  // 16-byte chunks
+        const size_t stride = static_cast<size_t>(Hkv) * kRB;
+        const char* kb = static_cast<const char*>(a.key_cache) + static_cast<size_t>(h0) * kRB;
+        const char* vb = static_cast<const char*>(a.value_cache) + static_cast<size_t>(h0) * kRB;
         if constexpr (FP8) {
-          const uint32_t to = smem_u32(se) + lane * 2 * bt;
-          if (bt == 1 << shift) {
-            tc::bulk_load(to, e, 2 * bt, bar);
-          } else {  // half of a block of 64
-            tc::bulk_load(to, e, bt, bar);
-            tc::bulk_load(to + bt, e + (1 << shift), bt, bar);
+          // exponents: (token, head) pairs, all loads before the stores
+          uint8_t ek[4], ev[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // ST * Hc = 128 pairs
+            const int x = (lane + 32 * k) % ST, hh = (lane + 32 * k) / ST;
+            const uint32_t id = row_id(ids.v, x);
+            ek[k] = ev[k] = 0;
+            if (id < kBad) {
+              const uint8_t* e = a.scales + ((static_cast<size_t>(id >> shift) * Hkv + h0 + hh) * 2 << shift) +
+                                 (id & ((1u << shift) - 1));
+              ek[k] = __ldg(e);
+              ev[k] = __ldg(e + (1 << shift));
+            }
+          }
+          for (int i = lane; i < ST * run; i += 32) {
+            const int x = i / run, c = i % run, hh = c / Geo::kChunks, cc = c % Geo::kChunks;
+            const uint32_t o = hh * ST * kRB + Geo::off(x, cc);
+            const uint32_t v = row_id(ids.v, x);
+            const bool live = v < kBad;
+            const size_t from = (live ? v : 0u) * stride + c * 16;
+            cp_async_16(sk + o, kb + from, live);
+            cp_async_16(sv + o, vb + from, live);
+          }
+          tc::cp_async_mbar_arrive_noinc(full(st));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int x = (lane + 32 * k) % ST, hh = (lane + 32 * k) / ST;
+            se[hh * 2 * ST + x] = ek[k];
+            se[hh * 2 * ST + ST + x] = ev[k];
+          }
+        } else {
+          for (int i = lane; i < ST * run; i += 32) {
+            const int x = i / run, c = i % run, hh = c / Geo::kChunks, cc = c % Geo::kChunks;
+            const uint32_t o = hh * ST * kRB + Geo::off(x, cc);
+            const uint32_t v = row_id(ids.v, x);
+            const bool live = v < kBad;
+            const size_t from = (live ? v : 0u) * stride + c * 16;
+            cp_async_16(sk + o, kb + from, live);
+            cp_async_16(sv + o, vb + from, live);
+          }
+          tc::cp_async_mbar_arrive_noinc(full(st));
+        }
+        __syncwarp();
+        tc::mbar_arrive(full(st));  // releases this lane's plain stores
+      } else {
+        const uint32_t id = ids.v[0];
+        const unsigned bad = __ballot_sync(kFull, id == kBad);
+        const unsigned live = __ballot_sync(kFull, id < kBad);
+        const int block_bytes = Hc * bt * kRB;
+        if (bad != 0) {  // rejected blocks read as zeros
+          for (int i = 0; i < ST / bt; ++i) {
+            if (!((bad >> i) & 1u)) continue;
+            for (int c = lane * 16; c < block_bytes; c += 512) {
+              st_shared_zero16(sk + i * block_bytes + c);
+              st_shared_zero16(sv + i * block_bytes + c);
+            }
+            if constexpr (FP8) {
+              for (int c = lane; c < Hc * 2 * bt; c += 32) se[i * Hc * 2 * bt + c] = 0;
+            }
+          }
+          tc::fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0)
+          tc::mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(__popc(live)) *
+                                                  (2 * block_bytes + (FP8 ? Hc * 2 * bt : 0)));
+        __syncwarp();
+        if (id < kBad) {
+          const int grp = static_cast<int>(id >> 3);
+          tc::tma_load_5d(sk + lane * block_bytes, &kmap, full(st), 0, 0, 0, grp, h0);
+          tc::tma_load_5d(sv + lane * block_bytes, &vmap, full(st), 0, 0, 0, grp, h0);
+          if constexpr (FP8) {
+            const uint8_t* e = a.scales + ((static_cast<size_t>(id >> shift) * Hkv + h0) * 2 << shift) +
+                               (id & ((1u << shift) - 1));
+            const uint32_t to = smem_u32(se) + lane * Hc * 2 * bt;
+            if (bt == 1 << shift) {
+              tc::bulk_load(to, e, Hc * 2 * bt, full(st));
+            } else {  // part of a block: K's and V's of each head
+              for (int i = 0; i < 2 * Hc; ++i) tc::bulk_load(to + i * bt, e + (i << shift), bt, full(st));
+            }
           }
         }
       }
-    }
-    ++issued;
-    --is_left;
-    is_next();
-#pragma unroll
-    for (int k = 0; k + 1 < kIdDepth; ++k) idq[k] = idq[k + 1];
-    --idn;
-    fill_ids();
-  };
+      ++filled;
+    };
 
-  // ---- batches -----------------------------------------------------------------
-  auto look = [&]() {  // takes up the records of a new batch
-    ++made;
-    id_next();
-    is_next();
-    fill_ids();
-  };
-  bool going = make_batch(0);
-  if (going) {
-    look();
-    while (issued < kStages && is_left > 0) issue();
-  }
-  for (int b = 0; going; ++b) {
-    going = make_batch((b + 1) & 1);
-    look();
-    const int nseg = misc.nseg[b & 1];
-    if (nseg > 0) load_q(sSeg[(b & 1) * kBatch]);
-    st.reset();
-    for (int sg = 0; sg < nseg; ++sg) {
-      const Seg g = sSeg[(b & 1) * kBatch + sg];
-      int t0 = (g.tile0 + first_of(g)) * kTT;
-      for (int left = count_of(g); left > 0; --left, t0 += Wh * kTT) {
-        __syncwarp();  // every lane is done with the stage that is refilled
-        while (issued - consumed < kStages && is_left > 0) issue();
-        const int stage = static_cast<int>(consumed % kStages);
-        if (issued - consumed == 1) store_scales();
-        if (!gave_up) {
-          // bounded; once a wait has given up (counted), the launch winds down
-          // without further ones
-          gave_up = !__all_sync(kFull, tc::mbar_wait(bars + 8 * stage, (consumed / kStages) & 1));
-          if (gave_up && lane == 0) atomicAdd(a.timeouts, 1ull);
+    unsigned unit = blockIdx.x;
+    if (unit >= misc.nstat)
+      unit = whole ? misc.nunits : misc.nstat + __shfl_sync(kFull, claim(), 0);
+    while (unit < misc.nunits && ok) {
+      const unsigned next = whole ? 0u : claim();  // of lane 0: the claim after this unit, ahead of time
+      const bool stat = unit < misc.nstat;
+      const unsigned u0 = stat ? unit * misc.T1 : misc.W1 + (unit - misc.nstat) * misc.T2;
+      const unsigned u1 = stat ? min(u0 + misc.T1, misc.W1) : min(u0 + misc.T2, misc.W);
+      // the row that holds position u0: its run of sequences, then the sequence
+      int hg = static_cast<int>(u0 / misc.Wseq), s;
+      unsigned p;
+      {
+        const unsigned off = u0 - hg * misc.Wseq;
+        int before = 0;
+#pragma unroll
+        for (int k = 0; k < kChunks / 32; ++k) before += sBase[lane + 32 * k] <= off ? 1 : 0;
+        const int c = __reduce_add_sync(kFull, before) - 1;
+        s = c * per;
+        p = sBase[c];
+        for (;;) {
+          const unsigned n = s + lane < min(S, (c + 1) * per) ? row_of(s + lane).n : 0u;
+          unsigned incl = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += v;
+          }
+          const unsigned hit = __ballot_sync(kFull, n > 0 && p + incl > off);
+          if (hit != 0) {
+            const int l = __ffs(hit) - 1;
+            p += __shfl_sync(kFull, incl - n, l);
+            s += l;
+            break;
+          }
+          p += __shfl_sync(kFull, incl, 31);
+          s += 32;
+          if (s >= S) break;  // not reached
         }
-        ++consumed;
+        p += hg * misc.Wseq;
+      }
+      // rows from there on, 32 at a time
+      bool more = true;
+      while (more && ok) {
+        const unsigned at = static_cast<unsigned>(s) + lane;
+        const int my_hg = hg + static_cast<int>(at / S), my_s = static_cast<int>(at % S);
+        Row r{0, 0, 0, 0};
+        if (my_hg < NG) r = row_of(my_s);
+        unsigned end = r.n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned v = __shfl_up_sync(kFull, end, o);
+          if (lane >= o) end += v;
+        }
+        end += p;
+        const unsigned start = end - r.n;
+        // a row without cuts belongs to the unit that it starts in
+        const unsigned from = whole ? start : max(start, u0), to = whole ? end : min(end, u1);
+        const bool in = my_hg < NG && start < u1 && (!whole || start >= u0);
+        int slot = -1;
+        if (in) {
+          const unsigned first = whole ? unit : unit_of(start), last = whole ? unit : unit_of(end - 1);
+          const bool pieces = last > first || r.before > 0;
+          if (pieces) slot = my_hg * S + my_s + static_cast<int>(unit);
+          // the merge kernel finds the row's pieces here (none: the row is finished)
+          if (unit == first && a.ws_rows != nullptr) {
+            for (int i = 0; i < Hc; ++i)
+              a.ws_rows[static_cast<size_t>(my_s) * Hkv + my_hg * Hc + i] =
+                  make_int2(slot, pieces ? static_cast<int>(last - first) + 1 : 0);
+          }
+        }
+        const int stage0 = r.lo / ST + static_cast<int>(from - start);
+        const int stages = in ? static_cast<int>(to - from) : 0;
+        for (unsigned left = __ballot_sync(kFull, in); left != 0 && ok; left &= left - 1) {
+          const int l = __ffs(left) - 1;
+          Note note;
+          note.s = __shfl_sync(kFull, my_s, l);
+          note.hg = __shfl_sync(kFull, my_hg, l);
+          note.lo = __shfl_sync(kFull, r.lo, l);
+          note.hi = __shfl_sync(kFull, r.hi, l);
+          note.slot = __shfl_sync(kFull, slot, l);
+          note.t0 = __shfl_sync(kFull, stage0, l) * ST;
+          note.pad = 0;
+          const int n = __shfl_sync(kFull, stages, l);
+          const int32_t* row = a.block_tables + static_cast<size_t>(note.s) * a.max_blocks_per_seq;
+          Ids ids = load_ids(row, note.t0, note.lo, note.hi);
+          for (int i = 0; i < n && ok; ++i) {
+            note.flags = (i == 0 ? kFirst : 0) | (i == n - 1 ? kLast : 0);
+            fill(note, ids);
+            note.t0 += ST;
+            if (i + 1 < n) ids = load_ids(row, note.t0, note.lo, note.hi);  // a stage ahead
+          }
+        }
+        more = __shfl_sync(kFull, my_hg < NG && end < u1, 31);
+        p = __shfl_sync(kFull, end, 31);
+        hg += (s + 32) / S;
+        s = (s + 32) % S;
+      }
+      unit = whole ? misc.nunits : misc.nstat + __shfl_sync(kFull, next, 0);
+    }
+    if (ok) {  // the end of all work
+      const uint32_t st = next_stage();
+      if (ok) {
+        if (lane == 0) notes[st].flags = kEnd;
         __syncwarp();
-        const uint32_t sk = ring + stage * R::kStageBytes, sv = sk + Geo::kBytes;
-        const int lo = FP8 ? 0 : g.lo - t0, hi = g.hi - t0;
+        if (ROWS || lane == 0) tc::mbar_arrive(full(st));
+        if (ROWS) tc::mbar_arrive(full(st));
+      }
+    } else {  // what was issued must land before the CTA ends
+      for (uint32_t i = filled - min(filled, static_cast<uint32_t>(kStages)); i != filled; ++i)
+        tc::mbar_wait(full(i % kStages), (i / kStages) & 1);
+    }
+  } else {
+    // ======================= the computing warps ================================
+    const int hsub = warp / Wh, wsub = warp % Wh;  // this warp's head, and its tile of a stage
+    // where this lane's rows for ldmatrix lie in the K and V halves of a stage
+    auto row_at = [&](int x) {
+      return static_cast<uint32_t>((x / lb * Hc + hsub) * lb * kRB + (x % lb >> 3) * 8 * kRB);
+    };
+    const int x0 = wsub * kTT, mi = lane >> 3;
+    const uint32_t k_at = row_at(x0 + ((mi & 1) << 3));
+    const uint32_t k_next = FP8 ? row_at(x0 + 16 + ((mi & 1) << 3)) - k_at : 0u;  // the next 16 tokens
+    const uint32_t v_at = row_at(FP8 ? x0 + (lane & 24) : x0 + ((mi >> 1) << 3));
+    const int e_at = ((x0 + lane) / lb * Hc + hsub) * 2 * lb + (x0 + lane) % lb;
+    float* sStats = reinterpret_cast<float*>(smem + R::kStats);
+    float* sJoin = reinterpret_cast<float*>(smem + R::kJoin);
+    State<D, NT> st;
+    Query<D, NT> q;
+    uint32_t joins = 0;
+    // the warps of this warp's head meet
+    auto meet = [&]() {
+      __syncwarp();
+      if (Wh == 1) return true;
+      if (lane == 0) tc::mbar_arrive(join_bar(hsub));
+      return wait(join_bar(hsub), joins++ & 1);
+    };
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t stage = n % kStages;
+      ok = *aborted == 0 && wait(full(stage), (n / kStages) & 1);
+      if (!ok) break;
+      const Note note = notes[stage];
+      if (note.flags & kEnd) break;
+      if (note.flags & kFirst) {
+        const T* qh = static_cast<const T*>(a.query) +
+                      (static_cast<size_t>(note.s) * a.num_q_heads + static_cast<size_t>(note.hg * Hc + hsub) * G) * D;
+        load_query<Ty, D, NT, FP8, SPLIT>(qh, G, a.scale_log2, q);
+        st.reset();
+      }
+      const int t0 = note.t0 + x0;
+      const int lo = FP8 ? 0 : note.lo - t0, hi = note.hi - t0;
+      if (hi > max(lo, 0) && lo < kTT) {
+        const uint32_t sk = ring + stage * 2 * R::kHalf, sv = sk + R::kHalf;
         if (!ROWS && (lo > 0 || hi < kTT)) {
           // rows that do not count may hold anything: V's must not be NaN
           for (int c = lane; c < kTT * Geo::kChunks; c += 32) {
             const int row = c / Geo::kChunks;
-            if (row < lo || row >= hi) st_shared_zero16(sv + Geo::off(row, c % Geo::kChunks));
+            if (row < lo || row >= hi)
+              st_shared_zero16(sv + row_at(x0 + row) + Geo::in_group(row & 7, c % Geo::kChunks));
           }
           tc::fence_async_smem();
           __syncwarp();
         }
         if constexpr (FP8) {
-          const unsigned char* e = wscales + stage * R::kScaleBytes + lane / bt * 2 * bt + lane % bt;
-          tile_8<D, NT, SPLIT>(sk, sv, e[0], e[bt], lo, hi, q, st);
+          const unsigned char* e = smem + R::kScales + stage * R::kScaleBytes + e_at;
+          tile_8<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, e[0], e[lb], lo, hi, q, st);
         } else {
-          tile_16<Ty, D, NT, SPLIT>(sk, sv, lo, hi, q, st);
+          tile_16<Ty, D, NT, SPLIT>(sk + k_at, sv + v_at, lo, hi, q, st);
         }
       }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(empty(stage));
+      if (!(note.flags & kLast)) continue;
 
       // ---- segment end: join the states of the head's warps ---------------
 #pragma unroll
@@ -567,10 +579,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           for (int e = 0; e < 4; ++e) st.o[mt][0][e] += __shfl_xor_sync(kFull, st.o[mt][0][e], 2);
       }
       const int r8 = lane >> 2, tq = 2 * (lane & 3);
-      const size_t row0 = static_cast<size_t>(g.s) * a.num_q_heads +
-                          static_cast<size_t>(g.hg * Hc + hsub) * G;
-      for (int h0 = 0; h0 < G; h0 += kJoinHeads) {
-        meet();  // the area was read by the join before
+      const size_t row0 = static_cast<size_t>(note.s) * a.num_q_heads +
+                          static_cast<size_t>(note.hg * Hc + hsub) * G;
+      for (int h0 = 0; h0 < G && ok; h0 += kJoinHeads) {
+        ok = meet();  // the area was read by the join before
+        if (!ok) break;
         float* mine_o = sJoin + warp * kJoinHeads * R::kOStride;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -596,7 +609,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               stat_w[2 * R::kHeads] = static_cast<float>(st.r);
             }
           }
-        meet();
+        ok = meet();
+        if (!ok) break;
         const int heads = min(G - h0, kJoinHeads), w0 = warp - wsub;
         for (int i = wsub * 32 + lane; i < heads * (D / 4); i += Wh * 32) {
           const int at = i / (D / 4), c4 = i % (D / 4) * 4, head = h0 + at;
@@ -625,8 +639,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if constexpr (FP8) iv *= ex2(top - (127 + kWeightShift));
           acc = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
           const size_t row = row0 + head;
-          if (g.slot >= 0) {
-            const size_t piece = (static_cast<size_t>(g.slot) * Hc + hsub) * G + head;
+          if (note.slot >= 0) {
+            const size_t piece = (static_cast<size_t>(note.slot) * Hc + hsub) * G + head;
             *reinterpret_cast<float4*>(a.seg_out + piece * D + c4) = acc;
             if (c4 == 0) a.seg_lse[piece] = l == 0.f ? -INFINITY : M + __log2f(l);
           } else if (a.out_f32) {
@@ -637,19 +651,13 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
         }
       }
-      st.reset();
-      if (sg + 1 < nseg) load_q(sSeg[(b & 1) * kBatch + sg + 1]);
     }
-    __syncthreads();  // the batch's records are overwritten next
   }
-  if (gave_up) {  // what was issued must land before the CTA ends
-    for (uint32_t i = issued - min(issued, static_cast<uint32_t>(kStages)); i != issued; ++i)
-      tc::mbar_wait(bars + 8 * (i % kStages), (i / kStages) & 1);
-  }
+  __syncthreads();  // every copy has landed, every claim has been made
   // no CTA ends before the prefix pass does: the merge kernel behind this one
   // then waits for both
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!whole && tid == 0) {
+  if (!whole && tid == kWarps * 32) {  // the lane that claims
     // the last CTA to finish (every claim made) leaves the counters at zero
     __threadfence();
     if (atomicAdd(a.ws_done, 1u) == static_cast<unsigned>(gridDim.x - 1)) {
@@ -776,10 +784,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const St
 // Launch
 // ---------------------------------------------------------------------------
 // One pool [num_slots, Hkv, row bytes] viewed, innermost first, as (bytes of a
-// slice, 8 slots, slices, slot groups, kv head); a box is `rows` slots of one kv
-// head, in the tile order of Tile::off.
+// slice, 8 slots, slices, slot groups, kv head); a box is `rows` slots of
+// `heads` kv heads, head by head, each in the order of Tile::off.
 inline bool encode_pool_map(CUtensorMap* map, const void* cache, long long num_slots, int hkv,
-                            int row_bytes, int rows) {
+                            int row_bytes, int rows, int heads) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (enc == nullptr) return false;
   const cuuint64_t slice = row_bytes < 128 ? row_bytes : 128;
@@ -789,7 +797,7 @@ inline bool encode_pool_map(CUtensorMap* map, const void* cache, long long num_s
                               static_cast<cuuint64_t>(hkv)};
   const cuuint64_t strides[4] = {slot, 128, 8 * slot, static_cast<cuuint64_t>(row_bytes)};
   const cuuint32_t box[5] = {static_cast<cuuint32_t>(slice), 8, static_cast<cuuint32_t>(slices),
-                             static_cast<cuuint32_t>(rows / 8), 1};
+                             static_cast<cuuint32_t>(rows / 8), static_cast<cuuint32_t>(heads)};
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(cache), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -822,9 +830,10 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   CUtensorMap km{}, vm{};
   if constexpr (!ROWS) {
     const long long slots = static_cast<long long>(a.num_blocks) << a.block_shift;
-    const int rows = std::min(1 << a.block_shift, Tile<D, FP8>::kTokens);
-    if (!encode_pool_map(&km, a.key_cache, slots, a.num_kv_heads, Tile<D, FP8>::kRowBytes, rows) ||
-        !encode_pool_map(&vm, a.value_cache, slots, a.num_kv_heads, Tile<D, FP8>::kRowBytes, rows))
+    const int rows = std::min(1 << a.block_shift, Tile<D, FP8>::kTokens * kWarps / a.heads_at_a_time);
+    const int row_bytes = Tile<D, FP8>::kRowBytes;
+    if (!encode_pool_map(&km, a.key_cache, slots, a.num_kv_heads, row_bytes, rows, a.heads_at_a_time) ||
+        !encode_pool_map(&vm, a.value_cache, slots, a.num_kv_heads, row_bytes, rows, a.heads_at_a_time))
       return cudaErrorInvalidValue;
   }
   const long long ctas = std::min((NT == 1 ? 3 : 2) * num_sms, kMaxCtas);

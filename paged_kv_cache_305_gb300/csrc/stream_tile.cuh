@@ -120,23 +120,25 @@ struct State {
   }
 };
 
-// Tile geometry. off(row, chunk): byte offset of a row's 16-byte chunk, in the
-// order in which a tensor copy with the 128-byte swizzle (64-byte for rows of
-// 64 bytes) leaves it: 8 rows of one 128-byte slice after the other, chunks
-// XORed by the row. The 8 rows of every ldmatrix phase fall in distinct banks.
+// Tile geometry. A tensor copy with the 128-byte swizzle (64-byte for rows of 64
+// bytes) leaves rows in groups of 8: of a group, one 128-byte slice of all 8 rows
+// after the other, the 16-byte chunks of a slice XORed by the row. The 8 rows of
+// every ldmatrix phase then fall in distinct banks.
 template <int D, bool FP8>
 struct Tile {
   static constexpr int kTokens = FP8 ? 32 : 16;
   static constexpr int kRowBytes = FP8 ? D : 2 * D;
   static constexpr int kSlice = kRowBytes < 128 ? kRowBytes : 128;
-  static constexpr int kSlices = kRowBytes / kSlice;
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kBytes = kTokens * kRowBytes;
-  static __device__ __forceinline__ uint32_t off(int row, int chunk) {
+  // Byte offset of a row's 16-byte chunk in its group.
+  static __device__ __forceinline__ uint32_t in_group(int row, int chunk) {
     if constexpr (kSlice == 64)
       return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
-    return static_cast<uint32_t>((row >> 3) * (8 * kRowBytes) + (chunk >> 3) * 1024 + (row & 7) * 128 +
-                                 (((chunk & 7) ^ (row & 7)) << 4));
+    return static_cast<uint32_t>((chunk >> 3) * 1024 + row * 128 + (((chunk & 7) ^ row) << 4));
+  }
+  static __device__ __forceinline__ uint32_t off(int row, int chunk) {
+    return static_cast<uint32_t>((row >> 3) * (8 * kRowBytes)) + in_group(row & 7, chunk);
   }
   // Head dim of fragment element e of m-tile mt, for fragment row r8 = lane / 4.
   static __device__ __forceinline__ int dim_of(int mt, int e, int r8) {
@@ -215,11 +217,12 @@ __device__ __forceinline__ void weight_parts(float w0, float w1, uint32_t rest, 
   lo = SPLIT ? 0u : movmatrix_trans(part);
 }
 
-// 8-bit tile. sk, sv: K and V codes in shared memory; ek, ev: the exponent
-// bytes of token `lane`; tokens lo .. hi - 1 count (the others' V rows are zero).
+// 8-bit tile. sk: the group of K rows that this lane's addresses for ldmatrix lie
+// in (tokens 0-7 or 8-15 of the tile: lane & 8), sk + k_next that of the next 16
+// tokens; sv: the group of V rows of token `lane`; ek, ev: its exponent bytes; tokens lo .. hi - 1 count (the others' V rows are zero).
 template <int D, int NT, bool SPLIT>
-__device__ __forceinline__ void tile_8(uint32_t sk, uint32_t sv, int ek, int ev, int lo, int hi,
-                                       const Query<D, NT>& q, State<D, NT>& st) {
+__device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv, int ek, int ev,
+                                       int lo, int hi, const Query<D, NT>& q, State<D, NT>& st) {
   using Geo = Tile<D, true>;
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, r8 = lane >> 2;
@@ -252,7 +255,7 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t sv, int ek, int ev,
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t k[4];  // tokens 0-7, 8-15 of chunk 2 kp, then of the next
-      ldmatrix_x4(k, sk + Geo::off(hf * 16 + rr + ((mi & 1) << 3), 2 * kp + (mi >> 1)));
+      ldmatrix_x4(k, sk + hf * k_next + Geo::in_group(rr, 2 * kp + (mi >> 1)));
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const uint32_t a[4] = {e4m3x2_to_f16x2(k[2 * c]), e4m3x2_to_f16x2(k[2 * c + 1]),
@@ -303,7 +306,7 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t sv, int ek, int ev,
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) {
     uint32_t v[4];  // tokens 0-7, 8-15, 16-23, 24-31 of the m-tile's 16 dims
-    ldmatrix_x4_trans(v, sv + Geo::off(lane, mt));
+    ldmatrix_x4_trans(v, sv + Geo::in_group(rr, mt));
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const uint32_t p = __byte_perm(v[2 * hf], 0, 0x3120), s = __byte_perm(v[2 * hf + 1], 0, 0x3120);
@@ -318,7 +321,8 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t sv, int ek, int ev,
   }
 }
 
-// 16-bit tile.
+// 16-bit tile. sk, sv: the groups of rows that this lane's addresses for ldmatrix
+// lie in (K: lane & 8, V: lane & 16).
 template <typename Ty, int D, int NT, bool SPLIT>
 __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi,
                                         const Query<D, NT>& q, State<D, NT>& st) {
@@ -335,7 +339,7 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     uint32_t k[4];
-    ldmatrix_x4(k, sk + Geo::off(rr + ((mi & 1) << 3), 2 * kk + (mi >> 1)));
+    ldmatrix_x4(k, sk + Geo::in_group(rr, 2 * kk + (mi >> 1)));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) Ty::mma(sc[nt][kk & 1], k, q.b[kk][nt][0], q.b[kk][nt][1]);
   }
@@ -372,7 +376,7 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) {
     uint32_t v[4];
-    ldmatrix_x4_trans(v, sv + Geo::off(rr + ((mi >> 1) << 3), 2 * mt + (mi & 1)));
+    ldmatrix_x4_trans(v, sv + Geo::in_group(rr, 2 * mt + (mi & 1)));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       Ty::mma(st.o[mt][nt], v, ph[nt][0], ph[nt][1]);
