@@ -356,10 +356,11 @@ int pa_gather_cache_fp8(void* key_out, void* value_out,
  * of two for each head, so that its bits are kept), softmax weights, times V's
  * factors, as the sum of two fp16 parts.
  * Work is cut into equal shares, inside rows as it comes (shares are not under
- * partition_tokens tokens where that is given; 0 = the default); a second kernel
- * joins a row's pieces in order, and the result does not depend on which CTA
- * computed which. workspace: pa_decode_fp8_workspace_bytes(...) bytes, with the
- * zeroing and sharing rules of pa_decode_workspace_bytes. num_seqs *
+ * partition_tokens tokens where that is given; 0 = the default), and a second
+ * kernel joins a row's pieces in order; where they are cut depends on the lengths
+ * and the sizes alone. workspace: pa_decode_fp8_workspace_bytes(...) bytes; its
+ * contents need no initialisation, and calls that share it must not overlap on
+ * the GPU (pa_decode may use it in between). num_seqs *
  * num_kv_heads * max_blocks_per_seq * block_size / 32 must be below 2^31.
  * Other arguments, sizes and errors as for pa_decode.
  */
@@ -403,8 +404,8 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
  * the arrays is touched).
  * num_groups in [1, 65535] (unless num_seqs is 0), num_blocks * block_size
  * and num_seqs * num_kv_heads * max_blocks_per_seq * block_size / 16 below 2^31. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
- * with the zeroing and sharing rules of pa_decode_workspace_bytes. Arithmetic,
- * other arguments and errors as for pa_decode.
+ * which need no initialisation; calls that share it must not overlap on the GPU.
+ * Arithmetic, other arguments and errors as for pa_decode.
  */
 int pa_decode_shared_prefix(void* out, const void* query,
                             const void* key_cache, const void* value_cache,

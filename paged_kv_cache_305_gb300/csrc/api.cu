@@ -250,11 +250,9 @@ StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_h
   if (!w.cut && max_chunks == 0) return w;
   const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
   const size_t group = static_cast<size_t>(w.heads) * (num_q_heads / num_kv_heads);
-  // one slot for each (row, unit) boundary on the line of tiles
-  const size_t slots = static_cast<size_t>(num_seqs) * (num_kv_heads / w.heads) +
-                       (w.cut ? static_cast<size_t>(kMaxCtas) * (1 + kClaims) : kMaxCtas);
-  w.row_off = kWorkspaceHeader;
-  w.pre_lse = round_up(w.row_off + static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(int2), 256);
+  // one slot for each boundary of a row or a share on the line
+  const size_t slots = static_cast<size_t>(num_seqs) * (num_kv_heads / w.heads) + kMaxCtas;
+  w.pre_lse = round_up(static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(int2), 256);
   w.seg_lse = w.pre_lse + round_up(rows * max_chunks * sizeof(float), 256);
   w.pre_out = w.seg_lse + round_up(slots * group * sizeof(float), 256);
   w.seg_out = w.pre_out + rows * max_chunks * head_dim * sizeof(float);
@@ -871,11 +869,8 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   if (rc != PA_OK) return rc;
   rc = counter(true, &timeouts);
   if (rc != PA_OK) return rc;
-  if (wl.total > 0) {
-    // only the header has to be zero, and is left so
-    cudaError_t e = prepare_workspace(workspace, pa::kWorkspaceHeader, pa::kWorkspaceHeader, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace counters)");
-  }
+  // nothing has to be zero, and nothing is left so for a pa_decode on this workspace
+  if (wl.total > 0) prepare_workspace(workspace, 0, 0, stream);
 
   char* ws = static_cast<char*>(workspace);
   pa::StreamArgs a{};
@@ -900,9 +895,7 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   a.cut = wl.cut ? 1 : 0;
   a.least_tiles = std::max(partition_tokens / (fp8 ? 32 : 16), pa::kLeastTiles);
   if (wl.total > 0) {
-    a.ws_claim = reinterpret_cast<unsigned long long*>(ws);
-    a.ws_done = reinterpret_cast<unsigned*>(ws + 8);
-    a.ws_rows = reinterpret_cast<int2*>(ws + wl.row_off);
+    a.ws_rows = reinterpret_cast<int2*>(ws);
     a.pre_lse = reinterpret_cast<float*>(ws + wl.pre_lse);
     a.pre_out = reinterpret_cast<float*>(ws + wl.pre_out);
     a.seg_lse = reinterpret_cast<float*>(ws + wl.seg_lse);

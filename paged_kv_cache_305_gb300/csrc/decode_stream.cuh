@@ -9,27 +9,27 @@
 // copies of the 128-sequence case without any arithmetic: 222 us with one head,
 // 197 us with two or four; 216 and 116 us for d = 64). A row is one (sequence, head
 // group); its tokens (those behind the shared prefix, where there is one) are
-// taken in tiles of 8 KB a head (K and V of 32 8-bit or 16 16-bit tokens of d =
-// 128), cut at multiples of the tile's tokens. All tiles in (head group,
-// sequence, tile) order form one line, which is cut into units wherever equal
-// shares end, inside rows as it comes: first one static unit for each CTA of
-// the persistent grid (kStaticShare of the work), then smaller units that CTAs
-// claim from a counter when they are done. CTAs run at uneven speed, and the
-// claimed units even that out. The cuts depend on the lengths and the grid
-// alone, so which CTA computes a unit does not change the result.
+// taken in stages of 32 KB (at d = 128: K and V of 32 8-bit or 16 16-bit tokens
+// for each computing warp), cut at multiples of the stage's tokens. All stages, in
+// (head group, sequence, stage) order, form one line, which is cut into equal
+// shares, one for each CTA of the persistent grid, inside rows as it comes. The
+// cuts depend on the lengths and the grid alone. (Shares of 80 to 90 % with the
+// rest claimed from a counter at run time were 3 to 15 % slower on every case:
+// CTAs end within a few percent of each other, and every further segment has its
+// query to load, its states to join and a piece to merge.)
 //
-// Pieces. The part of a row inside a unit is a segment. A row that is one
+// Pieces. The part of a row inside a share is a segment. A row that is one
 // segment is finished at once; otherwise each segment leaves a piece (fp32
 // normalised output and base-2 log-sum-exp), and a merge kernel behind this one
 // joins them, in order. A piece is stored and forgotten: a merge by the last
 // one to arrive would fence, count and read the others back while its CTA waits
-// (that cost 10 % of the 128-sequence case). Segment (row R of the line, unit
-// u) has the slot R + u: along the line every row and every unit begins one
-// boundary, so slots rise, those of a row follow each other, and there are as
-// many as rows and units together, however long a row is.
+// (that cost 10 % of the 128-sequence case). Segment (row R, share u) has the
+// slot R + u: every row and every share begins one boundary, so slots rise along
+// the line, those of a row follow each other, and there are as many as rows and
+// shares together, however long a row is.
 //
-// Streaming. Four warps compute, a fifth feeds them: it claims units, finds their
-// rows, reads the block table and fills the stages of a ring in shared memory,
+// Streaming. Four warps compute, a fifth feeds them: it finds the rows
+// of the CTA's share, reads the block table and fills the stages of a ring in shared memory,
 // 32 KB each at d = 128: one tile for every computing warp, the tiles of the
 // CTA's heads side by side. A lane issues a tensor copy per block for K and for
 // V, straight from the block table and for all heads at once, and a bulk copy
@@ -37,7 +37,7 @@
 // tensor map's reach, are copied row by row with cp.async (ROWS). A stage carries
 // a note of what it holds, so the computing warps know of nothing but stages:
 // they load the query at a segment's first one and join their states at its
-// last one, while the copies run on across segments and units. All waits are
+// last one, while the copies run on across segments. All waits are
 // bounded; one that gives up is counted, and the CTA winds down.
 #pragma once
 
@@ -90,7 +90,7 @@ struct Ring {
   static constexpr int kStats = kBars + (2 * kStages + kWarps) * 8;  // [warp][m, l, r][head]
   static constexpr int kBase = kStats + kWarps * 3 * kHeads * 4;     // [kChunks]
   static constexpr int kMisc = kBase + kChunks * 4;
-  static constexpr int kJoin = (kMisc + 64 + 15) / 16 * 16;          // [warp][head][kOStride]
+  static constexpr int kJoin = (kMisc + 32 + 15) / 16 * 16;          // [warp][head][kOStride]
   static constexpr int kBytes = kJoin + kWarps * kJoinHeads * kOStride * 4;
   static_assert(kStages >= 2, "a stage lands while another is computed");
   static_assert(kStats % 8 == 0 && kBars % 8 == 0 && kNotes % 16 == 0, "alignment");
@@ -103,13 +103,10 @@ __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
 // Shared scratch. Positions on the line are 32-bit: the host refuses sizes that
 // could have 2^31 of them.
 struct Misc {
-  unsigned scan[kWarps];
-  unsigned Wseq, W;        // stages of one head group's rows, and of all
-  unsigned T1, W1, nstat;  // stages of a static unit, end and number of those
-  unsigned T2, nunits;     // stages of a claimed unit, number of all units
-  int abort;               // a wait has given up
+  unsigned scan[kWarps];  // stages of a head group's rows, by the warp that summed them
+  int abort;              // a wait has given up
 };
-static_assert(sizeof(Misc) <= 64, "room reserved in Ring");
+static_assert(sizeof(Misc) <= 32, "room reserved in Ring");
 
 // ROWS: the entry of token x, held by lane x % 32 at x / 32 (x differs by lane; all
 // lanes of the warp call this together).
@@ -176,7 +173,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     }
   }
 
-  // ---- the line of stages ----------------------------------------------------
+  // ---- the line of stages ---------------------------------------------------
+  const bool whole = a.cut == 0;
   struct Row {
     int lo, hi;  // tokens
     int n;       // stages; one (without tokens) for an empty row
@@ -216,46 +214,12 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       if (lane >= off) incl += v;
     }
     if (lane == 31) misc.scan[warp] = incl;
-    sBase[tid] = incl - mine;
-  }
-  __syncthreads();
-  const bool whole = a.cut == 0;
-  if (warp < kWarps) {
-    unsigned before = 0;
-    for (int w = 0; w < warp; ++w) before += misc.scan[w];
-    sBase[tid] += before;
-  }
-  // Units: T1 stages for each of the first C, then T2 for each that is claimed.
-  // Where rows are not cut a unit takes the rows that start in it.
-  if (tid == 0) {
-    const unsigned C = gridDim.x, least = (a.least_tiles + Wh - 1) / Wh;
-    unsigned Wseq = 0;
-    for (int w = 0; w < kWarps; ++w) Wseq += misc.scan[w];
-    const unsigned W = Wseq * NG;
-    unsigned T1 = (W + C - 1) / C, T2 = 1;
-    if (!whole) {
-      const unsigned share = static_cast<unsigned>(static_cast<float>(W) * (kStaticShare / 100.f)) / C;
-      T2 = max(least, (W - share * C + C * kClaims - 1) / (C * kClaims));
-      T1 = share < least ? max(T1, least) : share;
-    }
-    misc.Wseq = Wseq;
-    misc.W = W;
-    misc.T1 = T1;
-    misc.W1 = T1 >= (W + C - 1) / C ? W : T1 * C;
-    misc.nstat = (misc.W1 + T1 - 1) / T1;
-    misc.T2 = T2;
-    misc.nunits = misc.nstat + (W - misc.W1 + T2 - 1) / T2;
+    sBase[tid] = incl - mine;  // within the warp's sequences
   }
   __syncthreads();
 
   if (warp == kWarps) {
     // ======================= the feeding warp ==================================
-    auto unit_of = [&](unsigned pos) {
-      return pos < misc.W1 ? pos / misc.T1 : misc.nstat + (pos - misc.W1) / misc.T2;
-    };
-    auto claim = [&]() -> unsigned {  // of lane 0
-      return lane == 0 ? static_cast<unsigned>(atomicAdd(a.ws_claim, 1ull)) : 0u;
-    };
     const int bt = ROWS ? 1 : lb;  // tokens a lane's table entry stands for
     constexpr uint32_t kNone = 0xffffffffu, kBad = 0xfffffffeu;
     constexpr int kPer = ROWS ? 4 : 1;  // entries of a lane: tokens lane, lane + 32, .. (at most 128)
@@ -391,34 +355,39 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       ++filled;
     };
 
-    unsigned unit = blockIdx.x;
-    if (unit >= misc.nstat)
-      unit = whole ? misc.nunits : misc.nstat + __shfl_sync(kFull, claim(), 0);
-    while (unit < misc.nunits && ok) {
-      const unsigned next = whole ? 0u : claim();  // of lane 0: the claim after this unit, ahead of time
-      const bool stat = unit < misc.nstat;
-      const unsigned u0 = stat ? unit * misc.T1 : misc.W1 + (unit - misc.nstat) * misc.T2;
-      const unsigned u1 = stat ? min(u0 + misc.T1, misc.W1) : min(u0 + misc.T2, misc.W);
+    // the CTA's share of the line; where rows are not cut, the rows that start in it
+    unsigned group = 0;  // stages of a head group's rows
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) group += misc.scan[w];
+    const unsigned all = group * NG;
+    const unsigned share = max((all + gridDim.x - 1) / gridDim.x,
+                               static_cast<unsigned>(whole ? 1 : (a.least_tiles + Wh - 1) / Wh));
+    const unsigned u0 = blockIdx.x * share, u1 = min(u0 + share, all);
+    if (u0 < all) {
       // the row that holds position u0: its run of sequences, then the sequence
-      int hg = static_cast<int>(u0 / misc.Wseq), s;
+      int hg = static_cast<int>(u0 / group), s;
       unsigned p;
       {
-        const unsigned off = u0 - hg * misc.Wseq;
-        int before = 0;
+        const unsigned off = u0 - hg * group;
+        unsigned at_w = 0;  // stages before the runs of warp w
+        int c = -1;
 #pragma unroll
-        for (int k = 0; k < kChunks / 32; ++k) before += sBase[lane + 32 * k] <= off ? 1 : 0;
-        const int c = __reduce_add_sync(kFull, before) - 1;
+        for (int w = 0; w < kWarps; ++w) {
+          c += __popc(__ballot_sync(kFull, at_w + sBase[w * 32 + lane] <= off));
+          at_w += misc.scan[w];
+        }
         s = c * per;
         p = sBase[c];
+        for (int w = 0; w < c >> 5; ++w) p += misc.scan[w];
         for (;;) {
           const unsigned n = s + lane < min(S, (c + 1) * per) ? row_of(s + lane).n : 0u;
           unsigned incl = n;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const unsigned v = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o) incl += v;
+            const unsigned t = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += t;
           }
-          const unsigned hit = __ballot_sync(kFull, n > 0 && p + incl > off);
+          const unsigned hit = __ballot_sync(kFull, p + incl > off);
           if (hit != 0) {
             const int l = __ffs(hit) - 1;
             p += __shfl_sync(kFull, incl - n, l);
@@ -427,9 +396,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           p += __shfl_sync(kFull, incl, 31);
           s += 32;
-          if (s >= S) break;  // not reached
         }
-        p += hg * misc.Wseq;
+        p += hg * group;
       }
       // rows from there on, 32 at a time
       bool more = true;
@@ -441,21 +409,21 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         unsigned end = r.n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const unsigned v = __shfl_up_sync(kFull, end, o);
-          if (lane >= o) end += v;
+          const unsigned t = __shfl_up_sync(kFull, end, o);
+          if (lane >= o) end += t;
         }
         end += p;
         const unsigned start = end - r.n;
-        // a row without cuts belongs to the unit that it starts in
         const unsigned from = whole ? start : max(start, u0), to = whole ? end : min(end, u1);
         const bool in = my_hg < NG && start < u1 && (!whole || start >= u0);
         int slot = -1;
         if (in) {
-          const unsigned first = whole ? unit : unit_of(start), last = whole ? unit : unit_of(end - 1);
+          const unsigned first = whole ? blockIdx.x : start / share;
+          const unsigned last = whole ? blockIdx.x : (end - 1) / share;
           const bool pieces = last > first || r.before > 0;
-          if (pieces) slot = my_hg * S + my_s + static_cast<int>(unit);
+          if (pieces) slot = my_hg * S + my_s + static_cast<int>(blockIdx.x);
           // the merge kernel finds the row's pieces here (none: the row is finished)
-          if (unit == first && a.ws_rows != nullptr) {
+          if (blockIdx.x == first && a.ws_rows != nullptr) {
             for (int i = 0; i < Hc; ++i)
               a.ws_rows[static_cast<size_t>(my_s) * Hkv + my_hg * Hc + i] =
                   make_int2(slot, pieces ? static_cast<int>(last - first) + 1 : 0);
@@ -473,14 +441,14 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           note.slot = __shfl_sync(kFull, slot, l);
           note.t0 = __shfl_sync(kFull, stage0, l) * ST;
           note.pad = 0;
-          const int n = __shfl_sync(kFull, stages, l);
+          const int count = __shfl_sync(kFull, stages, l);
           const int32_t* row = a.block_tables + static_cast<size_t>(note.s) * a.max_blocks_per_seq;
           Ids ids = load_ids(row, note.t0, note.lo, note.hi);
-          for (int i = 0; i < n && ok; ++i) {
-            note.flags = (i == 0 ? kFirst : 0) | (i == n - 1 ? kLast : 0);
+          for (int i = 0; i < count && ok; ++i) {
+            note.flags = (i == 0 ? kFirst : 0) | (i == count - 1 ? kLast : 0);
             fill(note, ids);
             note.t0 += ST;
-            if (i + 1 < n) ids = load_ids(row, note.t0, note.lo, note.hi);  // a stage ahead
+            if (i + 1 < count) ids = load_ids(row, note.t0, note.lo, note.hi);  // a stage ahead
           }
         }
         more = __shfl_sync(kFull, my_hg < NG && end < u1, 31);
@@ -488,7 +456,6 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         hg += (s + 32) / S;
         s = (s + 32) % S;
       }
-      unit = whole ? misc.nunits : misc.nstat + __shfl_sync(kFull, next, 0);
     }
     if (ok) {  // the end of all work
       const uint32_t st = next_stage();
@@ -653,29 +620,20 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       }
     }
   }
-  __syncthreads();  // every copy has landed, every claim has been made
   // no CTA ends before the prefix pass does: the merge kernel behind this one
   // then waits for both
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!whole && tid == kWarps * 32) {  // the lane that claims
-    // the last CTA to finish (every claim made) leaves the counters at zero
-    __threadfence();
-    if (atomicAdd(a.ws_done, 1u) == static_cast<unsigned>(gridDim.x - 1)) {
-      atomicExch(a.ws_claim, 0ull);
-      atomicExch(a.ws_done, 0u);
-    }
-  }
 }
 
 // ---------------------------------------------------------------------------
 // Merge
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
-constexpr long long kTogetherRows = 4 * 152 * 16;  // fewer query rows: a CTA for each
+constexpr long long kTogetherRows = 152 * 16;  // fewer query rows: a CTA for each
 
 // out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over a query row's pieces,
-// the prefix pass's first, in order. A row without segments in the list was
-// finished by the streaming kernel. TOGETHER: a CTA takes a row, each warp a
+// the prefix pass's first, in order. A row without segments was finished by the
+// streaming kernel. TOGETHER: a CTA takes a row, each warp a
 // share of its pieces (few rows, of many pieces); otherwise each warp takes one.
 template <typename Ty, int D, bool TOGETHER>
 __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const StreamArgs a) {
@@ -695,17 +653,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const St
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 mine = __ldcg(a.ws_rows + static_cast<size_t>(s) * a.num_kv_heads + h);
   if (mine.y == 0) return;
-  const int n = mine.y + before;
+  const int n = before + mine.y;
   const int Hc = a.heads_at_a_time, G = a.group;
   {
-    // piece k: of the prefix pass, or in the row's k - before-th slot
+    // piece k: of the prefix pass, or in one of the row's slots
     const size_t pre = row * a.groups.max_chunks, step = static_cast<size_t>(Hc) * G;
-    const size_t seg = static_cast<size_t>(mine.x) * step + static_cast<size_t>(h % Hc) * G + g;
+    const size_t in_slot = static_cast<size_t>(h % Hc) * G + g;
+    auto piece_at = [&](int k) { return static_cast<size_t>(mine.x + k - before) * step + in_slot; };
     auto lse_at = [&](int k) {
-      return __ldcg(k < before ? a.pre_lse + pre + k : a.seg_lse + seg + (k - before) * step);
+      return __ldcg(k < before ? a.pre_lse + pre + k : a.seg_lse + piece_at(k));
     };
     auto out_at = [&](int k) {
-      const float* p = k < before ? a.pre_out + (pre + k) * D : a.seg_out + (seg + (k - before) * step) * D;
+      const float* p = k < before ? a.pre_out + (pre + k) * D : a.seg_out + piece_at(k) * D;
       return __ldcg(reinterpret_cast<const Vec*>(p) + lane);
     };
     const int share = TOGETHER ? (n + kMergeWarps - 1) / kMergeWarps : n;

@@ -39,10 +39,8 @@ struct StreamArgs {
   float scale_log2;     // scale * log2(e)
   int out_f32;
   PrefixArgs groups;    // shared prefixes (num_groups 0: none)
-  int cut;              // 1: rows may be cut between units
-  int least_tiles;      // shortest unit that cuts rows, in tiles
-  unsigned long long* ws_claim;  // units claimed so far (zero between calls)
-  unsigned* ws_done;             // CTAs finished (zero between calls)
+  int cut;              // 1: rows may be cut between CTAs
+  int least_tiles;      // shortest share that cuts rows, in tiles
   int2* ws_rows;        // [S, Hkv] first slot and number of a row's segments (0: the row is finished)
   float* pre_lse;       // [S, Hq, max_chunks] pieces of the prefix pass: base-2 log-sum-exp
   float* pre_out;       // and normalised fp32 rows [.., d]
@@ -78,23 +76,19 @@ constexpr int kPrefixMinChunk = 256;
 void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
                  int max_prefix_len, int max_group_size);
 
-// Schedule of the streaming decode kernel: three CTAs on each of the 152 SMs;
-// the share (%) of the work that is dealt out to them beforehand, and about how
-// many units each claims of the rest; the shortest unit that may cut a row, in
-// tiles; tables of up to kUncutTokens leave rows whole.
+// Schedule of the streaming decode kernel: three CTAs on each of the 152 SMs; the
+// shortest share of the work that may cut a row, in tiles; tables of up to
+// kUncutTokens leave rows whole.
 constexpr int kMaxCtas = 456;
-constexpr int kStaticShare = 80;
-constexpr int kClaims = 4;
 constexpr int kLeastTiles = 4;
 constexpr long long kUncutTokens = 512;
 constexpr int kGroupTiles = 16;  // see stream_heads
 
-// Workspace of the streaming decode kernel: the header (claims, CTAs finished),
-// the rows' segment counts, then the pieces.
+// Workspace of the streaming decode kernel: the rows' segments, then the pieces.
 struct StreamLayout {
   int heads;  // kv heads at a time
   bool cut;   // rows may be cut
-  size_t row_off, pre_lse, seg_lse, pre_out, seg_out, total;
+  size_t pre_lse, seg_lse, pre_out, seg_out, total;
 };
 StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                            long long lmax, int max_chunks);
