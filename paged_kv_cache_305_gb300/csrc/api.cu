@@ -229,23 +229,23 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   x->max_chunks = max_group_size > 0 ? (x->max_prefix_len + x->chunk_tokens - 1) / x->chunk_tokens : 0;
 }
 
-// Kv heads that a CTA of the streaming kernel takes at a time. 16-bit rows of one
-// head (256 bytes at d = 128) are long enough by themselves; 8-bit ones are read
-// with their neighbours while that leaves every CTA kGroupTiles tiles of the
-// longest lengths to share.
+// Kv heads that a CTA of the streaming kernel takes at a time: neighbours are read
+// together while that leaves every CTA kGroupTiles tiles of the longest lengths to
+// share (behind the longest prefix, where there is one).
 int stream_heads(bool fp8, int num_seqs, int num_kv_heads, long long lmax) {
-  for (int hc = 4; fp8 && hc > 1; hc /= 2)
+  for (int hc = 4; hc > 1; hc /= 2)
     if (num_kv_heads % hc == 0 &&
-        static_cast<double>(num_seqs) * (num_kv_heads / hc) * (static_cast<double>(lmax) / 32) >=
+        static_cast<double>(num_seqs) * (num_kv_heads / hc) * (static_cast<double>(lmax) / (fp8 ? 32 : 16)) >=
             static_cast<double>(kMaxCtas) * kGroupTiles)
       return hc;
   return 1;
 }
 
 StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                           long long lmax, int max_chunks) {
+                           long long lmax, const PrefixArgs& groups) {
   StreamLayout w{};
-  w.heads = stream_heads(fp8, num_seqs, num_kv_heads, lmax);
+  const int max_chunks = groups.max_chunks;
+  w.heads = stream_heads(fp8, num_seqs, num_kv_heads, lmax - groups.max_prefix_len);
   w.cut = lmax > kUncutTokens;
   if (!w.cut && max_chunks == 0) return w;
   const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
@@ -854,7 +854,7 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
     return fail(PA_ERR_INVALID, "block_tables and seq_lens must be 4-byte aligned");
   if (!aligned16(scales)) return fail(PA_ERR_INVALID, "cache_scales must be 16-byte aligned");
   const pa::StreamLayout wl = pa::stream_layout(fp8, num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                                lmax, groups.max_chunks);
+                                                lmax, groups);
   if (wl.total > 0) {
     if (workspace == nullptr || workspace_bytes < wl.total)
       return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", wl.total,
@@ -969,7 +969,7 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
       (head_dim != 64 && head_dim != 128) || max_blocks_per_seq < 1 || log2_pow2(block_size) < 0)
     return 0;
   return pa::stream_layout(true, num_seqs, num_q_heads, num_kv_heads, head_dim,
-                           static_cast<long long>(max_blocks_per_seq) * block_size, 0)
+                           static_cast<long long>(max_blocks_per_seq) * block_size, pa::PrefixArgs{})
       .total;
 }
 
@@ -986,7 +986,7 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
   pa::PrefixArgs x{};
   pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads, static_cast<int>(lmax),
                   max_prefix_len, max_group_size);
-  return pa::stream_layout(false, num_seqs, num_q_heads, num_kv_heads, head_dim, lmax, x.max_chunks)
+  return pa::stream_layout(false, num_seqs, num_q_heads, num_kv_heads, head_dim, lmax, x)
       .total;
 }
 

@@ -34,8 +34,10 @@
 // CTA's heads side by side. A lane issues a tensor copy per block for K and for
 // V, straight from the block table and for all heads at once, and a bulk copy
 // for the block's exponent bytes. Blocks under 8 tokens, and pools beyond a
-// tensor map's reach, are copied row by row with cp.async (ROWS). A stage carries
-// a note of what it holds, so the computing warps know of nothing but stages:
+// tensor map's reach, are copied row by row: the feeding warp hands out the slots
+// of the stage's tokens, and each computing warp copies its own tile with
+// cp.async, a stage ahead (ROWS; one warp alone cannot issue that many copies:
+// 350 us for the 128 sequences). A stage carries a note of what it holds, so the computing warps know of nothing but stages:
 // they load the query at a segment's first one and join their states at its
 // last one, while the copies run on across segments. All waits are
 // bounded; one that gives up is counted, and the CTA winds down.
@@ -91,7 +93,9 @@ struct Ring {
   static constexpr int kBase = kStats + kWarps * 3 * kHeads * 4;     // [kChunks]
   static constexpr int kMisc = kBase + kChunks * 4;
   static constexpr int kJoin = (kMisc + 32 + 15) / 16 * 16;          // [warp][head][kOStride]
-  static constexpr int kBytes = kJoin + kWarps * kJoinHeads * kOStride * 4;
+  static constexpr int kSlots = kJoin + kWarps * kJoinHeads * kOStride * 4;  // ROWS: [stage][token]
+  static constexpr int kBytes = kSlots;
+  static constexpr int kRowsBytes = kSlots + kStages * kWarps * T::kTokens * 4;
   static_assert(kStages >= 2, "a stage lands while another is computed");
   static_assert(kStats % 8 == 0 && kBars % 8 == 0 && kNotes % 16 == 0, "alignment");
 };
@@ -107,19 +111,6 @@ struct Misc {
   int abort;              // a wait has given up
 };
 static_assert(sizeof(Misc) <= 32, "room reserved in Ring");
-
-// ROWS: the entry of token x, held by lane x % 32 at x / 32 (x differs by lane; all
-// lanes of the warp call this together).
-template <int N>
-__device__ __forceinline__ uint32_t row_id(const uint32_t (&v)[N], int x) {
-  uint32_t got = 0;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const uint32_t t = __shfl_sync(kFull, v[j], x & 31);
-    if (j == x >> 5) got = t;
-  }
-  return got;
-}
 
 // SPLIT: at most 4 query heads a kv head (stream_tile.cuh).
 template <typename Ty, int D, int NT, bool FP8, bool ROWS, bool SPLIT>
@@ -144,6 +135,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   Misc& misc = *reinterpret_cast<Misc*>(smem + R::kMisc);
   Note* notes = reinterpret_cast<Note*>(smem + R::kNotes);
   unsigned* sBase = reinterpret_cast<unsigned*>(smem + R::kBase);
+  [[maybe_unused]] uint32_t* slots = reinterpret_cast<uint32_t*>(smem + R::kSlots);
+  constexpr uint32_t kNone = 0xffffffffu, kBad = 0xfffffffeu;  // in the place of a slot
   const uint32_t ring = smem_u32(smem), bars = smem_u32(smem + R::kBars);
   auto full = [&](uint32_t st) { return bars + 8 * st; };
   auto empty = [&](uint32_t st) { return bars + 8 * (kStages + st); };
@@ -161,7 +154,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(full(i), ROWS ? 64 : 1);
+      tc::mbar_init(full(i), 1);
       tc::mbar_init(empty(i), kWarps);
     }
     for (int i = 0; i < kWarps; ++i) tc::mbar_init(join_bar(i), Wh);
@@ -221,7 +214,6 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   if (warp == kWarps) {
     // ======================= the feeding warp ==================================
     const int bt = ROWS ? 1 : lb;  // tokens a lane's table entry stands for
-    constexpr uint32_t kNone = 0xffffffffu, kBad = 0xfffffffeu;
     constexpr int kPer = ROWS ? 4 : 1;  // entries of a lane: tokens lane, lane + 32, .. (at most 128)
     uint32_t filled = 0;  // stages
     bool ok = true;
@@ -263,56 +255,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       const int h0 = note.hg * Hc;
       if (lane == 0) notes[st] = note;
       if constexpr (ROWS) {
-        // the CTA's heads of a token are neighbours: Hc rows are one run
-        const int run = Hc * Geo::kChunks;  // 16-byte chunks
-        const size_t stride = static_cast<size_t>(Hkv) * kRB;
-        const char* kb = static_cast<const char*>(a.key_cache) + static_cast<size_t>(h0) * kRB;
-        const char* vb = static_cast<const char*>(a.value_cache) + static_cast<size_t>(h0) * kRB;
-        if constexpr (FP8) {
-          // exponents: (token, head) pairs, all loads before the stores
-          uint8_t ek[4], ev[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // ST * Hc = 128 pairs
-            const int x = (lane + 32 * k) % ST, hh = (lane + 32 * k) / ST;
-            const uint32_t id = row_id(ids.v, x);
-            ek[k] = ev[k] = 0;
-            if (id < kBad) {
-              const uint8_t* e = a.scales + ((static_cast<size_t>(id >> shift) * Hkv + h0 + hh) * 2 << shift) +
-                                 (id & ((1u << shift) - 1));
-              ek[k] = __ldg(e);
-              ev[k] = __ldg(e + (1 << shift));
-            }
-          }
-          for (int i = lane; i < ST * run; i += 32) {
-            const int x = i / run, c = i % run, hh = c / Geo::kChunks, cc = c % Geo::kChunks;
-            const uint32_t o = hh * ST * kRB + Geo::off(x, cc);
-            const uint32_t v = row_id(ids.v, x);
-            const bool live = v < kBad;
-            const size_t from = (live ? v : 0u) * stride + c * 16;
-            cp_async_16(sk + o, kb + from, live);
-            cp_async_16(sv + o, vb + from, live);
-          }
-          tc::cp_async_mbar_arrive_noinc(full(st));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int x = (lane + 32 * k) % ST, hh = (lane + 32 * k) / ST;
-            se[hh * 2 * ST + x] = ek[k];
-            se[hh * 2 * ST + ST + x] = ev[k];
-          }
-        } else {
-          for (int i = lane; i < ST * run; i += 32) {
-            const int x = i / run, c = i % run, hh = c / Geo::kChunks, cc = c % Geo::kChunks;
-            const uint32_t o = hh * ST * kRB + Geo::off(x, cc);
-            const uint32_t v = row_id(ids.v, x);
-            const bool live = v < kBad;
-            const size_t from = (live ? v : 0u) * stride + c * 16;
-            cp_async_16(sk + o, kb + from, live);
-            cp_async_16(sv + o, vb + from, live);
-          }
-          tc::cp_async_mbar_arrive_noinc(full(st));
-        }
+        for (int j = 0; j < kPer; ++j)
+          if (lane + 32 * j < ST) slots[st * (kWarps * kTT) + lane + 32 * j] = ids.v[j];
         __syncwarp();
-        tc::mbar_arrive(full(st));  // releases this lane's plain stores
+        if (lane == 0) tc::mbar_arrive(full(st));
       } else {
         const uint32_t id = ids.v[0];
         const unsigned bad = __ballot_sync(kFull, id == kBad);
@@ -462,8 +409,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       if (ok) {
         if (lane == 0) notes[st].flags = kEnd;
         __syncwarp();
-        if (ROWS || lane == 0) tc::mbar_arrive(full(st));
-        if (ROWS) tc::mbar_arrive(full(st));
+        if (lane == 0) tc::mbar_arrive(full(st));
       }
     } else {  // what was issued must land before the CTA ends
       for (uint32_t i = filled - min(filled, static_cast<uint32_t>(kStages)); i != filled; ++i)
@@ -494,12 +440,63 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       return wait(join_bar(hsub), joins++ & 1);
     };
     bool ok = true;
-    for (uint32_t n = 0; ok; ++n) {
+    // waits for stage n and reads its note. ROWS: begins the copies of this warp's
+    // tile, rows that do not count as zeros, and reads its token's exponents.
+    [[maybe_unused]] int ek = 0, ev = 0;
+    auto take = [&](uint32_t n) {
       const uint32_t stage = n % kStages;
       ok = *aborted == 0 && wait(full(stage), (n / kStages) & 1);
-      if (!ok) break;
-      const Note note = notes[stage];
-      if (note.flags & kEnd) break;
+      Note note = notes[stage];
+      if (!ok) note.flags = kEnd;
+      if constexpr (ROWS) {
+        if (!(note.flags & kEnd)) {
+          constexpr int kRowsPerCopy = 32 / Geo::kChunks;
+          const int h = note.hg * Hc + hsub, cc = lane % Geo::kChunks;
+          const uint32_t mine = slots[stage * (kWarps * kTT) + x0 + lane % kTT];
+          const size_t stride = static_cast<size_t>(Hkv) * kRB;
+          const size_t hoff = static_cast<size_t>(h) * kRB + cc * 16;
+          const char* kb = static_cast<const char*>(a.key_cache) + hoff;
+          const char* vb = static_cast<const char*>(a.value_cache) + hoff;
+          const uint32_t sk = ring + stage * 2 * R::kHalf + hsub * ST * kRB, sv = sk + R::kHalf;
+#pragma unroll
+          for (int i = 0; i < kTT / kRowsPerCopy; ++i) {
+            const int r = lane / Geo::kChunks + i * kRowsPerCopy;
+            const uint32_t slot = __shfl_sync(kFull, mine, r);
+            const bool live = slot < kBad;
+            const size_t from = (live ? slot : 0u) * stride;
+            const uint32_t o = Geo::off(x0 + r, cc);
+            cp_async_16(sk + o, kb + from, live);
+            cp_async_16(sv + o, vb + from, live);
+          }
+          if constexpr (FP8) {
+            const uint8_t* e = a.scales + ((static_cast<size_t>(mine >> shift) * Hkv + h) * 2 << shift) +
+                               (mine & ((1u << shift) - 1));
+            ek = mine < kBad ? __ldg(e) : 0;
+            ev = mine < kBad ? __ldg(e + (1 << shift)) : 0;
+          }
+        }
+        cp_async_commit();
+      }
+      return note;
+    };
+    [[maybe_unused]] Note ahead;
+    if constexpr (ROWS) ahead = take(0);
+    for (uint32_t n = 0;; ++n) {
+      const uint32_t stage = n % kStages;
+      Note note;
+      [[maybe_unused]] int my_ek = 0, my_ev = 0;
+      if constexpr (ROWS) {
+        note = ahead;
+        if (note.flags & kEnd) break;
+        my_ek = ek;
+        my_ev = ev;
+        ahead = take(n + 1);
+        cp_async_wait<1>();
+        __syncwarp();
+      } else {
+        note = take(n);
+        if (note.flags & kEnd) break;
+      }
       if (note.flags & kFirst) {
         const T* qh = static_cast<const T*>(a.query) +
                       (static_cast<size_t>(note.s) * a.num_q_heads + static_cast<size_t>(note.hg * Hc + hsub) * G) * D;
@@ -521,8 +518,12 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           __syncwarp();
         }
         if constexpr (FP8) {
-          const unsigned char* e = smem + R::kScales + stage * R::kScaleBytes + e_at;
-          tile_8<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, e[0], e[lb], lo, hi, q, st);
+          if constexpr (!ROWS) {
+            const unsigned char* e = smem + R::kScales + stage * R::kScaleBytes + e_at;
+            my_ek = e[0];
+            my_ev = e[lb];
+          }
+          tile_8<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, my_ek, my_ev, lo, hi, q, st);
         } else {
           tile_16<Ty, D, NT, SPLIT>(sk + k_at, sv + v_at, lo, hi, q, st);
         }
@@ -548,9 +549,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       const int r8 = lane >> 2, tq = 2 * (lane & 3);
       const size_t row0 = static_cast<size_t>(note.s) * a.num_q_heads +
                           static_cast<size_t>(note.hg * Hc + hsub) * G;
-      for (int h0 = 0; h0 < G && ok; h0 += kJoinHeads) {
-        ok = meet();  // the area was read by the join before
-        if (!ok) break;
+      for (int h0 = 0; h0 < G; h0 += kJoinHeads) {
+        if (!meet()) break;  // the area was read by the join before
         float* mine_o = sJoin + warp * kJoinHeads * R::kOStride;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -576,8 +576,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               stat_w[2 * R::kHeads] = static_cast<float>(st.r);
             }
           }
-        ok = meet();
-        if (!ok) break;
+        if (!meet()) break;
         const int heads = min(G - h0, kJoinHeads), w0 = warp - wsub;
         for (int i = wsub * 32 + lane; i < heads * (D / 4); i += Wh * 32) {
           const int at = i / (D / 4), c4 = i % (D / 4) * 4, head = h0 + at;
@@ -619,6 +618,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
       }
     }
+    if constexpr (ROWS) cp_async_wait<0>();
   }
   // no CTA ends before the prefix pass does: the merge kernel behind this one
   // then waits for both
@@ -783,8 +783,9 @@ struct Dependent {
 template <typename Ty, int D, int NT, bool FP8, bool ROWS, bool SPLIT>
 cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   using R = Ring<D, FP8, NT>;
+  constexpr int kSmem = ROWS ? R::kRowsBytes : R::kBytes;
   auto kern = paged_stream_kernel<Ty, D, NT, FP8, ROWS, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   CUtensorMap km{}, vm{};
   if constexpr (!ROWS) {
@@ -799,7 +800,7 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.num_seqs) * (a.num_kv_heads / a.heads_at_a_time);
   const long long most = (static_cast<long long>(a.max_blocks_per_seq) << a.block_shift) / Tile<D, FP8>::kTokens + 2;
   const long long grid = std::min(ctas, rows * (a.cut ? (most + a.least_tiles - 1) / a.least_tiles : 1));
-  Dependent d(dim3(static_cast<unsigned>(std::max(grid, 1ll))), kThreads, R::kBytes, stream,
+  Dependent d(dim3(static_cast<unsigned>(std::max(grid, 1ll))), kThreads, kSmem, stream,
               a.groups.max_chunks > 0);  // behind a prefix pass
   e = cudaLaunchKernelEx(&d.cfg, kern, km, vm, a);
   if (e != cudaSuccess || a.ws_rows == nullptr) return e;  // rows are whole, and there is no prefix

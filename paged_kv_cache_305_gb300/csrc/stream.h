@@ -91,7 +91,7 @@ struct StreamLayout {
   size_t pre_lse, seg_lse, pre_out, seg_out, total;
 };
 StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                           long long lmax, int max_chunks);
+                           long long lmax, const PrefixArgs& groups);
 
 cudaError_t launch_decode_fp8(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
                               cudaStream_t stream);
