@@ -206,9 +206,12 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   const long long tiles = (static_cast<long long>(max_group_size) + members - 1) / members;
   const long long per_chunk = tiles * num_groups * num_kv_heads;
   const long long most = std::max(x->max_prefix_len / kPrefixMinChunk, 1);
-  x->beside_decode = per_chunk <= kPrefixSms ? 1 : 0;
+  // a pass of some length that is one CTA for each SM runs beside the decode
+  // kernel, one CTA of each on an SM (8192 tokens before 128 sequences: 79 us, 83
+  // with both at full width; 16 sequences: 26 and 31; but 1024 tokens: 70 and 67)
+  x->beside_decode = per_chunk <= kPrefixSms && x->max_prefix_len >= kBesideTokens ? 1 : 0;
   long long best = 1;
-  if (x->beside_decode) {
+  if (per_chunk <= kPrefixSms) {
     best = std::min(most, kPrefixSms / std::max(per_chunk, 1ll));
   } else {
     // more CTAs than SMs whatever the chunk: two on each SM at a time, in the

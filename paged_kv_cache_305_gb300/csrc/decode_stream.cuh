@@ -80,24 +80,25 @@ enum : int { kFirst = 1, kLast = 2, kEnd = 4 };  // of the segment; of all work
 template <int D, bool FP8, int NT>
 struct Ring {
   using T = Tile<D, FP8>;
-  static constexpr int kHalf = kWarps * T::kBytes;       // K (or V) of a stage
-  static constexpr int kStages = 65536 / (2 * kHalf);
-  static constexpr int kScaleBytes = kWarps * 64;        // exponent bytes of a stage
+  static constexpr int kHalf = kWarps * T::kBytes;   // K (or V) of a stage
+  static constexpr int kStages = 65536 / (2 * kHalf);  // three CTAs on an SM
+  static constexpr int kMost = FP8 ? kStages : kStages * 3 / 2;  // one, beside one of the prefix pass
+  static constexpr int kScaleBytes = kWarps * 64;      // exponent bytes of a stage
   static constexpr int kHeads = NT * 8;
   static constexpr int kOStride = D + 4;
-  // offsets in shared memory
-  static constexpr int kScales = kStages * 2 * kHalf;
+  // offsets in shared memory; the stages follow the rest
+  static constexpr int kScales = 0;
   static constexpr int kNotes = kScales + (FP8 ? kStages * kScaleBytes : 0);
-  static constexpr int kBars = kNotes + kStages * static_cast<int>(sizeof(Note));  // full, empty, joins
-  static constexpr int kStats = kBars + (2 * kStages + kWarps) * 8;  // [warp][m, l, r][head]
-  static constexpr int kBase = kStats + kWarps * 3 * kHeads * 4;     // [kChunks]
+  static constexpr int kBars = kNotes + kMost * static_cast<int>(sizeof(Note));  // full, empty, joins
+  static constexpr int kStats = kBars + (2 * kMost + kWarps) * 8;  // [warp][m, l, r][head]
+  static constexpr int kBase = kStats + kWarps * 3 * kHeads * 4;   // [kChunks]
   static constexpr int kMisc = kBase + kChunks * 4;
-  static constexpr int kJoin = (kMisc + 32 + 15) / 16 * 16;          // [warp][head][kOStride]
+  static constexpr int kJoin = (kMisc + 32 + 15) / 16 * 16;        // [warp][head][kOStride]
   static constexpr int kSlots = kJoin + kWarps * kJoinHeads * kOStride * 4;  // ROWS: [stage][token]
-  static constexpr int kBytes = kSlots;
-  static constexpr int kRowsBytes = kSlots + kStages * kWarps * T::kTokens * 4;
+  template <bool ROWS>
+  static constexpr int kFixed = (kSlots + (ROWS ? kMost * kWarps * T::kTokens * 4 : 0) + 1023) / 1024 * 1024;
   static_assert(kStages >= 2, "a stage lands while another is computed");
-  static_assert(kStats % 8 == 0 && kBars % 8 == 0 && kNotes % 16 == 0, "alignment");
+  static_assert(NT > 1 || 3 * (kFixed<true> + 65536 + 1024) <= 228 * 1024, "three CTAs on an SM");
 };
 
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
@@ -120,7 +121,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   using R = Ring<D, FP8, NT>;
   using Geo = Tile<D, FP8>;
   using T = typename Ty::T;
-  constexpr int kTT = Geo::kTokens, kStages = R::kStages, kRB = Geo::kRowBytes;
+  constexpr int kTT = Geo::kTokens, kRB = Geo::kRowBytes;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -137,10 +138,21 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   unsigned* sBase = reinterpret_cast<unsigned*>(smem + R::kBase);
   [[maybe_unused]] uint32_t* slots = reinterpret_cast<uint32_t*>(smem + R::kSlots);
   constexpr uint32_t kNone = 0xffffffffu, kBad = 0xfffffffeu;  // in the place of a slot
-  const uint32_t ring = smem_u32(smem), bars = smem_u32(smem + R::kBars);
-  auto full = [&](uint32_t st) { return bars + 8 * st; };
-  auto empty = [&](uint32_t st) { return bars + 8 * (kStages + st); };
-  auto join_bar = [&](int h) { return bars + 8 * (2 * kStages + h); };
+  const uint32_t ring = smem_u32(smem) + R::template kFixed<ROWS>, bars = smem_u32(smem + R::kBars);
+  auto full = [&](int st) { return bars + 8 * st; };
+  auto empty = [&](int st) { return bars + 8 * (R::kMost + st); };
+  auto join_bar = [&](int h) { return bars + 8 * (2 * R::kMost + h); };
+  // a place in the ring: the stage, and the parity of its round
+  struct Place {
+    int st = 0;
+    uint32_t round = 0;
+  };
+  auto step = [&](Place& p) {
+    if (++p.st == a.stages) {
+      p.st = 0;
+      p.round ^= 1;
+    }
+  };
   // bounded wait of a warp; false once any wait of the CTA has given up
   volatile int* aborted = &misc.abort;
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -153,7 +165,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   };
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < a.stages; ++i) {
       tc::mbar_init(full(i), 1);
       tc::mbar_init(empty(i), kWarps);
     }
@@ -215,7 +227,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     // ======================= the feeding warp ==================================
     const int bt = ROWS ? 1 : lb;  // tokens a lane's table entry stands for
     constexpr int kPer = ROWS ? 4 : 1;  // entries of a lane: tokens lane, lane + 32, .. (at most 128)
-    uint32_t filled = 0;  // stages
+    Place to;              // the stage to fill next
+    int filled = 0;        // stages, up to the ring's number
     bool ok = true;
 
     // what a lane knows of a stage: the slots of its blocks (ROWS: tokens); kNone:
@@ -241,15 +254,13 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       }
       return ids;
     };
-    // the next stage, free to be filled
-    auto next_stage = [&]() {
-      const uint32_t st = filled % kStages;
-      if (filled >= kStages && ok) ok = *aborted == 0 && wait(empty(st), (filled / kStages - 1) & 1);
-      return st;
+    auto wait_empty = [&]() {  // emptied as often as it was filled
+      if (filled == a.stages && ok) ok = *aborted == 0 && wait(empty(to.st), to.round ^ 1);
     };
     auto fill = [&](const Note& note, const Ids& ids) {
-      const uint32_t st = next_stage();
+      wait_empty();
       if (!ok) return;
+      const int st = to.st;
       const uint32_t sk = ring + st * 2 * R::kHalf, sv = sk + R::kHalf;
       unsigned char* se = smem + R::kScales + st * R::kScaleBytes;
       const int h0 = note.hg * Hc;
@@ -290,16 +301,17 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if constexpr (FP8) {
             const uint8_t* e = a.scales + ((static_cast<size_t>(id >> shift) * Hkv + h0) * 2 << shift) +
                                (id & ((1u << shift) - 1));
-            const uint32_t to = smem_u32(se) + lane * Hc * 2 * bt;
+            const uint32_t dst = smem_u32(se) + lane * Hc * 2 * bt;
             if (bt == 1 << shift) {
-              tc::bulk_load(to, e, Hc * 2 * bt, full(st));
+              tc::bulk_load(dst, e, Hc * 2 * bt, full(st));
             } else {  // part of a block: K's and V's of each head
-              for (int i = 0; i < 2 * Hc; ++i) tc::bulk_load(to + i * bt, e + (i << shift), bt, full(st));
+              for (int i = 0; i < 2 * Hc; ++i) tc::bulk_load(dst + i * bt, e + (i << shift), bt, full(st));
             }
           }
         }
       }
-      ++filled;
+      step(to);
+      filled = min(filled + 1, a.stages);
     };
 
     // the CTA's share of the line; where rows are not cut, the rows that start in it
@@ -404,16 +416,16 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         s = (s + 32) % S;
       }
     }
+    wait_empty();
     if (ok) {  // the end of all work
-      const uint32_t st = next_stage();
-      if (ok) {
-        if (lane == 0) notes[st].flags = kEnd;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(full(st));
+      if (lane == 0) notes[to.st].flags = kEnd;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(full(to.st));
+    } else {  // what was issued must land before the CTA ends: the stages' latest rounds
+      for (int i = 0; i < filled; ++i) {
+        const int st = (to.st + a.stages - filled + i) % a.stages;
+        tc::mbar_wait(full(st), to.round ^ (st >= to.st ? 1u : 0u));
       }
-    } else {  // what was issued must land before the CTA ends
-      for (uint32_t i = filled - min(filled, static_cast<uint32_t>(kStages)); i != filled; ++i)
-        tc::mbar_wait(full(i % kStages), (i / kStages) & 1);
     }
   } else {
     // ======================= the computing warps ================================
@@ -443,9 +455,9 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     // waits for stage n and reads its note. ROWS: begins the copies of this warp's
     // tile, rows that do not count as zeros, and reads its token's exponents.
     [[maybe_unused]] int ek = 0, ev = 0;
-    auto take = [&](uint32_t n) {
-      const uint32_t stage = n % kStages;
-      ok = *aborted == 0 && wait(full(stage), (n / kStages) & 1);
+    auto take = [&](const Place& p) {
+      const int stage = p.st;
+      ok = *aborted == 0 && wait(full(stage), p.round);
       Note note = notes[stage];
       if (!ok) note.flags = kEnd;
       if constexpr (ROWS) {
@@ -479,10 +491,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       }
       return note;
     };
+    Place at, at_ahead;
     [[maybe_unused]] Note ahead;
-    if constexpr (ROWS) ahead = take(0);
-    for (uint32_t n = 0;; ++n) {
-      const uint32_t stage = n % kStages;
+    if constexpr (ROWS) ahead = take(at_ahead);
+    for (;; step(at)) {
+      const int stage = at.st;
       Note note;
       [[maybe_unused]] int my_ek = 0, my_ev = 0;
       if constexpr (ROWS) {
@@ -490,11 +503,12 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         if (note.flags & kEnd) break;
         my_ek = ek;
         my_ev = ev;
-        ahead = take(n + 1);
+        step(at_ahead);
+        ahead = take(at_ahead);
         cp_async_wait<1>();
         __syncwarp();
       } else {
-        note = take(n);
+        note = take(at);
         if (note.flags & kEnd) break;
       }
       if (note.flags & kFirst) {
@@ -783,9 +797,13 @@ struct Dependent {
 template <typename Ty, int D, int NT, bool FP8, bool ROWS, bool SPLIT>
 cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   using R = Ring<D, FP8, NT>;
-  constexpr int kSmem = ROWS ? R::kRowsBytes : R::kBytes;
+  // beside the prefix pass one CTA on each SM, with a longer ring; else three (two)
+  const bool beside = !FP8 && a.groups.max_chunks > 0 && a.groups.beside_decode != 0;
+  a.stages = beside ? R::kMost : R::kStages;
+  const int smem = R::template kFixed<ROWS> + a.stages * 2 * R::kHalf;
   auto kern = paged_stream_kernel<Ty, D, NT, FP8, ROWS, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       R::template kFixed<ROWS> + R::kMost * 2 * R::kHalf);
   if (e != cudaSuccess) return e;
   CUtensorMap km{}, vm{};
   if constexpr (!ROWS) {
@@ -796,11 +814,11 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
         !encode_pool_map(&vm, a.value_cache, slots, a.num_kv_heads, row_bytes, rows, a.heads_at_a_time))
       return cudaErrorInvalidValue;
   }
-  const long long ctas = std::min((NT == 1 ? 3 : 2) * num_sms, kMaxCtas);
+  const long long ctas = std::min((beside ? 1 : NT == 1 ? 3 : 2) * num_sms, kMaxCtas);
   const long long rows = static_cast<long long>(a.num_seqs) * (a.num_kv_heads / a.heads_at_a_time);
   const long long most = (static_cast<long long>(a.max_blocks_per_seq) << a.block_shift) / Tile<D, FP8>::kTokens + 2;
   const long long grid = std::min(ctas, rows * (a.cut ? (most + a.least_tiles - 1) / a.least_tiles : 1));
-  Dependent d(dim3(static_cast<unsigned>(std::max(grid, 1ll))), kThreads, kSmem, stream,
+  Dependent d(dim3(static_cast<unsigned>(std::max(grid, 1ll))), kThreads, smem, stream,
               a.groups.max_chunks > 0);  // behind a prefix pass
   e = cudaLaunchKernelEx(&d.cfg, kern, km, vm, a);
   if (e != cudaSuccess || a.ws_rows == nullptr) return e;  // rows are whole, and there is no prefix

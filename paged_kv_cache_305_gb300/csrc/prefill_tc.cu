@@ -93,9 +93,6 @@ struct TcGeo {
   // (2 x 256 tensor-memory columns) share an SM
   static constexpr int kSmem = kBarOff + 128 + 1024 > 80 * 1024 ? kBarOff + 128 + 1024 : 80 * 1024;
 };
-// Prefix pass beside the decode kernel: more than half of an SM's 228 KB, so
-// that one CTA of the pass and one of the decode kernel (under 104 KB) share it.
-constexpr int kBesideSmem = 118 * 1024;
 static_assert(kStages == 2, "stage and S buffer of tile j are both j & 1");
 
 // barrier slots (8 bytes each) after the tiles
@@ -797,17 +794,19 @@ cudaError_t launch_kernel(const CUtensorMap& km, const CUtensorMap& vm,
                           const std::conditional_t<PREFIX, PrefixPassArgs, PrefillArgs>& a, dim3 grid,
                           bool after_convert, cudaStream_t stream) {
   auto kern = paged_prefill_tc_kernel<Ty, D, SINGLE, PREFIX>;
-  int smem = TcGeo<D>::kSmem, most = smem;
+  constexpr int kSmem = TcGeo<D>::kSmem;
   if constexpr (PREFIX) {
-    most = std::max(smem, kBesideSmem);
-    if (a.groups.beside_decode) smem = most;
+    // the SM's whole shared memory, so that the decode kernel's CTAs find room in it
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
   }
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
