@@ -802,8 +802,11 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   a.stages = beside ? R::kMost : R::kStages;
   const int smem = R::template kFixed<ROWS> + a.stages * 2 * R::kHalf;
   auto kern = paged_stream_kernel<Ty, D, NT, FP8, ROWS, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       R::template kFixed<ROWS> + R::kMost * 2 * R::kHalf);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_context(done, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                R::template kFixed<ROWS> + R::kMost * 2 * R::kHalf);
+  });
   if (e != cudaSuccess) return e;
   CUtensorMap km{}, vm{};
   if constexpr (!ROWS) {

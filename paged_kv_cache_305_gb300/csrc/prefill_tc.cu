@@ -794,19 +794,21 @@ cudaError_t launch_kernel(const CUtensorMap& km, const CUtensorMap& vm,
                           const std::conditional_t<PREFIX, PrefixPassArgs, PrefillArgs>& a, dim3 grid,
                           bool after_convert, cudaStream_t stream) {
   auto kern = paged_prefill_tc_kernel<Ty, D, SINGLE, PREFIX>;
-  constexpr int kSmem = TcGeo<D>::kSmem;
-  if constexpr (PREFIX) {
-    // the SM's whole shared memory, so that the decode kernel's CTAs find room in it
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
-  }
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = once_per_context(done, [&] {
+    if constexpr (PREFIX) {
+      // the SM's whole shared memory, so that the decode kernel's CTAs find room in it
+      cudaError_t c = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                           cudaSharedmemCarveoutMaxShared);
+      if (c != cudaSuccess) return c;
+    }
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcGeo<D>::kSmem);
+  });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = TcGeo<D>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -443,10 +443,30 @@ def _need_fp8_pool(key_cache: torch.Tensor, value_cache: torch.Tensor,
           "cache_scales must be uint8 [num_blocks, num_kv_heads, 2, block_size]")
 
 
-def _need_same_device(first: torch.Tensor, *rest: torch.Tensor) -> None:
-    for t in (first,) + rest:
-        _need(t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors")
-        _need(t.device == first.device, "tensors must be on one device")
+def _device_of(*tensors: torch.Tensor) -> int:
+    """The CUDA device that all of these contiguous tensors are on."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != index:
+            raise ValueError("tensors must be on one device")
+        if index < 0 or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors")
+    return index
+
+
+def _enqueue(entry, device: int, stream, *args) -> None:
+    """Calls a library entry on `device`, with its current stream unless one is given."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == device:
+        rc = entry(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = entry(*args, raw)
+    if rc != 0:
+        raise PagedAttnError(rc, last_error())
 
 
 def alloc_fp8_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device="cuda"):
@@ -469,35 +489,29 @@ def reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, key_cache: tor
     distinct.
     """
     _need_fp8_pool(key_cache, value_cache, cache_scales)
-    _need_same_device(key, value, key_cache, value_cache, cache_scales, slot_mapping)
+    device = _device_of(key, value, key_cache, value_cache, cache_scales, slot_mapping)
     NB, B, Hkv, d = key_cache.shape
     T = key.shape[0]
     _need(key.shape == (T, Hkv, d) and value.shape == (T, Hkv, d), "key/value shape mismatch")
     _need(key.dtype == value.dtype, "dtype mismatch")
     _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,),
           "slot_mapping must be int64 [num_tokens]")
-    code = _dtype_code(key)
-    L = load_library()
-    with torch.cuda.device(key.device):
-        _check(L.pa_reshape_and_cache_fp8(key.data_ptr(), value.data_ptr(), key_cache.data_ptr(),
-                                          value_cache.data_ptr(), cache_scales.data_ptr(),
-                                          slot_mapping.data_ptr(), T, Hkv, d, B, NB, code,
-                                          _stream(key, stream)))
+    _enqueue(load_library().pa_reshape_and_cache_fp8, device, stream, key.data_ptr(), value.data_ptr(),
+             key_cache.data_ptr(), value_cache.data_ptr(), cache_scales.data_ptr(),
+             slot_mapping.data_ptr(), T, Hkv, d, B, NB, _dtype_code(key))
 
 
 def copy_blocks_fp8(key_cache: torch.Tensor, value_cache: torch.Tensor, cache_scales: torch.Tensor,
                     src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """:func:`copy_blocks` for an 8-bit pool (codes and exponent bytes)."""
     _need_fp8_pool(key_cache, value_cache, cache_scales)
-    _need_same_device(key_cache, value_cache, cache_scales, src, dst)
+    device = _device_of(key_cache, value_cache, cache_scales, src, dst)
     _need(src.dtype == torch.int32 and dst.dtype == torch.int32 and src.shape == dst.shape
           and src.dim() == 1, "src/dst must be 1-D int32 tensors")
     NB, B, Hkv, d = key_cache.shape
-    L = load_library()
-    with torch.cuda.device(key_cache.device):
-        _check(L.pa_copy_blocks_fp8(key_cache.data_ptr(), value_cache.data_ptr(),
-                                    cache_scales.data_ptr(), src.data_ptr(), dst.data_ptr(),
-                                    src.numel(), Hkv, d, B, NB, _stream(key_cache, stream)))
+    _enqueue(load_library().pa_copy_blocks_fp8, device, stream, key_cache.data_ptr(),
+             value_cache.data_ptr(), cache_scales.data_ptr(), src.data_ptr(), dst.data_ptr(),
+             src.shape[0], Hkv, d, B, NB)
 
 
 def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: torch.Tensor,
@@ -512,8 +526,8 @@ def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: 
     viewed as [rows / B, B, Hkv, d], are pools for :func:`prefill`.
     """
     _need_fp8_pool(key_cache, value_cache, cache_scales)
-    _need_same_device(key_out, value_out, key_cache, value_cache, cache_scales, block_tables,
-                      seq_lens, out_start)
+    device = _device_of(key_out, value_out, key_cache, value_cache, cache_scales, block_tables,
+                        seq_lens, out_start)
     NB, B, Hkv, d = key_cache.shape
     _need(key_out.dim() == 3 and key_out.shape[1:] == (Hkv, d) and value_out.shape == key_out.shape
           and key_out.dtype == value_out.dtype, "key_out/value_out dtype or shape mismatch")
@@ -523,32 +537,29 @@ def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: 
     _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
           "block_tables/seq_lens shape mismatch")
     _need(out_start.dtype == torch.int64 and out_start.shape == (S,), "out_start must be int64 [num_seqs]")
-    code = _dtype_code(key_out)
-    L = load_library()
-    with torch.cuda.device(key_cache.device):
-        _check(L.pa_gather_cache_fp8(key_out.data_ptr(), value_out.data_ptr(), key_cache.data_ptr(),
-                                     value_cache.data_ptr(), cache_scales.data_ptr(),
-                                     block_tables.data_ptr(), seq_lens.data_ptr(),
-                                     out_start.data_ptr(), key_out.shape[0], S, Hkv, d, B,
-                                     block_tables.shape[1], NB, code, _stream(key_cache, stream)))
+    _enqueue(load_library().pa_gather_cache_fp8, device, stream, key_out.data_ptr(),
+             value_out.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+             cache_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+             out_start.data_ptr(), key_out.shape[0], S, Hkv, d, B, block_tables.shape[1], NB,
+             _dtype_code(key_out))
 
 
 def _need_decode(out: torch.Tensor, query: torch.Tensor, head_dim: int, block_tables: torch.Tensor,
-                 seq_lens: torch.Tensor, workspace: Optional[torch.Tensor]):
-    """The checks of decode calls; returns (out dtype code, workspace pointer, workspace bytes)."""
+                 seq_lens: torch.Tensor, workspace: Optional[torch.Tensor], *others: torch.Tensor):
+    """The checks of decode calls; returns (device, out dtype code, workspace pointer and bytes)."""
     _need(query.dim() == 3 and query.shape[2] == head_dim, "cache shape mismatch")
     _need(out.shape == query.shape and out.dtype in (query.dtype, torch.float32),
           "out dtype or shape mismatch")
-    S = query.shape[0]
     _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32,
           "block_tables and seq_lens must be int32")
+    S = query.shape[0]
     _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
           "block_tables/seq_lens shape mismatch")
     code = PA_FLOAT32 if out.dtype == torch.float32 else _dtype_code(query)
     if workspace is None:
-        return code, 0, 0
-    _need_same_device(query, workspace)
-    return code, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        return _device_of(query, out, block_tables, seq_lens, *others), code, 0, 0
+    device = _device_of(query, out, block_tables, seq_lens, workspace, *others)
+    return device, code, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -562,16 +573,13 @@ def decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
     """
     _need_fp8_pool(key_cache, value_cache, cache_scales)
     NB, B, Hkv, d = key_cache.shape
-    odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace)
-    _need_same_device(out, query, key_cache, value_cache, cache_scales, block_tables, seq_lens)
+    device, odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace,
+                                                 key_cache, value_cache, cache_scales)
     S, Hq, _ = query.shape
-    L = load_library()
-    with torch.cuda.device(query.device):
-        _check(L.pa_decode_fp8(out.data_ptr(), query.data_ptr(), key_cache.data_ptr(),
-                               value_cache.data_ptr(), cache_scales.data_ptr(),
-                               block_tables.data_ptr(), seq_lens.data_ptr(), S, Hq, Hkv, d, B,
-                               float(scale), block_tables.shape[1], NB, partition_tokens,
-                               _dtype_code(query), odt, ws_ptr, ws_bytes, _stream(query, stream)))
+    _enqueue(load_library().pa_decode_fp8, device, stream, out.data_ptr(), query.data_ptr(),
+             key_cache.data_ptr(), value_cache.data_ptr(), cache_scales.data_ptr(),
+             block_tables.data_ptr(), seq_lens.data_ptr(), S, Hq, Hkv, d, B, float(scale),
+             block_tables.shape[1], NB, int(partition_tokens), _dtype_code(query), odt, ws_ptr, ws_bytes)
     return out
 
 
@@ -612,24 +620,19 @@ def decode_shared_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torc
     NB, B, Hkv, d = key_cache.shape
     _need(value_cache.shape == key_cache.shape, "cache shape mismatch")
     _need(query.dtype == key_cache.dtype == value_cache.dtype, "query/cache dtype mismatch")
-    odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace)
     _need(group_start.dtype == torch.int32 and prefix_lens.dtype == torch.int32,
           "group_start and prefix_lens must be int32")
     _need(prefix_lens.dim() == 1 and group_start.shape == (prefix_lens.shape[0] + 1,),
           "group_start/prefix_lens shape mismatch")
-    _need_same_device(out, query, key_cache, value_cache, block_tables, seq_lens, group_start,
-                      prefix_lens)
+    device, odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace,
+                                                 key_cache, value_cache, group_start, prefix_lens)
     S, Hq, _ = query.shape
-    L = load_library()
-    with torch.cuda.device(query.device):
-        _check(L.pa_decode_shared_prefix(out.data_ptr(), query.data_ptr(), key_cache.data_ptr(),
-                                         value_cache.data_ptr(), block_tables.data_ptr(),
-                                         seq_lens.data_ptr(), group_start.data_ptr(),
-                                         prefix_lens.data_ptr(), S, prefix_lens.shape[0], Hq, Hkv, d,
-                                         B, float(scale), block_tables.shape[1], NB,
-                                         int(max_prefix_len), int(max_group_size),
-                                         _dtype_code(query), odt, ws_ptr, ws_bytes,
-                                         _stream(query, stream)))
+    _enqueue(load_library().pa_decode_shared_prefix, device, stream, out.data_ptr(),
+             query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+             block_tables.data_ptr(), seq_lens.data_ptr(), group_start.data_ptr(),
+             prefix_lens.data_ptr(), S, prefix_lens.shape[0], Hq, Hkv, d, B, float(scale),
+             block_tables.shape[1], NB, int(max_prefix_len), int(max_group_size),
+             _dtype_code(query), odt, ws_ptr, ws_bytes)
     return out
 
 
