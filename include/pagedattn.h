@@ -354,14 +354,20 @@ int pa_gather_cache_fp8(void* key_out, void* value_out,
  * (and of out, unless that is fp32). Arithmetic is fp32 around fp16 products of
  * the exact codes: the query enters as its fp16 value (bf16: scaled by a power
  * of two for each head, so that its bits are kept), softmax weights, times V's
- * factors, as the sum of two fp16 parts.
+ * factors, as the sum of two fp16 parts relative to the largest factor so far:
+ * the error is 2^-20 of the largest weighted V, so what V rows 2^20 times
+ * smaller add to it may be lost.
  * Work is cut into equal shares, inside rows as it comes (shares are not under
  * partition_tokens tokens where that is given; 0 = the default), and a second
  * kernel joins a row's pieces in order; where they are cut depends on the lengths
  * and the sizes alone. workspace: pa_decode_fp8_workspace_bytes(...) bytes; its
  * contents need no initialisation, and calls that share it must not overlap on
- * the GPU (pa_decode may use it in between). num_seqs *
- * num_kv_heads * max_blocks_per_seq * block_size / 32 must be below 2^31.
+ * the GPU. Eager calls of pa_decode may use it in between; but a replayed graph
+ * that holds this call leaves it as no pa_decode expects it, and a captured
+ * pa_decode does not expect what this call leaves: give graphs of the two
+ * workspaces of their own (or zero it in between). num_seqs * num_kv_heads *
+ * (max_blocks_per_seq * block_size / 32 + 2) must be below 2^31. A wait for
+ * a copy that gives up is counted (pa_wait_timeout_count).
  * Other arguments, sizes and errors as for pa_decode.
  */
 int pa_decode_fp8(void* out, const void* query,
@@ -403,9 +409,11 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
  * table. If group_start decreases, outputs are unspecified (nothing outside
  * the arrays is touched).
  * num_groups in [1, 65535] (unless num_seqs is 0), num_blocks * block_size
- * and num_seqs * num_kv_heads * max_blocks_per_seq * block_size / 16 below 2^31. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
- * which need no initialisation; calls that share it must not overlap on the GPU.
- * Arithmetic, other arguments and errors as for pa_decode.
+ * and num_seqs * num_kv_heads * (max_blocks_per_seq * block_size / 16 + 2)
+ * below 2^31. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
+ * shared with other calls as pa_decode_fp8's. Softmax weights enter as the sum
+ * of two parts of the cache's type; waits that give up are counted as there.
+ * Other arguments and errors as for pa_decode.
  */
 int pa_decode_shared_prefix(void* out, const void* query,
                             const void* key_cache, const void* value_cache,

@@ -194,7 +194,7 @@ size_t prefill_v16_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_b
   return round_up(static_cast<size_t>(slots) * num_kv_heads * head_dim * 2, 256);
 }
 
-// How the prefix pass cuts the prefix: a CTA takes one chunk of tokens for 128
+// How the prefix pass cuts the prefix (x->num_seqs is set): a CTA takes one chunk of tokens for 128
 // rows (members x query heads) of a group and a kv head, and leaves an fp32
 // piece of each row behind. Chunks are whole 64-token tiles, at least
 // kPrefixMinChunk long.
@@ -203,7 +203,8 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   x->max_prefix_len = std::min(max_prefix_len, lmax);
   x->max_group_size = max_group_size;
   const int members = std::max(kPrefixRows / std::max(group, 1), 1);
-  const long long tiles = (static_cast<long long>(max_group_size) + members - 1) / members;
+  const long long largest = std::min(max_group_size, x->num_seqs);
+  const long long tiles = (largest + members - 1) / members;
   const long long per_chunk = tiles * num_groups * num_kv_heads;
   const long long most = std::max(x->max_prefix_len / kPrefixMinChunk, 1);
   // a pass of some length that is one CTA for each SM runs beside the decode
@@ -987,6 +988,7 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
       max_prefix_len < 0 || max_group_size < 0 || lmax > 0x7fffffffll)
     return 0;
   pa::PrefixArgs x{};
+  x.num_seqs = num_seqs;
   pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads, static_cast<int>(lmax),
                   max_prefix_len, max_group_size);
   return pa::stream_layout(false, num_seqs, num_q_heads, num_kv_heads, head_dim, lmax, x)

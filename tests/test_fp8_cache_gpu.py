@@ -408,6 +408,89 @@ def test_write_and_decode_in_a_captured_graph_on_another_stream():
     assert torch.isfinite(want).all()
 
 
+# wide tables: neighbouring kv heads are taken 4 and 2 at a time
+GROUPED = [
+    # dtype, d, Hq, Hkv, B, lengths, table tokens
+    ("bf16", 128, 32, 8, 16, [900, 33, 0, 1, 257, 64], 19456),
+    ("fp16", 64, 12, 12, 8, [31, 700, 5, 64, 65], 16384),
+    ("bf16", 128, 42, 6, 64, [1500, 1, 129, 0, 63, 64, 300], 11264),
+    ("fp16", 64, 24, 2, 32, [40, 1030, 96, 513], 58880),
+    ("bf16", 128, 16, 4, 4, [333, 20, 0, 129, 77, 3, 64, 65], 29184),
+    ("fp16", 64, 4, 2, 1, [50, 260, 31, 33], 58880),
+]
+
+
+@pytest.mark.parametrize("idx", range(len(GROUPED)))
+def test_decode_with_neighbouring_heads_together(idx):
+    dtype, d, Hq, Hkv, B, lens, width = GROUPED[idx]
+    rng = np.random.default_rng(100 + idx)
+    NB = sum(-(-n // B) for n in lens) + 3
+    kc, vc, sc = random_pool(rng, NB, B, Hkv, d)
+    bt = tables_for(rng, lens, B, NB, MB=width // B)
+    query = W.normal_bits((len(lens), Hq, d), dtype, 100 + idx, 2)
+    check_decode(query, kc, vc, sc, bt, lens, B, 1 / np.sqrt(d), dtype, what=str(GROUPED[idx][:5]))
+
+
+def test_decode_workspace_may_hold_anything():
+    rng = np.random.default_rng(21)
+    lens, B, Hkv, d = [2000, 1, 0, 513, 1024], 16, 2, 128
+    kc, vc, sc = random_pool(rng, 300, B, Hkv, d)
+    bt = tables_for(rng, lens, B, 300)
+    query = W.normal_bits((5, 8, d), "bf16", 21, 2)
+    n = pa.decode_fp8_workspace_bytes(5, 8, Hkv, d, bt.shape[1], B)
+    first = None
+    for byte in (0, 0xFF, 0x7F, 0x80):
+        ws = torch.full((n,), byte, dtype=torch.uint8, device="cuda")
+        o = check_decode(query, kc, vc, sc, bt, lens, B, 0.09, "bf16", ws=ws)
+        first = o if first is None else first
+        assert torch.equal(o, first)
+
+
+def test_two_captured_graphs_on_one_workspace():
+    rng = np.random.default_rng(22)
+    B, Hkv, d = 16, 2, 64
+    kc, vc, sc = random_pool(rng, 200, B, Hkv, d)
+    kd, vd, sd = up8(kc), up8(vc), up(sc)
+    made = []
+    ws = torch.full((1 << 22,), 0x5A, dtype=torch.uint8, device="cuda")
+    for lens in ([1500, 40, 700], [1100, 0]):
+        bt = tables_for(rng, lens, B, 200)
+        q = dev_bits(W.normal_bits((len(lens), 8, d), "fp16", 22, len(lens)), "fp16")
+        out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+        args = (out, q, kd, vd, sd, up(bt), up(np.array(lens, np.int32)), 0.125, 0, ws)
+        pa.decode_fp8(*args)
+        want = out.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pa.decode_fp8(*args)
+        made.append((g, out, want, args))
+    for _ in range(3):
+        for g, out, want, _ in made:
+            out.fill_(float("nan"))
+            g.replay()
+            assert torch.equal(out, want)
+
+
+def test_calls_on_two_streams_at_once():
+    rng = np.random.default_rng(23)
+    B, Hkv, d, lens = 16, 2, 128, [3000, 900, 2500]
+    kc, vc, sc = random_pool(rng, 450, B, Hkv, d)
+    bt = tables_for(rng, lens, B, 450)
+    q = dev_bits(W.normal_bits((3, 8, d), "bf16", 23, 2), "bf16")
+    kd, vd, sd, btd, sl = up8(kc), up8(vc), up(sc), up(bt), up(np.array(lens, np.int32))
+    want = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    pa.decode_fp8(want, q, kd, vd, sd, btd, sl, 0.09, 0, pa.alloc_workspace(q, kd, btd))
+    outs = [torch.empty_like(want) for _ in range(2)]
+    spaces = [pa.alloc_workspace(q, kd, btd) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for o, w, st in zip(outs, spaces, streams):
+            pa.decode_fp8(o, q, kd, vd, sd, btd, sl, 0.09, 0, w, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
 # ------------------------------------------------------------ all together --
 @pytest.mark.parametrize("dtype,B,Hq,Hkv,d", [("bf16", 16, 8, 2, 128), ("fp16", 8, 4, 4, 64), ("bf16", 2, 6, 3, 64)])
 def test_serving_loop_on_an_8_bit_pool(dtype, B, Hq, Hkv, d):

@@ -178,6 +178,36 @@ def test_shared_prefix_refusals(lib, kw, code, msg):
     assert msg in pa.last_error()
 
 
+def test_decode_workspace_holds_the_pieces_where_rows_may_be_cut(lib):
+    f = pa.decode_fp8_workspace_bytes
+    assert f(8, 8, 2, 128, 32, 16) == 0 and f(8, 8, 2, 128, 512, 1) == 0  # 512 tokens: rows stay whole
+    a = f(8, 8, 2, 128, 33, 16)
+    assert a > 0 and f(16, 8, 2, 128, 33, 16) > a and f(8, 16, 2, 128, 33, 16) > a
+    for bad in [(-1, 8, 2, 128, 64, 16), (8, 0, 2, 128, 64, 16), (8, 8, 0, 128, 64, 16), (8, 8, 3, 128, 64, 16),
+                (8, 8, 2, 96, 64, 16), (8, 8, 2, 128, 0, 16), (8, 8, 2, 128, 64, 12)]:
+        assert f(*bad) == 0
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(pt=-16), -1, "partition_tokens"), (dict(pt=32, B=64), -1, "partition_tokens"),
+    (dict(pt=1 << 30), -2, "partition_tokens"), (dict(S=65536), -2, "65535"), (dict(Hq=65536, Hkv=65536), -2, "65535"),
+    (dict(MB=1 << 28), -2, "overflows"), (dict(S=65535, Hq=4096, Hkv=4096, MB=100), -2, "too large"),
+    (dict(MB=0), -1, "max_blocks_per_seq"), (dict(NB=0), -1, "num_blocks"), (dict(bt=FAKE + 2), -1, "aligned"),
+])
+def test_decode_refusals_of_sizes(lib, kw, code, msg):
+    assert _decode(lib, **kw) == code
+    assert msg in pa.last_error()
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(S=65536), -2, "65535"), (dict(MB=1 << 28), -2, "overflows"),
+    (dict(S=65535, Hq=2048, Hkv=2048, MB=100), -2, "too large"), (dict(gs=FAKE + 1), -1, "aligned"),
+])
+def test_shared_prefix_refusals_of_sizes(lib, kw, code, msg):
+    assert _prefix(lib, **kw) == code
+    assert msg in pa.last_error()
+
+
 def test_shared_prefix_workspace_grows_with_what_it_holds(lib):
     f = pa.decode_shared_prefix_workspace_bytes
     a = f(8, 1, 8, 2, 128, 64, 16, 512, 8)

@@ -123,6 +123,46 @@ def test_grid(idx):
     assert np.array_equal(host_bits(o16), want)
 
 
+# a long pass beside the decode kernel, and neighbouring heads of the suffixes together
+LONG = [
+    # dtype, d, Hq, Hkv, B, group starts, prefixes, lengths, table tokens
+    ("bf16", 128, 8, 2, 16, [0, 5], [2100], [2100, 2101, 2200, 2731, 2115], None),
+    ("fp16", 64, 16, 2, 64, [0, 2, 6], [2300, 2048], [2301, 2400, 2048, 2050, 2111, 2600], None),
+    ("fp16", 128, 4, 4, 4, [0, 3], [2050], [2051, 2300, 2099], None),
+    ("bf16", 128, 8, 8, 16, [0, 4, 6], [300, 40], [301, 400, 555, 300, 41, 99], 20480),
+    ("fp16", 64, 24, 6, 8, [0, 6], [100], [100, 101, 340, 163, 164, 229], 8192),
+    ("bf16", 64, 20, 2, 16, [0, 4], [64], [64, 100, 399, 80], 32768),
+    ("bf16", 128, 4, 4, 2, [0, 4, 8], [33, 5], [34, 90, 129, 33, 5, 6, 70, 200], 16384),
+    # a long prefix of a large table, with both
+    ("fp16", 64, 8, 4, 16, [0, 7], [2500], [2500 + 33 * i for i in range(7)], 20480),
+]
+
+
+@pytest.mark.parametrize("idx", range(len(LONG)))
+def test_long_prefixes_and_wide_tables(idx):
+    *sizes, width = LONG[idx]
+    case = Case(*sizes, seed=50 + idx, MB=width // sizes[4] if width else None)
+    pa.bad_index_count(clear=True)
+    out = case.run()
+    assert pa.bad_index_count(clear=True) == 0
+    case.check(out, what=str(sizes[:5]))
+    # the bounds given size the grid and the cuts, never what is computed
+    case.check(case.run(max_prefix=case.max_prefix + 1000, max_group=10 ** 6), what=str(sizes[:5]))
+    assert pa.bad_index_count(clear=True) == 0
+
+
+def test_workspace_may_hold_anything():
+    case = Case("bf16", 128, 8, 2, 16, [0, 4, 7], [600, 100], [601, 1500, 600, 900, 100, 5, 2000])
+    case.upload()
+    n = pa.decode_shared_prefix_workspace_bytes(7, 2, 8, 2, 128, case.bt.shape[1], 16, 600, 4)
+    first = None
+    for byte in (0, 0xFF, 0x7F, 0x80):
+        out = case.run(torch.full((n,), byte, dtype=torch.uint8, device="cuda"))
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    case.check(first)
+
+
 def test_sequences_shorter_than_the_prefix_are_computed_alone():
     case = Case("bf16", 128, 8, 2, 16, [0, 6], [100], [120, 40, 0, 100, 99, 101])
     case.check(case.run())
