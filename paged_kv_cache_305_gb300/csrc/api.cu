@@ -207,13 +207,16 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   const long long tiles = (largest + members - 1) / members;
   const long long per_chunk = tiles * num_groups * num_kv_heads;
   const long long most = std::max(x->max_prefix_len / kPrefixMinChunk, 1);
-  // a pass of some length that is one CTA for each SM runs beside the decode
-  // kernel, one CTA of each on an SM (8192 tokens before 128 sequences: 79 us, 83
-  // with both at full width; 16 sequences: 26 and 31; but 1024 tokens: 70 and 67)
-  x->beside_decode = per_chunk <= kPrefixSms && x->max_prefix_len >= kBesideTokens ? 1 : 0;
   long long best = 1;
   if (per_chunk <= kPrefixSms) {
-    best = std::min(most, kPrefixSms / std::max(per_chunk, 1ll));
+    // The pass runs beside the decode kernel, which gets what the pass leaves of
+    // the SMs (launch_stream); the shorter of the two hides behind the other. 64
+    // CTAs, or 101 where their chunks would be above 2048 tokens. 128 suffixes of
+    // 512 tokens on average behind 2048 tokens: 61.9 us with 64, 64.8 with 101, 70.4
+    // with 152; behind 8192: 81.3, 70.7 and 75.3.
+    const long long per = std::max(per_chunk, 1ll);
+    best = std::min(most, std::max(kPrefixFew / per, 1ll));
+    if (x->max_prefix_len > best * kPrefixLongChunk) best = std::min(most, std::max(kPrefixMost / per, 1ll));
   } else {
     // more CTAs than SMs whatever the chunk: two on each SM at a time, in the
     // fewest chunks whose CTAs fill nine tenths of their waves, or three waves
@@ -231,6 +234,7 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   const long long t = (x->max_prefix_len + best - 1) / best;
   x->chunk_tokens = static_cast<int>(std::min(std::max((t + 63) / 64 * 64, 64ll), 1ll << 30));
   x->max_chunks = max_group_size > 0 ? (x->max_prefix_len + x->chunk_tokens - 1) / x->chunk_tokens : 0;
+  x->pass_ctas = per_chunk * x->max_chunks;
 }
 
 // Kv heads that a CTA of the streaming kernel takes at a time: neighbours are read

@@ -82,21 +82,20 @@ struct Ring {
   using T = Tile<D, FP8>;
   static constexpr int kHalf = kWarps * T::kBytes;   // K (or V) of a stage
   static constexpr int kStages = 65536 / (2 * kHalf);  // three CTAs on an SM
-  static constexpr int kMost = FP8 ? kStages : kStages * 3 / 2;  // one, beside one of the prefix pass
   static constexpr int kScaleBytes = kWarps * 64;      // exponent bytes of a stage
   static constexpr int kHeads = NT * 8;
   static constexpr int kOStride = D + 4;
   // offsets in shared memory; the stages follow the rest
   static constexpr int kScales = 0;
   static constexpr int kNotes = kScales + (FP8 ? kStages * kScaleBytes : 0);
-  static constexpr int kBars = kNotes + kMost * static_cast<int>(sizeof(Note));  // full, empty, joins
-  static constexpr int kStats = kBars + (2 * kMost + kWarps) * 8;  // [warp][m, l, r][head]
+  static constexpr int kBars = kNotes + kStages * static_cast<int>(sizeof(Note));  // full, empty, joins
+  static constexpr int kStats = kBars + (2 * kStages + kWarps) * 8;  // [warp][m, l, r][head]
   static constexpr int kBase = kStats + kWarps * 3 * kHeads * 4;   // [kChunks]
   static constexpr int kMisc = kBase + kChunks * 4;
   static constexpr int kJoin = (kMisc + 32 + 15) / 16 * 16;        // [warp][head][kOStride]
   static constexpr int kSlots = kJoin + kWarps * kJoinHeads * kOStride * 4;  // ROWS: [stage][token]
   template <bool ROWS>
-  static constexpr int kFixed = (kSlots + (ROWS ? kMost * kWarps * T::kTokens * 4 : 0) + 1023) / 1024 * 1024;
+  static constexpr int kFixed = (kSlots + (ROWS ? kStages * kWarps * T::kTokens * 4 : 0) + 1023) / 1024 * 1024;
   static_assert(kStages >= 2, "a stage lands while another is computed");
   static_assert(NT > 1 || 3 * (kFixed<true> + 65536 + 1024) <= 228 * 1024, "three CTAs on an SM");
 };
@@ -140,15 +139,15 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   constexpr uint32_t kNone = 0xffffffffu, kBad = 0xfffffffeu;  // in the place of a slot
   const uint32_t ring = smem_u32(smem) + R::template kFixed<ROWS>, bars = smem_u32(smem + R::kBars);
   auto full = [&](int st) { return bars + 8 * st; };
-  auto empty = [&](int st) { return bars + 8 * (R::kMost + st); };
-  auto join_bar = [&](int h) { return bars + 8 * (2 * R::kMost + h); };
+  auto empty = [&](int st) { return bars + 8 * (R::kStages + st); };
+  auto join_bar = [&](int h) { return bars + 8 * (2 * R::kStages + h); };
   // a place in the ring: the stage, and the parity of its round
   struct Place {
     int st = 0;
     uint32_t round = 0;
   };
   auto step = [&](Place& p) {
-    if (++p.st == a.stages) {
+    if (++p.st == R::kStages) {
       p.st = 0;
       p.round ^= 1;
     }
@@ -165,7 +164,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   };
 
   if (tid == 0) {
-    for (int i = 0; i < a.stages; ++i) {
+    for (int i = 0; i < R::kStages; ++i) {
       tc::mbar_init(full(i), 1);
       tc::mbar_init(empty(i), kWarps);
     }
@@ -255,7 +254,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       return ids;
     };
     auto wait_empty = [&]() {  // emptied as often as it was filled
-      if (filled == a.stages && ok) ok = *aborted == 0 && wait(empty(to.st), to.round ^ 1);
+      if (filled == R::kStages && ok) ok = *aborted == 0 && wait(empty(to.st), to.round ^ 1);
     };
     auto fill = [&](const Note& note, const Ids& ids) {
       wait_empty();
@@ -311,7 +310,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
       }
       step(to);
-      filled = min(filled + 1, a.stages);
+      filled = min(filled + 1, R::kStages);
     };
 
     // the CTA's share of the line; where rows are not cut, the rows that start in it
@@ -423,7 +422,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       if (lane == 0) tc::mbar_arrive(full(to.st));
     } else {  // what was issued must land before the CTA ends: the stages' latest rounds
       for (int i = 0; i < filled; ++i) {
-        const int st = (to.st + a.stages - filled + i) % a.stages;
+        const int st = (to.st + R::kStages - filled + i) % R::kStages;
         tc::mbar_wait(full(st), to.round ^ (st >= to.st ? 1u : 0u));
       }
     }
@@ -797,15 +796,11 @@ struct Dependent {
 template <typename Ty, int D, int NT, bool FP8, bool ROWS, bool SPLIT>
 cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   using R = Ring<D, FP8, NT>;
-  // beside the prefix pass one CTA on each SM, with a longer ring; else three (two)
-  const bool beside = !FP8 && a.groups.max_chunks > 0 && a.groups.beside_decode != 0;
-  a.stages = beside ? R::kMost : R::kStages;
-  const int smem = R::template kFixed<ROWS> + a.stages * 2 * R::kHalf;
+  const int smem = R::template kFixed<ROWS> + R::kStages * 2 * R::kHalf;
   auto kern = paged_stream_kernel<Ty, D, NT, FP8, ROWS, SPLIT>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_context(done, [&] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                R::template kFixed<ROWS> + R::kMost * 2 * R::kHalf);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap km{}, vm{};
@@ -817,7 +812,13 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
         !encode_pool_map(&vm, a.value_cache, slots, a.num_kv_heads, row_bytes, rows, a.heads_at_a_time))
       return cudaErrorInvalidValue;
   }
-  const long long ctas = std::min((beside ? 1 : NT == 1 ? 3 : 2) * num_sms, kMaxCtas);
+  // Three (two) CTAs on an SM, all at once: a CTA that waited for the prefix pass to
+  // end would do its equal share behind it. Beside a CTA of the pass there is room
+  // for one. 64 suffixes of 512 tokens behind 1024: 42 us, 47 us if the pass is not
+  // counted; 8192 tokens before 128: 71 and 88. A pass of more CTAs than there are
+  // SMs runs two on each, and this kernel behind most of it.
+  const long long pass = a.groups.pass_ctas <= num_sms ? a.groups.pass_ctas : 0;
+  const long long ctas = std::min<long long>((NT == 1 ? 3 : 2) * (num_sms - pass) + pass, kMaxCtas);
   const long long rows = static_cast<long long>(a.num_seqs) * (a.num_kv_heads / a.heads_at_a_time);
   const long long most = (static_cast<long long>(a.max_blocks_per_seq) << a.block_shift) / Tile<D, FP8>::kTokens + 2;
   const long long grid = std::min(ctas, rows * (a.cut ? (most + a.least_tiles - 1) / a.least_tiles : 1));

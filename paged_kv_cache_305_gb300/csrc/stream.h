@@ -15,8 +15,8 @@ struct PrefixArgs {
   int max_prefix_len;
   int max_group_size;
   int chunk_tokens;   // tokens of the prefix that one CTA of the prefix pass takes
-  int max_chunks;     // ceil(max_prefix_len / chunk_tokens)
-  int beside_decode;  // one CTA of the pass and one of the decode kernel on an SM
+  int max_chunks;     // ceil(max_prefix_len / chunk_tokens); 0: no prefix pass
+  long long pass_ctas;  // of the prefix pass
 };
 
 // The streaming decode kernel and its merge (decode_stream.cuh).
@@ -39,7 +39,6 @@ struct StreamArgs {
   float scale_log2;     // scale * log2(e)
   int out_f32;
   PrefixArgs groups;    // shared prefixes (num_groups 0: none)
-  int stages;           // of the ring (set by the launcher)
   int cut;              // 1: rows may be cut between CTAs
   int least_tiles;      // shortest share that cuts rows, in tiles
   int2* ws_rows;        // [S, Hkv] first slot and number of a row's segments (0: the row is finished)
@@ -70,11 +69,11 @@ struct Fp8Pool {
   int num_blocks;
 };
 
-// The prefix pass: 128 rows per CTA, chunks sized for the 152 SMs.
+// The prefix pass: 128 rows per CTA, chunks sized for the 152 SMs (plan_prefix).
 constexpr int kPrefixRows = 128;
 constexpr long long kPrefixSms = 152;
-constexpr int kPrefixMinChunk = 256;
-constexpr int kBesideTokens = 2048;
+constexpr long long kPrefixFew = 64, kPrefixMost = 101;  // CTAs of a pass that leaves SMs free
+constexpr int kPrefixMinChunk = 256, kPrefixLongChunk = 2048;
 void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
                  int max_prefix_len, int max_group_size);
 
