@@ -11,6 +11,7 @@
 #include <cmath>
 #include <mutex>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "internal.h"
@@ -209,14 +210,16 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   const long long most = std::max(x->max_prefix_len / kPrefixMinChunk, 1);
   long long best = 1;
   if (per_chunk <= kPrefixSms) {
-    // The pass runs beside the decode kernel, which gets what the pass leaves of
-    // the SMs (launch_stream); the shorter of the two hides behind the other. 64
-    // CTAs, or 101 where their chunks would be above 2048 tokens. 128 suffixes of
-    // 512 tokens on average behind 2048 tokens: 61.9 us with 64, 64.8 with 101, 70.4
-    // with 152; behind 8192: 81.3, 70.7 and 75.3.
-    const long long per = std::max(per_chunk, 1ll);
-    best = std::min(most, std::max(kPrefixFew / per, 1ll));
-    if (x->max_prefix_len > best * kPrefixLongChunk) best = std::min(most, std::max(kPrefixMost / per, 1ll));
+    // The pass runs beside the decode kernel, which gets what the pass leaves of the
+    // SMs (launch_stream), and a tile of 64 tokens takes it about a microsecond: 64
+    // CTAs while their chunks are at most 2048 tokens, 101 up to 2816, otherwise one
+    // for each SM. 128 suffixes of 512 tokens on average behind 2048 tokens take 61.9,
+    // 64.8 and 70.4 us with 64, 101 and 152; behind 8192, 82.6, 71.5 and 76.3; behind
+    // 16384, 124, 96 and 84 (two on an SM: 101).
+    for (const auto& [ctas, longest] : {std::pair{64ll, 2048ll}, {101ll, 2816ll}, {kPrefixSms, 0ll}}) {
+      best = std::min(most, std::max(ctas / std::max(per_chunk, 1ll), 1ll));
+      if ((x->max_prefix_len + best - 1) / best <= longest) break;
+    }
   } else {
     // more CTAs than SMs whatever the chunk: two on each SM at a time, in the
     // fewest chunks whose CTAs fill nine tenths of their waves, or three waves

@@ -72,8 +72,7 @@ struct Fp8Pool {
 // The prefix pass: 128 rows per CTA, chunks sized for the 152 SMs (plan_prefix).
 constexpr int kPrefixRows = 128;
 constexpr long long kPrefixSms = 152;
-constexpr long long kPrefixFew = 64, kPrefixMost = 101;  // CTAs of a pass that leaves SMs free
-constexpr int kPrefixMinChunk = 256, kPrefixLongChunk = 2048;
+constexpr int kPrefixMinChunk = 256;
 void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
                  int max_prefix_len, int max_group_size);
 
