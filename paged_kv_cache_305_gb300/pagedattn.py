@@ -435,12 +435,15 @@ def copy_blocks(key_cache: torch.Tensor, value_cache: torch.Tensor, src: torch.T
 
 
 def _need_fp8_pool(key_cache: torch.Tensor, value_cache: torch.Tensor,
-                   cache_scales: torch.Tensor) -> None:
-    _need(key_cache.dim() == 4 and value_cache.shape == key_cache.shape, "cache shape mismatch")
+                   cache_scales: torch.Tensor) -> torch.Size:
+    """The checks of an 8-bit pool; returns (num_blocks, block_size, num_kv_heads, head_dim)."""
+    shape = key_cache.shape
+    _need(len(shape) == 4 and value_cache.shape == shape, "cache shape mismatch")
     _need(key_cache.dtype == value_cache.dtype == torch.float8_e4m3fn, "the caches must be float8_e4m3fn")
-    NB, B, Hkv, _ = key_cache.shape
+    NB, B, Hkv, _ = shape
     _need(cache_scales.dtype == torch.uint8 and cache_scales.shape == (NB, Hkv, 2, B),
           "cache_scales must be uint8 [num_blocks, num_kv_heads, 2, block_size]")
+    return shape
 
 
 def _device_of(*tensors: torch.Tensor) -> int:
@@ -460,7 +463,7 @@ def _enqueue(entry, device: int, stream, *args) -> None:
         raw = torch._C._cuda_getCurrentRawStream(device)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         rc = entry(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -488,9 +491,8 @@ def reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, key_cache: tor
     an element is its code times 2**(byte - 127). Non-negative slots must be
     distinct.
     """
-    _need_fp8_pool(key_cache, value_cache, cache_scales)
+    NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
     device = _device_of(key, value, key_cache, value_cache, cache_scales, slot_mapping)
-    NB, B, Hkv, d = key_cache.shape
     T = key.shape[0]
     _need(key.shape == (T, Hkv, d) and value.shape == (T, Hkv, d), "key/value shape mismatch")
     _need(key.dtype == value.dtype, "dtype mismatch")
@@ -504,11 +506,10 @@ def reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, key_cache: tor
 def copy_blocks_fp8(key_cache: torch.Tensor, value_cache: torch.Tensor, cache_scales: torch.Tensor,
                     src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """:func:`copy_blocks` for an 8-bit pool (codes and exponent bytes)."""
-    _need_fp8_pool(key_cache, value_cache, cache_scales)
+    NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
     device = _device_of(key_cache, value_cache, cache_scales, src, dst)
     _need(src.dtype == torch.int32 and dst.dtype == torch.int32 and src.shape == dst.shape
           and src.dim() == 1, "src/dst must be 1-D int32 tensors")
-    NB, B, Hkv, d = key_cache.shape
     _enqueue(load_library().pa_copy_blocks_fp8, device, stream, key_cache.data_ptr(),
              value_cache.data_ptr(), cache_scales.data_ptr(), src.data_ptr(), dst.data_ptr(),
              src.shape[0], Hkv, d, B, NB)
@@ -525,10 +526,9 @@ def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: 
     rows stay as they are. With starts that are multiples of B the outputs,
     viewed as [rows / B, B, Hkv, d], are pools for :func:`prefill`.
     """
-    _need_fp8_pool(key_cache, value_cache, cache_scales)
+    NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
     device = _device_of(key_out, value_out, key_cache, value_cache, cache_scales, block_tables,
                         seq_lens, out_start)
-    NB, B, Hkv, d = key_cache.shape
     _need(key_out.dim() == 3 and key_out.shape[1:] == (Hkv, d) and value_out.shape == key_out.shape
           and key_out.dtype == value_out.dtype, "key_out/value_out dtype or shape mismatch")
     S = seq_lens.shape[0]
@@ -571,8 +571,7 @@ def decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
     ``query`` is float16 or bfloat16; the workspace comes from
     :func:`alloc_workspace` with the 8-bit ``key_cache``.
     """
-    _need_fp8_pool(key_cache, value_cache, cache_scales)
-    NB, B, Hkv, d = key_cache.shape
+    NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
     device, odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace,
                                                  key_cache, value_cache, cache_scales)
     S, Hq, _ = query.shape
