@@ -29,16 +29,16 @@
 // shares together, however long a row is.
 //
 // Streaming. Four warps compute, a fifth feeds them: it finds the rows
-// of the CTA's share, reads the block table and fills the stages of a ring in shared memory,
-// 32 KB each at d = 128: one tile for every computing warp, the tiles of the
+// of the CTA's share, reads the block table and fills the stages of a ring in shared
+// memory, 32 KB each at d = 128: one tile for every computing warp, the tiles of the
 // CTA's heads side by side. A lane issues a tensor copy per block for K and for
 // V, straight from the block table and for all heads at once, and a bulk copy
 // for the block's exponent bytes. Blocks under 8 tokens, and pools beyond a
 // tensor map's reach, are copied row by row: the feeding warp hands out the slots
 // of the stage's tokens, and each computing warp copies its own tile with
 // cp.async, a stage ahead (ROWS; one warp alone cannot issue that many copies:
-// 350 us for the 128 sequences). A stage carries a note of what it holds, so the computing warps know of nothing but stages:
-// they load the query at a segment's first one and join their states at its
+// 350 us for the 128 sequences, 198 us this way). A stage carries a note of what
+// it holds, so the computing warps know of nothing but stages: they load the query at a segment's first one and join their states at its
 // last one, while the copies run on across segments. All waits are
 // bounded; one that gives up is counted, and the CTA winds down.
 #pragma once

@@ -146,8 +146,8 @@ struct Tile {
   }
 };
 
-// qh: the first of the kv head's G query rows; sl2 = scale log2(e). 8-bit: fp16 in the k order above;
-// bf16 queries are scaled for each head by the power of two that brings the
+// qh: the first of the kv head's G query rows; sl2 = scale log2(e). 8-bit: fp16 in
+// the k order above; bf16 queries are scaled for each head by the power of two that brings the
 // largest element to [2^14, 2^15): their 8 bits fit into fp16's 11, and what
 // falls below fp16's range is under 2^-39 of the largest.
 template <typename Ty, int D, int NT, bool FP8, bool SPLIT>
@@ -190,7 +190,7 @@ __device__ __forceinline__ void load_query(const typename Ty::T* qh, int G, floa
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = min(268 - static_cast<int>(top >> 23), 254);  // 127 + 14 - (its exponent)
+        const int e = min(268 - static_cast<int>(top >> 23), 253);  // 127 + 14 - (its exponent); 2^(127 - e) is normal
         const float f = exponent_factor(e);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -219,7 +219,8 @@ __device__ __forceinline__ void weight_parts(float w0, float w1, uint32_t rest, 
 
 // 8-bit tile. sk: the group of K rows that this lane's addresses for ldmatrix lie
 // in (tokens 0-7 or 8-15 of the tile: lane & 8), sk + k_next that of the next 16
-// tokens; sv: the group of V rows of token `lane`; ek, ev: its exponent bytes; tokens lo .. hi - 1 count (the others' V rows are zero).
+// tokens; sv: the group of V rows of token `lane`; ek, ev: its exponent bytes;
+// tokens lo .. hi - 1 count (the others' V rows are zero).
 template <int D, int NT, bool SPLIT>
 __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv, int ek, int ev,
                                        int lo, int hi, const Query<D, NT>& q, State<D, NT>& st) {

@@ -297,6 +297,28 @@ def test_decode_bf16_queries_of_any_size(size):
     check_decode(query, kc, vc, sc, bt, [n], B, 1 / (np.sqrt(d) * size), "bf16")
 
 
+@pytest.mark.parametrize("size", [2.0 ** -118, 2.0 ** -125])
+def test_decode_bf16_queries_next_to_the_smallest(size):
+    rng = np.random.default_rng(24)
+    B, n, d = 16, 50, 64
+    kc, vc, sc = random_pool(rng, 6, B, 1, d, 2)
+    bt = tables_for(rng, [n], B, 6)
+    q = rng.uniform(1, 2, (1, 3, d)) * rng.choice([-1, 1], (1, 3, d))  # normal bf16 numbers
+    query = W.f32_to_bits((q * size).astype(np.float32), "bf16")
+    check_decode(query, kc, vc, sc, bt, [n], B, 0.125 / size, "bf16")
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1.5])
+@pytest.mark.parametrize("dtype,Hq,B", [("bf16", 8, 16), ("fp16", 14, 2)])
+def test_decode_scales(scale, dtype, Hq, B):
+    rng = np.random.default_rng(25)
+    lens = [130, 1, 600]
+    NB = sum(-(-n // B) for n in lens)
+    kc, vc, sc = random_pool(rng, NB, B, 2, 64, 0)
+    bt = tables_for(rng, lens, B, NB)
+    check_decode(W.normal_bits((3, Hq, 64), dtype, 25, 2), kc, vc, sc, bt, lens, B, scale, dtype)
+
+
 def test_decode_zero_query_and_zero_pool():
     kd, vd, sd = pa.alloc_fp8_cache(4, 16, 1, 64)
     q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")

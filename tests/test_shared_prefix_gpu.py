@@ -163,6 +163,14 @@ def test_workspace_may_hold_anything():
     case.check(first)
 
 
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1.5])
+@pytest.mark.parametrize("dtype,Hq,B", [("bf16", 8, 16), ("fp16", 14, 2)])
+def test_scales(scale, dtype, Hq, B):
+    case = Case(dtype, 64, Hq, 2, B, [0, 3, 5], [200, 33], [200, 333, 201, 40, 700], seed=70)
+    case.scale = scale
+    case.check(case.run())
+
+
 def test_sequences_shorter_than_the_prefix_are_computed_alone():
     case = Case("bf16", 128, 8, 2, 16, [0, 6], [100], [120, 40, 0, 100, 99, 101])
     case.check(case.run())
