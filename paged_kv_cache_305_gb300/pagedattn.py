@@ -546,20 +546,22 @@ def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: 
 
 def _need_decode(out: torch.Tensor, query: torch.Tensor, head_dim: int, block_tables: torch.Tensor,
                  seq_lens: torch.Tensor, workspace: Optional[torch.Tensor], *others: torch.Tensor):
-    """The checks of decode calls; returns (device, out dtype code, workspace pointer and bytes)."""
-    _need(query.dim() == 3 and query.shape[2] == head_dim, "cache shape mismatch")
-    _need(out.shape == query.shape and out.dtype in (query.dtype, torch.float32),
-          "out dtype or shape mismatch")
+    """The checks of decode calls; returns the device, the shapes (num_seqs, num_q_heads,
+    max_blocks_per_seq) and what the entry takes after them: types and workspace."""
+    shape, tables = query.shape, block_tables.shape
+    _need(len(shape) == 3 and shape[2] == head_dim, "cache shape mismatch")
+    _need(out.shape == shape and out.dtype in (query.dtype, torch.float32), "out dtype or shape mismatch")
     _need(block_tables.dtype == torch.int32 and seq_lens.dtype == torch.int32,
           "block_tables and seq_lens must be int32")
-    S = query.shape[0]
-    _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
+    _need(len(tables) == 2 and tables[0] == shape[0] and seq_lens.shape == shape[:1],
           "block_tables/seq_lens shape mismatch")
-    code = PA_FLOAT32 if out.dtype == torch.float32 else _dtype_code(query)
+    code = _dtype_code(query)
+    types = code, PA_FLOAT32 if out.dtype == torch.float32 else code
+    sizes = shape[0], shape[1], tables[1]
     if workspace is None:
-        return _device_of(query, out, block_tables, seq_lens, *others), code, 0, 0
+        return _device_of(query, out, block_tables, seq_lens, *others), sizes, (*types, 0, 0)
     device = _device_of(query, out, block_tables, seq_lens, workspace, *others)
-    return device, code, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return device, sizes, (*types, workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -572,13 +574,12 @@ def decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
     :func:`alloc_workspace` with the 8-bit ``key_cache``.
     """
     NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
-    device, odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace,
-                                                 key_cache, value_cache, cache_scales)
-    S, Hq, _ = query.shape
+    device, (S, Hq, MB), rest = _need_decode(out, query, d, block_tables, seq_lens, workspace,
+                                             key_cache, value_cache, cache_scales)
     _enqueue(load_library().pa_decode_fp8, device, stream, out.data_ptr(), query.data_ptr(),
              key_cache.data_ptr(), value_cache.data_ptr(), cache_scales.data_ptr(),
              block_tables.data_ptr(), seq_lens.data_ptr(), S, Hq, Hkv, d, B, float(scale),
-             block_tables.shape[1], NB, int(partition_tokens), _dtype_code(query), odt, ws_ptr, ws_bytes)
+             MB, NB, int(partition_tokens), *rest)
     return out
 
 
@@ -623,15 +624,13 @@ def decode_shared_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torc
           "group_start and prefix_lens must be int32")
     _need(prefix_lens.dim() == 1 and group_start.shape == (prefix_lens.shape[0] + 1,),
           "group_start/prefix_lens shape mismatch")
-    device, odt, ws_ptr, ws_bytes = _need_decode(out, query, d, block_tables, seq_lens, workspace,
-                                                 key_cache, value_cache, group_start, prefix_lens)
-    S, Hq, _ = query.shape
+    device, (S, Hq, MB), rest = _need_decode(out, query, d, block_tables, seq_lens, workspace,
+                                             key_cache, value_cache, group_start, prefix_lens)
     _enqueue(load_library().pa_decode_shared_prefix, device, stream, out.data_ptr(),
              query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
              block_tables.data_ptr(), seq_lens.data_ptr(), group_start.data_ptr(),
              prefix_lens.data_ptr(), S, prefix_lens.shape[0], Hq, Hkv, d, B, float(scale),
-             block_tables.shape[1], NB, int(max_prefix_len), int(max_group_size),
-             _dtype_code(query), odt, ws_ptr, ws_bytes)
+             MB, NB, int(max_prefix_len), int(max_group_size), *rest)
     return out
 
 
