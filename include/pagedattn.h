@@ -380,9 +380,9 @@ int pa_decode_fp8(void* out, const void* query,
                   cudaStream_t stream);
 
 /*
- * Workspace bytes of pa_decode_fp8 (any partition_tokens): 0 where
- * max_blocks_per_seq * block_size is at most 512 (rows are not cut then), and
- * for invalid sizes.
+ * Workspace bytes of pa_decode_fp8 (any partition_tokens): 0 where rows are not
+ * cut, which is so for max_blocks_per_seq * block_size up to 256, or up to 512
+ * with many sequences and heads; and for invalid sizes.
  */
 size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                      int max_blocks_per_seq, int block_size);
@@ -390,9 +390,11 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
 /*
  * pa_decode for batches in which groups of sequences begin with the same
  * tokens: one system prompt before every request, or several candidates of one
- * prompt (pa_bm_fork). The K/V of a group's prefix are read once for all its
- * members and multiplied on the tensor cores; the rest of each sequence is
- * read as in pa_decode, and the parts are joined by log-sum-exp.
+ * prompt (pa_bm_fork). Where that saves enough reading (some 30 MB, by the sizes and
+ * bounds given), the K/V of a group's prefix are read once for all its members
+ * and multiplied on the tensor cores, the rest of each sequence is read as in
+ * pa_decode, and the parts are joined by log-sum-exp. Otherwise each sequence
+ * reads the prefix itself.
  *
  * Group g holds the sequences group_start[g] .. group_start[g+1] - 1
  * (group_start: DEVICE int32 [num_groups + 1], non-decreasing, from 0 to
@@ -426,7 +428,11 @@ int pa_decode_shared_prefix(void* out, const void* query,
                             pa_dtype dtype, pa_dtype out_dtype,
                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Workspace bytes of pa_decode_shared_prefix; 0 for invalid sizes. */
+/*
+ * Workspace bytes of pa_decode_shared_prefix: 0 where rows are not cut (tables of
+ * up to 128 tokens, or up to 512 with many sequences and heads) and the prefix
+ * is not computed for its group at once, and for invalid sizes.
+ */
 size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,
                                                int num_kv_heads, int head_dim,
                                                int max_blocks_per_seq, int block_size,

@@ -198,8 +198,8 @@ size_t prefill_v16_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_b
 // How the prefix pass cuts the prefix (x->num_seqs is set): a CTA takes one chunk of tokens for 128
 // rows (members x query heads) of a group and a kv head, and leaves an fp32
 // piece of each row behind. Chunks are whole 64-token tiles, at least
-// kPrefixMinChunk long.
-void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
+// kPrefixMinChunk long. Or that there is no pass (max_chunks 0).
+void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int head_dim, int lmax,
                  int max_prefix_len, int max_group_size) {
   x->max_prefix_len = std::min(max_prefix_len, lmax);
   x->max_group_size = max_group_size;
@@ -236,7 +236,18 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   }
   const long long t = (x->max_prefix_len + best - 1) / best;
   x->chunk_tokens = static_cast<int>(std::min(std::max((t + 63) / 64 * 64, 64ll), 1ll << 30));
-  x->max_chunks = max_group_size > 0 ? (x->max_prefix_len + x->chunk_tokens - 1) / x->chunk_tokens : 0;
+  // The pass is worth its launch, its pieces and the SMs that it takes from the
+  // decode kernel where it saves enough reading (from L2, mostly). Without it every
+  // sequence reads the prefix itself, through its group's table. With fewer CTAs a
+  // chunk than a quarter of the SMs the two met at about 32 MB: 26 sequences in 3
+  // groups behind 2790 tokens of one head, 33 MB: 20.8 us, 25.7 without; 21 behind
+  // 916 of three, 21 MB: 14.7 and 15.5; 7 behind 333: 12.9 and 11.3. With more CTAs,
+  // at about 128: 230 sequences in 146 groups behind 1150 of three heads, 74 MB: 59
+  // and 49; 67 in 4 groups behind 709 of 16, 366 MB: 25 and 37.
+  const double saved =
+      static_cast<double>(x->num_seqs - num_groups) * x->max_prefix_len * num_kv_heads * head_dim * 4;
+  const bool pass = max_group_size > 0 && saved > (per_chunk <= kPrefixSms / 4 ? kPassBytes : kWidePassBytes);
+  x->max_chunks = pass ? (x->max_prefix_len + x->chunk_tokens - 1) / x->chunk_tokens : 0;
   x->pass_ctas = per_chunk * x->max_chunks;
 }
 
@@ -256,8 +267,12 @@ StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_h
                            long long lmax, const PrefixArgs& groups) {
   StreamLayout w{};
   const int max_chunks = groups.max_chunks;
-  w.heads = stream_heads(fp8, num_seqs, num_kv_heads, lmax - groups.max_prefix_len);
-  w.cut = lmax > kUncutTokens;
+  w.heads = stream_heads(fp8, num_seqs, num_kv_heads, max_chunks > 0 ? lmax - groups.max_prefix_len : lmax);
+  // Whole rows need no merge, cut ones share the SMs. Four sequences of up to 512
+  // 8-bit tokens, 16 rows: 8.9 us cut, 12.6 us whole; 100 sequences, 400 rows: 13.4
+  // us whole, 13.8 us cut.
+  const bool few = static_cast<long long>(num_seqs) * (num_kv_heads / w.heads) < kFewRows;
+  w.cut = lmax > (few ? kUncutTiles * (fp8 ? 32 : 16) : kUncutTokens);
   if (!w.cut && max_chunks == 0) return w;
   const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
   const size_t group = static_cast<size_t>(w.heads) * (num_q_heads / num_kv_heads);
@@ -853,8 +868,8 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
     groups.prefix_lens = prefix_lens;
     groups.num_groups = num_groups;
     groups.num_seqs = num_seqs;
-    pa::plan_prefix(&groups, num_groups, group, num_kv_heads, static_cast<int>(lmax), max_prefix_len,
-                    max_group_size);
+    pa::plan_prefix(&groups, num_groups, group, num_kv_heads, head_dim, static_cast<int>(lmax),
+                    max_prefix_len, max_group_size);
   }
   if (num_seqs == 0) return PA_OK;
   if (!out || !query || !key_cache || !value_cache || !block_tables || !seq_lens || (fp8 && !scales))
@@ -996,8 +1011,8 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
     return 0;
   pa::PrefixArgs x{};
   x.num_seqs = num_seqs;
-  pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads, static_cast<int>(lmax),
-                  max_prefix_len, max_group_size);
+  pa::plan_prefix(&x, num_groups, num_q_heads / num_kv_heads, num_kv_heads, head_dim,
+                  static_cast<int>(lmax), max_prefix_len, max_group_size);
   return pa::stream_layout(false, num_seqs, num_q_heads, num_kv_heads, head_dim, lmax, x)
       .total;
 }

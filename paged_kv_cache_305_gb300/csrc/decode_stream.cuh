@@ -8,7 +8,8 @@
 // at a lower rate than when the neighbours are read at the same time (the
 // copies of the 128-sequence case without any arithmetic: 222 us with one head,
 // 197 us with two or four; 216 and 116 us for d = 64). A row is one (sequence, head
-// group); its tokens (those behind the shared prefix, where there is one) are
+// group); its tokens (those behind the shared prefix, where a pass of its own
+// computes that; otherwise the prefix's first, through the group's table) are
 // taken in stages of 32 KB (at d = 128: K and V of 32 8-bit or 16 16-bit tokens
 // for each computing warp), cut at multiples of the stage's tokens. All stages, in
 // (head group, sequence, stage) order, form one line, which is cut into equal
@@ -183,19 +184,21 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     int lo, hi;  // tokens
     int n;       // stages; one (without tokens) for an empty row
     int before;  // pieces of the prefix pass
+    int shared;  // without a pass: the first stages, of the tokens before lo
+    int lead;    // and the sequence through whose table they are read
   };
   auto row_of = [&](int s) {
     Row r;
     r.hi = min(max(__ldg(a.seq_lens + s), 0), Lmax);
-    r.lo = r.before = 0;
+    r.lo = r.before = r.shared = r.lead = 0;
     if constexpr (!FP8) {
       if (a.groups.num_groups > 0) {
-        int lead;
-        r.lo = prefix_of(a.groups, s, r.hi, Lmax, &lead);
+        r.lo = prefix_of(a.groups, s, r.hi, Lmax, &r.lead);
         r.before = prefix_pieces(a.groups, r.lo);
+        if (a.groups.max_chunks == 0) r.shared = (r.lo + ST - 1) / ST;
       }
     }
-    r.n = max((r.hi + ST - 1) / ST - r.lo / ST, 1);
+    r.n = max(r.shared + (r.hi > r.lo ? (r.hi + ST - 1) / ST - r.lo / ST : 0), 1);
     return r;
   };
   const int per = (S + kChunks - 1) / kChunks;
@@ -362,7 +365,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       while (more && ok) {
         const unsigned at = static_cast<unsigned>(s) + lane;
         const int my_hg = hg + static_cast<int>(at / S), my_s = static_cast<int>(at % S);
-        Row r{0, 0, 0, 0};
+        Row r{};
         if (my_hg < NG) r = row_of(my_s);
         unsigned end = r.n;
 #pragma unroll
@@ -387,7 +390,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                   make_int2(slot, pieces ? static_cast<int>(last - first) + 1 : 0);
           }
         }
-        const int stage0 = r.lo / ST + static_cast<int>(from - start);
+        const int stage0 = static_cast<int>(from - start);
         const int stages = in ? static_cast<int>(to - from) : 0;
         for (unsigned left = __ballot_sync(kFull, in); left != 0 && ok; left &= left - 1) {
           const int l = __ffs(left) - 1;
@@ -397,16 +400,27 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           note.lo = __shfl_sync(kFull, r.lo, l);
           note.hi = __shfl_sync(kFull, r.hi, l);
           note.slot = __shfl_sync(kFull, slot, l);
-          note.t0 = __shfl_sync(kFull, stage0, l) * ST;
           note.pad = 0;
-          const int count = __shfl_sync(kFull, stages, l);
-          const int32_t* row = a.block_tables + static_cast<size_t>(note.s) * a.max_blocks_per_seq;
-          Ids ids = load_ids(row, note.t0, note.lo, note.hi);
+          const int k0 = __shfl_sync(kFull, stage0, l), count = __shfl_sync(kFull, stages, l);
+          const int shared = __shfl_sync(kFull, r.shared, l), lead = __shfl_sync(kFull, r.lead, l);
+          const int lo = note.lo, hi = note.hi;
+          // stage k of the row: its tokens, and the blocks that hold them
+          auto stage_at = [&](int k) {
+            const bool of_prefix = !FP8 && k < shared;
+            note.t0 = (of_prefix ? k : k - shared + lo / ST) * ST;
+            note.lo = of_prefix ? 0 : lo;
+            note.hi = of_prefix ? lo : hi;
+            const int32_t* row =
+                a.block_tables + static_cast<size_t>(of_prefix ? lead : note.s) * a.max_blocks_per_seq;
+            return load_ids(row, note.t0, note.lo, note.hi);
+          };
+          Ids ids = stage_at(k0);
           for (int i = 0; i < count && ok; ++i) {
             note.flags = (i == 0 ? kFirst : 0) | (i == count - 1 ? kLast : 0);
-            fill(note, ids);
-            note.t0 += ST;
-            if (i + 1 < count) ids = load_ids(row, note.t0, note.lo, note.hi);  // a stage ahead
+            const Note filling = note;
+            const Ids now = ids;
+            if (i + 1 < count) ids = stage_at(k0 + i + 1);  // a stage ahead
+            fill(filling, now);
           }
         }
         more = __shfl_sync(kFull, my_hg < NG && end < u1, 31);

@@ -27,9 +27,10 @@ __device__ __forceinline__ int group_of(const PrefixArgs& x, int s) {
   return lo;
 }
 
-// Pieces that the prefix pass leaves for a sequence of which it computed `shared` tokens.
+// Pieces that the prefix pass, where there is one, leaves for a sequence with
+// `shared` tokens of prefix.
 __device__ __forceinline__ int prefix_pieces(const PrefixArgs& x, int shared) {
-  return (shared + x.chunk_tokens - 1) / x.chunk_tokens;
+  return x.max_chunks == 0 ? 0 : (shared + x.chunk_tokens - 1) / x.chunk_tokens;
 }
 
 // Counts the groups whose start, size or prefix is out of range (one thread a
@@ -45,7 +46,7 @@ __device__ __forceinline__ void count_bad_groups(const PrefixArgs& x, int tid, i
   }
 }
 
-// Tokens of sequence s (length L) that are read once for its group: the
+// Tokens of sequence s (length L) that are read through its group's table: the
 // group's prefix, or 0 for a sequence that is computed alone (shorter than the
 // prefix, beyond max_group_size members, or outside its group). *lead is the
 // sequence whose table the prefix is read through.

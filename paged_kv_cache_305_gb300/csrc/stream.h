@@ -15,7 +15,8 @@ struct PrefixArgs {
   int max_prefix_len;
   int max_group_size;
   int chunk_tokens;   // tokens of the prefix that one CTA of the prefix pass takes
-  int max_chunks;     // ceil(max_prefix_len / chunk_tokens); 0: no prefix pass
+  int max_chunks;     // ceil(max_prefix_len / chunk_tokens); 0: no prefix pass, every sequence
+                      // reads its group's prefix itself
   long long pass_ctas;  // of the prefix pass
 };
 
@@ -73,15 +74,17 @@ struct Fp8Pool {
 constexpr int kPrefixRows = 128;
 constexpr long long kPrefixSms = 152;
 constexpr int kPrefixMinChunk = 256;
-void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int lmax,
+constexpr double kPassBytes = 32e6, kWidePassBytes = 128e6;
+void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int head_dim, int lmax,
                  int max_prefix_len, int max_group_size);
 
 // Schedule of the streaming decode kernel: three CTAs on each of the 152 SMs; the
 // shortest share of the work that may cut a row, in tiles; tables of up to
-// kUncutTokens leave rows whole.
+// kUncutTokens leave rows whole, or of up to kUncutTiles tiles where there are
+// fewer rows than kFewRows (stream_layout).
 constexpr int kMaxCtas = 456;
 constexpr int kLeastTiles = 4;
-constexpr long long kUncutTokens = 512;
+constexpr long long kUncutTokens = 512, kUncutTiles = 8, kFewRows = 152;
 constexpr int kGroupTiles = 16;  // see stream_heads
 
 // Workspace of the streaming decode kernel: the rows' segments, then the pieces.

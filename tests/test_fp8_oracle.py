@@ -171,7 +171,8 @@ def _prefix(lib, **kw):
     (dict(Hq=6, Hkv=4), -1, "multiple"), (dict(Hkv=0), -1, "must be >= 1"), (dict(Hq=34, Hkv=2), -2, "per kv head"),
     (dict(d=96), -2, "head_dim"), (dict(B=12), -2, "block_size"), (dict(MB=0), -1, "max_blocks_per_seq"),
     (dict(NB=1 << 27, B=16), -2, "2^31"), (dict(scale=float("inf")), -1, "scale"), (dict(out=None), -1, "NULL"),
-    (dict(ws=None), -3, "workspace"), (dict(wsb=64), -3, "workspace"), (dict(ws=FAKE + 8), -1, "aligned"),
+    (dict(MB=400, ws=None), -3, "workspace"), (dict(MB=400, wsb=64), -3, "workspace"),
+    (dict(MB=400, ws=FAKE + 8), -1, "aligned"), (dict(S=200, mp=64, mg=200, Hkv=8, ws=None), -3, "workspace"),
 ])
 def test_shared_prefix_refusals(lib, kw, code, msg):
     assert _prefix(lib, **kw) == code
@@ -180,7 +181,9 @@ def test_shared_prefix_refusals(lib, kw, code, msg):
 
 def test_decode_workspace_holds_the_pieces_where_rows_may_be_cut(lib):
     f = pa.decode_fp8_workspace_bytes
-    assert f(8, 8, 2, 128, 32, 16) == 0 and f(8, 8, 2, 128, 512, 1) == 0  # 512 tokens: rows stay whole
+    assert f(8, 8, 2, 128, 16, 16) == 0 and f(8, 8, 2, 128, 256, 1) == 0  # 256 tokens: rows stay whole
+    assert f(8, 8, 2, 128, 17, 16) > 0
+    assert f(100, 8, 2, 128, 32, 16) == 0 and f(100, 8, 2, 128, 33, 16) > 0  # more rows than SMs: up to 512
     a = f(8, 8, 2, 128, 33, 16)
     assert a > 0 and f(16, 8, 2, 128, 33, 16) > a and f(8, 16, 2, 128, 33, 16) > a
     for bad in [(-1, 8, 2, 128, 64, 16), (8, 0, 2, 128, 64, 16), (8, 8, 0, 128, 64, 16), (8, 8, 3, 128, 64, 16),
@@ -211,7 +214,10 @@ def test_shared_prefix_refusals_of_sizes(lib, kw, code, msg):
 def test_shared_prefix_workspace_grows_with_what_it_holds(lib):
     f = pa.decode_shared_prefix_workspace_bytes
     a = f(8, 1, 8, 2, 128, 64, 16, 512, 8)
-    assert a > pa.decode_workspace_bytes(8, 8, 128, 64, 16)  # the prefix adds pieces
+    assert a > pa.decode_workspace_bytes(8, 8, 128, 64, 16)
+    # a prefix pass adds a piece for each query row and chunk; few members have none
+    assert f(100, 1, 8, 2, 128, 64, 16, 1000, 100) >= f(100, 1, 8, 2, 128, 64, 16, 0, 100) + 100 * 8 * 128 * 4
+    assert a == f(8, 1, 8, 2, 128, 64, 16, 0, 8)
     assert f(16, 1, 8, 2, 128, 64, 16, 512, 8) > a
     # one chunk at least holds any prefix; no chunk without a prefix or members
     assert f(8, 1, 8, 2, 128, 64, 16, 1, 8) >= f(8, 1, 8, 2, 128, 64, 16, 0, 8) > 0

@@ -65,6 +65,14 @@ class Case:
         self.max_prefix = int(max(prefixes)) if len(prefixes) else 0
         self.max_group = int(max(np.diff(starts)))
 
+    def passes(self):
+        """Whether the prefix is computed for its group at once: the reading that this saves, in
+        bytes, against a bound that is higher where a chunk takes many CTAs of 128 rows."""
+        S, Hq, d = self.query.shape
+        Hkv, groups = self.kc.shape[2], len(self.prefixes)
+        ctas = -(-self.max_group // (128 // (Hq // Hkv))) * groups * Hkv
+        return (S - groups) * self.max_prefix * Hkv * d * 4 > (32e6 if ctas <= 38 else 128e6)
+
     def upload(self):
         self.q, self.kd, self.vd = (dev_bits(x, self.dtype) for x in (self.query, self.kc, self.vc))
         self.btd, self.sl, self.gs, self.pl = up(self.table), up(self.lens), up(self.starts), up(self.prefixes)
@@ -107,24 +115,45 @@ GRID = [
     ("fp16", 128, 8, 8, 32, [0, 0, 1, 1, 4, 4], [50, 20, 9, 1, 3], [33, 1, 2, 64]),
     # more members than one tile of 128 rows holds, chunked prefix
     ("bf16", 64, 16, 1, 16, [0, 30], [1500], [1500 + i for i in range(30)]),
-    ("fp16", 128, 2, 2, 16, [0, 140, 150], [129, 515], [130 + i % 3 for i in range(140)] + [515] * 10),
 ]
 
 
-@pytest.mark.parametrize("idx", range(len(GRID)))
+# the same for groups whose prefix is computed for all members at once
+PASS = [
+    ("bf16", 128, 8, 2, 16, [0, 100, 104], [600, 300], [600 + 3 * i for i in range(100)] + [300, 301, 499, 600]),
+    # more members than one tile of 128 rows holds
+    ("fp16", 64, 4, 4, 16, [0, 130, 133], [500, 77], [500 + i % 70 for i in range(130)] + [77, 78, 200]),
+    ("bf16", 64, 6, 3, 4, [0, 120], [777], [777 + i % 90 for i in range(120)]),
+    ("fp16", 128, 16, 1, 8, [0, 90, 91], [1000, 5], [1000 + 2 * i for i in range(90)] + [6]),
+    ("bf16", 128, 4, 4, 1, [0, 140, 145], [257, 40], [257 + i % 20 for i in range(140)] + [40, 41, 60, 99, 299]),
+    ("fp16", 64, 14, 2, 64, [0, 150], [700], [700 + i for i in range(150)]),
+    ("bf16", 128, 12, 4, 2, [0, 1, 2, 110], [30, 65, 400], [31, 70] + [400 + i % 33 for i in range(108)]),
+    # groups that are empty, and of one member; more CTAs a chunk
+    ("fp16", 128, 8, 8, 32, [0, 0, 1, 1, 130, 130], [50, 20, 9, 300, 3], [33] + [300 + i % 65 for i in range(129)]),
+    ("fp16", 128, 2, 2, 16, [0, 140, 150], [129, 515], [130 + i % 3 for i in range(140)] + [515] * 10),
+    # chunks of a long prefix
+    ("bf16", 64, 16, 1, 16, [0, 40], [6001], [6001 + 5 * i for i in range(40)]),
+]
+
+
+@pytest.mark.parametrize("idx", range(len(GRID) + len(PASS)))
 def test_grid(idx):
-    case = Case(*GRID[idx], seed=idx)
+    case = Case(*(GRID + PASS)[idx], seed=idx)
+    assert case.passes() == (idx >= len(GRID))
     pa.bad_index_count(clear=True)
     out = case.run()
     assert pa.bad_index_count(clear=True) == 0  # the hidden entries were never read
-    case.check(out, what=str(GRID[idx][:5]))
+    case.check(out, what=str((GRID + PASS)[idx][:5]))
     o16 = case.run(f32=False)
     want = oracle.round_to_dtype(out.double().cpu().numpy(), case.dtype)
     assert np.array_equal(host_bits(o16), want)
 
 
-# a long pass beside the decode kernel, and neighbouring heads of the suffixes together
+# long prefixes, and neighbouring heads of the suffixes together
 LONG = [
+    # with a pass
+    ("bf16", 128, 8, 8, 16, [0, 40], [1000], [1000 + 5 * i for i in range(40)], 20480),
+    ("fp16", 64, 24, 6, 8, [0, 60], [900], [900 + 3 * i for i in range(60)], 8192),
     # dtype, d, Hq, Hkv, B, group starts, prefixes, lengths, table tokens
     ("bf16", 128, 8, 2, 16, [0, 5], [2100], [2100, 2101, 2200, 2731, 2115], None),
     ("fp16", 64, 16, 2, 64, [0, 2, 6], [2300, 2048], [2301, 2400, 2048, 2050, 2111, 2600], None),
@@ -151,10 +180,13 @@ def test_long_prefixes_and_wide_tables(idx):
     assert pa.bad_index_count(clear=True) == 0
 
 
-def test_workspace_may_hold_anything():
-    case = Case("bf16", 128, 8, 2, 16, [0, 4, 7], [600, 100], [601, 1500, 600, 900, 100, 5, 2000])
+@pytest.mark.parametrize("more", [0, 80])
+def test_workspace_may_hold_anything(more):
+    case = Case("bf16", 128, 8, 2, 16, [0, 4 + more, 7 + more], [600, 100],
+                [601, 1500, 600, 900] + [605 + i for i in range(more)] + [100, 5, 2000])
+    assert case.passes() == (more > 0)
     case.upload()
-    n = pa.decode_shared_prefix_workspace_bytes(7, 2, 8, 2, 128, case.bt.shape[1], 16, 600, 4)
+    n = pa.decode_shared_prefix_workspace_bytes(7 + more, 2, 8, 2, 128, case.bt.shape[1], 16, 600, 4 + more)
     first = None
     for byte in (0, 0xFF, 0x7F, 0x80):
         out = case.run(torch.full((n,), byte, dtype=torch.uint8, device="cuda"))
@@ -164,27 +196,37 @@ def test_workspace_may_hold_anything():
 
 
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 1.5])
-@pytest.mark.parametrize("dtype,Hq,B", [("bf16", 8, 16), ("fp16", 14, 2)])
-def test_scales(scale, dtype, Hq, B):
-    case = Case(dtype, 64, Hq, 2, B, [0, 3, 5], [200, 33], [200, 333, 201, 40, 700], seed=70)
+@pytest.mark.parametrize("dtype,Hq,B,more", [("bf16", 8, 16, 0), ("fp16", 14, 2, 0), ("bf16", 8, 16, 200),
+                                             ("fp16", 10, 2, 200)])
+def test_scales(scale, dtype, Hq, B, more):
+    case = Case(dtype, 64, Hq, 2, B, [0, 3 + more, 5 + more], [400, 33],
+                [400, 533, 401] + [400 + i % 50 for i in range(more)] + [40, 700], seed=70)
+    assert case.passes() == (more > 0)
     case.scale = scale
     case.check(case.run())
 
 
-def test_sequences_shorter_than_the_prefix_are_computed_alone():
-    case = Case("bf16", 128, 8, 2, 16, [0, 6], [100], [120, 40, 0, 100, 99, 101])
+@pytest.mark.parametrize("more", [0, 400])
+def test_sequences_shorter_than_the_prefix_are_computed_alone(more):
+    case = Case("bf16", 128, 8, 2, 16, [0, 6 + more], [100],
+                [120, 40, 0, 100, 99, 101] + [90 + i % 30 for i in range(more)])
+    assert case.passes() == (more > 0)
     case.check(case.run())
 
 
-def test_first_member_shorter_than_the_prefix():
+@pytest.mark.parametrize("prefix,more", [(64, 0), (512, 150)])
+def test_first_member_shorter_than_the_prefix(prefix, more):
     # its table still names the prefix's blocks for the others
-    case = Case("fp16", 64, 4, 2, 8, [0, 3], [64], [80, 90, 64])
+    case = Case("fp16", 64, 4, 2, 8, [0, 3 + more], [prefix], [prefix + 16, prefix + 26, prefix] + [prefix + 3] * more)
+    assert case.passes() == (more > 0)
     case.lens[0] = 17
     case.check(case.run())
 
 
-def test_prefixes_and_groups_above_the_bounds_given():
-    case = Case("bf16", 128, 8, 2, 16, [0, 5, 7], [300, 20], [301, 320, 333, 400, 350, 20, 25], hide=False)
+@pytest.mark.parametrize("more", [0, 160])
+def test_prefixes_and_groups_above_the_bounds_given(more):
+    case = Case("bf16", 128, 8, 2, 16, [0, 5, 7 + more], [300, 280],
+                [301, 320, 333, 400, 350, 280, 285] + [281 + i % 40 for i in range(more)], hide=False)
     # members' tables agree with the first one's where a prefix is cut short
     for g in range(2):
         a, b, n = case.starts[g], case.starts[g + 1], case.prefixes[g]
@@ -192,7 +234,8 @@ def test_prefixes_and_groups_above_the_bounds_given():
         case.bt[a:b, :j] = case.bt[a, :j]
     case.table = case.bt.copy()
     pa.bad_index_count(clear=True)
-    for mp, mg in ((100, 5), (300, 2), (0, 5), (300, 0), (64, 1)):
+    assert case.passes() == (more > 0)
+    for mp, mg in ((100, 5), (300, 2), (0, 5), (300, 0), (64, 1), (250, 2 + more)):
         case.check(case.run(max_prefix=mp, max_group=mg), what=f"max_prefix {mp}, max_group {mg}")
         assert pa.bad_index_count(clear=True) > 0
 
@@ -221,22 +264,29 @@ def test_infinite_and_nan_slots_behind_the_lengths_are_not_read():
     case.check(case.run())
 
 
-def test_bad_blocks_in_prefix_and_suffix_read_as_zeros():
-    case = Case("bf16", 64, 4, 2, 16, [0, 3], [64], [80, 90, 100])
+@pytest.mark.parametrize("prefix,more", [(64, 0), (512, 150)])
+def test_bad_blocks_in_prefix_and_suffix_read_as_zeros(prefix, more):
+    case = Case("bf16", 64, 4, 2, 16, [0, 3 + more], [prefix],
+                [prefix + 16, prefix + 26, prefix + 36] + [prefix + 9] * more)
+    assert case.passes() == (more > 0)
     case.table[0, 1] = 10 ** 6   # in the prefix, of the first member: for the whole group
-    case.table[2, 5] = -5        # in a suffix
+    last = case.lens[2] // 16 - 1
+    case.table[2, last] = -5     # in a suffix
     NB = case.kc.shape[0]
     case.upload()
     pa.bad_index_count(clear=True)
     out = case.run()
     assert pa.bad_index_count(clear=True) > 0
     case.kc, case.vc = (np.concatenate([x, np.zeros_like(x[:1])]) for x in (case.kc, case.vc))
-    case.bt[0, 1], case.bt[2, 5] = NB, NB
+    case.bt[0, 1], case.bt[2, last] = NB, NB
     case.check(out)
 
 
-def test_group_starts_that_make_no_sense_touch_nothing_else():
-    case = Case("bf16", 64, 4, 2, 16, [0, 2, 4], [32, 32], [40, 50, 60, 33], hide=False)
+@pytest.mark.parametrize("prefix,more", [(32, 0), (512, 150)])
+def test_group_starts_that_make_no_sense_touch_nothing_else(prefix, more):
+    case = Case("bf16", 64, 4, 2, 16, [0, 2, 4 + more], [prefix, prefix],
+                [prefix + 8, prefix + 18, prefix + 28, prefix + 1] + [prefix + 2] * more, hide=False)
+    assert case.passes() == (more > 0)
     case.upload()
     case.gs = up(np.array([3, -7, 99], np.int32))
     case.pl = up(np.array([-4, 10 ** 9], np.int32))
@@ -246,10 +296,13 @@ def test_group_starts_that_make_no_sense_touch_nothing_else():
     assert torch.isfinite(out).all()
 
 
-def test_repeated_calls_and_other_calls_on_one_workspace():
-    case = Case("bf16", 128, 8, 2, 16, [0, 12], [900], [900 + 97 * i for i in range(12)])
+@pytest.mark.parametrize("more", [0, 40])
+def test_repeated_calls_and_other_calls_on_one_workspace(more):
+    case = Case("bf16", 128, 8, 2, 16, [0, 12 + more], [900], [900 + 97 * i for i in range(12)] + [931] * more)
+    assert case.passes() == (more > 0)
     case.upload()
-    n = pa.decode_shared_prefix_workspace_bytes(12, 1, 8, 2, 128, case.bt.shape[1], 16, 900, 12)
+    S = 12 + more
+    n = pa.decode_shared_prefix_workspace_bytes(S, 1, 8, 2, 128, case.bt.shape[1], 16, 900, S)
     ws = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
     first = case.run(ws)
     case.check(first)
@@ -258,19 +311,22 @@ def test_repeated_calls_and_other_calls_on_one_workspace():
     for _ in range(3):
         other.check(other.run(ws))
         pa.decode(plain, case.q, case.kd, case.vd, up(case.bt), case.sl, case.scale, 64,
-                  torch.zeros(pa.decode_workspace_bytes(12, 8, 128, case.bt.shape[1], 16, 64), dtype=torch.uint8,
+                  torch.zeros(pa.decode_workspace_bytes(S, 8, 128, case.bt.shape[1], 16, 64), dtype=torch.uint8,
                               device="cuda"))
         assert torch.equal(case.run(ws), first)
 
 
-def test_captured_and_replayed_with_other_lengths():
-    case = Case("bf16", 128, 8, 2, 16, [0, 4, 6], [256, 64], [300, 280, 257, 500, 70, 64])
+@pytest.mark.parametrize("more", [0, 160])
+def test_captured_and_replayed_with_other_lengths(more):
+    case = Case("bf16", 128, 8, 2, 16, [0, 4 + more, 6 + more], [256, 64],
+                [300, 280, 257, 500] + [260 + i % 33 for i in range(more)] + [70, 64])
+    assert case.passes() == (more > 0)
     case.upload()
-    ws = pa.alloc_shared_prefix_workspace(case.q, case.kd, case.btd, case.gs, 256, 4)
+    ws = pa.alloc_shared_prefix_workspace(case.q, case.kd, case.btd, case.gs, 256, 4 + more)
     out = torch.empty(case.query.shape, dtype=torch.float32, device="cuda")
 
     def step():
-        pa.decode_shared_prefix(out, case.q, case.kd, case.vd, case.btd, case.sl, case.gs, case.pl, 256, 4,
+        pa.decode_shared_prefix(out, case.q, case.kd, case.vd, case.btd, case.sl, case.gs, case.pl, 256, 4 + more,
                                 case.scale, ws)
 
     side = torch.cuda.Stream()
@@ -284,7 +340,7 @@ def test_captured_and_replayed_with_other_lengths():
         step()
     for lens, prefixes in (([300, 280, 257, 500, 70, 64], [256, 64]), ([290, 256, 257, 300, 66, 65], [128, 33]),
                            ([10, 20, 30, 0, 70, 64], [0, 64])):
-        case.lens[:], case.prefixes[:] = lens, prefixes
+        case.lens[:4], case.lens[4 + more:], case.prefixes[:] = lens[:4], lens[4:], prefixes
         case.btd.copy_(torch.from_numpy(case.bt))
         case.sl.copy_(torch.from_numpy(case.lens))
         case.pl.copy_(torch.from_numpy(case.prefixes))
