@@ -655,20 +655,26 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 // ---------------------------------------------------------------------------
 // Merge
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 4;
-constexpr long long kTogetherRows = 152 * 16;  // fewer query rows: a CTA for each
+// Up to kTogetherRows query rows: a CTA of 8 warps for each (512 rows of 57 pieces:
+// the call takes 218 us, 220 with 4 warps, 214 and 212 with 16 and 8 on a faster
+// box, 228 with a warp for each). More rows: a warp for each (2048 rows: 52 us, 58
+// with 8 warps).
+template <bool TOGETHER>
+constexpr int kMergeWarps = TOGETHER ? 8 : 4;
+constexpr long long kTogetherRows = 152 * 8;
 
 // out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over a query row's pieces,
 // the prefix pass's first, in order. A row without segments was finished by the
 // streaming kernel. TOGETHER: a CTA takes a row, each warp a
 // share of its pieces (few rows, of many pieces); otherwise each warp takes one.
 template <typename Ty, int D, bool TOGETHER>
-__global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const StreamArgs a) {
+__global__ void __launch_bounds__(kMergeWarps<TOGETHER> * 32) decode_merge_kernel(const StreamArgs a) {
   using T = typename Ty::T;
+  constexpr int W = kMergeWarps<TOGETHER>;
   constexpr int E = D / 32;  // columns per lane
   using Vec = std::conditional_t<E == 4, float4, float2>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = TOGETHER ? blockIdx.x : static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
+  const long long row = TOGETHER ? blockIdx.x : static_cast<long long>(blockIdx.x) * W + warp;
   const int s = static_cast<int>(row / a.num_q_heads), hq = static_cast<int>(row % a.num_q_heads);
   const int h = hq / a.group, g = hq % a.group;
   const int Lmax = a.max_blocks_per_seq << a.block_shift;
@@ -694,7 +700,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const St
       const float* p = k < before ? a.pre_out + (pre + k) * D : a.seg_out + piece_at(k) * D;
       return __ldcg(reinterpret_cast<const Vec*>(p) + lane);
     };
-    const int share = TOGETHER ? (n + kMergeWarps - 1) / kMergeWarps : n;
+    const int share = TOGETHER ? (n + W - 1) / W : n;
     const int k_lo = TOGETHER ? min(warp * share, n) : 0, k_hi = min(k_lo + share, n);
     float M = -INFINITY;
     for (int k = k_lo + lane; k < k_hi; k += 32) M = fmaxf(M, lse_at(k));
@@ -724,7 +730,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const St
       }
     }
     if constexpr (TOGETHER) {
-      __shared__ float sM[kMergeWarps], sDen[kMergeWarps], sAcc[kMergeWarps][D];
+      __shared__ float sM[W], sDen[W], sAcc[W][D];
       if (lane == 0) {
         sM[warp] = M;
         sDen[warp] = den;
@@ -734,11 +740,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const St
       __syncthreads();
       if (warp != 0) return;
       float top = -INFINITY;
-      for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, sM[w]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, sM[w]);
       den = 0.f;
 #pragma unroll
       for (int i = 0; i < E; ++i) acc[i] = 0.f;
-      for (int w = 0; w < kMergeWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float f = sM[w] == -INFINITY ? 0.f : ex2(sM[w] - top);
         den += f * sDen[w];
 #pragma unroll
@@ -834,17 +840,21 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   const long long pass = a.groups.pass_ctas <= num_sms ? a.groups.pass_ctas : 0;
   const long long ctas = std::min<long long>((NT == 1 ? 3 : 2) * (num_sms - pass) + pass, kMaxCtas);
   const long long rows = static_cast<long long>(a.num_seqs) * (a.num_kv_heads / a.heads_at_a_time);
-  const long long most = (static_cast<long long>(a.max_blocks_per_seq) << a.block_shift) / Tile<D, FP8>::kTokens + 2;
-  const long long grid = std::min(ctas, rows * (a.cut ? (most + a.least_tiles - 1) / a.least_tiles : 1));
+  // no more CTAs than the longest rows have shares, in stages of ST tokens
+  const int warps_a_head = kWarps / a.heads_at_a_time, ST = warps_a_head * Tile<D, FP8>::kTokens;
+  const long long most = (static_cast<long long>(a.max_blocks_per_seq) << a.block_shift) / ST + 2;
+  const long long least = (a.least_tiles + warps_a_head - 1) / warps_a_head;
+  const long long grid = std::min(ctas, rows * (a.cut ? (most + least - 1) / least : 1));
   Dependent d(dim3(static_cast<unsigned>(std::max(grid, 1ll))), kThreads, smem, stream,
               a.groups.max_chunks > 0);  // behind a prefix pass
   e = cudaLaunchKernelEx(&d.cfg, kern, km, vm, a);
   if (e != cudaSuccess || a.ws_rows == nullptr) return e;  // rows are whole, and there is no prefix
   const long long q_rows = static_cast<long long>(a.num_seqs) * a.num_q_heads;
   const bool together = q_rows <= kTogetherRows;
-  const long long blocks = together ? q_rows : (q_rows + kMergeWarps - 1) / kMergeWarps;
+  const int warps = together ? kMergeWarps<true> : kMergeWarps<false>;
+  const long long blocks = together ? q_rows : (q_rows + warps - 1) / warps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  Dependent m(dim3(static_cast<unsigned>(blocks)), 32 * kMergeWarps, 0, stream, true);
+  Dependent m(dim3(static_cast<unsigned>(blocks)), 32 * warps, 0, stream, true);
   return together ? cudaLaunchKernelEx(&m.cfg, decode_merge_kernel<Ty, D, true>, a)
                   : cudaLaunchKernelEx(&m.cfg, decode_merge_kernel<Ty, D, false>, a);
 }
