@@ -241,7 +241,7 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   // sequence reads the prefix itself, through its group's table. With fewer CTAs a
   // chunk than a quarter of the SMs the two met at about 32 MB: 26 sequences in 3
   // groups behind 2790 tokens of one head, 33 MB: 20.8 us, 25.7 without; 21 behind
-  // 916 of three, 21 MB: 14.7 and 15.5; 7 behind 333: 12.9 and 11.3. With more CTAs,
+  // 916 of three, 21 MB: 14.7 and 15.5; 7 behind 333: 12.9 and 9.8. With more CTAs,
   // at about 128: 230 sequences in 146 groups behind 1150 of three heads, 74 MB: 59
   // and 49; 67 in 4 groups behind 709 of 16, 366 MB: 25 and 37.
   const double saved =
