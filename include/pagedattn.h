@@ -506,10 +506,11 @@ int pa_bad_index_count(unsigned long long* count, int clear);
 
 /*
  * Number of bounded waits inside the kernels on the CURRENT device that gave
- * up since the counter was last cleared. The tensor-core prefill kernel's
- * warps wait on each other through shared-memory barriers; every such wait
- * has a limit of about one second, after which the kernel counts it here and
- * winds down instead of hanging (its output is then invalid). Always 0 in
+ * up since the counter was last cleared. The warps of the tensor-core prefill
+ * kernel and of the streaming decode kernel (pa_decode_fp8,
+ * pa_decode_shared_prefix) wait on each other through shared-memory barriers;
+ * every such wait has a limit of about one second, after which the kernel counts
+ * it here and winds down instead of hanging (its output is then invalid). Always 0 in
  * correct operation. Synchronises the device; *count is a host pointer;
  * clears the counter when `clear` is non-zero.
  * Errors: PA_ERR_INVALID (count is NULL), PA_ERR_CUDA.

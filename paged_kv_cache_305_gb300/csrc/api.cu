@@ -811,7 +811,8 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
                 int max_blocks_per_seq, int num_blocks, int partition_tokens, pa_dtype dtype,
                 pa_dtype out_dtype, void* workspace, size_t workspace_bytes, bool fp8,
                 const uint8_t* scales, const int32_t* group_start, const int32_t* prefix_lens,
-                int num_groups, int max_prefix_len, int max_group_size, cudaStream_t stream) {
+                int num_groups, int max_prefix_len, int max_group_size, int stall_for_test,
+                cudaStream_t stream) {
   g_error.clear();
   int rc = check_dtype(dtype);
   if (rc != PA_OK) return rc;
@@ -929,6 +930,7 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   }
   a.bad = bad;
   a.timeouts = timeouts;
+  a.stall_for_test = stall_for_test;
   const bool bf16 = dtype == PA_BFLOAT16;
   cudaError_t e = cudaSuccess;
   if (groups.max_chunks > 0) {
@@ -971,7 +973,20 @@ int pa_decode_fp8(void* out, const void* query, const void* key_cache, const voi
   return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
                      num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, true,
-                     cache_scales, nullptr, nullptr, 0, 0, 0, stream);
+                     cache_scales, nullptr, nullptr, 0, 0, 0, 0, stream);
+}
+
+int pa_testing_decode_fp8_stalled(void* out, const void* query, const void* key_cache,
+                                  const void* value_cache, const uint8_t* cache_scales,
+                                  const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                                  int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  float scale, int max_blocks_per_seq, int num_blocks,
+                                  int partition_tokens, pa_dtype dtype, pa_dtype out_dtype,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
+                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, true,
+                     cache_scales, nullptr, nullptr, 0, 0, 0, 1, stream);
 }
 
 int pa_decode_shared_prefix(void* out, const void* query, const void* key_cache,
@@ -986,7 +1001,20 @@ int pa_decode_shared_prefix(void* out, const void* query, const void* key_cache,
   return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
                      num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, false, nullptr,
-                     group_start, prefix_lens, num_groups, max_prefix_len, max_group_size, stream);
+                     group_start, prefix_lens, num_groups, max_prefix_len, max_group_size, 0, stream);
+}
+
+int pa_testing_decode_shared_prefix_stalled(
+    void* out, const void* query, const void* key_cache, const void* value_cache,
+    const int32_t* block_tables, const int32_t* seq_lens, const int32_t* group_start,
+    const int32_t* prefix_lens, int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, float scale, int max_blocks_per_seq, int num_blocks,
+    int max_prefix_len, int max_group_size, pa_dtype dtype, pa_dtype out_dtype, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream) {
+  return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
+                     num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, false, nullptr,
+                     group_start, prefix_lens, num_groups, max_prefix_len, max_group_size, 1, stream);
 }
 
 size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,

@@ -360,9 +360,10 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
         p += hg * group;
       }
-      // rows from there on, 32 at a time
+      // rows from there on, 32 at a time; all of them, also when a wait has given up and
+      // nothing is filled any more: the merge kernel reads every row's entry of ws_rows
       bool more = true;
-      while (more && ok) {
+      while (more) {
         const unsigned at = static_cast<unsigned>(s) + lane;
         const int my_hg = hg + static_cast<int>(at / S), my_s = static_cast<int>(at % S);
         Row r{};
@@ -556,7 +557,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
       }
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(empty(stage));
+      if (lane == 0 && a.stall_for_test == 0) tc::mbar_arrive(empty(stage));
       if (!(note.flags & kLast)) continue;
 
       // ---- segment end: join the states of the head's warps ---------------

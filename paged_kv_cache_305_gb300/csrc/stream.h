@@ -49,6 +49,7 @@ struct StreamArgs {
   float* seg_out;
   unsigned long long* bad;
   unsigned long long* timeouts;  // bounded waits that gave up
+  int stall_for_test;   // 1: no stage is ever handed back to the feeding warp
 };
 
 // The prefix pass: a prefill whose positions are the sequences of a group.

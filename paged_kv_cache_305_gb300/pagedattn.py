@@ -28,7 +28,8 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_bytes", "pa_decode",
             "pa_decode_partition_tokens", "pa_reshape_and_cache_fp8", "pa_copy_blocks_fp8",
             "pa_gather_cache_fp8", "pa_decode_fp8", "pa_decode_shared_prefix",
             "pa_decode_fp8_workspace_bytes",
-            "pa_decode_shared_prefix_workspace_bytes")
+            "pa_decode_shared_prefix_workspace_bytes", "pa_testing_decode_fp8_stalled",
+            "pa_testing_decode_shared_prefix_stalled")
 PA_ERR_CAPACITY = -5
 
 _lib = None
@@ -93,12 +94,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.pa_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float,
                                 i32, i32, i32, i32, i32, vp, sz, vp]
     L.pa_decode_fp8.restype = i32
+    L.pa_testing_decode_fp8_stalled.argtypes = L.pa_decode_fp8.argtypes
+    L.pa_testing_decode_fp8_stalled.restype = i32
     L.pa_decode_fp8_workspace_bytes.argtypes = [i32] * 6
     L.pa_decode_fp8_workspace_bytes.restype = sz
     L.pa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                           i32, ctypes.c_float, i32, i32, i32, i32, i32, i32, vp, sz,
                                           vp]
     L.pa_decode_shared_prefix.restype = i32
+    L.pa_testing_decode_shared_prefix_stalled.argtypes = L.pa_decode_shared_prefix.argtypes
+    L.pa_testing_decode_shared_prefix_stalled.restype = i32
     L.pa_decode_shared_prefix_workspace_bytes.argtypes = [i32] * 9
     L.pa_decode_shared_prefix_workspace_bytes.restype = sz
     ip = ctypes.POINTER(ctypes.c_int)
@@ -573,10 +578,27 @@ def decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
     ``query`` is float16 or bfloat16; the workspace comes from
     :func:`alloc_workspace` with the 8-bit ``key_cache``.
     """
+    return _decode_fp8(load_library().pa_decode_fp8, out, query, key_cache, value_cache, cache_scales,
+                       block_tables, seq_lens, scale, partition_tokens, workspace, stream)
+
+
+def testing_decode_fp8_stalled(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor, cache_scales: torch.Tensor,
+                               block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                               partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
+                               stream=None) -> torch.Tensor:
+    """Test hook (include/pagedattn_testing.h): :func:`decode_fp8` whose ring is never
+    emptied, so bounded waits give up and the launches wind down."""
+    return _decode_fp8(load_library().pa_testing_decode_fp8_stalled, out, query, key_cache, value_cache,
+                       cache_scales, block_tables, seq_lens, scale, partition_tokens, workspace, stream)
+
+
+def _decode_fp8(entry, out, query, key_cache, value_cache, cache_scales, block_tables, seq_lens, scale,
+                partition_tokens, workspace, stream):
     NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
     device, (S, Hq, MB), rest = _need_decode(out, query, d, block_tables, seq_lens, workspace,
                                              key_cache, value_cache, cache_scales)
-    _enqueue(load_library().pa_decode_fp8, device, stream, out.data_ptr(), query.data_ptr(),
+    _enqueue(entry, device, stream, out.data_ptr(), query.data_ptr(),
              key_cache.data_ptr(), value_cache.data_ptr(), cache_scales.data_ptr(),
              block_tables.data_ptr(), seq_lens.data_ptr(), S, Hq, Hkv, d, B, float(scale),
              MB, NB, int(partition_tokens), *rest)
@@ -617,6 +639,27 @@ def decode_shared_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torc
     ``max_group_size`` bound both on the host. The workspace comes from
     :func:`alloc_shared_prefix_workspace`.
     """
+    return _decode_shared_prefix(load_library().pa_decode_shared_prefix, out, query, key_cache,
+                                 value_cache, block_tables, seq_lens, group_start, prefix_lens,
+                                 max_prefix_len, max_group_size, scale, workspace, stream)
+
+
+def testing_decode_shared_prefix_stalled(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                         value_cache: torch.Tensor, block_tables: torch.Tensor,
+                                         seq_lens: torch.Tensor, group_start: torch.Tensor,
+                                         prefix_lens: torch.Tensor, max_prefix_len: int,
+                                         max_group_size: int, scale: float,
+                                         workspace: Optional[torch.Tensor] = None,
+                                         stream=None) -> torch.Tensor:
+    """Test hook (include/pagedattn_testing.h): :func:`decode_shared_prefix` with the
+    streaming kernel of :func:`testing_decode_fp8_stalled`."""
+    return _decode_shared_prefix(load_library().pa_testing_decode_shared_prefix_stalled, out, query,
+                                 key_cache, value_cache, block_tables, seq_lens, group_start,
+                                 prefix_lens, max_prefix_len, max_group_size, scale, workspace, stream)
+
+
+def _decode_shared_prefix(entry, out, query, key_cache, value_cache, block_tables, seq_lens, group_start,
+                          prefix_lens, max_prefix_len, max_group_size, scale, workspace, stream):
     NB, B, Hkv, d = key_cache.shape
     _need(value_cache.shape == key_cache.shape, "cache shape mismatch")
     _need(query.dtype == key_cache.dtype == value_cache.dtype, "query/cache dtype mismatch")
@@ -626,7 +669,7 @@ def decode_shared_prefix(out: torch.Tensor, query: torch.Tensor, key_cache: torc
           "group_start/prefix_lens shape mismatch")
     device, (S, Hq, MB), rest = _need_decode(out, query, d, block_tables, seq_lens, workspace,
                                              key_cache, value_cache, group_start, prefix_lens)
-    _enqueue(load_library().pa_decode_shared_prefix, device, stream, out.data_ptr(),
+    _enqueue(entry, device, stream, out.data_ptr(),
              query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
              block_tables.data_ptr(), seq_lens.data_ptr(), group_start.data_ptr(),
              prefix_lens.data_ptr(), S, prefix_lens.shape[0], Hq, Hkv, d, B, float(scale),

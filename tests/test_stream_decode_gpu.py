@@ -1,0 +1,76 @@
+"""The streaming decode kernel where it could go wrong unseen: waits that run out."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import paged_kv_cache_305_gb300 as pa
+import workloads as W
+from gpu_util import dev_bits
+from test_fp8_cache_gpu import random_pool, tables_for, up, up8
+from test_shared_prefix_gpu import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_305_gb300 import build
+    build.build()
+    pa.wait_timeout_count(clear=True)
+    yield
+    torch.cuda.synchronize()
+    assert pa.wait_timeout_count(clear=True) == 0
+
+
+# ------------------------------------------------------ waits that run out --
+def rows_in_range(ws, rows, slots):
+    """Every row's entry (first slot, number of pieces) at the start of the workspace names slots that exist."""
+    first, pieces = ws[:8 * rows].view(torch.int32).view(rows, 2).long().unbind(1)
+    cut = pieces != 0
+    return bool(((pieces >= 0) & (pieces <= 456)).all()) and bool(
+        ((first >= 0) & (first + pieces <= slots))[cut].all())
+
+
+@pytest.mark.parametrize("B", [16, 4])
+def test_8_bit_decode_whose_waits_run_out_ends_and_is_counted(B):
+    # some 90 short rows a CTA: the wait gives up in the first rows of its share, and
+    # the merge kernel has to find an entry for the others too, whatever the workspace held
+    rng = np.random.default_rng(B)
+    S, Hq, Hkv, d, NB = 40000, 2, 1, 64, 64
+    lens = rng.integers(1, 40, S).astype(np.int32)
+    lens[::1000] = 700
+    kc, vc, sc = random_pool(rng, NB, B, Hkv, d, 1)
+    bt = torch.randint(0, NB, (S, 1024 // B), dtype=torch.int32, device="cuda")
+    q = dev_bits(W.normal_bits((S, Hq, d), "bf16", B, 2), "bf16")
+    n = pa.decode_fp8_workspace_bytes(S, Hq, Hkv, d, 1024 // B, B)
+    assert n > 0
+    args = (q, up8(kc), up8(vc), up(sc), bt, up(lens), 0.125, 0)
+    fresh = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    pa.decode_fp8(fresh, *args, torch.zeros(n, dtype=torch.uint8, device="cuda"))
+    pa.wait_timeout_count(clear=True)
+    ws = torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+    pa.testing_decode_fp8_stalled(torch.empty_like(fresh), *args, ws)
+    assert pa.wait_timeout_count(clear=True) >= 1
+    assert rows_in_range(ws, S * Hkv, S * Hkv + 456)
+    out = torch.full_like(fresh, float("nan"))
+    pa.decode_fp8(out, *args, ws)
+    assert torch.equal(out, fresh)
+    assert pa.wait_timeout_count(clear=True) == 0
+
+
+def test_shared_prefix_decode_whose_waits_run_out_ends_and_is_counted():
+    case = Case("bf16", 128, 8, 2, 16, [0, 100, 103], [600, 50], [600 + 20 * i for i in range(100)] + [50, 51, 900])
+    assert case.passes()
+    fresh = case.run()
+    n = pa.decode_shared_prefix_workspace_bytes(103, 2, 8, 2, 128, case.bt.shape[1], 16, 600, 100)
+    ws = torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+    pa.wait_timeout_count(clear=True)
+    pa.testing_decode_shared_prefix_stalled(torch.empty_like(fresh), case.q, case.kd, case.vd, case.btd, case.sl,
+                                            case.gs, case.pl, 600, 100, case.scale, ws)
+    assert pa.wait_timeout_count(clear=True) >= 1
+    assert rows_in_range(ws, 103 * 2, 103 * 2 + 456)
+    assert torch.equal(case.run(ws), fresh)
+    assert pa.wait_timeout_count(clear=True) == 0
