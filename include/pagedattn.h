@@ -365,8 +365,9 @@ int pa_gather_cache_fp8(void* key_out, void* value_out,
  * the GPU. Eager calls of pa_decode may use it in between; but a replayed graph
  * that holds this call leaves it as no pa_decode expects it, and a captured
  * pa_decode does not expect what this call leaves: give graphs of the two
- * workspaces of their own (or zero it in between). num_seqs * num_kv_heads *
- * (max_blocks_per_seq * block_size / 32 + 2) must be below 2^31. A wait for
+ * workspaces of their own (or zero it in between). max_blocks_per_seq *
+ * block_size must be at most 2^31 - 4096, and num_seqs * num_kv_heads *
+ * (max_blocks_per_seq * block_size / 32 + 2) below 2^31. A wait for
  * a copy that gives up is counted (pa_wait_timeout_count).
  * Other arguments, sizes and errors as for pa_decode.
  */
@@ -412,7 +413,7 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
  * the arrays is touched).
  * num_groups in [1, 65535] (unless num_seqs is 0), num_blocks * block_size
  * and num_seqs * num_kv_heads * (max_blocks_per_seq * block_size / 16 + 2)
- * below 2^31. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
+ * below 2^31, max_blocks_per_seq * block_size at most 2^31 - 4096. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
  * shared with other calls as pa_decode_fp8's. Softmax weights enter as the sum
  * of two parts of the cache's type; waits that give up are counted as there.
  * Other arguments and errors as for pa_decode.

@@ -247,7 +247,8 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   const double saved =
       static_cast<double>(x->num_seqs - num_groups) * x->max_prefix_len * num_kv_heads * head_dim * 4;
   const bool pass = max_group_size > 0 && saved > (per_chunk <= kPrefixSms / 4 ? kPassBytes : kWidePassBytes);
-  x->max_chunks = pass ? (x->max_prefix_len + x->chunk_tokens - 1) / x->chunk_tokens : 0;
+  x->max_chunks =
+      pass ? static_cast<int>((static_cast<long long>(x->max_prefix_len) + x->chunk_tokens - 1) / x->chunk_tokens) : 0;
   x->pass_ctas = per_chunk * x->max_chunks;
 }
 
@@ -847,8 +848,9 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   if (partition_tokens > pa::kMaxPartitionTokens)
     return fail(PA_ERR_UNSUPPORTED, "partition_tokens %d > %d", partition_tokens, pa::kMaxPartitionTokens);
   const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
-  if (lmax > 0x7fffffffll)
-    return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size = %lld overflows int", lmax);
+  if (lmax > pa::kMostTokens)
+    return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size = %lld above %lld: a tile's end overflows int",
+                lmax, pa::kMostTokens);
   if (num_seqs > 65535 || num_kv_heads > 65535)
     return fail(PA_ERR_UNSUPPORTED, "num_seqs %d / num_kv_heads %d above 65535", num_seqs, num_kv_heads);
   // positions on the line of tiles (of 16 or 32 tokens) are 32-bit in the kernel
@@ -1019,12 +1021,12 @@ int pa_testing_decode_shared_prefix_stalled(
 
 size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                      int max_blocks_per_seq, int block_size) {
+  const long long lmax = static_cast<long long>(max_blocks_per_seq) * block_size;
   if (num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 ||
-      (head_dim != 64 && head_dim != 128) || max_blocks_per_seq < 1 || log2_pow2(block_size) < 0)
+      (head_dim != 64 && head_dim != 128) || max_blocks_per_seq < 1 || log2_pow2(block_size) < 0 ||
+      lmax > pa::kMostTokens)
     return 0;
-  return pa::stream_layout(true, num_seqs, num_q_heads, num_kv_heads, head_dim,
-                           static_cast<long long>(max_blocks_per_seq) * block_size, pa::PrefixArgs{})
-      .total;
+  return pa::stream_layout(true, num_seqs, num_q_heads, num_kv_heads, head_dim, lmax, pa::PrefixArgs{}).total;
 }
 
 size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,
@@ -1035,7 +1037,7 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
   if (num_seqs < 0 || num_groups < 1 || num_q_heads < 1 || num_kv_heads < 1 ||
       num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > pa::kMaxGroup ||
       (head_dim != 64 && head_dim != 128) || max_blocks_per_seq < 1 || log2_pow2(block_size) < 0 ||
-      max_prefix_len < 0 || max_group_size < 0 || lmax > 0x7fffffffll)
+      max_prefix_len < 0 || max_group_size < 0 || lmax > pa::kMostTokens)
     return 0;
   pa::PrefixArgs x{};
   x.num_seqs = num_seqs;

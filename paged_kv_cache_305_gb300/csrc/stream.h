@@ -84,6 +84,9 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
 // kUncutTokens leave rows whole, or of up to kUncutTiles tiles where there are
 // fewer rows than kFewRows (stream_layout).
 constexpr int kMaxCtas = 456;
+// Tokens of a table: the kernels' ints hold positions up to a tile or a feeding
+// warp's 32 blocks of 64 tokens behind a row's last one.
+constexpr long long kMostTokens = (1ll << 31) - 4096;
 constexpr int kLeastTiles = 4;
 constexpr long long kUncutTokens = 512, kUncutTiles = 8, kFewRows = 152;
 constexpr int kGroupTiles = 16;  // see stream_heads
