@@ -630,8 +630,12 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           float iv = l > 0.f ? 1.f / l : 0.f;
           if (l != l) iv = l;  // NaN scores give NaN
-          if constexpr (FP8) iv *= ex2(top - (127 + kWeightShift));
+          if constexpr (FP8) iv *= 1.f / (1 << kWeightShift);
           acc = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+          if constexpr (FP8) {  // a factor of its own: 2^(top - 127), times the rest, may be subnormal
+            const float ft = exponent_factor(static_cast<int>(top));
+            acc = make_float4(acc.x * ft, acc.y * ft, acc.z * ft, acc.w * ft);
+          }
           const size_t row = row0 + head;
           if (note.slot >= 0) {
             const size_t piece = (static_cast<size_t>(note.slot) * Hc + hsub) * G + head;

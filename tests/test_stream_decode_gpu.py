@@ -1,12 +1,15 @@
-"""The streaming decode kernel where it could go wrong unseen: waits that run out."""
+"""The streaming decode kernel where it could go wrong unseen: waits that run out,
+the ends of the types' ranges."""
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
+import oracle
 import paged_kv_cache_305_gb300 as pa
 import workloads as W
 from gpu_util import dev_bits
+from oracle import fp8
 from test_fp8_cache_gpu import random_pool, tables_for, up, up8
 from test_shared_prefix_gpu import Case
 
@@ -74,3 +77,32 @@ def test_shared_prefix_decode_whose_waits_run_out_ends_and_is_counted():
     assert rows_in_range(ws, 103 * 2, 103 * 2 + 456)
     assert torch.equal(case.run(ws), fresh)
     assert pa.wait_timeout_count(clear=True) == 0
+
+
+# -------------------------------------------------- the ends of the ranges --
+def decode8(query, kc, vc, sc, bt, lens, B, scale, dtype):
+    """fp32 outputs of the kernel and the exact ones, both float64."""
+    q, kd, btd = dev_bits(query, dtype), up8(kc), up(bt)
+    out = torch.full(query.shape, float("nan"), dtype=torch.float32, device="cuda")
+    pa.decode_fp8(out, q, kd, up8(vc), up(sc), btd, up(np.asarray(lens, np.int32)), scale, 0,
+                  pa.alloc_workspace(q, kd, btd))
+    ref = fp8.attend(query, fp8.pool_values(kc, sc, 0), fp8.pool_values(vc, sc, 1), bt, lens, B, scale, dtype)
+    return out.double().cpu().numpy(), ref
+
+
+@pytest.mark.parametrize("dtype,Hq,B,n", [("bf16", 4, 16, 90), ("fp16", 9, 4, 700)])
+def test_8_bit_values_next_to_the_smallest(dtype, Hq, B, n):
+    # V rows with exponent bytes 1 to 7, as rows of bf16 numbers below 3.4e-34 have
+    rng = np.random.default_rng(n)
+    d = 64
+    kc, vc, sc = random_pool(rng, -(-n // B), B, 1, d, 1)
+    sc[:, :, 1] = rng.integers(1, 8, sc[:, :, 1].shape)
+    bt = tables_for(rng, [n], B, kc.shape[0])
+    query = W.normal_bits((1, Hq, d), dtype, n, 2)
+    got, ref = decode8(query, kc, vc, sc, bt, [n], B, 0.01, dtype)
+    K, V = (oracle.gather_kv(fp8.pool_values(c, sc, i), bt[0], n, B) for i, c in enumerate((kc, vc)))
+    bound = fp8.decode_bound(oracle.to_float64(query[0], dtype), K, V, 0.01, 2.0 ** -20)
+    # pieces, their products with the merge's weights and the sum round to the subnormal
+    # grid: 2^-150 each, of at most two stages a piece (64 tokens a stage at least)
+    assert np.max(np.abs(got - ref)) <= bound + (3 * (-(-n // 64)) + 2) * 2.0 ** -150
+    assert np.max(np.abs(ref)) > 10 * bound  # zeros in the place of the result would be seen
