@@ -279,9 +279,9 @@ StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_h
   const size_t group = static_cast<size_t>(w.heads) * (num_q_heads / num_kv_heads);
   // one slot for each boundary of a row or a share on the line
   const size_t slots = static_cast<size_t>(num_seqs) * (num_kv_heads / w.heads) + kMaxCtas;
-  w.pre_lse = round_up(static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(int2), 256);
-  w.seg_lse = w.pre_lse + round_up(rows * max_chunks * sizeof(float), 256);
-  w.pre_out = w.seg_lse + round_up(slots * group * sizeof(float), 256);
+  w.pre_stat = round_up(static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(int2), 256);
+  w.seg_stat = w.pre_stat + round_up(rows * max_chunks * sizeof(float2), 256);
+  w.pre_out = w.seg_stat + round_up(slots * group * sizeof(float2), 256);
   w.seg_out = w.pre_out + rows * max_chunks * head_dim * sizeof(float);
   w.total = w.seg_out + slots * group * head_dim * sizeof(float);
   return w;
@@ -925,9 +925,9 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   a.least_tiles = std::max(partition_tokens / (fp8 ? 32 : 16), pa::kLeastTiles);
   if (wl.total > 0) {
     a.ws_rows = reinterpret_cast<int2*>(ws);
-    a.pre_lse = reinterpret_cast<float*>(ws + wl.pre_lse);
+    a.pre_stat = reinterpret_cast<float2*>(ws + wl.pre_stat);
     a.pre_out = reinterpret_cast<float*>(ws + wl.pre_out);
-    a.seg_lse = reinterpret_cast<float*>(ws + wl.seg_lse);
+    a.seg_stat = reinterpret_cast<float2*>(ws + wl.seg_stat);
     a.seg_out = reinterpret_cast<float*>(ws + wl.seg_out);
   }
   a.bad = bad;
@@ -951,7 +951,7 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
     p.bad = bad;
     p.timeouts = timeouts;
     p.groups = groups;
-    p.pre_lse = a.pre_lse;
+    p.pre_stat = a.pre_stat;
     p.pre_out = a.pre_out;
     e = pa::launch_prefix_pass(p, head_dim, bf16, stream);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");

@@ -21,8 +21,8 @@
 //
 // Pieces. The part of a row inside a share is a segment. A row that is one
 // segment is finished at once; otherwise each segment leaves a piece (fp32
-// normalised output and base-2 log-sum-exp), and a merge kernel behind this one
-// joins them, in order. A piece is stored and forgotten: a merge by the last
+// normalised output, reference and sum of its weights), and a merge kernel behind
+// this one joins them, in order. A piece is stored and forgotten: a merge by the last
 // one to arrive would fence, count and read the others back while its CTA waits
 // (that cost 10 % of the 128-sequence case). Segment (row R, share u) has the
 // slot R + u: every row and every share begins one boundary, so slots rise along
@@ -599,7 +599,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             }
             if (r8 == 0) {
               float* stat_w = sStats + warp * 3 * R::kHeads + head;
-              stat_w[0] = st.fresh ? -INFINITY : -st.nm[nt][c];  // in binary orders
+              stat_w[0] = st.fresh ? -INFINITY : st.m[nt][c];
               stat_w[R::kHeads] = st.l[nt][c];
               stat_w[2 * R::kHeads] = static_cast<float>(st.r);
             }
@@ -640,7 +640,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if (note.slot >= 0) {
             const size_t piece = (static_cast<size_t>(note.slot) * Hc + hsub) * G + head;
             *reinterpret_cast<float4*>(a.seg_out + piece * D + c4) = acc;
-            if (c4 == 0) a.seg_lse[piece] = l == 0.f ? -INFINITY : M + __log2f(l);
+            if (c4 == 0) a.seg_stat[piece] = make_float2(M, l);
           } else if (a.out_f32) {
             *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + c4) = acc;
           } else {
@@ -668,7 +668,8 @@ template <bool TOGETHER>
 constexpr int kMergeWarps = TOGETHER ? 8 : 4;
 constexpr long long kTogetherRows = 152 * 8;
 
-// out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M) over a query row's pieces,
+// out = sum_k f_k o_k / sum_k f_k, f_k = l_k / Lm 2^(m_k - M), M and Lm the largest m
+// and l (weights of at most 1: sums of large V must not overflow), over a query row's pieces,
 // the prefix pass's first, in order. A row without segments was finished by the
 // streaming kernel. TOGETHER: a CTA takes a row, each warp a
 // share of its pieces (few rows, of many pieces); otherwise each warp takes one.
@@ -698,8 +699,8 @@ __global__ void __launch_bounds__(kMergeWarps<TOGETHER> * 32) decode_merge_kerne
     const size_t pre = row * a.groups.max_chunks, step = static_cast<size_t>(Hc) * G;
     const size_t in_slot = static_cast<size_t>(h % Hc) * G + g;
     auto piece_at = [&](int k) { return static_cast<size_t>(mine.x + k - before) * step + in_slot; };
-    auto lse_at = [&](int k) {
-      return __ldcg(k < before ? a.pre_lse + pre + k : a.seg_lse + piece_at(k));
+    auto stat_at = [&](int k) {
+      return __ldcg(k < before ? a.pre_stat + pre + k : a.seg_stat + piece_at(k));
     };
     auto out_at = [&](int k) {
       const float* p = k < before ? a.pre_out + (pre + k) * D : a.seg_out + piece_at(k) * D;
@@ -707,27 +708,35 @@ __global__ void __launch_bounds__(kMergeWarps<TOGETHER> * 32) decode_merge_kerne
     };
     const int share = TOGETHER ? (n + W - 1) / W : n;
     const int k_lo = TOGETHER ? min(warp * share, n) : 0, k_hi = min(k_lo + share, n);
-    float M = -INFINITY;
-    for (int k = k_lo + lane; k < k_hi; k += 32) M = fmaxf(M, lse_at(k));
+    float M = -INFINITY, Lm = 0.f;
+    for (int k = k_lo + lane; k < k_hi; k += 32) {
+      const float2 x = stat_at(k);
+      M = fmaxf(M, x.x);
+      Lm = fmaxf(Lm, x.y);
+    }
 #pragma unroll
-    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
+    for (int off = 16; off; off >>= 1) {
+      M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
+      Lm = fmaxf(Lm, __shfl_xor_sync(kFull, Lm, off));
+    }
+    const float unit = 1.f / Lm;  // not used where all sums are 0
     float acc[E], den = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.f;
     constexpr int kInFlight = 8;  // pieces whose loads are in flight together
     for (int k0 = k_lo; k0 < k_hi; k0 += kInFlight) {
       Vec v[kInFlight];
-      float w[kInFlight];
+      float2 w[kInFlight];
 #pragma unroll
       for (int u = 0; u < kInFlight; ++u) {
         const int k = min(k0 + u, k_hi - 1);
-        w[u] = lse_at(k);
+        w[u] = stat_at(k);
         v[u] = out_at(k);
       }
 #pragma unroll
       for (int u = 0; u < kInFlight; ++u) {
         if (k0 + u >= k_hi) break;
-        const float f = w[u] == -INFINITY ? 0.f : ex2(w[u] - M);
+        const float f = w[u].y == 0.f ? 0.f : w[u].y * unit * ex2(w[u].x - M);
         den += f;
         const float* x = reinterpret_cast<const float*>(&v[u]);
 #pragma unroll
@@ -735,22 +744,28 @@ __global__ void __launch_bounds__(kMergeWarps<TOGETHER> * 32) decode_merge_kerne
       }
     }
     if constexpr (TOGETHER) {
-      __shared__ float sM[W], sDen[W], sAcc[W][D];
+      __shared__ float sM[W], sLm[W], sDen[W], sAcc[W][D];
       if (lane == 0) {
         sM[warp] = M;
+        sLm[warp] = Lm;
         sDen[warp] = den;
       }
 #pragma unroll
       for (int i = 0; i < E; ++i) sAcc[warp][lane * E + i] = acc[i];
       __syncthreads();
       if (warp != 0) return;
-      float top = -INFINITY;
-      for (int w = 0; w < W; ++w) top = fmaxf(top, sM[w]);
+      float top = -INFINITY, top_l = 0.f;
+      for (int w = 0; w < W; ++w) {
+        top = fmaxf(top, sM[w]);
+        top_l = fmaxf(top_l, sLm[w]);
+      }
+      const float one = 1.f / top_l;
       den = 0.f;
 #pragma unroll
       for (int i = 0; i < E; ++i) acc[i] = 0.f;
       for (int w = 0; w < W; ++w) {
-        const float f = sM[w] == -INFINITY ? 0.f : ex2(sM[w] - top);
+        // a share without a sum holds zeros, or NaN
+        const float f = sLm[w] == 0.f ? 1.f : sLm[w] * one * ex2(sM[w] - top);
         den += f * sDen[w];
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] += f * sAcc[w][lane * E + i];

@@ -39,7 +39,7 @@
 // the sequences of a group take the place of a chunk's positions (a row is a
 // member and a head), every row attends to all tokens of the CTA's chunk of
 // the prefix, read through the table of the group's first member, and the
-// result is left as a piece (normalised fp32 row and base-2 log-sum-exp) for
+// result is left as a piece (normalised fp32 row, reference and sum) for
 // the merge of the decode kernel.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -149,6 +149,11 @@ __device__ __forceinline__ float2 f2_split(uint64_t r) {
 __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -300,6 +305,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float sl2 = fabsf(a.scale_log2);  // the query tile carries the sign
     float m = -INFINITY, l = 0.f;  // running max (base-2 units) and sum of weights
+    [[maybe_unused]] float mraw = -INFINITY;  // PREFIX: the raw score that m came from
     for (int j = 0; j < ntiles; ++j) {
       ok = warp_wait(bar(kBarSFull + (j & 1)), (j >> 1) & 1);
       if (!ok) break;
@@ -356,10 +362,13 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         if (rescale) {
           alpha = ex2(m - mn);  // 0 on the first tile (m = -inf)
           l *= alpha;
+          if (PREFIX && mn > m) mraw = mx;
           m = mn;
         }
         // weights 2^(s*sl2 - m), the exponent arguments by paired fp32
-        // multiply-adds. SINGLE: the fp16 rounding of each weight (scaled by
+        // multiply-adds; PREFIX: 2^((s - mraw)*sl2), so that equal scores have a
+        // weight of 1 however large they are (s*sl2 - m would be off by an ulp of m:
+        // infinite weights from scores of 2^30 on). SINGLE: the fp16 rounding of each weight (scaled by
         // 2^6), one product with fp16 V, and the row sum adds exactly those
         // rounded weights, so a weight's rounding error cancels between the
         // weighted sum and the sum. Otherwise (bf16 V): a bf16 head (the
@@ -367,12 +376,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // bf16 rounding of the remainder, two products (the operands of one
         // product share a type).
         constexpr float kOff = SINGLE ? kWeightLog2Offset : 0.f;
-        const uint64_t sl2x2 = f2(sl2, sl2), nmx2 = f2(kOff - m, kOff - m);
+        const uint64_t sl2x2 = f2(sl2, sl2);
+        const float ref = PREFIX ? -mraw : kOff - m;
+        const uint64_t refx2 = f2(ref, ref);
+        [[maybe_unused]] const uint64_t offx2 = f2(kOff, kOff);
         float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int c = 2 * i;
-          float2 arg = f2_split(f2_fma(f2(sv[c], sv[c + 1]), sl2x2, nmx2));
+          const uint64_t s2 = f2(sv[c], sv[c + 1]);
+          float2 arg = f2_split(PREFIX ? f2_fma(f2_add(s2, refx2), sl2x2, offx2) : f2_fma(s2, sl2x2, refx2));
           if constexpr (kMasked) {  // exact zeros past the limit (also for a zero scale)
             arg.x = c > lim ? -INFINITY : arg.x;
             arg.y = c + 1 > lim ? -INFINITY : arg.y;
@@ -447,7 +460,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
       if constexpr (PREFIX) {  // the chunk's piece of the row
         out = a.pre_out;
         row = row * a.groups.max_chunks + blockIdx.x / a.prefix_tiles;
-        if (row_valid) a.pre_lse[row] = l > 0.f ? m + __log2f(l) : -INFINITY;
+        if (row_valid) a.pre_stat[row] = make_float2(m, l);
       }
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {

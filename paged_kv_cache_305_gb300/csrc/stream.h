@@ -43,9 +43,12 @@ struct StreamArgs {
   int cut;              // 1: rows may be cut between CTAs
   int least_tiles;      // shortest share that cuts rows, in tiles
   int2* ws_rows;        // [S, Hkv] first slot and number of a row's segments (0: the row is finished)
-  float* pre_lse;       // [S, Hq, max_chunks] pieces of the prefix pass: base-2 log-sum-exp
-  float* pre_out;       // and normalised fp32 rows [.., d]
-  float* seg_lse;       // [slots, heads_at_a_time, G] pieces of segments, likewise
+  // Pieces: (m, l), the reference of a row's weights 2^(score - m) in binary orders and
+  // their sum, and normalised fp32 rows [.., d]. Not m + log2 l in one number: an ulp of
+  // a large m is more than log2 l can spare.
+  float2* pre_stat;     // [S, Hq, max_chunks] pieces of the prefix pass
+  float* pre_out;
+  float2* seg_stat;     // [slots, heads_at_a_time, G] pieces of segments
   float* seg_out;
   unsigned long long* bad;
   unsigned long long* timeouts;  // bounded waits that gave up
@@ -56,7 +59,7 @@ struct StreamArgs {
 struct PrefixPassArgs : PrefillArgs {
   PrefixArgs groups;
   int prefix_tiles;  // query tiles of a group (set by the launcher)
-  float* pre_lse;
+  float2* pre_stat;
   float* pre_out;
 };
 
@@ -95,7 +98,7 @@ constexpr int kGroupTiles = 16;  // see stream_heads
 struct StreamLayout {
   int heads;  // kv heads at a time
   bool cut;   // rows may be cut
-  size_t pre_lse, seg_lse, pre_out, seg_out, total;
+  size_t pre_stat, seg_stat, pre_out, seg_out, total;
 };
 StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                            long long lmax, const PrefixArgs& groups);

@@ -10,11 +10,13 @@
 // remainders, and one product serves both parts where two would leave half of
 // their columns empty (32 instead of 48 products a tile of 32 tokens).
 //
-// Softmax, base 2, in raw scores x = q . k (the sign of the scale is given to
-// q): weights p = 2^(x sl2 - m sl2), sl2 = |scale| log2(e). The reference m is
-// raised, and l and O rescaled, only when a score passes it by more than 8
-// binary orders: weights stay below 2^8, and most tiles take one vote in the
-// place of the reduction of their maxima.
+// Softmax, base 2: scores y = q . k sl2, sl2 = |scale| log2(e) (the sign of the
+// scale is given to q), weights p = 2^(y - m). y is rounded before m, itself some
+// y, is taken off: equal scores have a weight of exactly 1 however large they are
+// (2^(q . k sl2 - m) in one rounding would be off by an ulp of m, infinite from
+// scores of 2^28 on). The reference m is raised, and l and O rescaled, only when a
+// score passes it by more than 8 binary orders: weights stay below 2^8, and most
+// tiles take one vote in the place of the reduction of their maxima.
 //
 // 8-bit caches. A token's K row is its codes k8 times 2^(ek - 127), its V row
 // v8 times 2^(ev - 127). Codes become fp16 exactly (one conversion instruction
@@ -43,6 +45,7 @@
 namespace pa {
 
 constexpr float kRaiseAt = 8.f;  // binary orders a score may pass the reference by
+constexpr float kLowest = -3e38f;  // below every score that counts, and finite
 constexpr int kWeightShift = 7;  // V's weighted rows: weights below 2^(8 + 7)
 
 // The query heads of a kv head as B operand; sl2: factor of a column's scores.
@@ -56,7 +59,7 @@ struct Query {
 // nt belongs to column nt * 8 + 2 (lane % 4) + (e & 1).
 template <int D, int NT>
 struct State {
-  float m[NT][2], nm[NT][2];  // reference (raw score), and -m sl2
+  float m[NT][2];             // reference: a score, or kLowest
   float l[NT][2];             // sum of weights (this lane's tokens)
   float o[D / 16][NT][4];     // O^T
   int r;                      // 8-bit: the largest exponent byte of V so far
@@ -68,8 +71,8 @@ struct State {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[nt][c] = -INFINITY;
-        nm[nt][c] = l[nt][c] = 0.f;
+        m[nt][c] = kLowest;
+        l[nt][c] = 0.f;
       }
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
@@ -91,12 +94,12 @@ struct State {
   // Raises the references to the columns' maxima, of which mx are this lane's,
   // where any has been passed by kRaiseAt. `top`: the largest exponent byte of
   // the tile's V rows (0 for 16-bit caches).
-  __device__ __forceinline__ void raise(const float (&mx)[NT][2], int top, const Query<D, NT>& q) {
+  __device__ __forceinline__ void raise(const float (&mx)[NT][2], int top) {
     bool passed = fresh || top > r;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) passed |= (mx[nt][c] - m[nt][c]) * q.sl2[nt][c] > kRaiseAt;
+      for (int c = 0; c < 2; ++c) passed |= mx[nt][c] - m[nt][c] > kRaiseAt;
     if (!__any_sync(0xffffffffu, passed)) return;
     const float shrink = exponent_factor(max(127 - max(top - r, 0), 0));
     r = max(r, top);
@@ -109,11 +112,10 @@ struct State {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
         const float mn = fmaxf(m[nt][c], v);
-        const float f = fresh ? 0.f : ex2((m[nt][c] - mn) * q.sl2[nt][c]);
+        const float f = ex2(m[nt][c] - mn);  // l and O are zero where nothing was added yet
         l[nt][c] *= f;
         al[nt][c] = f * shrink;
         m[nt][c] = mn;
-        nm[nt][c] = -mn * q.sl2[nt][c];
       }
     if (!fresh) scale(al);
     fresh = false;
@@ -277,7 +279,7 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int e = (i & 1) * 2 + c;
-        x[nt][i][c] = (sc[i >> 1][0][nt][e] + sc[i >> 1][1][nt][e]) * fk[i];
+        x[nt][i][c] = __fmul_rn((sc[i >> 1][0][nt][e] + sc[i >> 1][1][nt][e]) * fk[i], q.sl2[nt][c]);
       }
     if (edge) {
 #pragma unroll
@@ -288,15 +290,14 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
     for (int c = 0; c < 2; ++c)
       mx[nt][c] = fmaxf(fmaxf(x[nt][0][c], x[nt][1][c]), fmaxf(x[nt][2][c], x[nt][3][c]));
   }
-  st.raise(mx, top, q);
+  st.raise(mx, top);
   const uint32_t rest = (lane & 2) != 0 ? kAll : 0u;  // SPLIT: columns 4-7
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) x[nt][i][c] = ex2(fmaf(x[nt][i][c], q.sl2[nt][c], st.nm[nt][c]));
-      if (edge && (r8 + 8 * i < lo || r8 + 8 * i >= hi)) x[nt][i][0] = x[nt][i][1] = 0.f;  // scale 0
+      for (int c = 0; c < 2; ++c) x[nt][i][c] = ex2(x[nt][i][c] - st.m[nt][c]);
       weight_parts<F16, SPLIT>(x[nt][i][0] * fv[i], x[nt][i][1] * fv[i], rest, ph[i >> 1][nt][i & 1],
                                pl[i >> 1][nt][i & 1]);
     }
@@ -351,7 +352,8 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) x[nt][i][c] = sc[nt][0][2 * i + c] + sc[nt][1][2 * i + c];
+      for (int c = 0; c < 2; ++c)
+        x[nt][i][c] = __fmul_rn(sc[nt][0][2 * i + c] + sc[nt][1][2 * i + c], q.sl2[nt][c]);
     if (edge) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -360,15 +362,14 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
 #pragma unroll
     for (int c = 0; c < 2; ++c) mx[nt][c] = fmaxf(x[nt][0][c], x[nt][1][c]);
   }
-  st.raise(mx, 0, q);
+  st.raise(mx, 0);
   const uint32_t rest = (lane & 2) != 0 ? 0xffffffffu : 0u;  // SPLIT: columns 4-7
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) x[nt][i][c] = ex2(fmaf(x[nt][i][c], q.sl2[nt][c], st.nm[nt][c]));
-      if (edge && (r8 + 8 * i < lo || r8 + 8 * i >= hi)) x[nt][i][0] = x[nt][i][1] = 0.f;  // scale 0
+      for (int c = 0; c < 2; ++c) x[nt][i][c] = ex2(x[nt][i][c] - st.m[nt][c]);
       weight_parts<Ty, SPLIT>(x[nt][i][0], x[nt][i][1], rest, ph[nt][i], pl[nt][i]);
     }
 #pragma unroll

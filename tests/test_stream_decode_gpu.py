@@ -106,3 +106,37 @@ def test_8_bit_values_next_to_the_smallest(dtype, Hq, B, n):
     # grid: 2^-150 each, of at most two stages a piece (64 tokens a stage at least)
     assert np.max(np.abs(got - ref)) <= bound + (3 * (-(-n // 64)) + 2) * 2.0 ** -150
     assert np.max(np.abs(ref)) > 10 * bound  # zeros in the place of the result would be seen
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype,size,B", [("fp16", 2.0 ** 15, 16), ("bf16", 2.0 ** 20, 4), ("bf16", 2.0 ** 58, 16)])
+def test_8_bit_decode_of_equal_scores_of_any_size(dtype, size, B, sign):
+    # the scores of all tokens are 2^30 and more, and equal: the result is the mean of V
+    rng = np.random.default_rng(B)
+    lens, Hkv, d = [1, 33, 700], 2, 64
+    kc, vc, sc = random_pool(rng, sum(-(-n // B) for n in lens), B, Hkv, d, 1)
+    kc[:] = 0x78 | (0x80 if sign < 0 else 0)  # 256
+    sc[:, :, 0] = 127 - 8 + int(np.log2(size))
+    bt = tables_for(rng, lens, B, kc.shape[0])
+    query = W.f32_to_bits(np.full((3, 4, d), size, np.float32), dtype)
+    got, ref = decode8(query, kc, vc, sc, bt, lens, B, 0.125, dtype)
+    V = np.max(np.abs(fp8.pool_values(vc, sc, 1)))
+    # weights of one: sums of n rows, and pieces joined by log-sum-exps with an ulp of
+    # the score's size; those are equal too
+    assert np.max(np.abs(got - ref)) <= V * (2 * 700 * 2.0 ** -23 + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("members", [3, 150])
+@pytest.mark.parametrize("dtype,size", [("fp16", 2.0 ** 15), ("bf16", 2.0 ** 20), ("bf16", 2.0 ** 57)])
+def test_shared_prefix_of_equal_scores_of_any_size(dtype, size, members, sign):
+    case = Case(dtype, 64, 8, 2, 16, [0, members], [700], [700 + i % 70 for i in range(members)])
+    assert case.passes() == (members > 3)
+    case.scale = 0.125
+    case.query = W.f32_to_bits(np.full(case.query.shape, size, np.float32), dtype)
+    case.kc = W.f32_to_bits(np.full(case.kc.shape, sign * size, np.float32), dtype)
+    got = case.run().double().cpu().numpy()
+    ref = fp8.shared_prefix_decode(case.query, case.kc, case.vc, case.bt, case.lens, case.starts, case.prefixes,
+                                   case.B, case.scale, dtype)
+    V = np.max(np.abs(oracle.to_float64(case.vc, dtype)))
+    assert np.max(np.abs(got - ref)) <= V * (2 * 770 * 2.0 ** -23 + 2.0 ** -18)
