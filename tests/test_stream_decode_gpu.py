@@ -140,3 +140,19 @@ def test_shared_prefix_of_equal_scores_of_any_size(dtype, size, members, sign):
                                    case.B, case.scale, dtype)
     V = np.max(np.abs(oracle.to_float64(case.vc, dtype)))
     assert np.max(np.abs(got - ref)) <= V * (2 * 770 * 2.0 ** -23 + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("B,Hq", [(16, 4), (2, 10)])
+def test_8_bit_decode_of_small_bf16_queries_and_large_keys(B, Hq):
+    # scores of ordinary size from queries near 2^-118 and keys near 2^118
+    rng = np.random.default_rng(B)
+    lens, d = [70, 600], 64
+    kc, vc, sc = random_pool(rng, sum(-(-n // B) for n in lens), B, 1, d, 2)
+    sc[:, :, 0] += 118
+    bt = tables_for(rng, lens, B, kc.shape[0])
+    query = W.f32_to_bits((rng.standard_normal((2, Hq, d)) * 2.0 ** -118).astype(np.float32), "bf16")
+    got, ref = decode8(query, kc, vc, sc, bt, lens, B, 0.125, "bf16")
+    for s, n in enumerate(lens):
+        K, V = (oracle.gather_kv(fp8.pool_values(c, sc, i), bt[s], n, B) for i, c in enumerate((kc, vc)))
+        assert np.max(np.abs(got[s] - ref[s])) <= fp8.decode_bound(oracle.to_float64(query[s], "bf16"), K, V, 0.125,
+                                                                   2.0 ** -20)
