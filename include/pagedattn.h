@@ -353,10 +353,11 @@ int pa_gather_cache_fp8(void* key_out, void* value_out,
  * definition with K_t and V_t the pool's values. dtype is the type of query
  * (and of out, unless that is fp32). Arithmetic is fp32 around fp16 products of
  * the exact codes: the query enters as its fp16 value (bf16: scaled by a power
- * of two for each head, so that its bits are kept), softmax weights, times V's
- * factors, as the sum of two fp16 parts relative to the largest factor so far:
- * the error is 2^-20 of the largest weighted V, so what V rows 2^20 times
- * smaller add to it may be lost.
+ * of two for each head, which keeps the bits of elements down to 2^-31 of the
+ * head's largest), softmax weights, times V's factors, as the sum of two fp16
+ * parts: each is off by 2^-22 of itself, or 2^-31 of the largest product of a
+ * weight and a factor where that is more. (Where one row's V factors lie more than
+ * 2^80 apart, the smaller ones may lose more.)
  * Work is cut into equal shares, inside rows as it comes (shares are not under
  * partition_tokens tokens where that is given; 0 = the default), and a second
  * kernel joins a row's pieces in order; where they are cut depends on the lengths

@@ -601,28 +601,31 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               float* stat_w = sStats + warp * 3 * R::kHeads + head;
               stat_w[0] = st.fresh ? -INFINITY : st.m[nt][c];
               stat_w[R::kHeads] = st.l[nt][c];
-              stat_w[2 * R::kHeads] = static_cast<float>(st.r);
+              if constexpr (FP8) stat_w[2 * R::kHeads] = static_cast<float>(st.r);
             }
           }
         if (!meet()) break;
         const int heads = min(G - h0, kJoinHeads), w0 = warp - wsub;
         for (int i = wsub * 32 + lane; i < heads * (D / 4); i += Wh * 32) {
           const int at = i / (D / 4), c4 = i % (D / 4) * 4, head = h0 + at;
-          float M = -INFINITY, top = 0.f;
-          for (int w = w0; w < w0 + Wh; ++w) {
-            M = fmaxf(M, sStats[w * 3 * R::kHeads + head]);
-            top = fmaxf(top, sStats[(w * 3 + 2) * R::kHeads + head]);
-          }
+          auto stat = [&](int w, int which) { return sStats[(w * 3 + which) * R::kHeads + head]; };
+          float M = -INFINITY;
+          for (int w = w0; w < w0 + Wh; ++w) M = fmaxf(M, stat(w, 0));
+          // 8-bit: the order of a warp's O, and the largest of them
+          auto order = [&](int w) { return stat(w, 2) + (stat(w, 0) - M); };
+          [[maybe_unused]] float top = kLowest;
+          if constexpr (FP8)
+            for (int w = w0; w < w0 + Wh; ++w) top = fmaxf(top, order(w));  // -inf or NaN: no tile
           float l = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int w = w0; w < w0 + Wh; ++w) {
-            const float m = sStats[w * 3 * R::kHeads + head];
+            const float m = stat(w, 0);
             const float f = m == -INFINITY ? 0.f : ex2(m - M);
-            // 8-bit: a warp's O is relative to its largest factor
-            const float fo = FP8 ? f * ex2(sStats[(w * 3 + 2) * R::kHeads + head] - top) : f;
+            float fo = f;
+            if constexpr (FP8) fo = m == -INFINITY ? 0.f : ex2(order(w) - top);
             const float4 v =
                 *reinterpret_cast<const float4*>(sJoin + (w * kJoinHeads + at) * R::kOStride + c4);
-            l += f * sStats[(w * 3 + 1) * R::kHeads + head];
+            l += f * stat(w, 1);
             acc.x += fo * v.x;
             acc.y += fo * v.y;
             acc.z += fo * v.z;
@@ -630,11 +633,12 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           float iv = l > 0.f ? 1.f / l : 0.f;
           if (l != l) iv = l;  // NaN scores give NaN
-          if constexpr (FP8) iv *= 1.f / (1 << kWeightShift);
           acc = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
-          if constexpr (FP8) {  // a factor of its own: 2^(top - 127), times the rest, may be subnormal
-            const float ft = exponent_factor(static_cast<int>(top));
-            acc = make_float4(acc.x * ft, acc.y * ft, acc.z * ft, acc.w * ft);
+          if constexpr (FP8) {
+            // times 2^(top - 127), as two factors apart: one, or the product with iv, may be subnormal
+            const int n = static_cast<int>(fminf(fmaxf(top - 127.f, -252.f), 252.f));
+            const float f0 = exponent_factor(127 + n / 2), f1 = exponent_factor(127 + n - n / 2);
+            acc = make_float4(acc.x * f0 * f1, acc.y * f0 * f1, acc.z * f0 * f1, acc.w * f0 * f1);
           }
           const size_t row = row0 + head;
           if (note.slot >= 0) {

@@ -12,9 +12,9 @@
 //
 // Softmax, base 2: scores y = q . k sl2, sl2 = |scale| log2(e) (the sign of the
 // scale is given to q), weights p = 2^(y - m). y is rounded before m, itself some
-// y, is taken off: equal scores have a weight of exactly 1 however large they are
-// (2^(q . k sl2 - m) in one rounding would be off by an ulp of m, infinite from
-// scores of 2^28 on). The reference m is raised, and l and O rescaled, only when a
+// y (8-bit: a whole number next to one), is taken off: equal scores have equal
+// weights near 1 however large they are (2^(q . k sl2 - m) in one rounding would be
+// off by an ulp of m, infinite from scores of 2^28 on). The reference m is raised, and l and O rescaled, only when a
 // score passes it by more than 8 binary orders: weights stay below 2^8, and most
 // tiles take one vote in the place of the reduction of their maxima.
 //
@@ -22,10 +22,15 @@
 // v8 times 2^(ev - 127). Codes become fp16 exactly (one conversion instruction
 // per two), the products run on fp16 with fp32 accumulation, and the factors
 // enter outside of them: K's multiplies the score, V's the softmax weight:
-//   O = sum p_t 2^(ev_t - r + 7) v8_t,   out = O 2^(r - 127 - 7) / l
-// with r the largest ev so far. A weight of O is below 2^15 and exact up to its
-// two fp16 parts, which reach down to 2^-25: V's rows may differ by 2^20 in
-// size before a row of normal size loses bits next to a huge one.
+//   p = 2^(y - m),   O = sum p_t 2^(ev_t - r) v8_t,   out = O 2^(r - 127) / l
+// with r the largest ev so far, one for all heads. The reference m of a head follows
+// its largest weighted row, y + ev - r, not its largest score: weights of O are
+// between 2^6 and 2^15 at the top, where their two fp16 parts reach down to 2^-25, and
+// what a token loses there is under 2^-31 of the largest p_t 2^ev_t, whichever token
+// that is. (With m at the largest score a huge row of no weight took all bits from
+// the others.) m stays within 2^kSpread of the largest score, for l: only if V's
+// rows differ by more than that do the smaller ones lose bits. m and r are whole
+// numbers, so that every rescaling is exact.
 //
 // Fragment orders of 8-bit tiles. ldmatrix moves 8x8 tiles of 16-bit units,
 // here pairs of codes. For K a lane gets four neighbouring codes of one token,
@@ -46,7 +51,8 @@ namespace pa {
 
 constexpr float kRaiseAt = 8.f;  // binary orders a score may pass the reference by
 constexpr float kLowest = -3e38f;  // below every score that counts, and finite
-constexpr int kWeightShift = 7;  // V's weighted rows: weights below 2^(8 + 7)
+constexpr float kWeightShift = 7.f;  // 8-bit: weights of O reach 2^7, and 2^(8 + 7) before m follows
+constexpr int kSpread = 80;          // 8-bit: weights p below 2^(80 + 15), of which 2^31 fit into l
 
 // The query heads of a kv head as B operand; sl2: factor of a column's scores.
 template <int D, int NT>
@@ -91,34 +97,57 @@ struct State {
         o[mt][nt][3] *= al[nt][1];
       }
   }
-  // Raises the references to the columns' maxima, of which mx are this lane's,
-  // where any has been passed by kRaiseAt. `top`: the largest exponent byte of
-  // the tile's V rows (0 for 16-bit caches).
-  __device__ __forceinline__ void raise(const float (&mx)[NT][2], int top) {
-    bool passed = fresh || top > r;
+  // The largest v of the column's lanes.
+  static __device__ __forceinline__ float column_max(float v) {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+  }
+  // Raises the references to the columns' maxima, of which mx are this lane's, where any
+  // has been passed by kRaiseAt. 16-bit caches: mx of the scores. 8-bit: of the weighted
+  // rows y + ev - r.
+  template <bool FP8>
+  __device__ __forceinline__ void raise(const float (&mx)[NT][2]) {
+    constexpr float kShift = FP8 ? kWeightShift : 0.f;
+    bool passed = fresh;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) passed |= mx[nt][c] - m[nt][c] > kRaiseAt;
+      for (int c = 0; c < 2; ++c) passed |= mx[nt][c] - m[nt][c] > kShift + kRaiseAt;
     if (!__any_sync(0xffffffffu, passed)) return;
-    const float shrink = exponent_factor(max(127 - max(top - r, 0), 0));
-    r = max(r, top);
     float al[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float v = mx[nt][c];
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-        const float mn = fmaxf(m[nt][c], v);
+        const float v = column_max(mx[nt][c]);
+        const float mn = fmaxf(m[nt][c], FP8 ? ceilf(v) - kShift : v);
         const float f = ex2(m[nt][c] - mn);  // l and O are zero where nothing was added yet
         l[nt][c] *= f;
-        al[nt][c] = f * shrink;
+        al[nt][c] = f;
         m[nt][c] = mn;
       }
     if (!fresh) scale(al);
     fresh = false;
+  }
+  // 8-bit: r to `top`, the largest exponent byte so far. What was added before has lost the
+  // orders in between against it: m goes down by as many, as far as l allows.
+  __device__ __forceinline__ void follow(int top) {
+    if (top == r) return;
+    const int more = top - r;
+    r = top;
+    if (fresh) return;
+    float al[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int down = min(more, max(kSpread + 127 - (__float_as_int(column_max(l[nt][c])) >> 23), 0));
+        m[nt][c] -= static_cast<float>(down);
+        l[nt][c] *= exponent_factor(127 + down);
+        al[nt][c] = exponent_factor(max(127 + down - more, 0));
+      }
+    scale(al);
   }
 };
 
@@ -233,16 +262,18 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
   const bool edge = lo > 0 || hi < Geo::kTokens;
   if (edge && (lane < lo || lane >= hi)) ev = 0;
 
-  // factors of this lane's tokens r8 + 8 i, as the upper halves of fp32 numbers
-  const int top = __reduce_max_sync(kAll, ev);
-  uint32_t pair = static_cast<uint32_t>(ek) << 23 |
-                  static_cast<uint32_t>(max(ev - max(top, st.r) + 127 + kWeightShift, 0)) << 7;
-  float fk[4], fv[4];
+  // factors of this lane's tokens r8 + 8 i, as the upper halves of fp32 numbers, and the
+  // orders of V's: no lower than -kSpread, so that p is bounded with p 2^(ev - top)
+  const int top = max(__reduce_max_sync(kAll, ev), st.r);
+  st.follow(top);
+  const uint32_t pair = static_cast<uint32_t>(ek) << 23 | static_cast<uint32_t>(ev == 0 ? 0 : max(ev - top + 127, 0)) << 7;
+  float fk[4], fv[4], ov[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t b = __shfl_sync(kAll, pair, r8 + 8 * i);
     fk[i] = __uint_as_float(b & 0xffff0000u);
     fv[i] = __uint_as_float(b << 16);
+    ov[i] = static_cast<float>(max((__float_as_int(fv[i]) >> 23) - 127, -kSpread));
   }
 
   // S^T of tokens 0-15 and 16-31, each in two accumulators: short chains
@@ -290,9 +321,9 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      mx[nt][c] = fmaxf(fmaxf(x[nt][0][c], x[nt][1][c]), fmaxf(x[nt][2][c], x[nt][3][c]));
+      mx[nt][c] = fmaxf(fmaxf(x[nt][0][c] + ov[0], x[nt][1][c] + ov[1]), fmaxf(x[nt][2][c] + ov[2], x[nt][3][c] + ov[3]));
   }
-  st.raise(mx, top);
+  st.template raise<true>(mx);
   const uint32_t rest = (lane & 2) != 0 ? kAll : 0u;  // SPLIT: columns 4-7
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -364,7 +395,7 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
 #pragma unroll
     for (int c = 0; c < 2; ++c) mx[nt][c] = fmaxf(x[nt][0][c], x[nt][1][c]);
   }
-  st.raise(mx, 0);
+  st.template raise<false>(mx);
   const uint32_t rest = (lane & 2) != 0 ? 0xffffffffu : 0u;  // SPLIT: columns 4-7
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {

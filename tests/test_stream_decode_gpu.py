@@ -156,3 +156,42 @@ def test_8_bit_decode_of_small_bf16_queries_and_large_keys(B, Hq):
         K, V = (oracle.gather_kv(fp8.pool_values(c, sc, i), bt[s], n, B) for i, c in enumerate((kc, vc)))
         assert np.max(np.abs(got[s] - ref[s])) <= fp8.decode_bound(oracle.to_float64(query[s], "bf16"), K, V, 0.125,
                                                                    2.0 ** -20)
+
+
+# ---------------------------------------------------- weights of any size --
+LN2 = float(np.float32(np.log(2.0)))  # this scale makes whole scores powers of two
+
+
+@pytest.mark.parametrize("at", [0, 150, -1])
+@pytest.mark.parametrize("dtype,B,n,Hq", [("bf16", 16, 200, 4), ("fp16", 4, 200, 9), ("fp16", 16, 1500, 3)])
+@pytest.mark.parametrize("binades", [12, 24, 40])
+def test_8_bit_decode_with_a_huge_row_of_negligible_weight(binades, dtype, B, n, Hq, at):
+    # one token has a V factor 2^binades above the others' and a softmax weight of 2^-60
+    # of theirs: the others keep their bits
+    rng = np.random.default_rng(n + binades)
+    d = 64
+    kc, vc, sc = random_pool(rng, -(-n // B), B, 1, d, 0)
+    bt = tables_for(rng, [n], B, kc.shape[0])
+    sc[:, :, 0] = 127 - 10  # scores of others: of the order of one
+    kc[..., 0] = 0
+    t = at % n
+    blk, off = bt[0, t // B], t % B
+    kc[blk, off] = 0
+    kc[blk, off, 0, 0] = 0xF4          # -192
+    sc[blk, 0, 0, off] = 127
+    sc[blk, 0, 1, off] += binades
+    q = rng.standard_normal((1, Hq, d)) * 0.02
+    q[..., 0] = 0.3125                 # 0.3125 * -192 = -60
+    query = W.f32_to_bits(q.astype(np.float32), dtype)
+    got, ref = decode8(query, kc, vc, sc, bt, [n], B, LN2, dtype)
+    K, V = (oracle.gather_kv(fp8.pool_values(c, sc, i), bt[0], n, B) for i, c in enumerate((kc, vc)))
+    qf = oracle.to_float64(query[0], dtype)
+    p = oracle.attention_weights(qf @ K[:, 0].T * LN2)
+    assert np.all(p[:, t] < 2.0 ** -55 * p.max(axis=1))
+    size = np.max(p @ np.abs(V[:, 0]))
+    factor = np.exp2(np.array([float(sc[bt[0, i // B], 0, 1, i % B]) for i in range(n)]) - 127)
+    # the bound with the weighted rows' size in the place of max |V|; what falls below fp16's
+    # grid, 2^-31 of the largest weighted factor for each token, times a code
+    rel = fp8.decode_bound(qf, K, np.ones_like(V), LN2, 2.0 ** -20)
+    assert np.max(np.abs(got - ref)) <= size * rel + n * 2.0 ** -31 * np.max(p * factor) * 448
+    assert np.max(np.abs(ref)) > 0.01 * size
