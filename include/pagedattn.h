@@ -416,7 +416,8 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
  * and num_seqs * num_kv_heads * (max_blocks_per_seq * block_size / 16 + 2)
  * below 2^31, max_blocks_per_seq * block_size at most 2^31 - 4096. workspace: pa_decode_shared_prefix_workspace_bytes(...) bytes,
  * shared with other calls as pa_decode_fp8's. Softmax weights enter as the sum
- * of two parts of the cache's type; waits that give up are counted as there.
+ * of two parts of the cache's type (fp16: off by 2^-22 of themselves, or 2^-32 of
+ * the row's largest where that is more); waits that give up are counted as there.
  * Other arguments and errors as for pa_decode.
  */
 int pa_decode_shared_prefix(void* out, const void* query,

@@ -633,6 +633,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           float iv = l > 0.f ? 1.f / l : 0.f;
           if (l != l) iv = l;  // NaN scores give NaN
+          if constexpr (!FP8) iv *= 1.f / kWeightScale<Ty>;
           acc = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
           if constexpr (FP8) {
             // times 2^(top - 127), as two factors apart: one, or the product with iv, may be subnormal

@@ -74,6 +74,10 @@ constexpr float kRescaleLog2 = 8.f;
 // fp16 inputs: the weights carry a factor 2^6 (at most 2^14 under the lazy
 // rescale), so weights down to 2^-20 of the reference max stay normal fp16
 constexpr float kWeightLog2Offset = 6.f;
+// Weights as two parts (the prefix pass, bf16 without the copy): fp16 parts carry 2^7
+// (at most 2^15), so that they reach down to 2^-32 of the reference; bf16 has the range.
+template <typename Ty>
+constexpr float kPartsLog2Offset = Ty::kIsBf16 ? 0.f : 7.f;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int D>
@@ -375,7 +379,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         // upper half of the fp32 weight, taken by byte selection) and the
         // bf16 rounding of the remainder, two products (the operands of one
         // product share a type).
-        constexpr float kOff = SINGLE ? kWeightLog2Offset : 0.f;
+        constexpr float kOff = SINGLE ? kWeightLog2Offset : kPartsLog2Offset<Ty>;
         const uint64_t sl2x2 = f2(sl2, sl2);
         const float ref = PREFIX ? -mraw : kOff - m;
         const uint64_t refx2 = f2(ref, ref);
@@ -460,7 +464,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
       if constexpr (PREFIX) {  // the chunk's piece of the row
         out = a.pre_out;
         row = row * a.groups.max_chunks + blockIdx.x / a.prefix_tiles;
-        if (row_valid) a.pre_stat[row] = make_float2(m, l);
+        if (row_valid) a.pre_stat[row] = make_float2(m, l * ex2(-kPartsLog2Offset<Ty>));
       }
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {

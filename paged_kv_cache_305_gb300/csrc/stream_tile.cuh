@@ -51,6 +51,10 @@ namespace pa {
 
 constexpr float kRaiseAt = 8.f;  // binary orders a score may pass the reference by
 constexpr float kLowest = -3e38f;  // below every score that counts, and finite
+// fp16 caches: weights enter O times 2^7, below 2^15. Their fp16 parts reach down to 2^-25,
+// 2^-32 of the largest weight's size: many small weights behind a large one are a result.
+template <typename Ty>
+constexpr float kWeightScale = Ty::kIsBf16 ? 1.f : 128.f;
 constexpr float kWeightShift = 7.f;  // 8-bit: weights of O reach 2^7, and 2^(8 + 7) before m follows
 constexpr int kSpread = 80;          // 8-bit: weights p below 2^(80 + 15), of which 2^31 fit into l
 
@@ -403,7 +407,8 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) x[nt][i][c] = ex2(x[nt][i][c] - st.m[nt][c]);
-      weight_parts<Ty, SPLIT>(x[nt][i][0], x[nt][i][1], rest, ph[nt][i], pl[nt][i]);
+      weight_parts<Ty, SPLIT>(x[nt][i][0] * kWeightScale<Ty>, x[nt][i][1] * kWeightScale<Ty>, rest, ph[nt][i],
+                              pl[nt][i]);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) st.l[nt][c] += x[nt][0][c] + x[nt][1][c];

@@ -195,3 +195,28 @@ def test_8_bit_decode_with_a_huge_row_of_negligible_weight(binades, dtype, B, n,
     rel = fp8.decode_bound(qf, K, np.ones_like(V), LN2, 2.0 ** -20)
     assert np.max(np.abs(got - ref)) <= size * rel + n * 2.0 ** -31 * np.max(p * factor) * 448
     assert np.max(np.abs(ref)) > 0.01 * size
+
+
+@pytest.mark.parametrize("low", [-27, -31])
+@pytest.mark.parametrize("members,dtype", [(2, "fp16"), (60, "fp16"), (60, "bf16"), (2, "bf16")])
+def test_shared_prefix_with_a_dominating_token_without_a_value(members, dtype, low):
+    # the first token takes nearly all of the weight and has V = 0: the result is
+    # the small weights of all others, 2^-27 and 2^-31 of the first one's
+    n, d = 3000, 64
+    case = Case(dtype, d, 16, 2, 16, [0, members], [2500], [n + i for i in range(members)])
+    assert case.passes() == (members > 2)
+    K, V = np.zeros(case.kc.shape), np.random.default_rng(1).integers(1, 9, case.vc.shape).astype(np.float64)
+    K[..., 0] = low
+    for s in range(members):
+        K[case.bt[s, 0], 0], V[case.bt[s, 0], 0] = 0, 0
+    q = np.zeros(case.query.shape)
+    q[..., 0] = 1
+    case.scale = LN2
+    case.query, case.kc, case.vc = (W.f32_to_bits(x.astype(np.float32), dtype) for x in (q, K, V))
+    got = case.run().double().cpu().numpy()
+    ref = fp8.shared_prefix_decode(case.query, case.kc, case.vc, case.bt, case.lens, case.starts, case.prefixes,
+                                   case.B, case.scale, dtype)
+    # a weight's relative error (exponent, exp2, parts), sums of n terms twice, and
+    # pieces joined by log-sum-exps of up to 32 in size (2^-18)
+    rel = 2 * (32 * 2.0 ** -24 + 2.0 ** -21 + 2 * (n + 60) * 2.0 ** -24 + 2.0 ** -18)
+    assert np.max(np.abs(got - ref)) <= rel * np.max(ref)
