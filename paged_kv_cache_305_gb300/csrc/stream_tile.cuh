@@ -89,6 +89,15 @@ struct State {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
   }
+  // A tile's part of O. The products of a tile start from zero and are added here: the tensor
+  // core cuts off what does not fit when it adds to its accumulator, and O, which grows with
+  // the row, would lose half an ulp each time (6e-6 of 10 K tokens' sum).
+  __device__ __forceinline__ void add(int mt, const float (&x)[NT][4]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[mt][nt][e] += x[nt][e];
+  }
   // O columns times al.
   __device__ __forceinline__ void scale(const float (&al)[NT][2]) {
 #pragma unroll
@@ -344,6 +353,7 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
   }
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) {
+    float o[NT][4] = {};
     uint32_t v[4];  // tokens 0-7, 8-15, 16-23, 24-31 of the m-tile's 16 dims
     ldmatrix_x4_trans(v, sv + Geo::in_group(rr, mt));
 #pragma unroll
@@ -353,10 +363,11 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
                              e4m3x2_to_f16x2(s >> 16)};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        F16::mma(st.o[mt][nt], a, ph[hf][nt][0], ph[hf][nt][1]);
-        if constexpr (!SPLIT) F16::mma(st.o[mt][nt], a, pl[hf][nt][0], pl[hf][nt][1]);
+        F16::mma(o[nt], a, ph[hf][nt][0], ph[hf][nt][1]);
+        if constexpr (!SPLIT) F16::mma(o[nt], a, pl[hf][nt][0], pl[hf][nt][1]);
       }
     }
+    st.add(mt, o);
   }
 }
 
@@ -415,13 +426,15 @@ __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi
   }
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) {
+    float o[NT][4] = {};
     uint32_t v[4];
     ldmatrix_x4_trans(v, sv + Geo::in_group(rr, 2 * mt + (mi & 1)));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      Ty::mma(st.o[mt][nt], v, ph[nt][0], ph[nt][1]);
-      if constexpr (!SPLIT) Ty::mma(st.o[mt][nt], v, pl[nt][0], pl[nt][1]);
+      Ty::mma(o[nt], v, ph[nt][0], ph[nt][1]);
+      if constexpr (!SPLIT) Ty::mma(o[nt], v, pl[nt][0], pl[nt][1]);
     }
+    st.add(mt, o);
   }
 }
 

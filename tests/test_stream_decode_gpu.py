@@ -220,3 +220,38 @@ def test_shared_prefix_with_a_dominating_token_without_a_value(members, dtype, l
     # pieces joined by log-sum-exps of up to 32 in size (2^-18)
     rel = 2 * (32 * 2.0 ** -24 + 2.0 ** -21 + 2 * (n + 60) * 2.0 ** -24 + 2.0 ** -18)
     assert np.max(np.abs(got - ref)) <= rel * np.max(ref)
+
+
+# ------------------------------------------------------------- long sums --
+@pytest.mark.parametrize("op,dtype", [("8-bit", "bf16"), ("8-bit", "fp16"), ("prefix", "fp16")])
+def test_sums_of_long_rows_do_not_drift(op, dtype):
+    # V is 1 everywhere, the first token's weight 1 and all others' 2^-0.7: the result is 1.
+    # 456 rows, one for each CTA, which a warp adds up in n / 128 (16-bit: n / 64) steps.
+    # Rounded to nearest, a sum of k terms is off by 6 sqrt(k) 2^-24 of itself at most but
+    # once in 10^7 (the roundings are as good as independent, each below half an ulp);
+    # sums that are cut off at every step lose about k 2^-25.
+    S, d, B, n, NB = 456, 64, 16, 131072, 64
+    score, steps = 0.7, n // 128 if op == "8-bit" else n // 64
+    bt = (torch.arange(n // B, device="cuda") % (NB - 1) + 1).to(torch.int32).repeat(S, 1)
+    bt[:, 0] = 0
+    lens = torch.full((S,), n, dtype=torch.int32, device="cuda")
+    K = np.zeros((NB, B, 1, d), np.float32)
+    K[..., 0] = -0.6875
+    K[0, 0] = 0
+    q = np.zeros((S, 1, d), np.float32)
+    q[..., 0] = 1
+    q, k = dev_bits(W.f32_to_bits(q, dtype), dtype), dev_bits(W.f32_to_bits(K, dtype), dtype)
+    v = torch.ones_like(k)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    scale = LN2 * score / 0.6875
+    if op == "8-bit":
+        pool = pa.alloc_fp8_cache(NB, B, 1, d)
+        pa.reshape_and_cache_fp8(k.view(-1, 1, d), v.view(-1, 1, d), *pool, torch.arange(NB * B, device="cuda"))
+        pa.decode_fp8(out, q, *pool, bt, lens, scale, 0, pa.alloc_workspace(q, pool[0], bt))
+    else:
+        starts, none = torch.arange(S + 1, dtype=torch.int32, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
+        pa.decode_shared_prefix(out, q, k, v, bt, lens, starts, none, 0, 1, scale,
+                                pa.alloc_shared_prefix_workspace(q, k, bt, starts, 0, 1))
+    # both sums; a tile's products and the weights' parts (2^-22 each, the same for every
+    # token), the joining of warps and pieces and the quotient
+    assert float((out - 1).abs().max()) <= 2 * 6 * np.sqrt(steps) * 2.0 ** -24 + 2 * 2.0 ** -22 + 8 * 2.0 ** -23
