@@ -10,7 +10,7 @@ import paged_kv_cache_305_gb300 as pa
 import workloads as W
 from gpu_util import dev_bits
 from oracle import fp8
-from test_fp8_cache_gpu import random_pool, tables_for, up, up8
+from test_fp8_cache_gpu import down8, random_pool, tables_for, up, up8
 from test_shared_prefix_gpu import Case
 
 pytestmark = pytest.mark.gpu
@@ -225,33 +225,37 @@ def test_shared_prefix_with_a_dominating_token_without_a_value(members, dtype, l
 # ------------------------------------------------------------- long sums --
 @pytest.mark.parametrize("op,dtype", [("8-bit", "bf16"), ("8-bit", "fp16"), ("prefix", "fp16")])
 def test_sums_of_long_rows_do_not_drift(op, dtype):
-    # V is 1 everywhere, the first token's weight 1 and all others' 2^-0.7: the result is 1.
-    # 456 rows, one for each CTA, which a warp adds up in n / 128 (16-bit: n / 64) steps.
-    # Rounded to nearest, a sum of k terms is off by 6 sqrt(k) 2^-24 of itself at most but
-    # once in 10^7 (the roundings are as good as independent, each below half an ulp);
-    # sums that are cut off at every step lose about k 2^-25.
+    # positive values of many bits: 456 rows, one for each CTA, which a warp adds up in
+    # n / 128 (16-bit: n / 64) steps. Rounded to nearest, a sum of k terms is off by
+    # 6 sqrt(k) 2^-24 of itself at most but once in 10^7 (the roundings are as good as
+    # independent, each below half an ulp); sums that are cut off at every step are too
+    # small by about k 2^-25.
     S, d, B, n, NB = 456, 64, 16, 131072, 64
-    score, steps = 0.7, n // 128 if op == "8-bit" else n // 64
-    bt = (torch.arange(n // B, device="cuda") % (NB - 1) + 1).to(torch.int32).repeat(S, 1)
-    bt[:, 0] = 0
+    steps = n // 128 if op == "8-bit" else n // 64
+    rng = np.random.default_rng(3)
+    bt = (torch.arange(n // B, device="cuda") % NB).to(torch.int32).repeat(S, 1)
     lens = torch.full((S,), n, dtype=torch.int32, device="cuda")
     K = np.zeros((NB, B, 1, d), np.float32)
-    K[..., 0] = -0.6875
-    K[0, 0] = 0
+    K[..., 0] = rng.uniform(-3, 0, K.shape[:3])
+    V = rng.uniform(0.5, 2, K.shape).astype(np.float32)
     q = np.zeros((S, 1, d), np.float32)
     q[..., 0] = 1
-    q, k = dev_bits(W.f32_to_bits(q, dtype), dtype), dev_bits(W.f32_to_bits(K, dtype), dtype)
-    v = torch.ones_like(k)
+    q, k, v = (dev_bits(W.f32_to_bits(x, dtype), dtype) for x in (q, K, V))
     out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
-    scale = LN2 * score / 0.6875
     if op == "8-bit":
         pool = pa.alloc_fp8_cache(NB, B, 1, d)
         pa.reshape_and_cache_fp8(k.view(-1, 1, d), v.view(-1, 1, d), *pool, torch.arange(NB * B, device="cuda"))
-        pa.decode_fp8(out, q, *pool, bt, lens, scale, 0, pa.alloc_workspace(q, pool[0], bt))
+        pa.decode_fp8(out, q, *pool, bt, lens, LN2, 0, pa.alloc_workspace(q, pool[0], bt))
+        kc, vc, sc = down8(pool[0]), down8(pool[1]), pool[2].cpu().numpy()
+        K, V = fp8.pool_values(kc, sc, 0), fp8.pool_values(vc, sc, 1)
     else:
         starts, none = torch.arange(S + 1, dtype=torch.int32, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
-        pa.decode_shared_prefix(out, q, k, v, bt, lens, starts, none, 0, 1, scale,
+        pa.decode_shared_prefix(out, q, k, v, bt, lens, starts, none, 0, 1, LN2,
                                 pa.alloc_shared_prefix_workspace(q, k, bt, starts, 0, 1))
-    # both sums; a tile's products and the weights' parts (2^-22 each, the same for every
-    # token), the joining of warps and pieces and the quotient
-    assert float((out - 1).abs().max()) <= 2 * 6 * np.sqrt(steps) * 2.0 ** -24 + 2 * 2.0 ** -22 + 8 * 2.0 ** -23
+        K, V = (x.double().cpu().numpy() for x in (k, v))
+    p = np.exp(K[:, :, 0, 0] * LN2)[..., None]
+    ref = (p * V[:, :, 0]).sum((0, 1)) / p.sum()
+    rel = np.abs(out.double().cpu().numpy() / ref - 1)
+    # both sums, the products of a tile (2^-21), a weight and its parts (2^-21), the
+    # joining of warps and pieces and the quotient
+    assert np.max(rel) <= 2 * 6 * np.sqrt(steps) * 2.0 ** -24 + 2 * 2.0 ** -21 + 8 * 2.0 ** -23
