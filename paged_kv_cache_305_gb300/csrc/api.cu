@@ -234,6 +234,7 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
       if (fill >= 0.9 || w >= 3.0) break;
     }
   }
+  best = std::max(best, (x->max_prefix_len + kPrefixMaxChunk - 1) / kPrefixMaxChunk);
   const long long t = (x->max_prefix_len + best - 1) / best;
   x->chunk_tokens = static_cast<int>(std::min(std::max((t + 63) / 64 * 64, 64ll), 1ll << 30));
   // The pass is worth its launch, its pieces and the SMs that it takes from the

@@ -259,3 +259,31 @@ def test_sums_of_long_rows_do_not_drift(op, dtype):
     # both sums, the products of a tile (2^-21), a weight and its parts (2^-21), the
     # joining of warps and pieces and the quotient
     assert np.max(rel) <= 2 * 6 * np.sqrt(steps) * 2.0 ** -24 + 2 * 2.0 ** -21 + 8 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_sums_of_long_prefixes_do_not_drift(dtype):
+    # 300 pairs of sequences behind 131072 tokens, in whole waves of CTAs of any chunk
+    # length. A chunk of at most 8192 tokens adds up 8 products for each 64 of them, and
+    # the tensor core may cut off: 2^-23 of the sum at each addition, as decode_bound has it
+    S, d, B, n, NB = 600, 64, 16, 131072, 64
+    rng = np.random.default_rng(4)
+    bt = (torch.arange(n // B, device="cuda") % NB).to(torch.int32).repeat(S, 1)
+    lens = torch.full((S,), n, dtype=torch.int32, device="cuda")
+    K = np.zeros((NB, B, 1, d), np.float32)
+    K[..., 0] = rng.uniform(-3, 0, K.shape[:3])
+    V = rng.uniform(0.5, 2, K.shape).astype(np.float32)
+    q = np.zeros((S, 1, d), np.float32)
+    q[..., 0] = 1
+    q, k, v = (dev_bits(W.f32_to_bits(x, dtype), dtype) for x in (q, K, V))
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    starts = torch.arange(0, S + 1, 2, dtype=torch.int32, device="cuda")
+    prefixes = torch.full((S // 2,), n, dtype=torch.int32, device="cuda")
+    pa.decode_shared_prefix(out, q, k, v, bt, lens, starts, prefixes, n, 2, LN2,
+                            pa.alloc_shared_prefix_workspace(q, k, bt, starts, n, 2))
+    K, V = (x.double().cpu().numpy() for x in (k, v))
+    p = np.exp(K[:, :, 0, 0] * LN2)[..., None]
+    ref = (p * V[:, :, 0]).sum((0, 1)) / p.sum()
+    rel = np.abs(out.double().cpu().numpy() / ref - 1)
+    # a weight's parts: 2^-16 at most for bf16, of random sign for each token
+    assert np.max(rel) <= 1024 * 2.0 ** -23 + (2.0 ** -18 if dtype == "bf16" else 2.0 ** -21) + 8 * 2.0 ** -23
