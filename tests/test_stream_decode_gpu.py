@@ -287,3 +287,107 @@ def test_sums_of_long_prefixes_do_not_drift(dtype):
     rel = np.abs(out.double().cpu().numpy() / ref - 1)
     # a weight's parts: 2^-16 at most for bf16, of random sign for each token
     assert np.max(rel) <= 1024 * 2.0 ** -23 + (2.0 ** -18 if dtype == "bf16" else 2.0 ** -21) + 8 * 2.0 ** -23
+
+
+# ------------------------------------------------------- every token once --
+# All scores are equal and the values whole numbers from -8 to 8: a result is the mean of
+# its tokens' values, and one token left out, or taken twice, moves it by |V_t - mean| / n.
+# Each test checks that every token's part is well above the tolerance. Slots that do not
+# belong to the row hold a score 2^5 higher and NaN.
+def mean_tolerance(n, chain):
+    """For sums of n weights and rows in chains of n / chain additions, each off by
+    6 sqrt(steps) 2^-24 (see above), pieces joined likewise; exp2, parts, quotient."""
+    return 8 * (2 * 6 * (np.sqrt(n / chain) + np.sqrt(n / 64)) * 2.0 ** -24 + 4 * 2.0 ** -21 + 8 * 2.0 ** -23)
+
+
+def check_means(got, values, chain, what, cut=0.0):
+    """got [Hq, d] against the means of values [n, Hkv, d]."""
+    n, Hkv, d = values.shape
+    mean = values.mean(0) if n else np.zeros((Hkv, d))
+    tol = mean_tolerance(n, chain) + 8 * cut
+    if n > 1:
+        part = np.abs(values - mean).max(2).min() / (n - 1)
+        assert part > 1.5 * tol, (what, part, tol)
+    err = np.max(np.abs(got - np.repeat(mean, got.shape[0] // Hkv, axis=0)))
+    assert err <= tol, (what, err, tol)
+
+
+ONCE = [
+    # dtype, d, Hq, Hkv, B, lengths, partition_tokens, table tokens
+    ("fp16", 128, 5, 5, 16, [5000], 0, None),
+    ("bf16", 64, 13, 1, 16, [3000, 2999], 0, None),
+    ("fp16", 128, 64, 8, 16, [2100, 600], 512, None),
+    ("bf16", 128, 14, 2, 32, [1100, 1023], 0, None),
+    ("fp16", 64, 8, 2, 64, [1500, 1025, 3], 128, None),
+    ("bf16", 128, 16, 4, 16, [12000], 0, None),
+    # neighbouring heads together; small blocks, copied by the computing warps
+    ("bf16", 128, 32, 8, 16, [900, 33, 0, 1, 257, 64, 9000], 0, 20480),
+    ("fp16", 64, 12, 12, 8, [31, 700, 5, 64, 65, 4001], 0, 16384),
+    ("bf16", 128, 32, 8, 4, [3333, 20, 0, 129, 777], 0, 19456),
+    ("fp16", 64, 4, 2, 1, [50, 2600, 31, 33], 0, 58880),
+    ("bf16", 64, 32, 2, 2, [7000, 1], 0, None),
+]
+
+
+@pytest.mark.parametrize("idx", range(len(ONCE)))
+def test_8_bit_decode_takes_every_token_once(idx):
+    dtype, d, Hq, Hkv, B, lens, pt, width = ONCE[idx]
+    rng = np.random.default_rng(300 + idx)
+    NB = sum(-(-n // B) for n in lens) + 3
+    bt = tables_for(rng, lens, B, NB, MB=width // B if width else max(-(-max(lens) // B) + 1, 1))
+    V = rng.integers(-8, 9, (NB, B, Hkv, d)).astype(np.float64)
+    kc, vc = np.zeros(V.shape, np.uint8), fp8.nearest_code(V)
+    sc = np.full((NB, Hkv, 2, B), 127, np.uint8)
+    used = np.zeros((NB, B), bool)
+    for s, n in enumerate(lens):
+        t = np.arange(n)
+        used[bt[s, t // B], t % B] = True
+    kc[..., 0] = np.where(used[..., None], 0x38, 0x60)  # 1 and 32
+    vc[~used] = 0x7F
+    q = np.zeros((len(lens), Hq, d), np.float32)
+    q[..., 0] = 1
+    qd, kd, btd = dev_bits(W.f32_to_bits(q, dtype), dtype), up8(kc), up(bt)
+    out = torch.full(q.shape, float("nan"), dtype=torch.float32, device="cuda")
+    pa.decode_fp8(out, qd, kd, up8(vc), up(sc), btd, up(np.array(lens, np.int32)), LN2, pt,
+                  pa.alloc_workspace(qd, kd, btd, pt))
+    for s, n in enumerate(lens):
+        check_means(out[s].double().cpu().numpy(), oracle.gather_kv(V, bt[s], n, B), 32, (ONCE[idx], s))
+
+
+SHARED_ONCE = [
+    # dtype, d, Hq, Hkv, B, group starts, prefixes, lengths, table tokens
+    ("bf16", 64, 16, 1, 16, [0, 60], [4001], [4001 + 5 * i for i in range(60)], None),
+    ("fp16", 128, 8, 2, 16, [0, 100, 104], [600, 300], [600 + 3 * i for i in range(100)] + [300, 301, 499, 600], None),
+    ("bf16", 128, 8, 8, 16, [0, 40], [1000], [1000 + 5 * i for i in range(40)], 20480),
+    ("fp16", 64, 6, 3, 4, [0, 120], [777], [777 + i % 90 for i in range(120)], None),
+    # without a pass
+    ("fp16", 128, 4, 4, 4, [0, 3], [2050], [2051, 2300, 2099], None),
+    ("bf16", 128, 8, 8, 16, [0, 4, 6], [300, 40], [301, 400, 555, 300, 41, 99], 20480),
+    ("bf16", 64, 20, 2, 16, [0, 1, 2], [64, 0], [64, 4399], None),
+]
+
+
+@pytest.mark.parametrize("idx", range(len(SHARED_ONCE)))
+def test_shared_prefix_takes_every_token_once(idx):
+    *sizes, width = SHARED_ONCE[idx]
+    case = Case(*sizes, seed=400 + idx, MB=width // sizes[4] if width else None)
+    assert case.passes() == (idx < 4)
+    B, V = case.B, np.random.default_rng(idx).integers(-8, 9, case.vc.shape).astype(np.float64)
+    used = np.zeros(V.shape[:2], bool)
+    for g, n in enumerate(case.prefixes):
+        for s in range(case.starts[g], case.starts[g + 1]):
+            t = np.arange(0 if s == case.starts[g] else min(n, case.lens[s]), case.lens[s])
+            used[case.bt[s, t // B], t % B] = True
+    K = np.zeros(V.shape)
+    K[..., 0] = np.where(used[..., None], 1, 32)
+    q = np.zeros(case.query.shape)
+    q[..., 0] = 1
+    case.scale = LN2
+    case.query, case.kc, case.vc = (W.f32_to_bits(x.astype(np.float32), case.dtype)
+                                    for x in (q, K, np.where(used[..., None, None], V, np.nan)))
+    out = case.run().double().cpu().numpy()
+    values = fp8.shared_prefix_values(V, case.bt, case.lens, case.starts, case.prefixes, B)
+    # the pass's sums may be cut off, by 2^-23 at each of the 8 products for 64 tokens
+    cut = case.max_prefix / 8 * 2.0 ** -23 if case.passes() else 0.0
+    for s in range(len(case.lens)):
+        check_means(out[s], values[s], 16, (SHARED_ONCE[idx][:5], s), cut)
