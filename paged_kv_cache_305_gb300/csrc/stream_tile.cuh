@@ -323,9 +323,9 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int e = (i & 1) * 2 + c;
-        // the query's factor first: its fp16 values may be 2^140 above the query, and the
-        // product with K's factor infinite where the score is of ordinary size
-        x[nt][i][c] = __fmul_rn((sc[i >> 1][0][nt][e] + sc[i >> 1][1][nt][e]) * q.sl2[nt][c], fk[i]);
+        // the two factors first: either alone may take the sum out of fp32's range where the
+        // score is of ordinary size
+        x[nt][i][c] = __fmul_rn(sc[i >> 1][0][nt][e] + sc[i >> 1][1][nt][e], q.sl2[nt][c] * fk[i]);
       }
     if (edge) {
 #pragma unroll

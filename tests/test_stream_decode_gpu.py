@@ -158,6 +158,21 @@ def test_8_bit_decode_of_small_bf16_queries_and_large_keys(B, Hq):
                                                                    2.0 ** -20)
 
 
+@pytest.mark.parametrize("B,Hq", [(16, 4), (2, 10)])
+def test_8_bit_decode_of_large_bf16_queries_and_small_keys(B, Hq):
+    rng = np.random.default_rng(B)
+    lens, d = [70, 600], 64
+    kc, vc, sc = random_pool(rng, sum(-(-n // B) for n in lens), B, 1, d, 2)
+    sc[:, :, 0] = 1 + sc[:, :, 0] % 3
+    bt = tables_for(rng, lens, B, kc.shape[0])
+    query = W.f32_to_bits((rng.standard_normal((2, Hq, d)) * 2.0 ** 122).astype(np.float32), "bf16")
+    got, ref = decode8(query, kc, vc, sc, bt, lens, B, 0.125, "bf16")
+    for s, n in enumerate(lens):
+        K, V = (oracle.gather_kv(fp8.pool_values(c, sc, i), bt[s], n, B) for i, c in enumerate((kc, vc)))
+        assert np.max(np.abs(got[s] - ref[s])) <= fp8.decode_bound(oracle.to_float64(query[s], "bf16"), K, V, 0.125,
+                                                                   2.0 ** -20)
+
+
 # ---------------------------------------------------- weights of any size --
 LN2 = float(np.float32(np.log(2.0)))  # this scale makes whole scores powers of two
 
