@@ -406,3 +406,39 @@ def test_shared_prefix_takes_every_token_once(idx):
     cut = case.max_prefix / 8 * 2.0 ** -23 if case.passes() else 0.0
     for s in range(len(case.lens)):
         check_means(out[s], values[s], 16, (SHARED_ONCE[idx][:5], s), cut)
+
+
+# ------------------------------------------------------ values that are NaN --
+@pytest.mark.parametrize("B", [16, 4])
+def test_8_bit_nan_reaches_its_own_outputs_alone(B):
+    rng = np.random.default_rng(B)
+    lens, Hkv, d = [700, 50, 1500, 33], 2, 64
+    kc, vc, sc = random_pool(rng, sum(-(-n // B) for n in lens), B, Hkv, d, 1)
+    bt = tables_for(rng, lens, B, kc.shape[0])
+    query = W.normal_bits((4, 10, d), "bf16", B, 2)
+    clean, _ = decode8(query, kc, vc, sc, bt, lens, B, 0.05, "bf16")
+    kc[bt[0, 650 // B], 650 % B, 1, 7] = 0x7F
+    vc[bt[2, 3 // B], 3 % B, 0, 5] = 0x7F
+    vc[bt[3, 32 // B], 32 % B, 1, 60] = 0xFF
+    got, _ = decode8(query, kc, vc, sc, bt, lens, B, 0.05, "bf16")
+    nan = np.zeros(got.shape, bool)
+    nan[0, 5:] = True
+    nan[2, :5, 5] = True
+    nan[3, 5:, 60] = True
+    assert np.array_equal(np.isnan(got), nan)
+    assert np.array_equal(got[~nan], clean[~nan])
+
+
+@pytest.mark.parametrize("members", [3, 150])
+def test_shared_prefix_nan_reaches_its_own_outputs_alone(members):
+    case = Case("fp16", 64, 8, 2, 16, [0, members, members + 2], [700, 20], [700 + i % 70 for i in range(members)] + [40, 900])
+    assert case.passes() == (members > 3)
+    clean = case.run().double().cpu().numpy()
+    case.kd[int(case.bt[0, 333 // 16]), 333 % 16, 1, 7] = float("nan")               # of the first prefix
+    case.vd[int(case.bt[members + 1, 850 // 16]), 850 % 16, 0, 5] = float("nan")     # of the last sequence
+    got = case.run().double().cpu().numpy()
+    nan = np.zeros(got.shape, bool)
+    nan[:members, 4:] = True
+    nan[members + 1, :4, 5] = True
+    assert np.array_equal(np.isnan(got), nan)
+    assert np.array_equal(got[~nan], clean[~nan])
