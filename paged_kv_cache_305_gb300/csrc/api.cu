@@ -215,7 +215,7 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
     // CTAs while their chunks are at most 2048 tokens, 101 up to 2816, otherwise one
     // for each SM. 128 suffixes of 512 tokens on average behind 2048 tokens take 61.9,
     // 64.8 and 70.4 us with 64, 101 and 152; behind 8192, 82.6, 71.5 and 76.3; behind
-    // 16384, 124, 96 and 84 (two on an SM: 101).
+    // 16384, 124, 96 and 84 (two on an SM: 101); replayed from a graph.
     for (const auto& [ctas, longest] : {std::pair{64ll, 2048ll}, {101ll, 2816ll}, {kPrefixSms, 0ll}}) {
       best = std::min(most, std::max(ctas / std::max(per_chunk, 1ll), 1ll));
       if ((x->max_prefix_len + best - 1) / best <= longest) break;

@@ -6,6 +6,9 @@
 // finds the 2 B factors of a block next to each other: one 32-byte sector for
 // B = 16, where bytes kept beside each token's row would cost a sector for
 // every few tokens of every head.
+//
+// Times in this file are of the kernel alone, replayed from a graph; an eager call at
+// these sizes takes 1 to 2 us more.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -148,8 +151,8 @@ copy_blocks_fp8_kernel(uint4* __restrict__ key_cache, uint4* __restrict__ value_
 // Read-back: 8 codes of K and of V per thread, 8 bytes loaded and 16 stored for
 // each, neighbours in a row: the warp loads and stores whole lines (65 us for 16
 // sequences of 2049 to 6143 tokens, 8 heads of 128; 73 us with 16 codes a thread, whose
-// two stores each skip every other 16 bytes). CTAs of one sequence take its
-// (token, head) rows in turn; tokens behind the length write nothing.
+// two stores each skip every other 16 bytes; 67 us on another box). CTAs of one sequence
+// take its (token, head) rows in turn; tokens behind the length write nothing.
 // ---------------------------------------------------------------------------
 template <typename Ty>
 __device__ __forceinline__ uint4 dequant8(const uint2& c, float f) {

@@ -7,7 +7,8 @@
 // (128 bytes of every kilobyte with 8 heads of 128 codes), and DRAM gives them
 // at a lower rate than when the neighbours are read at the same time (the
 // copies of the 128-sequence case without any arithmetic: 222 us with one head,
-// 197 us with two or four; 216 and 116 us for d = 64). A row is one (sequence, head
+// 197 us with two or four; 216 and 116 us for d = 64; times in this file are of a
+// call's kernels, replayed from a graph). A row is one (sequence, head
 // group); its tokens (those behind the shared prefix, where a pass of its own
 // computes that; otherwise the prefix's first, through the group's table) are
 // taken in stages of 32 KB (at d = 128: K and V of 32 8-bit or 16 16-bit tokens
@@ -666,7 +667,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 // Merge
 // ---------------------------------------------------------------------------
 // Up to kTogetherRows query rows: a CTA of 8 warps for each (512 rows of 57 pieces:
-// the call takes 218 us, 220 with 4 warps, 214 and 212 with 16 and 8 on a faster
+// the kernels take 218 us, 220 with 4 warps, 214 and 212 with 16 and 8 on a faster
 // box, 228 with a warp for each). More rows: a warp for each (2048 rows: 52 us, 58
 // with 8 warps).
 template <bool TOGETHER>
@@ -860,7 +861,7 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   // Three (two) CTAs on an SM, all at once: a CTA that waited for the prefix pass to
   // end would do its equal share behind it. Beside a CTA of the pass there is room
   // for one. 64 suffixes of 512 tokens behind 1024: 42 us, 47 us if the pass is not
-  // counted; 8192 tokens before 128: 71 and 88. A pass of more CTAs than there are
+  // counted; 8192 tokens before 128: 72 and 88. A pass of more CTAs than there are
   // SMs runs two on each, and this kernel behind most of it.
   const long long pass = a.groups.pass_ctas <= num_sms ? a.groups.pass_ctas : 0;
   const long long ctas = std::min<long long>((NT == 1 ? 3 : 2) * (num_sms - pass) + pass, kMaxCtas);
