@@ -1,5 +1,6 @@
-"""The streaming decode kernel where it could go wrong unseen: waits that run out,
-the ends of the types' ranges."""
+"""The streaming decode kernel, the prefix pass and the merge where they could go wrong
+unseen: waits that run out, the ends of the types' ranges, small weights beside large ones,
+long sums, single tokens, NaN."""
 import numpy as np
 import pytest
 
@@ -121,8 +122,8 @@ def test_8_bit_decode_of_equal_scores_of_any_size(dtype, size, B, sign):
     query = W.f32_to_bits(np.full((3, 4, d), size, np.float32), dtype)
     got, ref = decode8(query, kc, vc, sc, bt, lens, B, 0.125, dtype)
     V = np.max(np.abs(fp8.pool_values(vc, sc, 1)))
-    # weights of one: sums of n rows, and pieces joined by log-sum-exps with an ulp of
-    # the score's size; those are equal too
+    # equal weights: sums of n rows, which the tensor core may cut off, and pieces joined by
+    # the sums of their weights
     assert np.max(np.abs(got - ref)) <= V * (2 * 700 * 2.0 ** -23 + 2.0 ** -18)
 
 
@@ -232,7 +233,7 @@ def test_shared_prefix_with_a_dominating_token_without_a_value(members, dtype, l
     ref = fp8.shared_prefix_decode(case.query, case.kc, case.vc, case.bt, case.lens, case.starts, case.prefixes,
                                    case.B, case.scale, dtype)
     # a weight's relative error (exponent, exp2, parts), sums of n terms twice, and
-    # pieces joined by log-sum-exps of up to 32 in size (2^-18)
+    # pieces joined at references of up to 32 in size (2^-18)
     rel = 2 * (32 * 2.0 ** -24 + 2.0 ** -21 + 2 * (n + 60) * 2.0 ** -24 + 2.0 ** -18)
     assert np.max(np.abs(got - ref)) <= rel * np.max(ref)
 
