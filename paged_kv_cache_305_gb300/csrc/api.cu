@@ -234,9 +234,10 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
       if (fill >= 0.9 || w >= 3.0) break;
     }
   }
-  best = std::max(best, (x->max_prefix_len + kPrefixMaxChunk - 1) / kPrefixMaxChunk);
-  const long long t = (x->max_prefix_len + best - 1) / best;
-  x->chunk_tokens = static_cast<int>(std::min(std::max((t + 63) / 64 * 64, 64ll), 1ll << 30));
+  const long long t = std::min(std::max((x->max_prefix_len + best - 1) / best, 1ll), 1ll << 30);
+  const long long pieces = (t + kPrefixMaxPiece - 1) / kPrefixMaxPiece;  // of a chunk
+  x->piece_tokens = static_cast<int>((t + 64 * pieces - 1) / (64 * pieces) * 64);
+  x->chunk_tokens = static_cast<int>(pieces * x->piece_tokens);
   // The pass is worth its launch, its pieces and the SMs that it takes from the
   // decode kernel where it saves enough reading (from L2, mostly). Without it every
   // sequence reads the prefix itself, through its group's table. With fewer CTAs a
@@ -250,6 +251,7 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
   const bool pass = max_group_size > 0 && saved > (per_chunk <= kPrefixSms / 4 ? kPassBytes : kWidePassBytes);
   x->max_chunks =
       pass ? static_cast<int>((static_cast<long long>(x->max_prefix_len) + x->chunk_tokens - 1) / x->chunk_tokens) : 0;
+  x->max_pieces = pass ? static_cast<int>((static_cast<long long>(x->max_prefix_len) + x->piece_tokens - 1) / x->piece_tokens) : 0;
   x->pass_ctas = per_chunk * x->max_chunks;
 }
 
@@ -268,22 +270,22 @@ int stream_heads(bool fp8, int num_seqs, int num_kv_heads, long long lmax) {
 StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                            long long lmax, const PrefixArgs& groups) {
   StreamLayout w{};
-  const int max_chunks = groups.max_chunks;
-  w.heads = stream_heads(fp8, num_seqs, num_kv_heads, max_chunks > 0 ? lmax - groups.max_prefix_len : lmax);
+  const int max_pieces = groups.max_pieces;
+  w.heads = stream_heads(fp8, num_seqs, num_kv_heads, max_pieces > 0 ? lmax - groups.max_prefix_len : lmax);
   // Whole rows need no merge, cut ones share the SMs. Four sequences of up to 512
   // 8-bit tokens, 16 rows: 8.9 us cut, 12.6 us whole; 100 sequences, 400 rows: 13.4
   // us whole, 13.8 us cut.
   const bool few = static_cast<long long>(num_seqs) * (num_kv_heads / w.heads) < kFewRows;
   w.cut = lmax > (few ? kUncutTiles * (fp8 ? 32 : 16) : kUncutTokens);
-  if (!w.cut && max_chunks == 0) return w;
+  if (!w.cut && max_pieces == 0) return w;
   const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
   const size_t group = static_cast<size_t>(w.heads) * (num_q_heads / num_kv_heads);
   // one slot for each boundary of a row or a share on the line
   const size_t slots = static_cast<size_t>(num_seqs) * (num_kv_heads / w.heads) + kMaxCtas;
   w.pre_stat = round_up(static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(int2), 256);
-  w.seg_stat = w.pre_stat + round_up(rows * max_chunks * sizeof(float2), 256);
+  w.seg_stat = w.pre_stat + round_up(rows * max_pieces * sizeof(float2), 256);
   w.pre_out = w.seg_stat + round_up(slots * group * sizeof(float2), 256);
-  w.seg_out = w.pre_out + rows * max_chunks * head_dim * sizeof(float);
+  w.seg_out = w.pre_out + rows * max_pieces * head_dim * sizeof(float);
   w.total = w.seg_out + slots * group * head_dim * sizeof(float);
   return w;
 }

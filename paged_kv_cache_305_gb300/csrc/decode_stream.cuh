@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kMergeWarps<TOGETHER> * 32) decode_merge_kerne
   const int Hc = a.heads_at_a_time, G = a.group;
   {
     // piece k: of the prefix pass, or in one of the row's slots
-    const size_t pre = row * a.groups.max_chunks, step = static_cast<size_t>(Hc) * G;
+    const size_t pre = row * a.groups.max_pieces, step = static_cast<size_t>(Hc) * G;
     const size_t in_slot = static_cast<size_t>(h % Hc) * G + g;
     auto piece_at = [&](int k) { return static_cast<size_t>(mine.x + k - before) * step + in_slot; };
     auto stat_at = [&](int k) {

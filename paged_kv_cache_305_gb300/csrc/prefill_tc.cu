@@ -310,7 +310,48 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     const float sl2 = fabsf(a.scale_log2);  // the query tile carries the sign
     float m = -INFINITY, l = 0.f;  // running max (base-2 units) and sum of weights
     [[maybe_unused]] float mraw = -INFINITY;  // PREFIX: the raw score that m came from
+    [[maybe_unused]] int piece = 0, left = 0;  // PREFIX: the row's next piece, and its tiles still to come
+    if constexpr (PREFIX) piece = tile0 * kKeys / a.groups.piece_tokens;
+    // O of this row over its sum of weights, as fp32 or 16-bit values
+    auto store = [&](void* out, bool f32, size_t row) {
+      tc::tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t x[16];
+        tc::tmem_ld16(lane_addr + kColO + 16 * c, x);
+        tc::tmem_ld_wait16(x);
+        if (!row_valid) continue;
+        if (PREFIX || f32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * D + 16 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
+                               __uint_as_float(x[4 * i + 2]) * inv,
+                               __uint_as_float(x[4 * i + 3]) * inv);
+        } else {
+          uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(out) + row * D + 16 * c);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint4 w;
+            w.x = Ty::pack(__uint_as_float(x[8 * i]) * inv, __uint_as_float(x[8 * i + 1]) * inv);
+            w.y = Ty::pack(__uint_as_float(x[8 * i + 2]) * inv, __uint_as_float(x[8 * i + 3]) * inv);
+            w.z = Ty::pack(__uint_as_float(x[8 * i + 4]) * inv, __uint_as_float(x[8 * i + 5]) * inv);
+            w.w = Ty::pack(__uint_as_float(x[8 * i + 6]) * inv, __uint_as_float(x[8 * i + 7]) * inv);
+            o[i] = w;
+          }
+        }
+      }
+    };
+    const size_t out_row = static_cast<size_t>(q0 + j0 + r / G) * a.num_q_heads +
+                           static_cast<size_t>(h) * G + r % G;
     for (int j = 0; j < ntiles; ++j) {
+      bool first = j == 0;  // of O's sum
+      if constexpr (PREFIX) {
+        first = left == 0;
+        if (first) left = min(a.groups.piece_tokens / kKeys, ntiles - j);
+        --left;
+      }
       ok = warp_wait(bar(kBarSFull + (j & 1)), (j >> 1) & 1);
       if (!ok) break;
       tc::tc_fence_after();
@@ -424,7 +465,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         ok = warp_wait(bar(kBarODone + ((j - 1) & 1)), ((j - 1) >> 1) & 1);
         if (!ok) break;
         tc::tc_fence_after();
-        if (rescale) {
+        if (rescale && !first) {
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             uint32_t x[16];
@@ -453,45 +494,21 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
       tc::tmem_st_wait();
       tc::tc_fence_before();
       tc::mbar_arrive(bar(kBarPFull));
-    }
-    if (ok) ok = warp_wait(bar(kBarODone + ((ntiles - 1) & 1)), ((ntiles - 1) >> 1) & 1);
-    if (ok) {
-      tc::tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      size_t row = static_cast<size_t>(q0 + j0 + r / G) * a.num_q_heads +
-                   static_cast<size_t>(h) * G + r % G;
-      void* out = a.out;
-      if constexpr (PREFIX) {  // the chunk's piece of the row
-        out = a.pre_out;
-        row = row * a.groups.max_chunks + blockIdx.x / a.prefix_tiles;
-        if (row_valid) a.pre_stat[row] = make_float2(m, l * ex2(-kPartsLog2Offset<Ty>));
-      }
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t x[16];
-        tc::tmem_ld16(lane_addr + kColO + 16 * c, x);
-        tc::tmem_ld_wait16(x);
-        if (!row_valid) continue;
-        if (PREFIX || a.out_f32) {
-          float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * D + 16 * c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
-                               __uint_as_float(x[4 * i + 2]) * inv,
-                               __uint_as_float(x[4 * i + 3]) * inv);
-        } else {
-          uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D + 16 * c);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint4 w;
-            w.x = Ty::pack(__uint_as_float(x[8 * i]) * inv, __uint_as_float(x[8 * i + 1]) * inv);
-            w.y = Ty::pack(__uint_as_float(x[8 * i + 2]) * inv, __uint_as_float(x[8 * i + 3]) * inv);
-            w.z = Ty::pack(__uint_as_float(x[8 * i + 4]) * inv, __uint_as_float(x[8 * i + 5]) * inv);
-            w.w = Ty::pack(__uint_as_float(x[8 * i + 6]) * inv, __uint_as_float(x[8 * i + 7]) * inv);
-            o[i] = w;
-          }
+      if constexpr (PREFIX) {
+        if (left == 0) {  // the piece is complete: the next tile's P V starts O anew
+          ok = warp_wait(bar(kBarODone + (j & 1)), (j >> 1) & 1);
+          if (!ok) break;
+          const size_t at = out_row * a.groups.max_pieces + piece++;
+          if (row_valid) a.pre_stat[at] = make_float2(m, l * ex2(-kPartsLog2Offset<Ty>));
+          store(a.pre_out, true, at);
+          m = mraw = -INFINITY;
+          l = 0.f;
         }
       }
+    }
+    if constexpr (!PREFIX) {
+      if (ok) ok = warp_wait(bar(kBarODone + ((ntiles - 1) & 1)), ((ntiles - 1) >> 1) & 1);
+      if (ok) store(a.out, a.out_f32 != 0, out_row);
     }
   } else if (warp == kKWarp || warp == kVWarp) {
     // ---------------- producers: K (or V) tiles of 64 tokens through the block table
@@ -703,6 +720,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         last_parity = (j >> 1) & 1;
       }
     } else {
+      int begun = 0;  // tiles of O's sum: all, PREFIX: of the piece
       for (int j = 0; j < ntiles && ok; ++j) {
         const int b = j & 1;
         ok = tc::mbar_wait(bar(kBarPFull), j & 1) &&
@@ -718,8 +736,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
           for (int ks = 0; ks < kKeys / 16; ++ks)
             tc::mma_ts(tmem + kColO, colP + part * 32 + ks * 8, dv + ks * kVStep,
-                       id_o, (j > 0 || part > 0 || ks > 0) ? 1u : 0u);
+                       id_o, (begun > 0 || part > 0 || ks > 0) ? 1u : 0u);
         }
+        ++begun;
+        if constexpr (PREFIX) begun = begun == a.groups.piece_tokens / kKeys ? 0 : begun;
         tc::tc_commit(bar(kBarODone + b));
         last_bar = bar(kBarODone + b);
         last_parity = (j >> 1) & 1;

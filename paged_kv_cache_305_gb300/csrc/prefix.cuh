@@ -30,7 +30,7 @@ __device__ __forceinline__ int group_of(const PrefixArgs& x, int s) {
 // Pieces that the prefix pass, where there is one, leaves for a sequence with
 // `shared` tokens of prefix.
 __device__ __forceinline__ int prefix_pieces(const PrefixArgs& x, int shared) {
-  return x.max_chunks == 0 ? 0 : static_cast<int>((static_cast<unsigned>(shared) + x.chunk_tokens - 1) / x.chunk_tokens);
+  return x.max_chunks == 0 ? 0 : static_cast<int>((static_cast<unsigned>(shared) + x.piece_tokens - 1) / x.piece_tokens);
 }
 
 // Counts the groups whose start, size or prefix is out of range (one thread a

@@ -17,6 +17,8 @@ struct PrefixArgs {
   int chunk_tokens;   // tokens of the prefix that one CTA of the prefix pass takes
   int max_chunks;     // ceil(max_prefix_len / chunk_tokens); 0: no prefix pass, every sequence
                       // reads its group's prefix itself
+  int piece_tokens;   // tokens of a piece that the pass leaves; divides chunk_tokens
+  int max_pieces;     // ceil(max_prefix_len / piece_tokens), or 0
   long long pass_ctas;  // of the prefix pass
 };
 
@@ -46,7 +48,7 @@ struct StreamArgs {
   // Pieces: (m, l), the reference of a row's weights 2^(score - m) in binary orders and
   // their sum, and normalised fp32 rows [.., d]. Not m + log2 l in one number: an ulp of
   // a large m is more than log2 l can spare.
-  float2* pre_stat;     // [S, Hq, max_chunks] pieces of the prefix pass
+  float2* pre_stat;     // [S, Hq, max_pieces] pieces of the prefix pass
   float* pre_out;
   float2* seg_stat;     // [slots, heads_at_a_time, G] pieces of segments
   float* seg_out;
@@ -78,12 +80,13 @@ struct Fp8Pool {
 constexpr int kPrefixRows = 128;
 constexpr long long kPrefixSms = 152;
 constexpr int kPrefixMinChunk = 256;
-// A chunk's products add up in the tensor core, which cuts off: up to 2^-23 of a sum of
+// A piece's products add up in the tensor core, which cuts off: up to 2^-23 of a sum of
 // positive terms for each of a tile's eight. 8192 tokens lost 9e-5 of it at most (131072:
-// 1.6e-3, half a step of bf16). 96 sequences in 12 groups behind 16384 tokens of 8 heads
-// of 128, 96 CTAs a chunk: 186 us with 8192, 195 with 4096, 184 with 2048, 219 without a limit;
-// 128 in 32 groups: 373, 383, 385 and 366; one group of 128 behind 8192: 72, 72, 77 and 72.
-constexpr long long kPrefixMaxChunk = 8192;
+// 1.6e-3, half a step of bf16), so a CTA leaves a piece every 8192 tokens of its chunk. (Chunks
+// of at most 8192 tokens were no faster on the whole, and a bound far above the prefixes
+// then costs CTAs with nothing to do: 128 sequences behind 8192 tokens, bounds of 131072
+// and 1 M: 155 and 161 us.)
+constexpr long long kPrefixMaxPiece = 8192;
 constexpr double kPassBytes = 32e6, kWidePassBytes = 128e6;
 void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int head_dim, int lmax,
                  int max_prefix_len, int max_group_size);

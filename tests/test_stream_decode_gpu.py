@@ -443,3 +443,26 @@ def test_shared_prefix_nan_reaches_its_own_outputs_alone(members):
     nan[members + 1, :4, 5] = True
     assert np.array_equal(np.isnan(got), nan)
     assert np.array_equal(got[~nan], clean[~nan])
+
+
+def test_pieces_inside_a_chunk_of_a_shared_prefix():
+    # 300 groups fill the machine with one chunk each: a CTA leaves two pieces of 6016
+    # tokens. Whole numbers add up exactly, also where sums are cut off
+    S, Hq, d, B, n = 600, 2, 64, 16, 12000
+    NB = n // B + 1
+    V = np.random.default_rng(5).integers(-8, 9, (NB, B, 1, d)).astype(np.float64)
+    K, q = np.zeros(V.shape), np.zeros((S, Hq, d))
+    K[..., 0], q[..., 0] = 1, 1
+    bt = np.random.default_rng(6).permutation(NB).astype(np.int32)[None].repeat(S, 0)
+    lens = (n + np.arange(S) % 3).astype(np.int32)
+    qd, k, v = (dev_bits(W.f32_to_bits(x.astype(np.float32), "bf16"), "bf16") for x in (q, K, V))
+    starts = torch.arange(0, S + 1, 2, dtype=torch.int32, device="cuda")
+    prefixes = torch.full((S // 2,), n, dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, float("nan"), dtype=torch.float32, device="cuda")
+    btd = up(bt)
+    for bound in (n, NB * B):
+        pa.decode_shared_prefix(out, qd, k, v, btd, up(lens), starts, prefixes, bound, 2, LN2,
+                                pa.alloc_shared_prefix_workspace(qd, k, btd, starts, bound, 2))
+        got = out.double().cpu().numpy()
+        for s in range(S):
+            check_means(got[s], oracle.gather_kv(V, bt[s], int(lens[s]), B), 16, (bound, s))
