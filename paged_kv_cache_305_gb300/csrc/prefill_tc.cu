@@ -310,8 +310,6 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     const float sl2 = fabsf(a.scale_log2);  // the query tile carries the sign
     float m = -INFINITY, l = 0.f;  // running max (base-2 units) and sum of weights
     [[maybe_unused]] float mraw = -INFINITY;  // PREFIX: the raw score that m came from
-    [[maybe_unused]] int piece = 0, left = 0;  // PREFIX: the row's next piece, and its tiles still to come
-    if constexpr (PREFIX) piece = tile0 * kKeys / a.groups.piece_tokens;
     // O of this row over its sum of weights, as fp32 or 16-bit values
     auto store = [&](void* out, bool f32, size_t row) {
       tc::tc_fence_after();
@@ -345,13 +343,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
     };
     const size_t out_row = static_cast<size_t>(q0 + j0 + r / G) * a.num_q_heads +
                            static_cast<size_t>(h) * G + r % G;
-    for (int j = 0; j < ntiles; ++j) {
-      bool first = j == 0;  // of O's sum
-      if constexpr (PREFIX) {
-        first = left == 0;
-        if (first) left = min(a.groups.piece_tokens / kKeys, ntiles - j);
-        --left;
-      }
+    // O sums up tiles [begin, end): all of them; PREFIX: a piece's
+    int begin = 0, end = ntiles;
+    if constexpr (PREFIX) end = min(ntiles, a.groups.piece_tokens / kKeys);
+    for (int j = 0;; ++j) {
       ok = warp_wait(bar(kBarSFull + (j & 1)), (j >> 1) & 1);
       if (!ok) break;
       tc::tc_fence_after();
@@ -465,7 +460,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
         ok = warp_wait(bar(kBarODone + ((j - 1) & 1)), ((j - 1) >> 1) & 1);
         if (!ok) break;
         tc::tc_fence_after();
-        if (rescale && !first) {
+        if (rescale && j > begin) {
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             uint32_t x[16];
@@ -494,21 +489,22 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap,
       tc::tmem_st_wait();
       tc::tc_fence_before();
       tc::mbar_arrive(bar(kBarPFull));
-      if constexpr (PREFIX) {
-        if (left == 0) {  // the piece is complete: the next tile's P V starts O anew
-          ok = warp_wait(bar(kBarODone + (j & 1)), (j >> 1) & 1);
-          if (!ok) break;
-          const size_t at = out_row * a.groups.max_pieces + piece++;
-          if (row_valid) a.pre_stat[at] = make_float2(m, l * ex2(-kPartsLog2Offset<Ty>));
-          store(a.pre_out, true, at);
-          m = mraw = -INFINITY;
-          l = 0.f;
-        }
+      if (j + 1 < end) continue;
+      ok = warp_wait(bar(kBarODone + (j & 1)), (j >> 1) & 1);
+      if (!ok) break;
+      if constexpr (!PREFIX) {
+        store(a.out, a.out_f32 != 0, out_row);
+        break;
+      } else {
+        const size_t at = out_row * a.groups.max_pieces + (tile0 + begin) * kKeys / a.groups.piece_tokens;
+        if (row_valid) a.pre_stat[at] = make_float2(m, l * ex2(-kPartsLog2Offset<Ty>));
+        store(a.pre_out, true, at);
+        if (end == ntiles) break;
+        begin = end;  // the next tile's P V starts O anew
+        end = min(ntiles, end + a.groups.piece_tokens / kKeys);
+        m = mraw = -INFINITY;
+        l = 0.f;
       }
-    }
-    if constexpr (!PREFIX) {
-      if (ok) ok = warp_wait(bar(kBarODone + ((ntiles - 1) & 1)), ((ntiles - 1) >> 1) & 1);
-      if (ok) store(a.out, a.out_f32 != 0, out_row);
     }
   } else if (warp == kKWarp || warp == kVWarp) {
     // ---------------- producers: K (or V) tiles of 64 tokens through the block table
