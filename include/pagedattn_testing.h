@@ -38,7 +38,8 @@ int pa_testing_prefill_stalled(void* out, const void* query, const void* key_cac
  * and so do the computing warps that wait for the next stage; copies in flight
  * land, and the CTAs and then the merge kernel end. A CTA in which a wait gave up
  * is counted by pa_wait_timeout_count (at least once); rows of `out` may hold
- * anything. Arguments, checks and errors as for the two calls.
+ * anything. Where there is a prefix pass, its product-issuing threads stall as
+ * pa_testing_prefill_stalled's do. Arguments, checks and errors as for the two calls.
  */
 int pa_testing_decode_fp8_stalled(void* out, const void* query, const void* key_cache,
                                   const void* value_cache, const uint8_t* cache_scales,

@@ -954,6 +954,7 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
     p.bad = bad;
     p.timeouts = timeouts;
     p.groups = groups;
+    p.stall_for_test = stall_for_test;
     p.pre_stat = a.pre_stat;
     p.pre_out = a.pre_out;
     e = pa::launch_prefix_pass(p, head_dim, bf16, stream);

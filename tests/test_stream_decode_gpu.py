@@ -280,7 +280,7 @@ def test_sums_of_long_rows_do_not_drift(op, dtype):
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_sums_of_long_prefixes_do_not_drift(dtype):
     # 300 pairs of sequences behind 131072 tokens, in whole waves of CTAs of any chunk
-    # length. A chunk of at most 8192 tokens adds up 8 products for each 64 of them, and
+    # length. A piece of at most 8192 tokens adds up 8 products for each 64 of them, and
     # the tensor core may cut off: 2^-23 of the sum at each addition, as decode_bound has it
     S, d, B, n, NB = 600, 64, 16, 131072, 64
     rng = np.random.default_rng(4)

@@ -31,8 +31,8 @@ def test_workspaces_of_the_largest_tables(lib):
     f8, fp = pa.decode_fp8_workspace_bytes, pa.decode_shared_prefix_workspace_bytes
     assert 0 < f8(1, 1, 1, 64, MOST // 64, 64) < 2 ** 20
     assert f8(1, 1, 1, 64, MOST // 64 + 1, 64) == 0
-    # two sequences behind a prefix of the whole table, cut into chunks of 8192 tokens: a piece
-    # of 64 floats, their reference and sum for each row and chunk, and those of the cuts
+    # two sequences behind a prefix of the whole table, cut into pieces of up to 8192 tokens:
+    # 64 floats, their reference and sum for each row and piece, and those of the cuts
     for prefix in (2 ** 30, MOST - 64, MOST, 2 ** 31 - 1):
         n, chunks = fp(2, 1, 1, 1, 64, MOST // 64, 64, prefix, 2), -(-min(prefix, MOST) // 8192)
         assert 0 <= n - 2 * chunks * 66 * 4 < 2 ** 20, prefix
