@@ -390,6 +390,56 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
                                      int max_blocks_per_seq, int block_size);
 
 /*
+ * The 4-bit cache. A pool holds, for K and for V, e2m1 codes, two a byte,
+ *   key_cache, value_cache  [NB, B, Hkv, d / 2]   uint8; element 2 i of a row in
+ *                                                 bits 0-3 of byte i, 2 i + 1 in 4-7
+ * and one exponent byte for every 32 neighbouring elements of a row
+ *   cache_scales            [NB, Hkv, 2, B, d / 32]  uint8; K's at index 0, V's at 1
+ * Element i of the row of (slot, kv head) is code_i * 2^(e - 127), e the byte of
+ * its group of 32; e = 0 reads as a factor of zero (a zero-filled pool holds
+ * zeros), e = 255 as one of infinity. e2m1 is the format with a sign, two exponent
+ * bits and one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0 to 7; 8 to 15 are
+ * their negatives). A pool takes d / 2 + d / 32 bytes a row (68 for d = 128) where a
+ * 16-bit cache takes 2 d. Tables, slots, lengths and the block manager are those of
+ * the other caches.
+ *
+ * Quantising cache write: what pa_reshape_and_cache does, into a 4-bit pool. A
+ * group's e is the smallest of 1 .. 252 with max |x_i| <= 7 * 2^(e - 127) (252 where
+ * there is none, 0 for a group of zeros); code_i is x_i * 2^(127 - e) at the nearest
+ * e2m1 value, ties to even, magnitudes above 6 at 6. (6 and not 7 is the largest code:
+ * between them no element is off by more than those between 4 and 6 may be, and a
+ * larger factor would cost the others a bit.) A group with a NaN or an infinity is
+ * written as zero codes with e = 255, so that all 32 elements read as NaN. A group's
+ * values depend on that group alone. A slot must not occur twice among the
+ * non-negative slots. dtype: of key and value. Sizes, skipped and counted slots and
+ * errors as for pa_reshape_and_cache_fp8.
+ */
+int pa_reshape_and_cache_fp4(const void* key, const void* value,
+                             void* key_cache, void* value_cache, uint8_t* cache_scales,
+                             const int64_t* slot_mapping, int num_tokens,
+                             int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                             pa_dtype dtype, cudaStream_t stream);
+
+/* pa_copy_blocks for a 4-bit pool: codes and exponent bytes of whole blocks. */
+int pa_copy_blocks_fp4(void* key_cache, void* value_cache, uint8_t* cache_scales,
+                       const int32_t* src, const int32_t* dst, int num_copies,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       cudaStream_t stream);
+
+/*
+ * pa_gather_cache_fp8 for a 4-bit pool: rows of sequences as 16-bit values, exact
+ * unless out of the type's range (fp16: a group whose largest element is at the end of
+ * fp16's range may read back as infinite). Arguments, sizes and errors as there.
+ */
+int pa_gather_cache_fp4(void* key_out, void* value_out,
+                        const void* key_cache, const void* value_cache,
+                        const uint8_t* cache_scales, const int32_t* block_tables,
+                        const int32_t* seq_lens, const int64_t* out_start, int64_t num_out_rows,
+                        int num_seqs, int num_kv_heads, int head_dim, int block_size,
+                        int max_blocks_per_seq, int num_blocks, pa_dtype dtype,
+                        cudaStream_t stream);
+
+/*
  * pa_decode for batches in which groups of sequences begin with the same
  * tokens: one system prompt before every request, or several candidates of one
  * prompt (pa_bm_fork). Where that saves enough reading (some 30 MB, by the sizes and

@@ -381,10 +381,10 @@ int pa_copy_blocks(void* key_cache, void* value_cache, const int32_t* src, const
 
 namespace {
 
-// The checks that every entry point on an 8-bit pool shares; fills *p.
-int check_fp8_pool(const void* key_cache, const void* value_cache, const uint8_t* cache_scales,
-                   int num_kv_heads, int head_dim, int block_size, int num_blocks, bool pointers,
-                   pa::Fp8Pool* p) {
+// The checks that every entry point on an 8-bit or 4-bit pool shares; fills *p.
+int check_scaled_pool(const void* key_cache, const void* value_cache, const uint8_t* cache_scales,
+                      int num_kv_heads, int head_dim, int block_size, int num_blocks, bool pointers,
+                      pa::ScaledPool* p) {
   if (num_kv_heads < 1) return fail(PA_ERR_INVALID, "num_kv_heads %d < 1", num_kv_heads);
   if (head_dim != 64 && head_dim != 128)
     return fail(PA_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
@@ -409,21 +409,17 @@ int check_fp8_pool(const void* key_cache, const void* value_cache, const uint8_t
   return PA_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int pa_reshape_and_cache_fp8(const void* key, const void* value, void* key_cache,
-                             void* value_cache, uint8_t* cache_scales, const int64_t* slot_mapping,
-                             int num_tokens, int num_kv_heads, int head_dim, int block_size,
-                             int num_blocks, pa_dtype dtype, cudaStream_t stream) {
+// pa_reshape_and_cache_fp8 and _fp4, pa_copy_blocks_fp8 and _fp4, pa_gather_cache_fp8 and _fp4.
+int write_scaled(bool fp4, const void* key, const void* value, void* key_cache, void* value_cache,
+                 uint8_t* cache_scales, const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                 int head_dim, int block_size, int num_blocks, pa_dtype dtype, cudaStream_t stream) {
   g_error.clear();
   int rc = check_dtype(dtype);
   if (rc != PA_OK) return rc;
   if (num_tokens < 0) return fail(PA_ERR_INVALID, "num_tokens %d < 0", num_tokens);
-  pa::Fp8Pool p{};
-  rc = check_fp8_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
-                      num_blocks, num_tokens > 0, &p);
+  pa::ScaledPool p{};
+  rc = check_scaled_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
+                         num_blocks, num_tokens > 0, &p);
   if (rc != PA_OK || num_tokens == 0) return rc;
   if (!key || !value || !slot_mapping) return fail(PA_ERR_INVALID, "a pointer argument is NULL");
   if (!aligned16(key) || !aligned16(value))
@@ -433,37 +429,38 @@ int pa_reshape_and_cache_fp8(const void* key, const void* value, void* key_cache
   unsigned long long* bad = nullptr;
   rc = bad_counter(&bad);
   if (rc != PA_OK) return rc;
-  cudaError_t e = pa::launch_write_fp8(p, dtype == PA_BFLOAT16, key, value, slot_mapping,
-                                       num_tokens, bad, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "reshape_and_cache_fp8 launch");
+  const bool bf16 = dtype == PA_BFLOAT16;
+  cudaError_t e = fp4 ? pa::launch_write_fp4(p, bf16, key, value, slot_mapping, num_tokens, bad, stream)
+                      : pa::launch_write_fp8(p, bf16, key, value, slot_mapping, num_tokens, bad, stream);
+  if (e != cudaSuccess) return cuda_fail(e, fp4 ? "reshape_and_cache_fp4 launch" : "reshape_and_cache_fp8 launch");
   return PA_OK;
 }
 
-int pa_copy_blocks_fp8(void* key_cache, void* value_cache, uint8_t* cache_scales,
-                       const int32_t* src, const int32_t* dst, int num_copies, int num_kv_heads,
-                       int head_dim, int block_size, int num_blocks, cudaStream_t stream) {
+int copy_scaled(bool fp4, void* key_cache, void* value_cache, uint8_t* cache_scales, const int32_t* src,
+                const int32_t* dst, int num_copies, int num_kv_heads, int head_dim, int block_size,
+                int num_blocks, cudaStream_t stream) {
   g_error.clear();
   if (num_copies < 0) return fail(PA_ERR_INVALID, "num_copies %d < 0", num_copies);
-  pa::Fp8Pool p{};
-  int rc = check_fp8_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
-                          num_blocks, num_copies > 0, &p);
+  pa::ScaledPool p{};
+  int rc = check_scaled_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
+                             num_blocks, num_copies > 0, &p);
   if (rc != PA_OK || num_copies == 0) return rc;
   if (!src || !dst) return fail(PA_ERR_INVALID, "a pointer argument is NULL");
   if (!aligned4(src) || !aligned4(dst)) return fail(PA_ERR_INVALID, "src and dst must be 4-byte aligned");
   unsigned long long* bad = nullptr;
   rc = bad_counter(&bad);
   if (rc != PA_OK) return rc;
-  cudaError_t e = pa::launch_copy_blocks_fp8(p, src, dst, num_copies, bad, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "copy_blocks_fp8 launch");
+  const int row_bytes = fp4 ? head_dim / 2 : head_dim, group_bytes = fp4 ? head_dim / 32 : 1;
+  cudaError_t e = pa::launch_copy_blocks_scaled(p, row_bytes, group_bytes, src, dst, num_copies, bad, stream);
+  if (e != cudaSuccess) return cuda_fail(e, fp4 ? "copy_blocks_fp4 launch" : "copy_blocks_fp8 launch");
   return PA_OK;
 }
 
-int pa_gather_cache_fp8(void* key_out, void* value_out, const void* key_cache,
-                        const void* value_cache, const uint8_t* cache_scales,
-                        const int32_t* block_tables, const int32_t* seq_lens,
-                        const int64_t* out_start, int64_t num_out_rows, int num_seqs,
-                        int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
-                        int num_blocks, pa_dtype dtype, cudaStream_t stream) {
+int gather_scaled(bool fp4, void* key_out, void* value_out, const void* key_cache, const void* value_cache,
+                  const uint8_t* cache_scales, const int32_t* block_tables, const int32_t* seq_lens,
+                  const int64_t* out_start, int64_t num_out_rows, int num_seqs, int num_kv_heads,
+                  int head_dim, int block_size, int max_blocks_per_seq, int num_blocks, pa_dtype dtype,
+                  cudaStream_t stream) {
   g_error.clear();
   int rc = check_dtype(dtype);
   if (rc != PA_OK) return rc;
@@ -472,9 +469,9 @@ int pa_gather_cache_fp8(void* key_out, void* value_out, const void* key_cache,
   if (num_out_rows < 0)
     return fail(PA_ERR_INVALID, "num_out_rows %lld < 0", static_cast<long long>(num_out_rows));
   const bool work = num_seqs > 0 && num_out_rows > 0;
-  pa::Fp8Pool p{};
-  rc = check_fp8_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
-                      num_blocks, work, &p);
+  pa::ScaledPool p{};
+  rc = check_scaled_pool(key_cache, value_cache, cache_scales, num_kv_heads, head_dim, block_size,
+                         num_blocks, work, &p);
   if (rc != PA_OK) return rc;
   if (max_blocks_per_seq < 1)
     return fail(PA_ERR_INVALID, "max_blocks_per_seq %d < 1", max_blocks_per_seq);
@@ -492,11 +489,69 @@ int pa_gather_cache_fp8(void* key_out, void* value_out, const void* key_cache,
   unsigned long long* bad = nullptr;
   rc = bad_counter(&bad);
   if (rc != PA_OK) return rc;
-  cudaError_t e = pa::launch_gather_fp8(p, dtype == PA_BFLOAT16, key_out, value_out, num_out_rows,
-                                        block_tables, seq_lens, out_start, num_seqs,
-                                        max_blocks_per_seq, bad, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "gather_cache_fp8 launch");
+  const bool bf16 = dtype == PA_BFLOAT16;
+  cudaError_t e = fp4 ? pa::launch_gather_fp4(p, bf16, key_out, value_out, num_out_rows, block_tables, seq_lens,
+                                              out_start, num_seqs, max_blocks_per_seq, bad, stream)
+                      : pa::launch_gather_fp8(p, bf16, key_out, value_out, num_out_rows, block_tables, seq_lens,
+                                              out_start, num_seqs, max_blocks_per_seq, bad, stream);
+  if (e != cudaSuccess) return cuda_fail(e, fp4 ? "gather_cache_fp4 launch" : "gather_cache_fp8 launch");
   return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_reshape_and_cache_fp8(const void* key, const void* value, void* key_cache,
+                             void* value_cache, uint8_t* cache_scales, const int64_t* slot_mapping,
+                             int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, pa_dtype dtype, cudaStream_t stream) {
+  return write_scaled(false, key, value, key_cache, value_cache, cache_scales, slot_mapping, num_tokens,
+                      num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
+}
+
+int pa_reshape_and_cache_fp4(const void* key, const void* value, void* key_cache,
+                             void* value_cache, uint8_t* cache_scales, const int64_t* slot_mapping,
+                             int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, pa_dtype dtype, cudaStream_t stream) {
+  return write_scaled(true, key, value, key_cache, value_cache, cache_scales, slot_mapping, num_tokens,
+                      num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
+}
+
+int pa_copy_blocks_fp8(void* key_cache, void* value_cache, uint8_t* cache_scales,
+                       const int32_t* src, const int32_t* dst, int num_copies, int num_kv_heads,
+                       int head_dim, int block_size, int num_blocks, cudaStream_t stream) {
+  return copy_scaled(false, key_cache, value_cache, cache_scales, src, dst, num_copies, num_kv_heads, head_dim,
+                     block_size, num_blocks, stream);
+}
+
+int pa_copy_blocks_fp4(void* key_cache, void* value_cache, uint8_t* cache_scales,
+                       const int32_t* src, const int32_t* dst, int num_copies, int num_kv_heads,
+                       int head_dim, int block_size, int num_blocks, cudaStream_t stream) {
+  return copy_scaled(true, key_cache, value_cache, cache_scales, src, dst, num_copies, num_kv_heads, head_dim,
+                     block_size, num_blocks, stream);
+}
+
+int pa_gather_cache_fp8(void* key_out, void* value_out, const void* key_cache,
+                        const void* value_cache, const uint8_t* cache_scales,
+                        const int32_t* block_tables, const int32_t* seq_lens,
+                        const int64_t* out_start, int64_t num_out_rows, int num_seqs,
+                        int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                        int num_blocks, pa_dtype dtype, cudaStream_t stream) {
+  return gather_scaled(false, key_out, value_out, key_cache, value_cache, cache_scales, block_tables, seq_lens,
+                       out_start, num_out_rows, num_seqs, num_kv_heads, head_dim, block_size,
+                       max_blocks_per_seq, num_blocks, dtype, stream);
+}
+
+int pa_gather_cache_fp4(void* key_out, void* value_out, const void* key_cache,
+                        const void* value_cache, const uint8_t* cache_scales,
+                        const int32_t* block_tables, const int32_t* seq_lens,
+                        const int64_t* out_start, int64_t num_out_rows, int num_seqs,
+                        int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                        int num_blocks, pa_dtype dtype, cudaStream_t stream) {
+  return gather_scaled(true, key_out, value_out, key_cache, value_cache, cache_scales, block_tables, seq_lens,
+                       out_start, num_out_rows, num_seqs, num_kv_heads, head_dim, block_size,
+                       max_blocks_per_seq, num_blocks, dtype, stream);
 }
 
 }  // extern "C"

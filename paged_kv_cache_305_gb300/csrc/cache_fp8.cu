@@ -103,12 +103,13 @@ write_fp8_kernel(const uint4* __restrict__ key, const uint4* __restrict__ value,
 
 // ---------------------------------------------------------------------------
 // Block copy: the three arrays of a block, codes in 16-byte vectors (a block's
-// codes are a multiple of 64 bytes), exponent bytes in pairs. Bound by memory.
+// codes are a multiple of 32 bytes), exponent bytes in pairs. Bound by memory. It
+// copies blocks of 4-bit pools too.
 // Two vectors of K and of V in flight per thread: 1000 blocks of 64 tokens, 8 heads
 // of 128, 41.9 us (6.3 TB/s), 44 us with one, more with four (127 registers).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads)
-copy_blocks_fp8_kernel(uint4* __restrict__ key_cache, uint4* __restrict__ value_cache,
+copy_blocks_scaled_kernel(uint4* __restrict__ key_cache, uint4* __restrict__ value_cache,
                        uint16_t* __restrict__ scales, const int32_t* __restrict__ src,
                        const int32_t* __restrict__ dst, int num_copies, long long block_chunks,
                        long long scale_pairs, int num_blocks, unsigned long long* bad) {
@@ -224,7 +225,7 @@ gather_fp8_kernel(uint4* __restrict__ key_out, uint4* __restrict__ value_out,
 }
 
 template <typename Ty, int D>
-cudaError_t write_typed(const Fp8Pool& p, const void* key, const void* value,
+cudaError_t write_typed(const ScaledPool& p, const void* key, const void* value,
                         const int64_t* slot_mapping, int num_tokens, unsigned long long* bad,
                         cudaStream_t stream) {
   const long long rows = static_cast<long long>(num_tokens) * p.num_kv_heads;
@@ -239,7 +240,7 @@ cudaError_t write_typed(const Fp8Pool& p, const void* key, const void* value,
 }
 
 template <typename Ty, int D>
-cudaError_t gather_typed(const Fp8Pool& p, void* key_out, void* value_out, long long num_out_rows,
+cudaError_t gather_typed(const ScaledPool& p, void* key_out, void* value_out, long long num_out_rows,
                          const int32_t* block_tables, const int32_t* seq_lens,
                          const int64_t* out_start, int num_seqs, int max_blocks_per_seq,
                          unsigned long long* bad, cudaStream_t stream) {
@@ -261,7 +262,7 @@ cudaError_t gather_typed(const Fp8Pool& p, void* key_out, void* value_out, long 
 
 }  // namespace
 
-cudaError_t launch_write_fp8(const Fp8Pool& p, bool bf16, const void* key, const void* value,
+cudaError_t launch_write_fp8(const ScaledPool& p, bool bf16, const void* key, const void* value,
                              const int64_t* slot_mapping, int num_tokens, unsigned long long* bad,
                              cudaStream_t stream) {
   if (bf16)
@@ -271,16 +272,18 @@ cudaError_t launch_write_fp8(const Fp8Pool& p, bool bf16, const void* key, const
                           : write_typed<F16, 128>(p, key, value, slot_mapping, num_tokens, bad, stream);
 }
 
-cudaError_t launch_copy_blocks_fp8(const Fp8Pool& p, const int32_t* src, const int32_t* dst,
-                                   int num_copies, unsigned long long* bad, cudaStream_t stream) {
-  const long long scale_pairs = static_cast<long long>(p.num_kv_heads) << p.block_shift;
-  const long long chunks = scale_pairs * p.head_dim / 16;
+cudaError_t launch_copy_blocks_scaled(const ScaledPool& p, int row_bytes, int group_bytes, const int32_t* src,
+                                      const int32_t* dst, int num_copies, unsigned long long* bad,
+                                      cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.num_kv_heads) << p.block_shift;  // of K, and of V
+  const long long scale_pairs = rows * group_bytes;
+  const long long chunks = rows * row_bytes / 16;
   // few copies: spread them wide; many: several vectors for each thread
   const long long per = static_cast<long long>(kThreads) * (num_copies < 64 ? 1 : kCopyBatch);
   long long gx = (chunks + per - 1) / per;
   if (gx > 64) gx = 64;
   const int gy = num_copies < 65535 ? num_copies : 65535;
-  copy_blocks_fp8_kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kThreads, 0,
+  copy_blocks_scaled_kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kThreads, 0,
                            stream>>>(reinterpret_cast<uint4*>(p.key_cache),
                                      reinterpret_cast<uint4*>(p.value_cache),
                                      reinterpret_cast<uint16_t*>(p.scales), src, dst, num_copies,
@@ -288,7 +291,7 @@ cudaError_t launch_copy_blocks_fp8(const Fp8Pool& p, const int32_t* src, const i
   return cudaGetLastError();
 }
 
-cudaError_t launch_gather_fp8(const Fp8Pool& p, bool bf16, void* key_out, void* value_out,
+cudaError_t launch_gather_fp8(const ScaledPool& p, bool bf16, void* key_out, void* value_out,
                               long long num_out_rows, const int32_t* block_tables,
                               const int32_t* seq_lens, const int64_t* out_start, int num_seqs,
                               int max_blocks_per_seq, unsigned long long* bad, cudaStream_t stream) {

@@ -1,4 +1,4 @@
-// Internal interface of the 8-bit cache and of decode over a shared prefix,
+// Internal interface of the 8-bit and 4-bit caches and of decode over a shared prefix,
 // between the C-ABI layer (api.cu) and the kernel files.
 #pragma once
 
@@ -65,8 +65,9 @@ struct PrefixPassArgs : PrefillArgs {
   float* pre_out;
 };
 
-// An 8-bit pool: e4m3 codes [NB, B, Hkv, d] and exponent bytes [NB, Hkv, 2, B].
-struct Fp8Pool {
+// A pool of codes with exponent bytes. 8-bit: e4m3 codes [NB, B, Hkv, d], bytes
+// [NB, Hkv, 2, B]. 4-bit: e2m1 codes [NB, B, Hkv, d / 2], bytes [NB, Hkv, 2, B, d / 32].
+struct ScaledPool {
   uint8_t* key_cache;
   uint8_t* value_cache;
   uint8_t* scales;
@@ -118,12 +119,21 @@ cudaError_t launch_decode_prefix(const StreamArgs& a, int head_dim, bool bf16, i
                                  cudaStream_t stream);
 cudaError_t launch_prefix_pass(PrefixPassArgs a, int head_dim, bool bf16, cudaStream_t stream);
 
-cudaError_t launch_write_fp8(const Fp8Pool& p, bool bf16, const void* key, const void* value,
+cudaError_t launch_write_fp8(const ScaledPool& p, bool bf16, const void* key, const void* value,
                              const int64_t* slot_mapping, int num_tokens, unsigned long long* bad,
                              cudaStream_t stream);
-cudaError_t launch_copy_blocks_fp8(const Fp8Pool& p, const int32_t* src, const int32_t* dst,
-                                   int num_copies, unsigned long long* bad, cudaStream_t stream);
-cudaError_t launch_gather_fp8(const Fp8Pool& p, bool bf16, void* key_out, void* value_out,
+// row_bytes, group_bytes: codes and exponent bytes of a row (one token, one head, K or V)
+cudaError_t launch_copy_blocks_scaled(const ScaledPool& p, int row_bytes, int group_bytes, const int32_t* src,
+                                      const int32_t* dst, int num_copies, unsigned long long* bad,
+                                      cudaStream_t stream);
+cudaError_t launch_gather_fp8(const ScaledPool& p, bool bf16, void* key_out, void* value_out,
+                              long long num_out_rows, const int32_t* block_tables,
+                              const int32_t* seq_lens, const int64_t* out_start, int num_seqs,
+                              int max_blocks_per_seq, unsigned long long* bad, cudaStream_t stream);
+cudaError_t launch_write_fp4(const ScaledPool& p, bool bf16, const void* key, const void* value,
+                             const int64_t* slot_mapping, int num_tokens, unsigned long long* bad,
+                             cudaStream_t stream);
+cudaError_t launch_gather_fp4(const ScaledPool& p, bool bf16, void* key_out, void* value_out,
                               long long num_out_rows, const int32_t* block_tables,
                               const int32_t* seq_lens, const int64_t* out_start, int num_seqs,
                               int max_blocks_per_seq, unsigned long long* bad, cudaStream_t stream);

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 
@@ -29,7 +29,8 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_bytes", "pa_decode",
             "pa_gather_cache_fp8", "pa_decode_fp8", "pa_decode_shared_prefix",
             "pa_decode_fp8_workspace_bytes",
             "pa_decode_shared_prefix_workspace_bytes", "pa_testing_decode_fp8_stalled",
-            "pa_testing_decode_shared_prefix_stalled")
+            "pa_testing_decode_shared_prefix_stalled", "pa_reshape_and_cache_fp4",
+            "pa_copy_blocks_fp4", "pa_gather_cache_fp4")
 PA_ERR_CAPACITY = -5
 
 _lib = None
@@ -91,6 +92,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.pa_gather_cache_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, i32, i32, i32,
                                       i32, i32, i32, i32, vp]
     L.pa_gather_cache_fp8.restype = i32
+    for name in ("reshape_and_cache", "copy_blocks", "gather_cache"):
+        for what in ("argtypes", "restype"):
+            setattr(getattr(L, f"pa_{name}_fp4"), what, getattr(getattr(L, f"pa_{name}_fp8"), what))
     L.pa_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float,
                                 i32, i32, i32, i32, i32, vp, sz, vp]
     L.pa_decode_fp8.restype = i32
@@ -496,28 +500,15 @@ def reshape_and_cache_fp8(key: torch.Tensor, value: torch.Tensor, key_cache: tor
     an element is its code times 2**(byte - 127). Non-negative slots must be
     distinct.
     """
-    NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
-    device = _device_of(key, value, key_cache, value_cache, cache_scales, slot_mapping)
-    T = key.shape[0]
-    _need(key.shape == (T, Hkv, d) and value.shape == (T, Hkv, d), "key/value shape mismatch")
-    _need(key.dtype == value.dtype, "dtype mismatch")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,),
-          "slot_mapping must be int64 [num_tokens]")
-    _enqueue(load_library().pa_reshape_and_cache_fp8, device, stream, key.data_ptr(), value.data_ptr(),
-             key_cache.data_ptr(), value_cache.data_ptr(), cache_scales.data_ptr(),
-             slot_mapping.data_ptr(), T, Hkv, d, B, NB, _dtype_code(key))
+    _write_scaled(load_library().pa_reshape_and_cache_fp8, _need_fp8_pool, key, value, key_cache, value_cache,
+                  cache_scales, slot_mapping, stream)
 
 
 def copy_blocks_fp8(key_cache: torch.Tensor, value_cache: torch.Tensor, cache_scales: torch.Tensor,
                     src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """:func:`copy_blocks` for an 8-bit pool (codes and exponent bytes)."""
-    NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
-    device = _device_of(key_cache, value_cache, cache_scales, src, dst)
-    _need(src.dtype == torch.int32 and dst.dtype == torch.int32 and src.shape == dst.shape
-          and src.dim() == 1, "src/dst must be 1-D int32 tensors")
-    _enqueue(load_library().pa_copy_blocks_fp8, device, stream, key_cache.data_ptr(),
-             value_cache.data_ptr(), cache_scales.data_ptr(), src.data_ptr(), dst.data_ptr(),
-             src.shape[0], Hkv, d, B, NB)
+    _copy_scaled(load_library().pa_copy_blocks_fp8, _need_fp8_pool, key_cache, value_cache, cache_scales, src, dst,
+                 stream)
 
 
 def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: torch.Tensor,
@@ -531,7 +522,87 @@ def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: 
     rows stay as they are. With starts that are multiples of B the outputs,
     viewed as [rows / B, B, Hkv, d], are pools for :func:`prefill`.
     """
-    NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
+    _gather_scaled(load_library().pa_gather_cache_fp8, _need_fp8_pool, key_out, value_out, key_cache, value_cache,
+                   cache_scales, block_tables, seq_lens, out_start, stream)
+
+
+def _need_fp4_pool(key_cache: torch.Tensor, value_cache: torch.Tensor,
+                   cache_scales: torch.Tensor) -> Tuple[int, int, int, int]:
+    """The checks of a 4-bit pool; returns (num_blocks, block_size, num_kv_heads, head_dim)."""
+    shape = key_cache.shape
+    _need(len(shape) == 4 and value_cache.shape == shape, "cache shape mismatch")
+    _need(key_cache.dtype == value_cache.dtype == torch.uint8, "the caches must be uint8")
+    NB, B, Hkv, half = shape
+    _need(cache_scales.dtype == torch.uint8 and cache_scales.shape == (NB, Hkv, 2, B, half // 16),
+          "cache_scales must be uint8 [num_blocks, num_kv_heads, 2, block_size, head_dim / 32]")
+    return NB, B, Hkv, 2 * half
+
+
+def alloc_fp4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """Zero-filled 4-bit pool: (key_cache, value_cache, cache_scales)."""
+    codes = [torch.zeros((num_blocks, block_size, num_kv_heads, head_dim // 2), dtype=torch.uint8, device=device)
+             for _ in range(2)]
+    scales = torch.zeros((num_blocks, num_kv_heads, 2, block_size, head_dim // 32), dtype=torch.uint8,
+                         device=device)
+    return codes[0], codes[1], scales
+
+
+def reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor,
+                          value_cache: torch.Tensor, cache_scales: torch.Tensor,
+                          slot_mapping: torch.Tensor, stream=None) -> None:
+    """Quantise key/value [T, Hkv, d] rows into the 4-bit pool at slot_mapping [T] (int64).
+
+    Caches uint8 [NB, B, Hkv, d / 2], two e2m1 codes a byte (the element with the even index in the
+    low half); ``cache_scales`` uint8 [NB, Hkv, 2, B, d / 32] receives the biased power-of-two exponent
+    of every 32 elements (K at index 0, V at 1): an element is its code's value times 2**(byte - 127).
+    Non-negative slots must be distinct.
+    """
+    _write_scaled(load_library().pa_reshape_and_cache_fp4, _need_fp4_pool, key, value, key_cache, value_cache,
+                  cache_scales, slot_mapping, stream)
+
+
+def copy_blocks_fp4(key_cache: torch.Tensor, value_cache: torch.Tensor, cache_scales: torch.Tensor,
+                    src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """:func:`copy_blocks` for a 4-bit pool (codes and exponent bytes)."""
+    _copy_scaled(load_library().pa_copy_blocks_fp4, _need_fp4_pool, key_cache, value_cache, cache_scales, src, dst,
+                 stream)
+
+
+def gather_cache_fp4(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: torch.Tensor,
+                     value_cache: torch.Tensor, cache_scales: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, out_start: torch.Tensor,
+                     stream=None) -> None:
+    """Read sequences of a 4-bit pool back as 16-bit rows, as :func:`gather_cache_fp8` does."""
+    _gather_scaled(load_library().pa_gather_cache_fp4, _need_fp4_pool, key_out, value_out, key_cache, value_cache,
+                   cache_scales, block_tables, seq_lens, out_start, stream)
+
+
+def _write_scaled(entry, need_pool, key, value, key_cache, value_cache, cache_scales, slot_mapping, stream):
+    NB, B, Hkv, d = need_pool(key_cache, value_cache, cache_scales)
+    device = _device_of(key, value, key_cache, value_cache, cache_scales, slot_mapping)
+    T = key.shape[0]
+    _need(key.shape == (T, Hkv, d) and value.shape == (T, Hkv, d), "key/value shape mismatch")
+    _need(key.dtype == value.dtype, "dtype mismatch")
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,),
+          "slot_mapping must be int64 [num_tokens]")
+    _enqueue(entry, device, stream, key.data_ptr(), value.data_ptr(),
+             key_cache.data_ptr(), value_cache.data_ptr(), cache_scales.data_ptr(),
+             slot_mapping.data_ptr(), T, Hkv, d, B, NB, _dtype_code(key))
+
+
+def _copy_scaled(entry, need_pool, key_cache, value_cache, cache_scales, src, dst, stream):
+    NB, B, Hkv, d = need_pool(key_cache, value_cache, cache_scales)
+    device = _device_of(key_cache, value_cache, cache_scales, src, dst)
+    _need(src.dtype == torch.int32 and dst.dtype == torch.int32 and src.shape == dst.shape
+          and src.dim() == 1, "src/dst must be 1-D int32 tensors")
+    _enqueue(entry, device, stream, key_cache.data_ptr(),
+             value_cache.data_ptr(), cache_scales.data_ptr(), src.data_ptr(), dst.data_ptr(),
+             src.shape[0], Hkv, d, B, NB)
+
+
+def _gather_scaled(entry, need_pool, key_out, value_out, key_cache, value_cache, cache_scales, block_tables,
+                   seq_lens, out_start, stream):
+    NB, B, Hkv, d = need_pool(key_cache, value_cache, cache_scales)
     device = _device_of(key_out, value_out, key_cache, value_cache, cache_scales, block_tables,
                         seq_lens, out_start)
     _need(key_out.dim() == 3 and key_out.shape[1:] == (Hkv, d) and value_out.shape == key_out.shape
@@ -542,7 +613,7 @@ def gather_cache_fp8(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: 
     _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
           "block_tables/seq_lens shape mismatch")
     _need(out_start.dtype == torch.int64 and out_start.shape == (S,), "out_start must be int64 [num_seqs]")
-    _enqueue(load_library().pa_gather_cache_fp8, device, stream, key_out.data_ptr(),
+    _enqueue(entry, device, stream, key_out.data_ptr(),
              value_out.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
              cache_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
              out_start.data_ptr(), key_out.shape[0], S, Hkv, d, B, block_tables.shape[1], NB,
