@@ -440,6 +440,33 @@ int pa_gather_cache_fp4(void* key_out, void* value_out,
                         cudaStream_t stream);
 
 /*
+ * pa_decode over a 4-bit pool, without a 16-bit copy of it: the same definition with
+ * K_t and V_t the pool's values. Arithmetic is fp32 around fp16 products of the exact
+ * codes, as in pa_decode_fp8 (a bf16 query too); the factors of K's groups enter between
+ * the products of one group and the next. Softmax weights, times the factor of V's group,
+ * enter as the sum of two 16-bit parts. Where all factors of V in 32 neighbouring tokens
+ * of a kv head lie within 2^12 of the largest so far (zero groups apart), the parts are
+ * fp16, off by 2^-20 of themselves or 2^-32 of the largest weight times the largest factor
+ * so far, where that is more; otherwise they are bf16, off by 2^-17 of themselves.
+ * (Where one sequence's V factors lie more than 2^100 apart, the smaller ones may lose
+ * more.) A group that reads as NaN makes NaN of its 32 outputs (V), or of its head's (K).
+ * workspace: pa_decode_fp4_workspace_bytes(...) bytes. Other arguments, the cut of the
+ * work, sharing of workspaces, limits and errors as for pa_decode_fp8.
+ */
+int pa_decode_fp4(void* out, const void* query,
+                  const void* key_cache, const void* value_cache, const uint8_t* cache_scales,
+                  const int32_t* block_tables, const int32_t* seq_lens,
+                  int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                  int block_size, float scale,
+                  int max_blocks_per_seq, int num_blocks, int partition_tokens,
+                  pa_dtype dtype, pa_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/* Workspace bytes of pa_decode_fp4: those of pa_decode_fp8. */
+size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq, int block_size);
+
+/*
  * pa_decode for batches in which groups of sequences begin with the same
  * tokens: one system prompt before every request, or several candidates of one
  * prompt (pa_bm_fork). Where that saves enough reading (some 30 MB, by the sizes and

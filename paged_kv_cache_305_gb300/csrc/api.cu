@@ -258,25 +258,25 @@ void plan_prefix(PrefixArgs* x, int num_groups, int group, int num_kv_heads, int
 // Kv heads that a CTA of the streaming kernel takes at a time: neighbours are read
 // together while that leaves every CTA kGroupTiles tiles of the longest lengths to
 // share (behind the longest prefix, where there is one).
-int stream_heads(bool fp8, int num_seqs, int num_kv_heads, long long lmax) {
+int stream_heads(bool codes, int num_seqs, int num_kv_heads, long long lmax) {
   for (int hc = 4; hc > 1; hc /= 2)
     if (num_kv_heads % hc == 0 &&
-        static_cast<double>(num_seqs) * (num_kv_heads / hc) * (static_cast<double>(lmax) / (fp8 ? 32 : 16)) >=
+        static_cast<double>(num_seqs) * (num_kv_heads / hc) * (static_cast<double>(lmax) / (codes ? 32 : 16)) >=
             static_cast<double>(kMaxCtas) * kGroupTiles)
       return hc;
   return 1;
 }
 
-StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+StreamLayout stream_layout(bool codes, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                            long long lmax, const PrefixArgs& groups) {
   StreamLayout w{};
   const int max_pieces = groups.max_pieces;
-  w.heads = stream_heads(fp8, num_seqs, num_kv_heads, max_pieces > 0 ? lmax - groups.max_prefix_len : lmax);
+  w.heads = stream_heads(codes, num_seqs, num_kv_heads, max_pieces > 0 ? lmax - groups.max_prefix_len : lmax);
   // Whole rows need no merge, cut ones share the SMs. Four sequences of up to 512
   // 8-bit tokens, 16 rows: 8.9 us cut, 12.6 us whole; 100 sequences, 400 rows: 13.4
   // us whole, 13.8 us cut.
   const bool few = static_cast<long long>(num_seqs) * (num_kv_heads / w.heads) < kFewRows;
-  w.cut = lmax > (few ? kUncutTiles * (fp8 ? 32 : 16) : kUncutTokens);
+  w.cut = lmax > (few ? kUncutTiles * (codes ? 32 : 16) : kUncutTokens);
   if (!w.cut && max_pieces == 0) return w;
   const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
   const size_t group = static_cast<size_t>(w.heads) * (num_q_heads / num_kv_heads);
@@ -863,16 +863,18 @@ int pa_decode_append(void* out, const void* query, const void* new_key, const vo
 
 namespace {
 
-// pa_decode_fp8 (scales) and pa_decode_shared_prefix (groups).
+// pa_decode_fp8 and pa_decode_fp4 (codes of `bits`, scales) and pa_decode_shared_prefix (16,
+// groups).
 int stream_impl(void* out, const void* query, const void* key_cache, const void* value_cache,
                 const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
                 int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale,
                 int max_blocks_per_seq, int num_blocks, int partition_tokens, pa_dtype dtype,
-                pa_dtype out_dtype, void* workspace, size_t workspace_bytes, bool fp8,
+                pa_dtype out_dtype, void* workspace, size_t workspace_bytes, int bits,
                 const uint8_t* scales, const int32_t* group_start, const int32_t* prefix_lens,
                 int num_groups, int max_prefix_len, int max_group_size, int stall_for_test,
                 cudaStream_t stream) {
   g_error.clear();
+  const bool codes = bits < 16;
   int rc = check_dtype(dtype);
   if (rc != PA_OK) return rc;
   if (out_dtype != dtype && out_dtype != PA_FLOAT32)
@@ -897,7 +899,7 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   if (num_blocks < 1) return fail(PA_ERR_INVALID, "num_blocks %d < 1", num_blocks);
   if ((static_cast<long long>(num_blocks) << shift) > 0xfffffffeLL)
     return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size is 2^32 - 1 slots or more");
-  if (!fp8 && !pa::prefill_tc_supported(block_size, static_cast<long long>(num_blocks) << shift))
+  if (!codes && !pa::prefill_tc_supported(block_size, static_cast<long long>(num_blocks) << shift))
     return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size is 2^31 slots or more");
   if (!isfinite(scale)) return fail(PA_ERR_INVALID, "scale is not finite");
   if (partition_tokens < 0 || partition_tokens % 16 != 0 || partition_tokens % block_size != 0)
@@ -912,11 +914,11 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   if (num_seqs > 65535 || num_kv_heads > 65535)
     return fail(PA_ERR_UNSUPPORTED, "num_seqs %d / num_kv_heads %d above 65535", num_seqs, num_kv_heads);
   // positions on the line of tiles (of 16 or 32 tokens) are 32-bit in the kernel
-  if (static_cast<double>(num_seqs) * num_kv_heads * (static_cast<double>(lmax) / (fp8 ? 32 : 16) + 2.0) >=
+  if (static_cast<double>(num_seqs) * num_kv_heads * (static_cast<double>(lmax) / (codes ? 32 : 16) + 2.0) >=
       2147483648.0)
     return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_kv_heads * max sequence length too large");
   pa::PrefixArgs groups{};
-  if (!fp8 && num_seqs > 0) {
+  if (!codes && num_seqs > 0) {
     if (num_groups < 1) return fail(PA_ERR_INVALID, "num_groups %d < 1", num_groups);
     if (num_groups > 65535) return fail(PA_ERR_UNSUPPORTED, "num_groups %d above 65535", num_groups);
     if (max_prefix_len < 0) return fail(PA_ERR_INVALID, "max_prefix_len %d < 0", max_prefix_len);
@@ -933,14 +935,14 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
                     max_prefix_len, max_group_size);
   }
   if (num_seqs == 0) return PA_OK;
-  if (!out || !query || !key_cache || !value_cache || !block_tables || !seq_lens || (fp8 && !scales))
+  if (!out || !query || !key_cache || !value_cache || !block_tables || !seq_lens || (codes && !scales))
     return fail(PA_ERR_INVALID, "a pointer argument is NULL");
   if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache))
     return fail(PA_ERR_INVALID, "out, query and the caches must be 16-byte aligned");
   if (!aligned4(block_tables) || !aligned4(seq_lens))
     return fail(PA_ERR_INVALID, "block_tables and seq_lens must be 4-byte aligned");
   if (!aligned16(scales)) return fail(PA_ERR_INVALID, "cache_scales must be 16-byte aligned");
-  const pa::StreamLayout wl = pa::stream_layout(fp8, num_seqs, num_q_heads, num_kv_heads, head_dim,
+  const pa::StreamLayout wl = pa::stream_layout(codes, num_seqs, num_q_heads, num_kv_heads, head_dim,
                                                 lmax, groups);
   if (wl.total > 0) {
     if (workspace == nullptr || workspace_bytes < wl.total)
@@ -980,7 +982,7 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   a.out_f32 = out_dtype == PA_FLOAT32 ? 1 : 0;
   a.groups = groups;
   a.cut = wl.cut ? 1 : 0;
-  a.least_tiles = std::max(partition_tokens / (fp8 ? 32 : 16), pa::kLeastTiles);
+  a.least_tiles = std::max(partition_tokens / (codes ? 32 : 16), pa::kLeastTiles);
   if (wl.total > 0) {
     a.ws_rows = reinterpret_cast<int2*>(ws);
     a.pre_stat = reinterpret_cast<float2*>(ws + wl.pre_stat);
@@ -1015,8 +1017,9 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
     e = pa::launch_prefix_pass(p, head_dim, bf16, stream);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
   }
-  e = fp8 ? pa::launch_decode_fp8(a, head_dim, bf16, sms, stream)
-          : pa::launch_decode_prefix(a, head_dim, bf16, sms, stream);
+  e = bits == 4   ? pa::launch_decode_fp4(a, head_dim, bf16, sms, stream)
+      : bits == 8 ? pa::launch_decode_fp8(a, head_dim, bf16, sms, stream)
+                  : pa::launch_decode_prefix(a, head_dim, bf16, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "streaming decode launch");
   return PA_OK;
 }
@@ -1033,7 +1036,7 @@ int pa_decode_fp8(void* out, const void* query, const void* key_cache, const voi
                   void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
-                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, true,
+                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, 8,
                      cache_scales, nullptr, nullptr, 0, 0, 0, 0, stream);
 }
 
@@ -1046,7 +1049,32 @@ int pa_testing_decode_fp8_stalled(void* out, const void* query, const void* key_
                                   void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
-                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, true,
+                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, 8,
+                     cache_scales, nullptr, nullptr, 0, 0, 0, 1, stream);
+}
+
+int pa_decode_fp4(void* out, const void* query, const void* key_cache, const void* value_cache,
+                  const uint8_t* cache_scales, const int32_t* block_tables,
+                  const int32_t* seq_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                  int head_dim, int block_size, float scale, int max_blocks_per_seq,
+                  int num_blocks, int partition_tokens, pa_dtype dtype, pa_dtype out_dtype,
+                  void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
+                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, 4,
+                     cache_scales, nullptr, nullptr, 0, 0, 0, 0, stream);
+}
+
+int pa_testing_decode_fp4_stalled(void* out, const void* query, const void* key_cache,
+                                  const void* value_cache, const uint8_t* cache_scales,
+                                  const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                                  int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  float scale, int max_blocks_per_seq, int num_blocks,
+                                  int partition_tokens, pa_dtype dtype, pa_dtype out_dtype,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
+                     num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
+                     num_blocks, partition_tokens, dtype, out_dtype, workspace, workspace_bytes, 4,
                      cache_scales, nullptr, nullptr, 0, 0, 0, 1, stream);
 }
 
@@ -1061,7 +1089,7 @@ int pa_decode_shared_prefix(void* out, const void* query, const void* key_cache,
                             cudaStream_t stream) {
   return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
-                     num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, false, nullptr,
+                     num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, 16, nullptr,
                      group_start, prefix_lens, num_groups, max_prefix_len, max_group_size, 0, stream);
 }
 
@@ -1074,7 +1102,7 @@ int pa_testing_decode_shared_prefix_stalled(
     size_t workspace_bytes, cudaStream_t stream) {
   return stream_impl(out, query, key_cache, value_cache, block_tables, seq_lens, num_seqs,
                      num_q_heads, num_kv_heads, head_dim, block_size, scale, max_blocks_per_seq,
-                     num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, false, nullptr,
+                     num_blocks, 0, dtype, out_dtype, workspace, workspace_bytes, 16, nullptr,
                      group_start, prefix_lens, num_groups, max_prefix_len, max_group_size, 1, stream);
 }
 
@@ -1086,6 +1114,12 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
       lmax > pa::kMostTokens)
     return 0;
   return pa::stream_layout(true, num_seqs, num_q_heads, num_kv_heads, head_dim, lmax, pa::PrefixArgs{}).total;
+}
+
+size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq, int block_size) {
+  return pa_decode_fp8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                       block_size);  // tiles of as many tokens
 }
 
 size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,

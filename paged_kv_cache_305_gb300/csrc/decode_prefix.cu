@@ -6,7 +6,7 @@ namespace pa {
 
 cudaError_t launch_decode_prefix(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
                                  cudaStream_t stream) {
-  return launch_all<false>(a, head_dim, bf16, num_sms, stream);
+  return launch_all<16>(a, head_dim, bf16, num_sms, stream);
 }
 
 }  // namespace pa

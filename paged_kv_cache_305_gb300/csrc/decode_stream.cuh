@@ -1,5 +1,5 @@
-// Streaming paged decode attention: decode over 8-bit caches (pa_decode_fp8) and
-// over 16-bit ones behind a shared prefix (pa_decode_shared_prefix).
+// Streaming paged decode attention: decode over 8-bit and 4-bit caches (pa_decode_fp8,
+// pa_decode_fp4) and over 16-bit ones behind a shared prefix (pa_decode_shared_prefix).
 //
 // Work. The G query heads of a kv head are computed together, so a K/V byte is
 // read once. A CTA takes 4, 2 or 1 neighbouring kv heads at a time, with 1, 2 or
@@ -79,27 +79,30 @@ struct Note {
 };
 enum : int { kFirst = 1, kLast = 2, kEnd = 4 };  // of the segment; of all work
 
-template <int D, bool FP8, int NT>
+template <int D, int BITS, int NT>
 struct Ring {
-  using T = Tile<D, FP8>;
+  using T = Tile<D, BITS>;
   static constexpr int kHalf = kWarps * T::kBytes;   // K (or V) of a stage
-  static constexpr int kStages = 65536 / (2 * kHalf);  // three CTAs on an SM
-  static constexpr int kScaleBytes = kWarps * 64;      // exponent bytes of a stage
+  static constexpr int kRing = BITS == 4 ? 49152 : 65536;  // three CTAs on an SM
+  static constexpr int kStages = kRing / (2 * kHalf);
+  static constexpr int kScaleBytes = kWarps * T::kTokens * 2 * T::kGroups;  // exponent bytes of a stage
   static constexpr int kHeads = NT * 8;
   static constexpr int kOStride = D + 4;
   // offsets in shared memory; the stages follow the rest
   static constexpr int kScales = 0;
-  static constexpr int kNotes = kScales + (FP8 ? kStages * kScaleBytes : 0);
+  static constexpr int kNotes = kScales + kStages * kScaleBytes;
   static constexpr int kBars = kNotes + kStages * static_cast<int>(sizeof(Note));  // full, empty, joins
   static constexpr int kStats = kBars + (2 * kStages + kWarps) * 8;  // [warp][m, l, r][head]
   static constexpr int kBase = kStats + kWarps * 3 * kHeads * 4;   // [kChunks]
   static constexpr int kMisc = kBase + kChunks * 4;
   static constexpr int kJoin = (kMisc + 32 + 15) / 16 * 16;        // [warp][head][kOStride]
-  static constexpr int kSlots = kJoin + kWarps * kJoinHeads * kOStride * 4;  // ROWS: [stage][token]
+  static constexpr int kFactors = kJoin + kWarps * kJoinHeads * kOStride * 4;  // 4-bit: [warp]
+  static constexpr int kFactorBytes = BITS == 4 ? static_cast<int>(sizeof(Factors4<D>)) : 0;
+  static constexpr int kSlots = kFactors + kWarps * kFactorBytes;  // ROWS: [stage][token]
   template <bool ROWS>
   static constexpr int kFixed = (kSlots + (ROWS ? kStages * kWarps * T::kTokens * 4 : 0) + 1023) / 1024 * 1024;
   static_assert(kStages >= 2, "a stage lands while another is computed");
-  static_assert(NT > 1 || 3 * (kFixed<true> + 65536 + 1024) <= 228 * 1024, "three CTAs on an SM");
+  static_assert(NT > 1 || 3 * (kFixed<true> + kRing + 1024) <= 228 * 1024, "three CTAs on an SM");
 };
 
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
@@ -115,14 +118,15 @@ struct Misc {
 static_assert(sizeof(Misc) <= 32, "room reserved in Ring");
 
 // SPLIT: at most 4 query heads a kv head (stream_tile.cuh).
-template <typename Ty, int D, int NT, bool FP8, bool ROWS, bool SPLIT>
+template <typename Ty, int D, int NT, int BITS, bool ROWS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const StreamArgs a) {
-  using R = Ring<D, FP8, NT>;
-  using Geo = Tile<D, FP8>;
+  using R = Ring<D, BITS, NT>;
+  using Geo = Tile<D, BITS>;
   using T = typename Ty::T;
-  constexpr int kTT = Geo::kTokens, kRB = Geo::kRowBytes;
+  constexpr int kTT = Geo::kTokens, kRB = Geo::kRowBytes, kG = Geo::kGroups;
+  constexpr bool kCodes = BITS < 16;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -192,7 +196,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     Row r;
     r.hi = min(max(__ldg(a.seq_lens + s), 0), Lmax);
     r.lo = r.before = r.shared = r.lead = 0;
-    if constexpr (!FP8) {
+    if constexpr (!kCodes) {
       if (a.groups.num_groups > 0) {
         r.lo = prefix_of(a.groups, s, r.hi, Lmax, &r.lead);
         r.before = prefix_pieces(a.groups, r.lo);
@@ -212,7 +216,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         if (raw < 0 || raw > Lmax) atomicAdd(a.bad, 1ull);
       }
     }
-    if constexpr (!FP8) {
+    if constexpr (!kCodes) {
       if (blockIdx.x == 0) count_bad_groups(a.groups, tid, kChunks, a.bad);
     }
     unsigned incl = mine;
@@ -286,8 +290,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               st_shared_zero16(sk + i * block_bytes + c);
               st_shared_zero16(sv + i * block_bytes + c);
             }
-            if constexpr (FP8) {
-              for (int c = lane; c < Hc * 2 * bt; c += 32) se[i * Hc * 2 * bt + c] = 0;
+            if constexpr (kCodes) {
+              for (int c = lane; c < Hc * 2 * bt * kG; c += 32) se[i * Hc * 2 * bt * kG + c] = 0;
             }
           }
           tc::fence_async_smem();
@@ -295,20 +299,21 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         __syncwarp();
         if (lane == 0)
           tc::mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(__popc(live)) *
-                                                  (2 * block_bytes + (FP8 ? Hc * 2 * bt : 0)));
+                                                  (2 * block_bytes + Hc * 2 * bt * kG));
         __syncwarp();
         if (id < kBad) {
           const int grp = static_cast<int>(id >> 3);
           tc::tma_load_5d(sk + lane * block_bytes, &kmap, full(st), 0, 0, 0, grp, h0);
           tc::tma_load_5d(sv + lane * block_bytes, &vmap, full(st), 0, 0, 0, grp, h0);
-          if constexpr (FP8) {
-            const uint8_t* e = a.scales + ((static_cast<size_t>(id >> shift) * Hkv + h0) * 2 << shift) +
-                               (id & ((1u << shift) - 1));
-            const uint32_t dst = smem_u32(se) + lane * Hc * 2 * bt;
+          if constexpr (kCodes) {
+            const uint8_t* e = a.scales + (((static_cast<size_t>(id >> shift) * Hkv + h0) * 2 << shift) +
+                                           (id & ((1u << shift) - 1))) * kG;
+            const uint32_t dst = smem_u32(se) + lane * Hc * 2 * bt * kG;
             if (bt == 1 << shift) {
-              tc::bulk_load(dst, e, Hc * 2 * bt, full(st));
+              tc::bulk_load(dst, e, Hc * 2 * bt * kG, full(st));
             } else {  // part of a block: K's and V's of each head
-              for (int i = 0; i < 2 * Hc; ++i) tc::bulk_load(dst + i * bt, e + (i << shift), bt, full(st));
+              for (int i = 0; i < 2 * Hc; ++i)
+                tc::bulk_load(dst + i * bt * kG, e + (i << shift) * kG, bt * kG, full(st));
             }
           }
         }
@@ -408,7 +413,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           const int lo = note.lo, hi = note.hi;
           // stage k of the row: its tokens, and the blocks that hold them
           auto stage_at = [&](int k) {
-            const bool of_prefix = !FP8 && k < shared;
+            const bool of_prefix = !kCodes && k < shared;
             note.t0 = (of_prefix ? k : k - shared + lo / ST) * ST;
             note.lo = of_prefix ? 0 : lo;
             note.hi = of_prefix ? lo : hi;
@@ -451,9 +456,9 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     };
     const int x0 = wsub * kTT, mi = lane >> 3;
     const uint32_t k_at = row_at(x0 + ((mi & 1) << 3));
-    const uint32_t k_next = FP8 ? row_at(x0 + 16 + ((mi & 1) << 3)) - k_at : 0u;  // the next 16 tokens
-    const uint32_t v_at = row_at(FP8 ? x0 + (lane & 24) : x0 + ((mi >> 1) << 3));
-    const int e_at = ((x0 + lane) / lb * Hc + hsub) * 2 * lb + (x0 + lane) % lb;
+    const uint32_t k_next = kCodes ? row_at(x0 + 16 + ((mi & 1) << 3)) - k_at : 0u;  // the next 16 tokens
+    const uint32_t v_at = row_at(kCodes ? x0 + (lane & 24) : x0 + ((mi >> 1) << 3));
+    const int e_at = (((x0 + lane) / lb * Hc + hsub) * 2 * lb + (x0 + lane) % lb) * kG;
     float* sStats = reinterpret_cast<float*>(smem + R::kStats);
     float* sJoin = reinterpret_cast<float*>(smem + R::kJoin);
     State<D, NT> st;
@@ -469,7 +474,13 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     bool ok = true;
     // waits for stage n and reads its note. ROWS: begins the copies of this warp's
     // tile, rows that do not count as zeros, and reads its token's exponents.
-    [[maybe_unused]] int ek = 0, ev = 0;
+    using Exps = std::conditional_t<BITS == 4, uint32_t, int>;  // exponent bytes of a token, K's and V's
+    auto exps_at = [](const uint8_t* e) {
+      if constexpr (kG == 4) return *reinterpret_cast<const uint32_t*>(e);
+      if constexpr (kG == 2) return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(e));
+      return static_cast<Exps>(*e);
+    };
+    [[maybe_unused]] Exps ek = 0, ev = 0;
     auto take = [&](const Place& p) {
       const int stage = p.st;
       ok = *aborted == 0 && wait(full(stage), p.round);
@@ -495,11 +506,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             cp_async_16(sk + o, kb + from, live);
             cp_async_16(sv + o, vb + from, live);
           }
-          if constexpr (FP8) {
-            const uint8_t* e = a.scales + ((static_cast<size_t>(mine >> shift) * Hkv + h) * 2 << shift) +
-                               (mine & ((1u << shift) - 1));
-            ek = mine < kBad ? __ldg(e) : 0;
-            ev = mine < kBad ? __ldg(e + (1 << shift)) : 0;
+          if constexpr (kCodes) {
+            const uint8_t* e = a.scales + (((static_cast<size_t>(mine >> shift) * Hkv + h) * 2 << shift) +
+                                           (mine & ((1u << shift) - 1))) * kG;
+            ek = mine < kBad ? exps_at(e) : 0;
+            ev = mine < kBad ? exps_at(e + (kG << shift)) : 0;
           }
         }
         cp_async_commit();
@@ -512,7 +523,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     for (;; step(at)) {
       const int stage = at.st;
       Note note;
-      [[maybe_unused]] int my_ek = 0, my_ev = 0;
+      [[maybe_unused]] Exps my_ek = 0, my_ev = 0;
       if constexpr (ROWS) {
         note = ahead;
         if (note.flags & kEnd) break;
@@ -529,11 +540,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       if (note.flags & kFirst) {
         const T* qh = static_cast<const T*>(a.query) +
                       (static_cast<size_t>(note.s) * a.num_q_heads + static_cast<size_t>(note.hg * Hc + hsub) * G) * D;
-        load_query<Ty, D, NT, FP8, SPLIT>(qh, G, a.scale_log2, q);
+        load_query<Ty, D, NT, BITS, SPLIT>(qh, G, a.scale_log2, q);
         st.reset();
       }
       const int t0 = note.t0 + x0;
-      const int lo = FP8 ? 0 : note.lo - t0, hi = note.hi - t0;
+      const int lo = kCodes ? 0 : note.lo - t0, hi = note.hi - t0;
       if (hi > max(lo, 0) && lo < kTT) {
         const uint32_t sk = ring + stage * 2 * R::kHalf, sv = sk + R::kHalf;
         if (!ROWS && (lo > 0 || hi < kTT)) {
@@ -546,13 +557,18 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           tc::fence_async_smem();
           __syncwarp();
         }
-        if constexpr (FP8) {
+        if constexpr (kCodes) {
           if constexpr (!ROWS) {
             const unsigned char* e = smem + R::kScales + stage * R::kScaleBytes + e_at;
-            my_ek = e[0];
-            my_ev = e[lb];
+            my_ek = exps_at(e);
+            my_ev = exps_at(e + lb * kG);
           }
-          tile_8<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, my_ek, my_ev, lo, hi, q, st);
+          if constexpr (BITS == 8) {
+            tile_8<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, my_ek, my_ev, lo, hi, q, st);
+          } else {
+            Factors4<D>& fac = reinterpret_cast<Factors4<D>*>(smem + R::kFactors)[warp];
+            tile_4<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, my_ek, my_ev, fac, hi, q, st);
+          }
         } else {
           tile_16<Ty, D, NT, SPLIT>(sk + k_at, sv + v_at, lo, hi, q, st);
         }
@@ -590,7 +606,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
               float* p = mine_o + at * R::kOStride;
-              if constexpr (FP8) {  // two neighbouring dims
+              if constexpr (kCodes) {  // two neighbouring dims
                 *reinterpret_cast<float2*>(p + Geo::dim_of(mt, 0, r8)) =
                     make_float2(st.o[mt][nt][c], st.o[mt][nt][c + 2]);
               } else {
@@ -602,7 +618,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               float* stat_w = sStats + warp * 3 * R::kHeads + head;
               stat_w[0] = st.fresh ? -INFINITY : st.m[nt][c];
               stat_w[R::kHeads] = st.l[nt][c];
-              if constexpr (FP8) stat_w[2 * R::kHeads] = static_cast<float>(st.r);
+              if constexpr (kCodes) stat_w[2 * R::kHeads] = static_cast<float>(st.r);
             }
           }
         if (!meet()) break;
@@ -612,10 +628,14 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           auto stat = [&](int w, int which) { return sStats[(w * 3 + which) * R::kHeads + head]; };
           float M = -INFINITY;
           for (int w = w0; w < w0 + Wh; ++w) M = fmaxf(M, stat(w, 0));
-          // 8-bit: the order of a warp's O, and the largest of them
-          auto order = [&](int w) { return stat(w, 2) + (stat(w, 0) - M); };
+          // the order of a warp's O, and the largest of them. 8-bit: with the reference of its
+          // weights, a whole number; 4-bit: r alone, the reference is none
+          auto order = [&](int w) {
+            if (BITS == 4) return stat(w, 0) == -INFINITY ? kLowest : stat(w, 2);
+            return stat(w, 2) + (stat(w, 0) - M);
+          };
           [[maybe_unused]] float top = kLowest;
-          if constexpr (FP8)
+          if constexpr (kCodes)
             for (int w = w0; w < w0 + Wh; ++w) top = fmaxf(top, order(w));  // -inf or NaN: no tile
           float l = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -623,7 +643,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             const float m = stat(w, 0);
             const float f = m == -INFINITY ? 0.f : ex2(m - M);
             float fo = f;
-            if constexpr (FP8) fo = m == -INFINITY ? 0.f : ex2(order(w) - top);
+            if constexpr (BITS == 8) fo = m == -INFINITY ? 0.f : ex2(order(w) - top);
+            if constexpr (BITS == 4) fo = f * ex2(order(w) - top);
             const float4 v =
                 *reinterpret_cast<const float4*>(sJoin + (w * kJoinHeads + at) * R::kOStride + c4);
             l += f * stat(w, 1);
@@ -634,9 +655,9 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           float iv = l > 0.f ? 1.f / l : 0.f;
           if (l != l) iv = l;  // NaN scores give NaN
-          if constexpr (!FP8) iv *= 1.f / kWeightScale<Ty>;
+          if constexpr (!kCodes) iv *= 1.f / kWeightScale<Ty>;
           acc = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
-          if constexpr (FP8) {
+          if constexpr (kCodes) {
             // times 2^(top - 127), as two factors apart: one, or the product with iv, may be subnormal
             const int n = static_cast<int>(fminf(fmaxf(top - 127.f, -252.f), 252.f));
             const float f0 = exponent_factor(127 + n / 2), f1 = exponent_factor(127 + n - n / 2);
@@ -819,7 +840,9 @@ inline bool encode_pool_map(CUtensorMap* map, const void* cache, long long num_s
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(cache), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE,
-             slice == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             slice == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+             : slice == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                           : CU_TENSOR_MAP_SWIZZLE_32B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -839,11 +862,11 @@ struct Dependent {
   }
 };
 
-template <typename Ty, int D, int NT, bool FP8, bool ROWS, bool SPLIT>
+template <typename Ty, int D, int NT, int BITS, bool ROWS, bool SPLIT>
 cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
-  using R = Ring<D, FP8, NT>;
+  using R = Ring<D, BITS, NT>;
   const int smem = R::template kFixed<ROWS> + R::kStages * 2 * R::kHalf;
-  auto kern = paged_stream_kernel<Ty, D, NT, FP8, ROWS, SPLIT>;
+  auto kern = paged_stream_kernel<Ty, D, NT, BITS, ROWS, SPLIT>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = once_per_context(done, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -852,8 +875,8 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   CUtensorMap km{}, vm{};
   if constexpr (!ROWS) {
     const long long slots = static_cast<long long>(a.num_blocks) << a.block_shift;
-    const int rows = std::min(1 << a.block_shift, Tile<D, FP8>::kTokens * kWarps / a.heads_at_a_time);
-    const int row_bytes = Tile<D, FP8>::kRowBytes;
+    const int rows = std::min(1 << a.block_shift, Tile<D, BITS>::kTokens * kWarps / a.heads_at_a_time);
+    const int row_bytes = Tile<D, BITS>::kRowBytes;
     if (!encode_pool_map(&km, a.key_cache, slots, a.num_kv_heads, row_bytes, rows, a.heads_at_a_time) ||
         !encode_pool_map(&vm, a.value_cache, slots, a.num_kv_heads, row_bytes, rows, a.heads_at_a_time))
       return cudaErrorInvalidValue;
@@ -867,7 +890,7 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
   const long long ctas = std::min<long long>((NT == 1 ? 3 : 2) * (num_sms - pass) + pass, kMaxCtas);
   const long long rows = static_cast<long long>(a.num_seqs) * (a.num_kv_heads / a.heads_at_a_time);
   // no more CTAs than the longest rows have shares, in stages of ST tokens
-  const int warps_a_head = kWarps / a.heads_at_a_time, ST = warps_a_head * Tile<D, FP8>::kTokens;
+  const int warps_a_head = kWarps / a.heads_at_a_time, ST = warps_a_head * Tile<D, BITS>::kTokens;
   const long long most = (static_cast<long long>(a.max_blocks_per_seq) << a.block_shift) / ST + 2;
   const long long least = (a.least_tiles + warps_a_head - 1) / warps_a_head;
   const long long grid = std::min(ctas, rows * (a.cut ? (most + least - 1) / least : 1));
@@ -885,28 +908,28 @@ cudaError_t launch_stream(StreamArgs a, int num_sms, cudaStream_t stream) {
                   : cudaLaunchKernelEx(&m.cfg, decode_merge_kernel<Ty, D, false>, a);
 }
 
-template <typename Ty, int D, bool FP8, bool ROWS>
+template <typename Ty, int D, int BITS, bool ROWS>
 cudaError_t launch_group(const StreamArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.group <= 4) return launch_stream<Ty, D, 1, FP8, ROWS, true>(a, num_sms, stream);
-  if (a.group <= 8) return launch_stream<Ty, D, 1, FP8, ROWS, false>(a, num_sms, stream);
-  return launch_stream<Ty, D, 2, FP8, ROWS, false>(a, num_sms, stream);
+  if (a.group <= 4) return launch_stream<Ty, D, 1, BITS, ROWS, true>(a, num_sms, stream);
+  if (a.group <= 8) return launch_stream<Ty, D, 1, BITS, ROWS, false>(a, num_sms, stream);
+  return launch_stream<Ty, D, 2, BITS, ROWS, false>(a, num_sms, stream);
 }
 
-template <typename Ty, int D, bool FP8>
+template <typename Ty, int D, int BITS>
 cudaError_t launch_rows(const StreamArgs& a, int num_sms, cudaStream_t stream) {
   // tensor copies need whole groups of 8 slots and 31-bit slot numbers
   const bool rows = a.block_shift < 3 || (static_cast<long long>(a.num_blocks) << a.block_shift) > 0x7fffffffll;
-  return rows ? launch_group<Ty, D, FP8, true>(a, num_sms, stream)
-              : launch_group<Ty, D, FP8, false>(a, num_sms, stream);
+  return rows ? launch_group<Ty, D, BITS, true>(a, num_sms, stream)
+              : launch_group<Ty, D, BITS, false>(a, num_sms, stream);
 }
 
-template <bool FP8>
+template <int BITS>
 cudaError_t launch_all(const StreamArgs& a, int head_dim, bool bf16, int num_sms, cudaStream_t stream) {
   if (bf16)
-    return head_dim == 64 ? launch_rows<BF16, 64, FP8>(a, num_sms, stream)
-                          : launch_rows<BF16, 128, FP8>(a, num_sms, stream);
-  return head_dim == 64 ? launch_rows<F16, 64, FP8>(a, num_sms, stream)
-                        : launch_rows<F16, 128, FP8>(a, num_sms, stream);
+    return head_dim == 64 ? launch_rows<BF16, 64, BITS>(a, num_sms, stream)
+                          : launch_rows<BF16, 128, BITS>(a, num_sms, stream);
+  return head_dim == 64 ? launch_rows<F16, 64, BITS>(a, num_sms, stream)
+                        : launch_rows<F16, 128, BITS>(a, num_sms, stream);
 }
 
 }  // namespace

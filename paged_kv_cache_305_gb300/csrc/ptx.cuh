@@ -68,6 +68,10 @@ struct F16 {
   __device__ __forceinline__ static float2 unpack(uint32_t v) {
     return __half22float2(*reinterpret_cast<__half2*>(&v));
   }
+  __device__ __forceinline__ static uint32_t mul(uint32_t a, uint32_t b) {
+    const __half2 h = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
   __device__ __forceinline__ static void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
     asm volatile(

@@ -28,7 +28,7 @@ struct StreamArgs {
   const void* query;
   const void* key_cache;
   const void* value_cache;
-  const uint8_t* scales;  // 8-bit caches: exponent bytes [NB, Hkv, 2, B], else null
+  const uint8_t* scales;  // 8-bit caches: exponent bytes [NB, Hkv, 2, B]; 4-bit: [NB, Hkv, 2, B, d / 32]
   const int32_t* block_tables;
   const int32_t* seq_lens;
   int num_seqs;
@@ -110,10 +110,12 @@ struct StreamLayout {
   bool cut;   // rows may be cut
   size_t pre_stat, seg_stat, pre_out, seg_out, total;
 };
-StreamLayout stream_layout(bool fp8, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+StreamLayout stream_layout(bool codes, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                            long long lmax, const PrefixArgs& groups);
 
 cudaError_t launch_decode_fp8(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_decode_fp4(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
                               cudaStream_t stream);
 cudaError_t launch_decode_prefix(const StreamArgs& a, int head_dim, bool bf16, int num_sms,
                                  cudaStream_t stream);

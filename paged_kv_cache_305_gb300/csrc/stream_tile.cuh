@@ -1,8 +1,8 @@
 // One warp's work on a tile of K/V rows in shared memory, for the streaming
 // decode kernel (decode_stream.cuh): scores, online softmax and weighted sum,
-// for 8-bit caches (tiles of 32 tokens) and 16-bit ones (16 tokens).
+// for 8-bit and 4-bit caches (tiles of 32 tokens) and 16-bit ones (16 tokens).
 //
-// Both take the tile as S^T = K q^T with the legacy m16n8k16 product (16 tokens
+// All take the tile as S^T = K q^T with the legacy m16n8k16 product (16 tokens
 // x 8 columns, a column for a query head), and O^T = V^T P^T with the same
 // instruction, weights as two 16-bit parts. With up to 4 query heads (SPLIT)
 // columns 4-7 repeat the heads of columns 0-3: both halves compute the same
@@ -40,10 +40,31 @@
 // byte permutation separates the dims, which become the rows r and r + 8 of the
 // output fragment: fragment row r8 of m-tile mt is dim 16 mt + 2 r8, row
 // r8 + 8 the one after it.
+//
+// 4-bit caches. The factors belong to 32 dims of a row, so K's enter between the
+// products of one group and the next,
+//   y = sum_g (sum_{i in g} q_i k4_i) (2^(ek_g - 127) sl2),
+// and V's multiply the weights once for each group: the group's rows of O get weights
+// p_t 2^(ev_tg - r), r the largest finite ev so far. The weights' two fp16 parts are made
+// once a tile (of p 2^7, below 2^15) and multiplied by 2^(ev_tg - r) in fp16, which is exact
+// down to 2^-25: 2^-20 of what a weight of 1 leaves there with the smallest factor that
+// goes this way, 2^-12 of the largest. Tiles with factors further below r (none in caches
+// of ordinary activations; a group of zeros has byte 0 and does not count), or with NaN,
+// go through bf16, whose range is fp32's: parts of p_t 2^(ev_tg - r) for every group, off by
+// 2^-17 of themselves, against V's codes as bf16. m is the running maximum of the scores.
+//
+// Fragment orders of 4-bit tiles. A 16-byte chunk is one group of 32 dims. For K a lane
+// gets eight neighbouring codes of one token, 8 t to 8 t + 7 of the chunk: four conversion
+// instructions make them the A operand's pairs of two products, and q's fragment is built in
+// the same order. For V the transposing load gives four neighbouring dims of two tokens a
+// register; two byte permutations and shifts put the tokens' codes of a dim into one byte,
+// and the same instruction makes the pair. Fragment row r8 of m-tile 2 g + h is dim
+// 32 g + 4 r8 + 2 h, row r8 + 8 the one after it.
 #pragma once
 
 #include <math.h>
 
+#include "fp4.cuh"
 #include "fp8.cuh"
 #include "ptx.cuh"
 
@@ -89,14 +110,14 @@ struct State {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
   }
-  // A tile's part of O. The products of a tile start from zero and are added here: the tensor
+  // A tile's part of O, times f. The products of a tile start from zero and are added here: the tensor
   // core cuts off what does not fit when it adds to its accumulator, and O, which grows with
   // the row, would lose half an ulp each time (6e-6 of 10 K tokens' sum).
-  __device__ __forceinline__ void add(int mt, const float (&x)[NT][4]) {
+  __device__ __forceinline__ void add(int mt, const float (&x)[NT][4], float f = 1.f) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[mt][nt][e] += x[nt][e];
+      for (int e = 0; e < 4; ++e) o[mt][nt][e] = f == 1.f ? o[mt][nt][e] + x[nt][e] : fmaf(x[nt][e], f, o[mt][nt][e]);
   }
   // O columns times al.
   __device__ __forceinline__ void scale(const float (&al)[NT][2]) {
@@ -117,11 +138,11 @@ struct State {
     return v;
   }
   // Raises the references to the columns' maxima, of which mx are this lane's, where any
-  // has been passed by kRaiseAt. 16-bit caches: mx of the scores. 8-bit: of the weighted
-  // rows y + ev - r.
-  template <bool FP8>
+  // has been passed by kRaiseAt. 16-bit and 4-bit caches: mx of the scores. 8-bit (WEIGHTED):
+  // of the weighted rows y + ev - r.
+  template <bool WEIGHTED>
   __device__ __forceinline__ void raise(const float (&mx)[NT][2]) {
-    constexpr float kShift = FP8 ? kWeightShift : 0.f;
+    constexpr float kShift = WEIGHTED ? kWeightShift : 0.f;
     bool passed = fresh;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -134,7 +155,7 @@ struct State {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float v = column_max(mx[nt][c]);
-        const float mn = fmaxf(m[nt][c], FP8 ? ceilf(v) - kShift : v);
+        const float mn = fmaxf(m[nt][c], WEIGHTED ? ceilf(v) - kShift : v);
         const float f = ex2(m[nt][c] - mn);  // l and O are zero where nothing was added yet
         l[nt][c] *= f;
         al[nt][c] = f;
@@ -162,21 +183,33 @@ struct State {
       }
     scale(al);
   }
+  // 4-bit: r to `top`; m stays, and what was added before goes down with its factor.
+  __device__ __forceinline__ void follow_plain(int top) {
+    if (top == r) return;
+    float al[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) al[nt][0] = al[nt][1] = exponent_factor(max(127 - (top - r), 0));
+    r = top;
+    if (!fresh) scale(al);
+  }
 };
 
 // Tile geometry. A tensor copy with the 128-byte swizzle (64-byte for rows of 64
-// bytes) leaves rows in groups of 8: of a group, one 128-byte slice of all 8 rows
+// bytes, 32-byte for rows of 32) leaves rows in groups of 8: of a group, one 128-byte slice of all 8 rows
 // after the other, the 16-byte chunks of a slice XORed by the row. The 8 rows of
 // every ldmatrix phase then fall in distinct banks.
-template <int D, bool FP8>
+template <int D, int BITS>
 struct Tile {
-  static constexpr int kTokens = FP8 ? 32 : 16;
-  static constexpr int kRowBytes = FP8 ? D : 2 * D;
+  static constexpr int kTokens = BITS == 16 ? 16 : 32;
+  static constexpr int kRowBytes = D * BITS / 8;
+  static constexpr int kGroups = BITS == 16 ? 0 : BITS == 8 ? 1 : D / kFp4Group;  // exponent bytes of a row
   static constexpr int kSlice = kRowBytes < 128 ? kRowBytes : 128;
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kBytes = kTokens * kRowBytes;
   // Byte offset of a row's 16-byte chunk in its group.
   static __device__ __forceinline__ uint32_t in_group(int row, int chunk) {
+    if constexpr (kSlice == 32)
+      return static_cast<uint32_t>(row * 32 + ((chunk ^ (row >> 2)) << 4));
     if constexpr (kSlice == 64)
       return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
     return static_cast<uint32_t>((chunk >> 3) * 1024 + row * 128 + (((chunk & 7) ^ row) << 4));
@@ -186,7 +219,8 @@ struct Tile {
   }
   // Head dim of fragment element e of m-tile mt, for fragment row r8 = lane / 4.
   static __device__ __forceinline__ int dim_of(int mt, int e, int r8) {
-    return FP8 ? mt * 16 + 2 * r8 + (e >> 1) : mt * 16 + r8 + ((e & 2) << 2);
+    if constexpr (BITS == 4) return (mt >> 1) * 32 + 4 * r8 + 2 * (mt & 1) + (e >> 1);
+    return BITS == 8 ? mt * 16 + 2 * r8 + (e >> 1) : mt * 16 + r8 + ((e & 2) << 2);
   }
 };
 
@@ -194,7 +228,7 @@ struct Tile {
 // the k order above; bf16 queries are scaled for each head by the power of two that brings the
 // largest element to [2^14, 2^15): their 8 bits fit into fp16's 11, and what
 // falls below fp16's range is under 2^-39 of the largest.
-template <typename Ty, int D, int NT, bool FP8, bool SPLIT>
+template <typename Ty, int D, int NT, int BITS, bool SPLIT>
 __device__ __forceinline__ void load_query(const typename Ty::T* qh, int G, float sl2, Query<D, NT>& q) {
   const int lane = threadIdx.x & 31, r8 = lane >> 2, t = lane & 3;
   const uint32_t sign = sl2 < 0.f ? 0x80008000u : 0u;
@@ -204,7 +238,7 @@ __device__ __forceinline__ void load_query(const typename Ty::T* qh, int G, floa
     const int head = SPLIT ? r8 & 3 : nt * 8 + r8;
     const typename Ty::T* row = qh + head * D;
     q.sl2[nt][0] = q.sl2[nt][1] = sl2;
-    if constexpr (!FP8) {
+    if constexpr (BITS == 16) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const typename Ty::T* p = row + kk * 16 + 2 * t;
@@ -215,7 +249,8 @@ __device__ __forceinline__ void load_query(const typename Ty::T* qh, int G, floa
       uint2 w[D / 16];
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        w[kk] = head < G ? *reinterpret_cast<const uint2*>(row + kk * 16 + 4 * t) : make_uint2(0u, 0u);
+        const int at = BITS == 8 ? kk * 16 + 4 * t : (kk >> 1) * 32 + 8 * t + 4 * (kk & 1);
+        w[kk] = head < G ? *reinterpret_cast<const uint2*>(row + at) : make_uint2(0u, 0u);
         w[kk].x ^= sign;
         w[kk].y ^= sign;
       }
@@ -268,7 +303,7 @@ __device__ __forceinline__ void weight_parts(float w0, float w1, uint32_t rest, 
 template <int D, int NT, bool SPLIT>
 __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv, int ek, int ev,
                                        int lo, int hi, const Query<D, NT>& q, State<D, NT>& st) {
-  using Geo = Tile<D, true>;
+  using Geo = Tile<D, 8>;
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, r8 = lane >> 2;
   const int mi = lane >> 3, rr = lane & 7;
@@ -371,12 +406,239 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
   }
 }
 
+// Factors of a tile of 4-bit rows, from the lanes that own its tokens to those that use
+// them: K's of each token as fp32, V's over r as fp16 pairs of tokens 8 i + 2 t, + 1.
+template <int D>
+struct Factors4 {
+  static constexpr int kG = D / kFp4Group;
+  float k[32][kG];
+  uint32_t v[4][kG * 4 + 4];  // [t][g * 4 + i]; padded so that the writes of two t fall in other banks
+};
+constexpr int kTame = 12;  // binary orders below r within which factors multiply fp16 weights
+
+// 4-bit tile: as tile_8, with the exponent bytes of token `lane` in ek and ev.
+template <int D, int NT, bool SPLIT>
+__device__ __forceinline__ void tile_4(uint32_t sk, uint32_t k_next, uint32_t sv, uint32_t ek, uint32_t ev,
+                                       Factors4<D>& fac, int hi, const Query<D, NT>& q, State<D, NT>& st) {
+  using Geo = Tile<D, 4>;
+  constexpr unsigned kAll = 0xffffffffu;
+  constexpr int kG = Geo::kGroups;
+  const int lane = threadIdx.x & 31, r8 = lane >> 2, t = lane & 3;
+  const int mi = lane >> 3, rr = lane & 7;
+  const bool edge = hi < Geo::kTokens;
+  if (edge && lane >= hi) ev = 0;
+
+  // the largest and the smallest factor of V that count
+  int top = 0;
+  unsigned low = ~0u;
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    const unsigned b = ev >> (8 * g) & 255u;
+    top = max(top, static_cast<int>(b));
+    low = min(low, b - 1u);  // 0 does not count
+  }
+  top = __reduce_max_sync(kAll, top);
+  low = __reduce_min_sync(kAll, low);
+  bool wild = top == 255;
+  if (wild) {  // NaN: the largest finite one
+    top = 0;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      const int b = static_cast<int>(ev >> (8 * g) & 255u);
+      top = max(top, b == 255 ? 0 : b);
+    }
+    top = __reduce_max_sync(kAll, top);
+  }
+  top = max(top, st.r);
+  wild |= low < static_cast<unsigned>(max(top - kTame - 1, 0));
+  st.follow_plain(top);
+
+  {
+    float f[kG];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      f[g] = exponent_factor(static_cast<int>(ek >> (8 * g) & 255u));
+      const int e = static_cast<int>(ev >> (8 * g) & 255u);
+      reinterpret_cast<uint16_t*>(&fac.v[(lane & 7) >> 1][g * 4 + (lane >> 3)])[lane & 1] =
+          static_cast<uint16_t>(max(e - top + 15, 0) << 10);
+    }
+    if constexpr (kG == 4)
+      *reinterpret_cast<float4*>(fac.k[lane]) = make_float4(f[0], f[1], f[2], f[3]);
+    else
+      *reinterpret_cast<float2*>(fac.k[lane]) = make_float2(f[0], f[1]);
+  }
+  __syncwarp();
+
+  float x[NT][4][2], fk[4][kG];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kG == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(fac.k[r8 + 8 * i]);
+      fk[i][0] = f.x;
+      fk[i][1] = f.y;
+      fk[i][2] = f.z;
+      fk[i][3] = f.w;
+    } else {
+      const float2 f = *reinterpret_cast<const float2*>(fac.k[r8 + 8 * i]);
+      fk[i][0] = f.x;
+      fk[i][1] = f.y;
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[nt][i][0] = x[nt][i][1] = 0.f;
+#pragma unroll
+  for (int kp = 0; kp < kG / 2; ++kp) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t k[4];  // tokens 0-7, 8-15 of group 2 kp, then of the next
+      ldmatrix_x4(k, sk + hf * k_next + Geo::in_group(rr, 2 * kp + (mi >> 1)));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int g = 2 * kp + c;
+        uint32_t p[4], s[4];
+        e2m1x8_to_f16x2(k[2 * c], p);
+        e2m1x8_to_f16x2(k[2 * c + 1], s);
+        const uint32_t a0[4] = {p[0], s[0], p[1], s[1]}, a1[4] = {p[2], s[2], p[3], s[3]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float sc[4] = {};
+          F16::mma(sc, a0, q.b[2 * g][nt][0], q.b[2 * g][nt][1]);
+          F16::mma(sc, a1, q.b[2 * g + 1][nt][0], q.b[2 * g + 1][nt][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)  // the two factors first, as for 8 bits
+            x[nt][2 * hf + (e >> 1)][e & 1] =
+                fmaf(sc[e], fk[2 * hf + (e >> 1)][g] * q.sl2[nt][e & 1], x[nt][2 * hf + (e >> 1)][e & 1]);
+        }
+      }
+    }
+  }
+
+  float mx[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r8 + 8 * i >= hi) x[nt][i][0] = x[nt][i][1] = -INFINITY;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      mx[nt][c] = fmaxf(fmaxf(x[nt][0][c], x[nt][1][c]), fmaxf(x[nt][2][c], x[nt][3][c]));
+  }
+  st.template raise<false>(mx);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) x[nt][i][c] = ex2(x[nt][i][c] - st.m[nt][c]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      st.l[nt][c] += (x[nt][0][c] + x[nt][1][c]) + (x[nt][2][c] + x[nt][3][c]);
+  }
+
+  const uint32_t rest = (lane & 2) != 0 ? kAll : 0u;  // SPLIT: columns 4-7
+  // V's codes of a group as A operands of its two m-tiles: [tokens 0-15, 16-31][m-tile]
+  auto value = [&](int g, uint32_t (&a)[2][2][4]) {
+    uint32_t v[4];
+    ldmatrix_x4_trans(v, sv + Geo::in_group(rr, g));
+    constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      // codes of the even tokens, and of the odd ones
+      const uint32_t u = __byte_perm(v[2 * hf], v[2 * hf + 1], 0x5410);
+      const uint32_t w = __byte_perm(v[2 * hf], v[2 * hf + 1], 0x7632);
+      uint32_t e[4], o[4];  // dims 0, 2 and 1, 3 of tokens 0-7, then of 8-15
+      e2m1x8_to_f16x2((u & kLow) | (w << 4 & ~kLow), e);
+      e2m1x8_to_f16x2((u >> 4 & kLow) | (w & ~kLow), o);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        a[hf][h][0] = e[h];
+        a[hf][h][1] = o[h];
+        a[hf][h][2] = e[2 + h];
+        a[hf][h][3] = o[2 + h];
+      }
+    }
+  };
+  if (!wild) {
+    uint32_t ph[4][NT], pl[4][NT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        weight_parts<F16, SPLIT>(x[nt][i][0] * 128.f, x[nt][i][1] * 128.f, rest, ph[i][nt], pl[i][nt]);
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      uint32_t a[2][2][4];
+      value(g, a);
+      const uint4 fv = *reinterpret_cast<const uint4*>(&fac.v[t][g * 4]);
+      const uint32_t f[4] = {fv.x, fv.y, fv.z, fv.w};
+      float o[2][NT][4] = {};
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t b0 = F16::mul(ph[2 * hf][nt], f[2 * hf]), b1 = F16::mul(ph[2 * hf + 1][nt], f[2 * hf + 1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) F16::mma(o[h][nt], a[hf][h], b0, b1);
+          if constexpr (!SPLIT) {
+            const uint32_t c0 = F16::mul(pl[2 * hf][nt], f[2 * hf]), c1 = F16::mul(pl[2 * hf + 1][nt], f[2 * hf + 1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) F16::mma(o[h][nt], a[hf][h], c0, c1);
+          }
+        }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) st.add(2 * g + h, o[h], 1.f / 128.f);
+    }
+    return;
+  }
+  uint32_t evs[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) evs[i] = __shfl_sync(kAll, ev, r8 + 8 * i);
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    uint32_t a[2][2][4], bh[4][NT], bl[4][NT];
+    value(g, a);
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 c = F16::unpack(a[hf][h][k]);
+          a[hf][h][k] = BF16::pack(c.x, c.y);
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = static_cast<int>(evs[i] >> (8 * g) & 255u);
+      const float f = exponent_factor(e == 255 ? 255 : e == 0 ? 0 : max(e - top + 127, 0));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        weight_parts<BF16, SPLIT>(x[nt][i][0] * f, x[nt][i][1] * f, rest, bh[i][nt], bl[i][nt]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float o[NT][4] = {};
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          BF16::mma(o[nt], a[hf][h], bh[2 * hf][nt], bh[2 * hf + 1][nt]);
+          if constexpr (!SPLIT) BF16::mma(o[nt], a[hf][h], bl[2 * hf][nt], bl[2 * hf + 1][nt]);
+        }
+      st.add(2 * g + h, o);
+    }
+  }
+}
+
 // 16-bit tile. sk, sv: the groups of rows that this lane's addresses for ldmatrix
 // lie in (K: lane & 8, V: lane & 16).
 template <typename Ty, int D, int NT, bool SPLIT>
 __device__ __forceinline__ void tile_16(uint32_t sk, uint32_t sv, int lo, int hi,
                                         const Query<D, NT>& q, State<D, NT>& st) {
-  using Geo = Tile<D, false>;
+  using Geo = Tile<D, 16>;
   const int lane = threadIdx.x & 31, r8 = lane >> 2;
   const int mi = lane >> 3, rr = lane & 7;
   const bool edge = lo > 0 || hi < Geo::kTokens;

@@ -30,7 +30,8 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_bytes", "pa_decode",
             "pa_decode_fp8_workspace_bytes",
             "pa_decode_shared_prefix_workspace_bytes", "pa_testing_decode_fp8_stalled",
             "pa_testing_decode_shared_prefix_stalled", "pa_reshape_and_cache_fp4",
-            "pa_copy_blocks_fp4", "pa_gather_cache_fp4")
+            "pa_copy_blocks_fp4", "pa_gather_cache_fp4", "pa_decode_fp4",
+            "pa_decode_fp4_workspace_bytes", "pa_testing_decode_fp4_stalled")
 PA_ERR_CAPACITY = -5
 
 _lib = None
@@ -92,9 +93,6 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.pa_gather_cache_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, i32, i32, i32,
                                       i32, i32, i32, i32, vp]
     L.pa_gather_cache_fp8.restype = i32
-    for name in ("reshape_and_cache", "copy_blocks", "gather_cache"):
-        for what in ("argtypes", "restype"):
-            setattr(getattr(L, f"pa_{name}_fp4"), what, getattr(getattr(L, f"pa_{name}_fp8"), what))
     L.pa_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_float,
                                 i32, i32, i32, i32, i32, vp, sz, vp]
     L.pa_decode_fp8.restype = i32
@@ -102,6 +100,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.pa_testing_decode_fp8_stalled.restype = i32
     L.pa_decode_fp8_workspace_bytes.argtypes = [i32] * 6
     L.pa_decode_fp8_workspace_bytes.restype = sz
+    for name in ("reshape_and_cache_%s", "copy_blocks_%s", "gather_cache_%s", "decode_%s",
+                 "decode_%s_workspace_bytes", "testing_decode_%s_stalled"):
+        fp4, fp8 = getattr(L, "pa_" + name % "fp4"), getattr(L, "pa_" + name % "fp8")
+        fp4.argtypes, fp4.restype = fp8.argtypes, fp8.restype
     L.pa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                           i32, ctypes.c_float, i32, i32, i32, i32, i32, i32, vp, sz,
                                           vp]
@@ -193,6 +195,12 @@ def decode_fp8_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: in
                                                             max_blocks_per_seq, block_size))
 
 
+def decode_fp4_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                               max_blocks_per_seq: int, block_size: int) -> int:
+    return int(load_library().pa_decode_fp4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                            max_blocks_per_seq, block_size))
+
+
 def decode_partition_tokens(partition_tokens: int, block_size: int,
                             max_blocks_per_seq: int) -> int:
     """The split-K partition length pa_decode resolves these arguments to."""
@@ -206,10 +214,13 @@ def decode_partition_tokens(partition_tokens: int, block_size: int,
 def alloc_workspace(query: torch.Tensor, key_cache: torch.Tensor, block_tables: torch.Tensor,
                     partition_tokens: int = 0) -> Optional[torch.Tensor]:
     """Zero-filled workspace for :func:`decode` (or :func:`decode_fp8`, for a float8
-    ``key_cache``) with these shapes (None if none is needed)."""
+    ``key_cache``, or :func:`decode_fp4`, for a uint8 one) with these shapes (None if none is needed)."""
     S, Hq, d = query.shape
     if key_cache.dtype == torch.float8_e4m3fn:
         n = decode_fp8_workspace_bytes(S, Hq, key_cache.shape[2], d, block_tables.shape[1],
+                                       key_cache.shape[1])
+    elif key_cache.dtype == torch.uint8:
+        n = decode_fp4_workspace_bytes(S, Hq, key_cache.shape[2], d, block_tables.shape[1],
                                        key_cache.shape[1])
     else:
         n = decode_workspace_bytes(S, Hq, d, block_tables.shape[1], key_cache.shape[1], partition_tokens)
@@ -649,8 +660,8 @@ def decode_fp8(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
     ``query`` is float16 or bfloat16; the workspace comes from
     :func:`alloc_workspace` with the 8-bit ``key_cache``.
     """
-    return _decode_fp8(load_library().pa_decode_fp8, out, query, key_cache, value_cache, cache_scales,
-                       block_tables, seq_lens, scale, partition_tokens, workspace, stream)
+    return _decode_scaled(load_library().pa_decode_fp8, _need_fp8_pool, out, query, key_cache, value_cache,
+                          cache_scales, block_tables, seq_lens, scale, partition_tokens, workspace, stream)
 
 
 def testing_decode_fp8_stalled(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -660,13 +671,38 @@ def testing_decode_fp8_stalled(out: torch.Tensor, query: torch.Tensor, key_cache
                                stream=None) -> torch.Tensor:
     """Test hook (include/pagedattn_testing.h): :func:`decode_fp8` whose ring is never
     emptied, so bounded waits give up and the launches wind down."""
-    return _decode_fp8(load_library().pa_testing_decode_fp8_stalled, out, query, key_cache, value_cache,
-                       cache_scales, block_tables, seq_lens, scale, partition_tokens, workspace, stream)
+    return _decode_scaled(load_library().pa_testing_decode_fp8_stalled, _need_fp8_pool, out, query, key_cache,
+                          value_cache, cache_scales, block_tables, seq_lens, scale, partition_tokens, workspace,
+                          stream)
 
 
-def _decode_fp8(entry, out, query, key_cache, value_cache, cache_scales, block_tables, seq_lens, scale,
-                partition_tokens, workspace, stream):
-    NB, B, Hkv, d = _need_fp8_pool(key_cache, value_cache, cache_scales)
+def decode_fp4(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+               value_cache: torch.Tensor, cache_scales: torch.Tensor, block_tables: torch.Tensor,
+               seq_lens: torch.Tensor, scale: float, partition_tokens: int = 0,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """:func:`decode` over a 4-bit pool (see :func:`reshape_and_cache_fp4`).
+
+    ``query`` is float16 or bfloat16; the workspace comes from
+    :func:`alloc_workspace` with the 4-bit ``key_cache``.
+    """
+    return _decode_scaled(load_library().pa_decode_fp4, _need_fp4_pool, out, query, key_cache, value_cache,
+                          cache_scales, block_tables, seq_lens, scale, partition_tokens, workspace, stream)
+
+
+def testing_decode_fp4_stalled(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor, cache_scales: torch.Tensor,
+                               block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                               partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
+                               stream=None) -> torch.Tensor:
+    """Test hook: :func:`decode_fp4` with the streaming kernel of :func:`testing_decode_fp8_stalled`."""
+    return _decode_scaled(load_library().pa_testing_decode_fp4_stalled, _need_fp4_pool, out, query, key_cache,
+                          value_cache, cache_scales, block_tables, seq_lens, scale, partition_tokens, workspace,
+                          stream)
+
+
+def _decode_scaled(entry, need_pool, out, query, key_cache, value_cache, cache_scales, block_tables, seq_lens,
+                   scale, partition_tokens, workspace, stream):
+    NB, B, Hkv, d = need_pool(key_cache, value_cache, cache_scales)
     device, (S, Hq, MB), rest = _need_decode(out, query, d, block_tables, seq_lens, workspace,
                                              key_cache, value_cache, cache_scales)
     _enqueue(entry, device, stream, out.data_ptr(), query.data_ptr(),
