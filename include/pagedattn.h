@@ -294,6 +294,87 @@ int pa_copy_blocks(void* key_cache, void* value_cache,
                    pa_dtype dtype, cudaStream_t stream);
 
 /*
+ * Norms of query and key heads and their rotation by position, in one pass. For every
+ * token t and head row x of query or key (d elements):
+ *   with weights w (query_weight or key_weight, [d] of dtype; both or neither):
+ *     x <- x / sqrt(mean_i x_i^2 + eps) * w
+ *   then, with n = rotary_dim / 2, for pairs i < n, turned by the angle
+ *   phi_i = 2 pi positions[t] frequencies[i] / 2^64:
+ *     a' = factor (a cos phi_i - b sin phi_i),  b' = factor (b cos phi_i + a sin phi_i)
+ *   (a, b) = (x_i, x_{n+i}), or (x_{2i}, x_{2i+1}) if interleaved is 1 and not 0.
+ * Elements from rotary_dim on stay. Arithmetic is fp32, each result rounded once.
+ * frequencies: DEVICE uint64 [n], turns a position as 64-bit binary fractions, so that
+ * angles at far positions are exact to fp32's rounding of a fraction of a turn. Scaled
+ * frequencies are the caller's (the Python binding's rotary module has the usual ones).
+ * positions: DEVICE int64 [num_tokens], any value.
+ * Rows of one token are contiguous ([heads, d]); the strides, in elements, lead from one
+ * token to the next (multiples of 8, at least a token's rows): query and key may lie in
+ * the output of one projection. query_out may be query and key_out key, with the same
+ * stride; otherwise outputs must not overlap inputs.
+ * Sizes: num_tokens >= 0 (0 is a no-op), heads in [1, 65535], head_dim in {64, 128},
+ * rotary_dim a multiple of 16 up to head_dim, factor finite, eps at least 1e-20 (with
+ * weights). A row with an infinity or a NaN gives what the formula gives.
+ * Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA.
+ */
+int pa_rotate(void* query_out, void* key_out, const void* query, const void* key,
+              const int64_t* positions, const uint64_t* frequencies,
+              const void* query_weight, const void* key_weight, int num_tokens,
+              int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim, int interleaved,
+              float factor, float eps, int64_t query_out_stride, int64_t key_out_stride,
+              int64_t query_stride, int64_t key_stride, pa_dtype dtype, cudaStream_t stream);
+
+/*
+ * pa_rotate with pa_reshape_and_cache in the same pass: the rotated rows of key and the
+ * rows of value go to their slots of the caches (16-bit, of dtype). Slots as there: K and
+ * V of a token with a negative slot are not written, nor are those of one above the pool,
+ * which is counted; its query is rotated all the same. (For an 8-bit or 4-bit pool:
+ * pa_rotate, then that pool's write.)
+ */
+int pa_rotate_and_cache(void* query_out, const void* query, const void* key, const void* value,
+                        void* key_cache, void* value_cache, const int64_t* slot_mapping,
+                        const int64_t* positions, const uint64_t* frequencies,
+                        const void* query_weight, const void* key_weight, int num_tokens,
+                        int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                        int num_blocks, int rotary_dim, int interleaved, float factor, float eps,
+                        int64_t query_out_stride, int64_t query_stride, int64_t key_stride,
+                        int64_t value_stride, pa_dtype dtype, cudaStream_t stream);
+
+/*
+ * Block tables, slots and positions of a step's new tokens, on the device: pa_bm_append
+ * for sequences that share no block they write to, without the host, so that a captured
+ * decode loop can go on by itself. Sequence s has seq_lens[s] tokens, in the first
+ * ceil(seq_lens[s] / B) blocks of its row of block_tables, and gets
+ * query_start[s+1] - query_start[s] more, rows query_start[s] .. query_start[s+1] - 1 of
+ * the step. Its new blocks come from the stack free_blocks[0 .. *num_free - 1], from the
+ * end, in the sequences' order, and enter its table row behind those it has. For the
+ * i-th new token of s, with p = seq_lens[s] + i:
+ *   positions[query_start[s] + i] = p
+ *   slot_mapping[query_start[s] + i] = block_tables[s, p / B] * B + p % B
+ * Rows outside [query_start[0], query_start[num_seqs]) (a padded batch) get slot -1 and
+ * position 0. new_lens[s] = seq_lens[s] + its new tokens; *new_free = *num_free less the
+ * new blocks. new_lens may be seq_lens, and new_free num_free; nothing else may overlap.
+ * All or nothing: where the stack holds too few blocks, or a length or start is out of
+ * range (seq_lens[s] < 0, more tokens than max_blocks_per_seq * B, starts that decrease or
+ * leave [0, num_rows], *num_free outside [0, free_capacity]), every row gets slot -1 and
+ * position 0, tables stay, new_lens = seq_lens and *new_free = *num_free, and *status is
+ * raised to 1 (too few blocks) or 2 (out of range). The library never lowers *status: a
+ * loop of steps looks at it once. A block id outside [0, num_blocks) gives slot -1 for its
+ * tokens and is counted by pa_bad_index_count for each.
+ * DEVICE: new_lens, seq_lens int32 [num_seqs]; new_free, num_free, status int32 [1];
+ * slot_mapping, positions int64 [num_rows]; block_tables int32 [num_seqs,
+ * max_blocks_per_seq]; query_start int32 [num_seqs + 1]; free_blocks int32
+ * [free_capacity]. num_seqs at most 16384; other sizes as for pa_reshape_and_cache and
+ * pa_decode. Freed blocks are pushed by the caller (free_blocks[*num_free] = id, and one
+ * more in *num_free). Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA.
+ */
+int pa_append_tokens(int32_t* new_lens, int32_t* new_free, int64_t* slot_mapping,
+                     int64_t* positions, int32_t* block_tables, const int32_t* seq_lens,
+                     const int32_t* query_start, const int32_t* free_blocks,
+                     const int32_t* num_free, int32_t* status, int num_seqs, int num_rows,
+                     int free_capacity, int block_size, int max_blocks_per_seq,
+                     int num_blocks, cudaStream_t stream);
+
+/*
  * The 8-bit cache. A pool holds, for K and for V, e4m3 codes
  *   key_cache, value_cache  [NB, B, Hkv, d]     one byte an element
  * and the rows' exponent bytes

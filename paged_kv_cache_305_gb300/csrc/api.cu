@@ -17,6 +17,7 @@
 #include "internal.h"
 #include "pagedattn.h"
 #include "pagedattn_testing.h"
+#include "step.h"
 #include "stream.h"
 
 // Share (%) of every row's partitions that the decode kernel hands out at run
@@ -1138,6 +1139,197 @@ size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int
                   static_cast<int>(lmax), max_prefix_len, max_group_size);
   return pa::stream_layout(false, num_seqs, num_q_heads, num_kv_heads, head_dim, lmax, x)
       .total;
+}
+
+}  // extern "C"
+
+namespace {
+
+// pa_rotate (key_out) and pa_rotate_and_cache (value, caches, slot_mapping); fills in what the
+// kernel needs besides `a`'s pointers and strides.
+int rotate_impl(pa::RotateArgs a, bool cache, int head_dim, int interleaved, int block_size, int num_blocks,
+                pa_dtype dtype, cudaStream_t stream) {
+  g_error.clear();
+  int rc = check_dtype(dtype);
+  if (rc != PA_OK) return rc;
+  if (a.num_tokens < 0) return fail(PA_ERR_INVALID, "num_tokens %d < 0", a.num_tokens);
+  if (a.num_q_heads < 1 || a.num_kv_heads < 1)
+    return fail(PA_ERR_INVALID, "num_q_heads %d / num_kv_heads %d must be >= 1", a.num_q_heads, a.num_kv_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PA_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
+  if (a.num_q_heads > 65535 || a.num_kv_heads > 65535)
+    return fail(PA_ERR_UNSUPPORTED, "num_q_heads %d / num_kv_heads %d above 65535", a.num_q_heads, a.num_kv_heads);
+  if (a.rotary_dim < 2 || a.rotary_dim > head_dim || a.rotary_dim % 2 != 0)
+    return fail(PA_ERR_INVALID, "rotary_dim %d must be even and in [2, head_dim %d]", a.rotary_dim, head_dim);
+  if (a.rotary_dim % 16 != 0) return fail(PA_ERR_UNSUPPORTED, "rotary_dim %d is not a multiple of 16", a.rotary_dim);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(PA_ERR_INVALID, "interleaved %d is neither 0 nor 1", interleaved);
+  if (!isfinite(a.factor)) return fail(PA_ERR_INVALID, "factor is not finite");
+  if ((a.query_weight == nullptr) != (a.key_weight == nullptr))
+    return fail(PA_ERR_INVALID, "one of query_weight and key_weight is NULL");
+  if (a.query_weight != nullptr && !(a.eps >= 1e-20f && isfinite(a.eps)))
+    return fail(PA_ERR_INVALID, "eps %g is not a finite number of at least 1e-20", static_cast<double>(a.eps));
+  if (cache) {
+    if (log2_pow2(block_size) < 0)
+      return fail(PA_ERR_UNSUPPORTED, "block_size %d (supported: powers of two up to 64)", block_size);
+    if (num_blocks < 1) return fail(PA_ERR_INVALID, "num_blocks %d < 1", num_blocks);
+    a.num_slots = static_cast<long long>(num_blocks) * block_size;
+  }
+  const long long q_row = static_cast<long long>(a.num_q_heads) * head_dim;
+  const long long kv_row = static_cast<long long>(a.num_kv_heads) * head_dim;
+  const struct {
+    const void* p;
+    long long stride, row;
+    const char* name;
+  } rows[] = {{a.query, a.query_stride, q_row, "query"},
+              {a.query_out, a.query_out_stride, q_row, "query_out"},
+              {a.key, a.key_stride, kv_row, "key"},
+              {cache ? a.value : a.key_out, cache ? a.value_stride : a.key_out_stride, kv_row,
+               cache ? "value" : "key_out"}};
+  for (const auto& r : rows)
+    if (r.stride < r.row || r.stride % 8 != 0)
+      return fail(PA_ERR_INVALID, "%s stride %lld must be a multiple of 8 and at least %lld", r.name, r.stride, r.row);
+  if (a.num_tokens == 0) return PA_OK;
+  for (const auto& r : rows) {
+    if (r.p == nullptr) return fail(PA_ERR_INVALID, "%s is NULL", r.name);
+    if (!aligned16(r.p)) return fail(PA_ERR_INVALID, "%s must be 16-byte aligned", r.name);
+  }
+  if (!a.positions || !a.frequencies) return fail(PA_ERR_INVALID, "positions or frequencies is NULL");
+  if ((reinterpret_cast<uintptr_t>(a.positions) & 7u) != 0 || (reinterpret_cast<uintptr_t>(a.frequencies) & 7u) != 0)
+    return fail(PA_ERR_INVALID, "positions and frequencies must be 8-byte aligned");
+  if (a.query_weight != nullptr && (!aligned16(a.query_weight) || !aligned16(a.key_weight)))
+    return fail(PA_ERR_INVALID, "query_weight and key_weight must be 16-byte aligned");
+  if (cache) {
+    if (!a.key_cache || !a.value_cache || !a.slot_mapping)
+      return fail(PA_ERR_INVALID, "a cache or slot_mapping is NULL");
+    if (!aligned16(a.key_cache) || !aligned16(a.value_cache))
+      return fail(PA_ERR_INVALID, "the caches must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(a.slot_mapping) & 7u) != 0)
+      return fail(PA_ERR_INVALID, "slot_mapping must be 8-byte aligned");
+  }
+  rc = bad_counter(&a.bad);
+  if (rc != PA_OK) return rc;
+  const cudaError_t e = pa::launch_rotate(a, head_dim, dtype == PA_BFLOAT16, interleaved != 0, stream);
+  if (e != cudaSuccess) return cuda_fail(e, cache ? "rotate_and_cache launch" : "rotate launch");
+  return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_rotate(void* query_out, void* key_out, const void* query, const void* key, const int64_t* positions,
+              const uint64_t* frequencies, const void* query_weight, const void* key_weight, int num_tokens,
+              int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim, int interleaved, float factor,
+              float eps, int64_t query_out_stride, int64_t key_out_stride, int64_t query_stride,
+              int64_t key_stride, pa_dtype dtype, cudaStream_t stream) {
+  pa::RotateArgs a{};
+  a.query_out = query_out;
+  a.key_out = key_out;
+  a.query = query;
+  a.key = key;
+  a.positions = positions;
+  a.frequencies = reinterpret_cast<const unsigned long long*>(frequencies);
+  a.query_weight = query_weight;
+  a.key_weight = key_weight;
+  a.query_stride = query_stride;
+  a.key_stride = key_stride;
+  a.query_out_stride = query_out_stride;
+  a.key_out_stride = key_out_stride;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.rotary_dim = rotary_dim;
+  a.factor = factor;
+  a.eps = eps;
+  return rotate_impl(a, false, head_dim, interleaved, 1, 1, dtype, stream);
+}
+
+int pa_rotate_and_cache(void* query_out, const void* query, const void* key, const void* value, void* key_cache,
+                        void* value_cache, const int64_t* slot_mapping, const int64_t* positions,
+                        const uint64_t* frequencies, const void* query_weight, const void* key_weight,
+                        int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                        int num_blocks, int rotary_dim, int interleaved, float factor, float eps,
+                        int64_t query_out_stride, int64_t query_stride, int64_t key_stride,
+                        int64_t value_stride, pa_dtype dtype, cudaStream_t stream) {
+  pa::RotateArgs a{};
+  a.query_out = query_out;
+  a.query = query;
+  a.key = key;
+  a.value = value;
+  a.key_cache = key_cache;
+  a.value_cache = value_cache;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.frequencies = reinterpret_cast<const unsigned long long*>(frequencies);
+  a.query_weight = query_weight;
+  a.key_weight = key_weight;
+  a.query_stride = query_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.query_out_stride = query_out_stride;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.rotary_dim = rotary_dim;
+  a.factor = factor;
+  a.eps = eps;
+  return rotate_impl(a, true, head_dim, interleaved, block_size, num_blocks, dtype, stream);
+}
+
+int pa_append_tokens(int32_t* new_lens, int32_t* new_free, int64_t* slot_mapping, int64_t* positions,
+                     int32_t* block_tables, const int32_t* seq_lens, const int32_t* query_start,
+                     const int32_t* free_blocks, const int32_t* num_free, int32_t* status, int num_seqs,
+                     int num_rows, int free_capacity, int block_size, int max_blocks_per_seq, int num_blocks,
+                     cudaStream_t stream) {
+  g_error.clear();
+  if (num_seqs < 0) return fail(PA_ERR_INVALID, "num_seqs %d < 0", num_seqs);
+  if (num_seqs > pa::kAppendMaxSeqs)
+    return fail(PA_ERR_UNSUPPORTED, "num_seqs %d above %d", num_seqs, pa::kAppendMaxSeqs);
+  if (num_rows < 0) return fail(PA_ERR_INVALID, "num_rows %d < 0", num_rows);
+  if (free_capacity < 0) return fail(PA_ERR_INVALID, "free_capacity %d < 0", free_capacity);
+  const int shift = log2_pow2(block_size);
+  if (shift < 0)
+    return fail(PA_ERR_UNSUPPORTED, "block_size %d (supported: powers of two up to 64)", block_size);
+  if (max_blocks_per_seq < 1) return fail(PA_ERR_INVALID, "max_blocks_per_seq %d < 1", max_blocks_per_seq);
+  if (static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffll)
+    return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size overflows int");
+  if (num_blocks < 1) return fail(PA_ERR_INVALID, "num_blocks %d < 1", num_blocks);
+  if (!new_free || !num_free || !status) return fail(PA_ERR_INVALID, "new_free, num_free or status is NULL");
+  if (num_rows > 0 && (!slot_mapping || !positions))
+    return fail(PA_ERR_INVALID, "slot_mapping or positions is NULL");
+  if (num_seqs > 0 && (!new_lens || !block_tables || !seq_lens || !query_start))
+    return fail(PA_ERR_INVALID, "new_lens, block_tables, seq_lens or query_start is NULL");
+  if (free_capacity > 0 && !free_blocks) return fail(PA_ERR_INVALID, "free_blocks is NULL");
+  for (const void* p : {static_cast<const void*>(new_lens), static_cast<const void*>(new_free),
+                        static_cast<const void*>(block_tables), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(query_start), static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(num_free), static_cast<const void*>(status)})
+    if (!aligned4(p)) return fail(PA_ERR_INVALID, "int32 arrays must be 4-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0 || (reinterpret_cast<uintptr_t>(positions) & 7u) != 0)
+    return fail(PA_ERR_INVALID, "slot_mapping and positions must be 8-byte aligned");
+  pa::AppendArgs a{};
+  a.new_lens = new_lens;
+  a.new_free = new_free;
+  a.slots = slot_mapping;
+  a.positions = positions;
+  a.tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.query_start = query_start;
+  a.free_blocks = free_blocks;
+  a.num_free = num_free;
+  a.status = status;
+  a.num_seqs = num_seqs;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.block_shift = shift;
+  a.num_blocks = num_blocks;
+  a.free_capacity = free_capacity;
+  a.rows = num_rows;
+  const int rc = bad_counter(&a.bad);
+  if (rc != PA_OK) return rc;
+  const cudaError_t e = pa::launch_append(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "append_tokens launch");
+  return PA_OK;
 }
 
 }  // extern "C"

@@ -31,7 +31,8 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_bytes", "pa_decode",
             "pa_decode_shared_prefix_workspace_bytes", "pa_testing_decode_fp8_stalled",
             "pa_testing_decode_shared_prefix_stalled", "pa_reshape_and_cache_fp4",
             "pa_copy_blocks_fp4", "pa_gather_cache_fp4", "pa_decode_fp4",
-            "pa_decode_fp4_workspace_bytes", "pa_testing_decode_fp4_stalled")
+            "pa_decode_fp4_workspace_bytes", "pa_testing_decode_fp4_stalled", "pa_rotate",
+            "pa_rotate_and_cache", "pa_append_tokens")
 PA_ERR_CAPACITY = -5
 
 _lib = None
@@ -112,6 +113,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.pa_testing_decode_shared_prefix_stalled.restype = i32
     L.pa_decode_shared_prefix_workspace_bytes.argtypes = [i32] * 9
     L.pa_decode_shared_prefix_workspace_bytes.restype = sz
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    L.pa_rotate.argtypes = [vp] * 8 + [i32] * 6 + [f32] * 2 + [i64] * 4 + [i32, vp]
+    L.pa_rotate.restype = i32
+    L.pa_rotate_and_cache.argtypes = [vp] * 11 + [i32] * 8 + [f32] * 2 + [i64] * 4 + [i32, vp]
+    L.pa_rotate_and_cache.restype = i32
+    L.pa_append_tokens.argtypes = [vp] * 10 + [i32] * 6 + [vp]
+    L.pa_append_tokens.restype = i32
     ip = ctypes.POINTER(ctypes.c_int)
     L.pa_bm_create.argtypes = [i32, i32, i32, ctypes.POINTER(vp)]
     L.pa_bm_create.restype = i32
@@ -179,6 +187,113 @@ def reshape_and_cache(key: torch.Tensor, value: torch.Tensor, key_cache: torch.T
         _check(L.pa_reshape_and_cache(key.data_ptr(), value.data_ptr(), key_cache.data_ptr(),
                                       value_cache.data_ptr(), slot_mapping.data_ptr(), T, Hkv, d,
                                       B, NB, _dtype_code(key), _stream(key, stream)))
+
+
+def _need_rows(t: torch.Tensor, name: str, tokens: int, heads: int, head_dim: int, dtype, device: int) -> int:
+    """Checks [tokens, heads, head_dim] rows whose tokens may lie apart; returns the stride of a token."""
+    _need(t.shape == (tokens, heads, head_dim) and t.dtype == dtype, f"{name} dtype or shape mismatch")
+    _need(t.get_device() == device, "tensors must be on one device")
+    far, head, one = t.stride()
+    _need((one == 1 or head_dim == 1) and (head == head_dim or heads == 1),
+          f"the heads of a token of {name} must be contiguous")
+    return far if tokens > 1 else max(far, heads * head_dim)
+
+
+def _rotate(cache, query_out, key_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
+            frequencies, interleaved, factor, query_weight, key_weight, eps, stream):
+    _need(query.dim() == 3 and key.dim() == 3, "query and key must be [num_tokens, heads, head_dim]")
+    T, Hq, d = query.shape
+    Hkv = key.shape[1]
+    _need((query_weight is None) == (key_weight is None), "query_weight and key_weight: both or neither")
+    others = [positions, frequencies]
+    if query_weight is not None:
+        _need(query_weight.shape == key_weight.shape == (d,) and query_weight.dtype == key_weight.dtype == query.dtype,
+              "query_weight and key_weight must be [head_dim] of query's dtype")
+        others += [query_weight, key_weight]
+    _need(positions.dtype == torch.int64 and positions.shape == (T,), "positions must be int64 [num_tokens]")
+    _need(frequencies.dtype == torch.int64 and frequencies.dim() == 1, "frequencies must be int64 [rotary_dim / 2]")
+    if cache:
+        others += [key_cache, value_cache, slot_mapping]
+    device = _device_of(*others)
+    q_far = _need_rows(query, "query", T, Hq, d, query.dtype, device)
+    qo_far = _need_rows(query_out, "query_out", T, Hq, d, query.dtype, device)
+    k_far = _need_rows(key, "key", T, Hkv, d, query.dtype, device)
+    weights = (query_weight.data_ptr(), key_weight.data_ptr()) if query_weight is not None else (0, 0)
+    turn = 2 * frequencies.shape[0], int(bool(interleaved)), float(factor), float(eps)
+    code = _dtype_code(query)
+    if not cache:
+        ko_far = _need_rows(key_out, "key_out", T, Hkv, d, query.dtype, device)
+        _enqueue(load_library().pa_rotate, device, stream, query_out.data_ptr(), key_out.data_ptr(),
+                 query.data_ptr(), key.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), *weights,
+                 T, Hq, Hkv, d, *turn, qo_far, ko_far, q_far, k_far, code)
+        return
+    v_far = _need_rows(value, "value", T, Hkv, d, query.dtype, device)
+    _need(key_cache.dim() == 4 and key_cache.shape[2:] == (Hkv, d) and value_cache.shape == key_cache.shape
+          and key_cache.dtype == value_cache.dtype == query.dtype, "cache dtype or shape mismatch")
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,), "slot_mapping must be int64 [num_tokens]")
+    _enqueue(load_library().pa_rotate_and_cache, device, stream, query_out.data_ptr(), query.data_ptr(),
+             key.data_ptr(), value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+             slot_mapping.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), *weights, T, Hq, Hkv, d,
+             key_cache.shape[1], key_cache.shape[0], *turn, qo_far, q_far, k_far, v_far, code)
+
+
+def rotate(query_out: torch.Tensor, key_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+           positions: torch.Tensor, frequencies: torch.Tensor, interleaved: bool = False, factor: float = 1.0,
+           query_weight: Optional[torch.Tensor] = None, key_weight: Optional[torch.Tensor] = None,
+           eps: float = 1e-6, stream=None) -> None:
+    """Rotate ``query`` [T, Hq, d] and ``key`` [T, Hkv, d] by position, behind norms of their heads if weights are given.
+
+    The first 2 n elements of every head are turned in pairs (i, n + i), or (2 i, 2 i + 1) if
+    ``interleaved``, n the length of ``frequencies`` (int64, from :func:`rotary_frequencies`), by
+    ``positions`` [T] (int64) times the frequency; both results are multiplied by ``factor``. With
+    ``query_weight`` and ``key_weight`` [d] each head is first divided by its root mean square
+    (``eps`` is added to the mean square) and multiplied by them. The tokens of ``query``, ``key``
+    and the outputs may lie apart (slices of one projection's output); an output may be its input.
+    """
+    _rotate(False, query_out, key_out, query, key, None, None, None, None, positions, frequencies, interleaved,
+            factor, query_weight, key_weight, eps, stream)
+
+
+def rotate_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                     key_cache: torch.Tensor, value_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                     positions: torch.Tensor, frequencies: torch.Tensor, interleaved: bool = False,
+                     factor: float = 1.0, query_weight: Optional[torch.Tensor] = None,
+                     key_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
+    """:func:`rotate`, with the rotated keys and the rows of ``value`` written to their slots of the
+    caches [NB, B, Hkv, d] in the same pass, as :func:`reshape_and_cache` does."""
+    _rotate(True, query_out, None, query, key, value, key_cache, value_cache, slot_mapping, positions, frequencies,
+            interleaved, factor, query_weight, key_weight, eps, stream)
+
+
+def append_tokens(new_lens: torch.Tensor, new_free: torch.Tensor, slot_mapping: torch.Tensor,
+                  positions: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                  query_start: torch.Tensor, free_blocks: torch.Tensor, num_free: torch.Tensor,
+                  status: torch.Tensor, block_size: int, num_blocks: int, stream=None) -> None:
+    """Tables, slots and positions of a step's new tokens, on the GPU (see include/pagedattn.h).
+
+    Sequence s (``seq_lens[s]`` tokens so far) gets rows ``query_start[s] .. query_start[s+1] - 1`` of
+    ``slot_mapping`` and ``positions`` (int64 [rows]; rows outside all sequences get -1 and 0). New blocks
+    are popped from ``free_blocks`` (int32, the first ``num_free`` of them a stack) into its row of
+    ``block_tables`` [S, MB]. ``new_lens`` (may be ``seq_lens``) and ``new_free`` (may be ``num_free``) get
+    what is there afterwards. Where the step does not fit nothing changes, all slots are -1 and
+    ``status`` (int32 [1]) is raised to 1 (too few blocks) or 2 (lengths or starts out of range).
+    """
+    S = seq_lens.shape[0]
+    for name, t, shape in (("new_lens", new_lens, (S,)), ("seq_lens", seq_lens, (S,)), ("new_free", new_free, (1,)),
+                           ("num_free", num_free, (1,)), ("status", status, (1,)),
+                           ("query_start", query_start, (S + 1,))):
+        _need(t.dtype == torch.int32 and t.shape == shape, f"{name} must be int32 {list(shape)}")
+    _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == S,
+          "block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    _need(free_blocks.dtype == torch.int32 and free_blocks.dim() == 1, "free_blocks must be 1-D int32")
+    _need(slot_mapping.dtype == positions.dtype == torch.int64 and slot_mapping.dim() == 1
+          and slot_mapping.shape == positions.shape, "slot_mapping and positions must be int64 [rows]")
+    device = _device_of(new_lens, new_free, slot_mapping, positions, block_tables, seq_lens, query_start,
+                        free_blocks, num_free, status)
+    _enqueue(load_library().pa_append_tokens, device, stream, new_lens.data_ptr(), new_free.data_ptr(),
+             slot_mapping.data_ptr(), positions.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+             query_start.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(), status.data_ptr(), S,
+             slot_mapping.shape[0], free_blocks.shape[0], int(block_size), block_tables.shape[1], int(num_blocks))
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int,
