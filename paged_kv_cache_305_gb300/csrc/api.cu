@@ -983,7 +983,8 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   a.out_f32 = out_dtype == PA_FLOAT32 ? 1 : 0;
   a.groups = groups;
   a.cut = wl.cut ? 1 : 0;
-  a.least_tiles = std::max(partition_tokens / (codes ? 32 : 16), pa::kLeastTiles);
+  const int tile = bits == 4 ? 64 : bits == 8 ? 32 : 16;  // tokens of a warp in a stage
+  a.least_tiles = std::max(partition_tokens / tile, bits == 4 ? pa::kLeastTiles / 2 : pa::kLeastTiles);
   if (wl.total > 0) {
     a.ws_rows = reinterpret_cast<int2*>(ws);
     a.pre_stat = reinterpret_cast<float2*>(ws + wl.pre_stat);
@@ -1120,7 +1121,7 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
 size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                      int max_blocks_per_seq, int block_size) {
   return pa_decode_fp8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
-                                       block_size);  // tiles of as many tokens
+                                       block_size);
 }
 
 size_t pa_decode_shared_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads,

@@ -83,8 +83,7 @@ template <int D, int BITS, int NT>
 struct Ring {
   using T = Tile<D, BITS>;
   static constexpr int kHalf = kWarps * T::kBytes;   // K (or V) of a stage
-  static constexpr int kRing = BITS == 4 ? 49152 : 65536;  // three CTAs on an SM
-  static constexpr int kStages = kRing / (2 * kHalf);
+  static constexpr int kStages = 65536 / (2 * kHalf);  // three CTAs on an SM
   static constexpr int kScaleBytes = kWarps * T::kTokens * 2 * T::kGroups;  // exponent bytes of a stage
   static constexpr int kHeads = NT * 8;
   static constexpr int kOStride = D + 4;
@@ -96,13 +95,15 @@ struct Ring {
   static constexpr int kBase = kStats + kWarps * 3 * kHeads * 4;   // [kChunks]
   static constexpr int kMisc = kBase + kChunks * 4;
   static constexpr int kJoin = (kMisc + 32 + 15) / 16 * 16;        // [warp][head][kOStride]
-  static constexpr int kFactors = kJoin + kWarps * kJoinHeads * kOStride * 4;  // 4-bit: [warp]
+  // 4-bit: joined in the stage that the segment ends in
+  static constexpr int kJoinBytes = BITS == 4 ? 0 : kWarps * kJoinHeads * kOStride * 4;
+  static constexpr int kFactors = kJoin + kJoinBytes;  // 4-bit: [warp]
   static constexpr int kFactorBytes = BITS == 4 ? static_cast<int>(sizeof(Factors4<D>)) : 0;
   static constexpr int kSlots = kFactors + kWarps * kFactorBytes;  // ROWS: [stage][token]
   template <bool ROWS>
   static constexpr int kFixed = (kSlots + (ROWS ? kStages * kWarps * T::kTokens * 4 : 0) + 1023) / 1024 * 1024;
   static_assert(kStages >= 2, "a stage lands while another is computed");
-  static_assert(NT > 1 || 3 * (kFixed<true> + kRing + 1024) <= 228 * 1024, "three CTAs on an SM");
+  static_assert(NT > 1 || 3 * (kFixed<true> + 65536 + 1024) <= 228 * 1024, "three CTAs on an SM");
 };
 
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
@@ -233,7 +234,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   if (warp == kWarps) {
     // ======================= the feeding warp ==================================
     const int bt = ROWS ? 1 : lb;  // tokens a lane's table entry stands for
-    constexpr int kPer = ROWS ? 4 : 1;  // entries of a lane: tokens lane, lane + 32, .. (at most 128)
+    constexpr int kPer = ROWS ? (BITS == 4 ? 8 : 4) : 1;  // entries of a lane: tokens lane, lane + 32, ..
     Place to;              // the stage to fill next
     int filled = 0;        // stages, up to the ring's number
     bool ok = true;
@@ -454,11 +455,21 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     auto row_at = [&](int x) {
       return static_cast<uint32_t>((x / lb * Hc + hsub) * lb * kRB + (x % lb >> 3) * 8 * kRB);
     };
+    // the same for rows 8 i, by shifts: lb, Hc and Wh are powers of two
+    const int lb8 = 31 - __clz(lb >> 3);
+    auto eight_at = [&](int i) {
+      return (((((i >> lb8) * Hc + hsub) << lb8) + (i & ((1 << lb8) - 1))) * 8) * kRB;
+    };
     const int x0 = wsub * kTT, mi = lane >> 3;
     const uint32_t k_at = row_at(x0 + ((mi & 1) << 3));
     const uint32_t k_next = kCodes ? row_at(x0 + 16 + ((mi & 1) << 3)) - k_at : 0u;  // the next 16 tokens
     const uint32_t v_at = row_at(kCodes ? x0 + (lane & 24) : x0 + ((mi >> 1) << 3));
-    const int e_at = (((x0 + lane) / lb * Hc + hsub) * 2 * lb + (x0 + lane) % lb) * kG;
+    auto exps_of = [&](int x) { return ((x / lb * Hc + hsub) * 2 * lb + x % lb) * kG; };
+    const int e_at = exps_of(x0 + lane);
+    // 4-bit: from the tile of a warp's first 32 tokens to that of the others
+    const uint32_t next_rows = BITS == 4 ? row_at(x0 + 32 + (lane & 24)) - v_at : 0u;
+    const int next_exps = BITS == 4 ? exps_of(x0 + 32 + lane) - e_at : 0;
+    constexpr int kTiles = BITS == 4 ? 2 : 1;  // of a warp in a stage
     float* sStats = reinterpret_cast<float*>(smem + R::kStats);
     float* sJoin = reinterpret_cast<float*>(smem + R::kJoin);
     State<D, NT> st;
@@ -480,7 +491,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       if constexpr (kG == 2) return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(e));
       return static_cast<Exps>(*e);
     };
-    [[maybe_unused]] Exps ek = 0, ev = 0;
+    [[maybe_unused]] Exps ek[kTiles] = {}, ev[kTiles] = {};
     auto take = [&](const Place& p) {
       const int stage = p.st;
       ok = *aborted == 0 && wait(full(stage), p.round);
@@ -490,7 +501,9 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         if (!(note.flags & kEnd)) {
           constexpr int kRowsPerCopy = 32 / Geo::kChunks;
           const int h = note.hg * Hc + hsub, cc = lane % Geo::kChunks;
-          const uint32_t mine = slots[stage * (kWarps * kTT) + x0 + lane % kTT];
+          uint32_t mine[kTiles];
+#pragma unroll
+          for (int z = 0; z < kTiles; ++z) mine[z] = slots[stage * (kWarps * kTT) + x0 + 32 * z + lane % kTT];
           const size_t stride = static_cast<size_t>(Hkv) * kRB;
           const size_t hoff = static_cast<size_t>(h) * kRB + cc * 16;
           const char* kb = static_cast<const char*>(a.key_cache) + hoff;
@@ -499,7 +512,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
           for (int i = 0; i < kTT / kRowsPerCopy; ++i) {
             const int r = lane / Geo::kChunks + i * kRowsPerCopy;
-            const uint32_t slot = __shfl_sync(kFull, mine, r);
+            constexpr int kHalf = kTT / kRowsPerCopy / kTiles;  // copies of a tile
+            const uint32_t slot = __shfl_sync(kFull, mine[i / kHalf], r & 31);
             const bool live = slot < kBad;
             const size_t from = (live ? slot : 0u) * stride;
             const uint32_t o = Geo::off(x0 + r, cc);
@@ -507,10 +521,13 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             cp_async_16(sv + o, vb + from, live);
           }
           if constexpr (kCodes) {
-            const uint8_t* e = a.scales + (((static_cast<size_t>(mine >> shift) * Hkv + h) * 2 << shift) +
-                                           (mine & ((1u << shift) - 1))) * kG;
-            ek = mine < kBad ? exps_at(e) : 0;
-            ev = mine < kBad ? exps_at(e + (kG << shift)) : 0;
+#pragma unroll
+            for (int z = 0; z < kTiles; ++z) {
+              const uint8_t* e = a.scales + (((static_cast<size_t>(mine[z] >> shift) * Hkv + h) * 2 << shift) +
+                                             (mine[z] & ((1u << shift) - 1))) * kG;
+              ek[z] = mine[z] < kBad ? exps_at(e) : 0;
+              ev[z] = mine[z] < kBad ? exps_at(e + (kG << shift)) : 0;
+            }
           }
         }
         cp_async_commit();
@@ -523,12 +540,15 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     for (;; step(at)) {
       const int stage = at.st;
       Note note;
-      [[maybe_unused]] Exps my_ek = 0, my_ev = 0;
+      [[maybe_unused]] Exps my_ek[kTiles] = {}, my_ev[kTiles] = {};
       if constexpr (ROWS) {
         note = ahead;
         if (note.flags & kEnd) break;
-        my_ek = ek;
-        my_ev = ev;
+#pragma unroll
+        for (int z = 0; z < kTiles; ++z) {
+          my_ek[z] = ek[z];
+          my_ev[z] = ev[z];
+        }
         step(at_ahead);
         ahead = take(at_ahead);
         cp_async_wait<1>();
@@ -560,21 +580,33 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         if constexpr (kCodes) {
           if constexpr (!ROWS) {
             const unsigned char* e = smem + R::kScales + stage * R::kScaleBytes + e_at;
-            my_ek = exps_at(e);
-            my_ev = exps_at(e + lb * kG);
+#pragma unroll
+            for (int z = 0; z < kTiles; ++z) {
+              my_ek[z] = exps_at(e + z * next_exps);
+              my_ev[z] = exps_at(e + z * next_exps + lb * kG);
+            }
           }
           if constexpr (BITS == 8) {
-            tile_8<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, my_ek, my_ev, lo, hi, q, st);
+            tile_8<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, my_ek[0], my_ev[0], lo, hi, q, st);
           } else {
             Factors4<D>& fac = reinterpret_cast<Factors4<D>*>(smem + R::kFactors)[warp];
-            tile_4<D, NT, SPLIT>(sk + k_at, k_next, sv + v_at, my_ek, my_ev, fac, hi, q, st);
+#pragma unroll 1
+            for (int z = 0; z < kTiles && hi > 32 * z; ++z) {
+              const uint32_t rows = v_at + z * next_rows;
+              tile_4<D, NT, SPLIT>(sk + rows, sv + rows, z == 0 ? my_ek[0] : my_ek[kTiles - 1],
+                                   z == 0 ? my_ev[0] : my_ev[kTiles - 1], fac, hi - 32 * z, q, st);
+              __syncwarp();  // the factors have been read
+            }
           }
         } else {
           tile_16<Ty, D, NT, SPLIT>(sk + k_at, sv + v_at, lo, hi, q, st);
         }
       }
-      __syncwarp();
-      if (lane == 0 && a.stall_for_test == 0) tc::mbar_arrive(empty(stage));
+      auto release = [&]() {
+        __syncwarp();
+        if (lane == 0 && a.stall_for_test == 0) tc::mbar_arrive(empty(stage));
+      };
+      if (BITS != 4 || !(note.flags & kLast)) release();
       if (!(note.flags & kLast)) continue;
 
       // ---- segment end: join the states of the head's warps ---------------
@@ -594,18 +626,27 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       const int r8 = lane >> 2, tq = 2 * (lane & 3);
       const size_t row0 = static_cast<size_t>(note.s) * a.num_q_heads +
                           static_cast<size_t>(note.hg * Hc + hsub) * G;
-      for (int h0 = 0; h0 < G; h0 += kJoinHeads) {
-        if (!meet()) break;  // the area was read by the join before
-        float* mine_o = sJoin + warp * kJoinHeads * R::kOStride;
+      // Where warp w leaves row `at` of a round. 4-bit: in its own rows of the stage, which nobody
+      // reads any more, 8 of them (as many bytes as a row of O) for each head: all heads at once.
+      constexpr int kRound = BITS == 4 ? kMaxGroup : kJoinHeads;
+      auto o_at = [&](int w, int at) {
+        if constexpr (BITS == 4)
+          return reinterpret_cast<float*>(smem + R::template kFixed<ROWS> + stage * 2 * R::kHalf +
+                                          (at >> 3) * R::kHalf + eight_at((w & (Wh - 1)) * (kTT / 8) + (at & 7)));
+        else
+          return sJoin + (w * kJoinHeads + at) * R::kOStride;
+      };
+      for (int h0 = 0; h0 < G; h0 += kRound) {
+        if (BITS != 4 && !meet()) break;  // the area was read by the join before
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int head = nt * 8 + tq + c, at = head - h0;
-            if (at < 0 || at >= kJoinHeads || head >= G) continue;
+            if (at < 0 || at >= kRound || head >= G) continue;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
-              float* p = mine_o + at * R::kOStride;
+              float* p = o_at(warp, at);
               if constexpr (kCodes) {  // two neighbouring dims
                 *reinterpret_cast<float2*>(p + Geo::dim_of(mt, 0, r8)) =
                     make_float2(st.o[mt][nt][c], st.o[mt][nt][c + 2]);
@@ -618,11 +659,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               float* stat_w = sStats + warp * 3 * R::kHeads + head;
               stat_w[0] = st.fresh ? -INFINITY : st.m[nt][c];
               stat_w[R::kHeads] = st.l[nt][c];
-              if constexpr (kCodes) stat_w[2 * R::kHeads] = static_cast<float>(st.r);
+              if constexpr (kCodes) stat_w[2 * R::kHeads] = static_cast<float>(BITS == 4 ? st.r - 1 : st.r);
             }
           }
         if (!meet()) break;
-        const int heads = min(G - h0, kJoinHeads), w0 = warp - wsub;
+        const int heads = min(G - h0, kRound), w0 = warp - wsub;
         for (int i = wsub * 32 + lane; i < heads * (D / 4); i += Wh * 32) {
           const int at = i / (D / 4), c4 = i % (D / 4) * 4, head = h0 + at;
           auto stat = [&](int w, int which) { return sStats[(w * 3 + which) * R::kHeads + head]; };
@@ -645,8 +686,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             float fo = f;
             if constexpr (BITS == 8) fo = m == -INFINITY ? 0.f : ex2(order(w) - top);
             if constexpr (BITS == 4) fo = f * ex2(order(w) - top);
-            const float4 v =
-                *reinterpret_cast<const float4*>(sJoin + (w * kJoinHeads + at) * R::kOStride + c4);
+            const float4 v = *reinterpret_cast<const float4*>(o_at(w, at) + c4);
             l += f * stat(w, 1);
             acc.x += fo * v.x;
             acc.y += fo * v.y;
@@ -675,6 +715,11 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 make_uint2(Ty::pack(acc.x, acc.y), Ty::pack(acc.z, acc.w));
           }
         }
+      }
+      if constexpr (BITS == 4) {  // all have read: the stage may be filled again
+        meet();
+        tc::fence_async_smem();
+        release();
       }
     }
     if constexpr (ROWS) cp_async_wait<0>();

@@ -1,6 +1,7 @@
 // One warp's work on a tile of K/V rows in shared memory, for the streaming
 // decode kernel (decode_stream.cuh): scores, online softmax and weighted sum,
-// for 8-bit and 4-bit caches (tiles of 32 tokens) and 16-bit ones (16 tokens).
+// for 8-bit and 4-bit caches (tiles of 32 tokens, of which a 4-bit stage holds two for each
+// warp) and 16-bit ones (16 tokens).
 //
 // All take the tile as S^T = K q^T with the legacy m16n8k16 product (16 tokens
 // x 8 columns, a column for a query head), and O^T = V^T P^T with the same
@@ -43,15 +44,16 @@
 //
 // 4-bit caches. The factors belong to 32 dims of a row, so K's enter between the
 // products of one group and the next,
-//   y = sum_g (sum_{i in g} q_i k4_i) (2^(ek_g - 127) sl2),
+//   y = (sum_g (sum_{i in g} q_i k4_i) 2^(ek_g - 127)) sl2,
 // and V's multiply the weights once for each group: the group's rows of O get weights
-// p_t 2^(ev_tg - r), r the largest finite ev so far. The weights' two fp16 parts are made
-// once a tile (of p 2^7, below 2^15) and multiplied by 2^(ev_tg - r) in fp16, which is exact
-// down to 2^-25: 2^-20 of what a weight of 1 leaves there with the smallest factor that
-// goes this way, 2^-12 of the largest. Tiles with factors further below r (none in caches
-// of ordinary activations; a group of zeros has byte 0 and does not count), or with NaN,
-// go through bf16, whose range is fp32's: parts of p_t 2^(ev_tg - r) for every group, off by
-// 2^-17 of themselves, against V's codes as bf16. m is the running maximum of the scores.
+// p_t 2^(ev_tg - r + 1), r the largest finite ev so far. m lies 6 below the largest score, so
+// that weights p are 2^6 there, and below 2^14. Their two fp16 parts are made once a tile,
+// off by 2^-25, 2^-31 of the largest weight, and multiplied by 2^(ev_tg - r + 1) in fp16,
+// which is exact down to 2^-25: with the smallest factor that goes this way, 2^-15 of the
+// largest, 2^-17 of what the largest weight leaves. Tiles with factors further below r (none in
+// caches of ordinary activations; a group of zeros has byte 0 and does not count), or with NaN,
+// go through bf16, whose range is fp32's: parts of p_t 2^(ev_tg - r + 1) for every group, off
+// by 2^-17 of themselves, against V's codes as bf16.
 //
 // Fragment orders of 4-bit tiles. A 16-byte chunk is one group of 32 dims. For K a lane
 // gets eight neighbouring codes of one token, 8 t to 8 t + 7 of the chunk: four conversion
@@ -110,14 +112,14 @@ struct State {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
   }
-  // A tile's part of O, times f. The products of a tile start from zero and are added here: the tensor
+  // A tile's part of O. The products of a tile start from zero and are added here: the tensor
   // core cuts off what does not fit when it adds to its accumulator, and O, which grows with
   // the row, would lose half an ulp each time (6e-6 of 10 K tokens' sum).
-  __device__ __forceinline__ void add(int mt, const float (&x)[NT][4], float f = 1.f) {
+  __device__ __forceinline__ void add(int mt, const float (&x)[NT][4]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[mt][nt][e] = f == 1.f ? o[mt][nt][e] + x[nt][e] : fmaf(x[nt][e], f, o[mt][nt][e]);
+      for (int e = 0; e < 4; ++e) o[mt][nt][e] += x[nt][e];
   }
   // O columns times al.
   __device__ __forceinline__ void scale(const float (&al)[NT][2]) {
@@ -138,7 +140,7 @@ struct State {
     return v;
   }
   // Raises the references to the columns' maxima, of which mx are this lane's, where any
-  // has been passed by kRaiseAt. 16-bit and 4-bit caches: mx of the scores. 8-bit (WEIGHTED):
+  // has been passed by kRaiseAt. 16-bit caches: mx of the scores. 8-bit (WEIGHTED):
   // of the weighted rows y + ev - r.
   template <bool WEIGHTED>
   __device__ __forceinline__ void raise(const float (&mx)[NT][2]) {
@@ -159,6 +161,21 @@ struct State {
         const float f = ex2(m[nt][c] - mn);  // l and O are zero where nothing was added yet
         l[nt][c] *= f;
         al[nt][c] = f;
+        m[nt][c] = mn;
+      }
+    if (!fresh) scale(al);
+    fresh = false;
+  }
+  // 4-bit: the references to the largest mx of their columns.
+  __device__ __forceinline__ void raise_to(const float (&mx)[NT][2]) {
+    float al[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float mn = fmaxf(m[nt][c], column_max(mx[nt][c]));
+        al[nt][c] = ex2(m[nt][c] - mn);  // l and O are zero where nothing was added yet
+        l[nt][c] *= al[nt][c];
         m[nt][c] = mn;
       }
     if (!fresh) scale(al);
@@ -200,7 +217,7 @@ struct State {
 // every ldmatrix phase then fall in distinct banks.
 template <int D, int BITS>
 struct Tile {
-  static constexpr int kTokens = BITS == 16 ? 16 : 32;
+  static constexpr int kTokens = BITS == 16 ? 16 : BITS == 8 ? 32 : 64;  // of a warp in a stage
   static constexpr int kRowBytes = D * BITS / 8;
   static constexpr int kGroups = BITS == 16 ? 0 : BITS == 8 ? 1 : D / kFp4Group;  // exponent bytes of a row
   static constexpr int kSlice = kRowBytes < 128 ? kRowBytes : 128;
@@ -414,58 +431,76 @@ struct Factors4 {
   float k[32][kG];
   uint32_t v[4][kG * 4 + 4];  // [t][g * 4 + i]; padded so that the writes of two t fall in other banks
 };
-constexpr int kTame = 12;  // binary orders below r within which factors multiply fp16 weights
+constexpr int kTame = 15;  // binary orders below r within which factors multiply fp16 weights
+constexpr float kShift4 = 6.f;
 
-// 4-bit tile: as tile_8, with the exponent bytes of token `lane` in ek and ev.
+// 4-bit tile. sk, sv: the groups of K and V rows that this lane's addresses for ldmatrix lie in
+// (tokens 0-7, 8-15, 16-23 or 24-31 of the tile: lane & 24); ek, ev: exponent bytes of token
+// `lane`; tokens 0 .. hi - 1 count (the others' V rows are zero).
 template <int D, int NT, bool SPLIT>
-__device__ __forceinline__ void tile_4(uint32_t sk, uint32_t k_next, uint32_t sv, uint32_t ek, uint32_t ev,
+__device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, uint32_t ev,
                                        Factors4<D>& fac, int hi, const Query<D, NT>& q, State<D, NT>& st) {
   using Geo = Tile<D, 4>;
+  constexpr int kTokens = 32;  // half of the warp's in a stage
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int kG = Geo::kGroups;
   const int lane = threadIdx.x & 31, r8 = lane >> 2, t = lane & 3;
-  const int mi = lane >> 3, rr = lane & 7;
-  const bool edge = hi < Geo::kTokens;
-  if (edge && lane >= hi) ev = 0;
+  const int rr = lane & 7;
+  const bool edge = hi < kTokens;
+  if (edge && lane >= hi) ev = static_cast<uint32_t>(st.r) * 0x01010101u;
 
-  // the largest and the smallest factor of V that count
-  int top = 0;
-  unsigned low = ~0u;
+  // V's factors over 2^(r - 1) as fp16, two to a register. One vote says that all lie in
+  // [r - 15, r], and K's below 2^65, where no sum of a row's products overflows before it meets
+  // the query's factor; otherwise the bytes are looked at one by one.
+  bool wild = false;
+  float unit = 1.f;  // of K's factors
+  uint32_t f[kG / 2], out_of_range = 0;
 #pragma unroll
-  for (int g = 0; g < kG; ++g) {
-    const unsigned b = ev >> (8 * g) & 255u;
-    top = max(top, static_cast<int>(b));
-    low = min(low, b - 1u);  // 0 does not count
+  for (int k = 0; k < kG / 2; ++k) {
+    const uint32_t e = __byte_perm(ev, 0, k == 0 ? 0x4140 : 0x4342);
+    out_of_range |= e + static_cast<uint32_t>((15 - st.r) * 65537);
+    f[k] = e * 1024u + static_cast<uint32_t>((16 - st.r) * 65537) * 1024u;
   }
-  top = __reduce_max_sync(kAll, top);
-  low = __reduce_min_sync(kAll, low);
-  bool wild = top == 255;
-  if (wild) {  // NaN: the largest finite one
-    top = 0;
+  if (__any_sync(kAll, (out_of_range & 0xfff0fff0u) != 0 || (ek & ek << 1 & 0x80808080u) != 0)) {
+    if (__any_sync(kAll, (ek & ek << 1 & 0x80808080u) != 0)) unit = 0x1p64f;
+    int top = 0;
+    unsigned low = ~0u;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       const int b = static_cast<int>(ev >> (8 * g) & 255u);
+      wild |= b == 255;
       top = max(top, b == 255 ? 0 : b);
+      low = min(low, static_cast<unsigned>(b) - 1u);  // 0 does not count
     }
-    top = __reduce_max_sync(kAll, top);
-  }
-  top = max(top, st.r);
-  wild |= low < static_cast<unsigned>(max(top - kTame - 1, 0));
-  st.follow_plain(top);
-
-  {
-    float f[kG];
+    top = max(__reduce_max_sync(kAll, top), st.r);
+    low = __reduce_min_sync(kAll, low);
+    wild = __any_sync(kAll, wild) || low < static_cast<unsigned>(max(top - kTame - 1, 0));
+    st.follow_plain(top);
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      f[g] = exponent_factor(static_cast<int>(ek >> (8 * g) & 255u));
-      const int e = static_cast<int>(ev >> (8 * g) & 255u);
-      reinterpret_cast<uint16_t*>(&fac.v[(lane & 7) >> 1][g * 4 + (lane >> 3)])[lane & 1] =
-          static_cast<uint16_t>(max(e - top + 15, 0) << 10);
+      const int b = static_cast<int>(ev >> (8 * g) & 255u);
+      const uint32_t h = b == 0 ? 0u : static_cast<uint32_t>(max(b - top + 16, 0) << 10) & 0xffffu;
+      f[g >> 1] = (g & 1) != 0 ? f[g >> 1] | h << 16 : h;
+    }
+  }
+
+  // factors change hands
+#pragma unroll
+  for (int g = 0; g < kG; ++g)
+    reinterpret_cast<uint16_t*>(&fac.v[(lane & 7) >> 1][g * 4 + (lane >> 3)])[lane & 1] =
+        static_cast<uint16_t>((g & 1) != 0 ? f[g >> 1] >> 16 : f[g >> 1]);
+  {
+    float fk[kG];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) fk[g] = exponent_factor(static_cast<int>(ek >> (8 * g) & 255u));
+    if (unit != 1.f) {
+#pragma unroll
+      for (int g = 0; g < kG; ++g) fk[g] *= 0x1p-64f;
     }
     if constexpr (kG == 4)
-      *reinterpret_cast<float4*>(fac.k[lane]) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(fac.k[lane]) = make_float4(fk[0], fk[1], fk[2], fk[3]);
     else
-      *reinterpret_cast<float2*>(fac.k[lane]) = make_float2(f[0], f[1]);
+      *reinterpret_cast<float2*>(fac.k[lane]) = make_float2(fk[0], fk[1]);
   }
   __syncwarp();
 
@@ -484,50 +519,70 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t k_next, uint32_t sv
       fk[i][1] = f.y;
     }
   }
+  // A group's products are under way while the one before it is added up.
+  float sc[2][2][NT][4];  // [group & 1][tokens 0-15, 16-31]
+  auto add_scores = [&](int g) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 2 * hf + (e >> 1);
+          x[nt][i][e & 1] = g == 0 ? sc[0][hf][nt][e] * fk[i][0]
+                                   : fmaf(sc[g & 1][hf][nt][e], fk[i][g], x[nt][i][e & 1]);
+        }
+  };
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    uint32_t k[4], p[4][4];  // tokens 0-7, 8-15, 16-23, 24-31
+    ldmatrix_x4(k, sk + Geo::in_group(rr, g));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e2m1x8_to_f16x2(k[i], p[i]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t a[4] = {p[2 * hf][2 * c], p[2 * hf + 1][2 * c], p[2 * hf][2 * c + 1], p[2 * hf + 1][2 * c + 1]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          c == 0 ? F16::mma0(sc[g & 1][hf][nt], a, q.b[2 * g][nt][0], q.b[2 * g][nt][1])
+                 : F16::mma(sc[g & 1][hf][nt], a, q.b[2 * g + 1][nt][0], q.b[2 * g + 1][nt][1]);
+      }
+    if (g > 0) add_scores(g - 1);
+  }
+  add_scores(kG - 1);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[nt][i][0] = x[nt][i][1] = 0.f;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int kp = 0; kp < kG / 2; ++kp) {
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      uint32_t k[4];  // tokens 0-7, 8-15 of group 2 kp, then of the next
-      ldmatrix_x4(k, sk + hf * k_next + Geo::in_group(rr, 2 * kp + (mi >> 1)));
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int g = 2 * kp + c;
-        uint32_t p[4], s[4];
-        e2m1x8_to_f16x2(k[2 * c], p);
-        e2m1x8_to_f16x2(k[2 * c + 1], s);
-        const uint32_t a0[4] = {p[0], s[0], p[1], s[1]}, a1[4] = {p[2], s[2], p[3], s[3]};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float sc[4] = {};
-          F16::mma(sc, a0, q.b[2 * g][nt][0], q.b[2 * g][nt][1]);
-          F16::mma(sc, a1, q.b[2 * g + 1][nt][0], q.b[2 * g + 1][nt][1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)  // the two factors first, as for 8 bits
-            x[nt][2 * hf + (e >> 1)][e & 1] =
-                fmaf(sc[e], fk[2 * hf + (e >> 1)][g] * q.sl2[nt][e & 1], x[nt][2 * hf + (e >> 1)][e & 1]);
-        }
-      }
-    }
-  }
+      for (int c = 0; c < 2; ++c) x[nt][i][c] = __fmul_rn(x[nt][i][c], q.sl2[nt][c] * unit);
 
-  float mx[NT][2];
+  if (edge) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    if (edge) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (r8 + 8 * i >= hi) x[nt][i][0] = x[nt][i][1] = -INFINITY;
-    }
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      mx[nt][c] = fmaxf(fmaxf(x[nt][0][c], x[nt][1][c]), fmaxf(x[nt][2][c], x[nt][3][c]));
   }
-  st.template raise<false>(mx);
+  // the reference lies kShift4 below the largest score, so that weights reach 2^6, and 2^14
+  // before it is raised
+  float most = -INFINITY;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      most = fmaxf(most, fmaxf(x[nt][i][0] - st.m[nt][0], x[nt][i][1] - st.m[nt][1]));
+  if (__any_sync(kAll, st.fresh || most > kShift4 + kRaiseAt)) {
+    float mx[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        mx[nt][c] = fmaxf(fmaxf(x[nt][0][c], x[nt][1][c]), fmaxf(x[nt][2][c], x[nt][3][c])) - kShift4;
+    st.raise_to(mx);
+  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -568,30 +623,35 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t k_next, uint32_t sv
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        weight_parts<F16, SPLIT>(x[nt][i][0] * 128.f, x[nt][i][1] * 128.f, rest, ph[i][nt], pl[i][nt]);
+        weight_parts<F16, SPLIT>(x[nt][i][0], x[nt][i][1], rest, ph[i][nt], pl[i][nt]);
+    float o[2][2][NT][4];  // [group & 1][m-tile]
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       uint32_t a[2][2][4];
       value(g, a);
       const uint4 fv = *reinterpret_cast<const uint4*>(&fac.v[t][g * 4]);
-      const uint32_t f[4] = {fv.x, fv.y, fv.z, fv.w};
-      float o[2][NT][4] = {};
+      const uint32_t fg[4] = {fv.x, fv.y, fv.z, fv.w};
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint32_t b0 = F16::mul(ph[2 * hf][nt], f[2 * hf]), b1 = F16::mul(ph[2 * hf + 1][nt], f[2 * hf + 1]);
+          const uint32_t b0 = F16::mul(ph[2 * hf][nt], fg[2 * hf]), b1 = F16::mul(ph[2 * hf + 1][nt], fg[2 * hf + 1]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) F16::mma(o[h][nt], a[hf][h], b0, b1);
+          for (int h = 0; h < 2; ++h)
+            hf == 0 ? F16::mma0(o[g & 1][h][nt], a[hf][h], b0, b1) : F16::mma(o[g & 1][h][nt], a[hf][h], b0, b1);
           if constexpr (!SPLIT) {
-            const uint32_t c0 = F16::mul(pl[2 * hf][nt], f[2 * hf]), c1 = F16::mul(pl[2 * hf + 1][nt], f[2 * hf + 1]);
+            const uint32_t c0 = F16::mul(pl[2 * hf][nt], fg[2 * hf]), c1 = F16::mul(pl[2 * hf + 1][nt], fg[2 * hf + 1]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) F16::mma(o[h][nt], a[hf][h], c0, c1);
+            for (int h = 0; h < 2; ++h) F16::mma(o[g & 1][h][nt], a[hf][h], c0, c1);
           }
         }
+      if (g > 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) st.add(2 * g + h, o[h], 1.f / 128.f);
+        for (int h = 0; h < 2; ++h) st.add(2 * g - 2 + h, o[(g - 1) & 1][h]);
+      }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) st.add(2 * kG - 2 + h, o[(kG - 1) & 1][h]);
     return;
   }
   uint32_t evs[4];
@@ -613,7 +673,7 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t k_next, uint32_t sv
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = static_cast<int>(evs[i] >> (8 * g) & 255u);
-      const float f = exponent_factor(e == 255 ? 255 : e == 0 ? 0 : max(e - top + 127, 0));
+      const float f = exponent_factor(e == 255 ? 255 : e == 0 ? 0 : max(e - st.r + 128, 0));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         weight_parts<BF16, SPLIT>(x[nt][i][0] * f, x[nt][i][1] * f, rest, bh[i][nt], bl[i][nt]);

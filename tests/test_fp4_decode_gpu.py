@@ -15,14 +15,16 @@ from test_fp4_cache_gpu import random_pool, tables_for, up
 
 pytestmark = pytest.mark.gpu
 
-# Weights' two parts. V's factors within 2^12 of each other: fp16, off by 2^-20 of themselves, or
-# 2^-32 of the largest weight times the largest factor: over n tokens n 2^-32 of the largest value
-# (the sum of weights is at least the largest), 2^(2 spread) times that of a group's. Otherwise bf16.
+# Weights' two parts. V's factors within 2^15 of the largest: fp16 parts of weights that are at least 2^6
+# at the top, off by 2^-22 of themselves or 2^-25, 2^-31 of the largest weight; multiplied by the factor over
+# half the largest, 2^(1 - 2 spread) or more, they are off by 2^-25 again, 2^(2 spread - 32) of what the largest
+# weight leaves there. Over n tokens that is n times as much of the largest value (the sum of weights is at
+# least the largest one). Otherwise the parts are bf16.
 FAR = 2.0 ** -17
 
 
 def weight_error(n, spread):
-    return 2.0 ** -20 + n * 2.0 ** (2 * spread - 32) if 2 * spread <= 12 else FAR
+    return 2.0 ** -20 + n * (2.0 ** -31 + 2.0 ** (2 * spread - 32)) if 2 * spread <= 12 else FAR
 
 
 @pytest.fixture(scope="module", autouse=True)
