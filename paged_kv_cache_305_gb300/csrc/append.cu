@@ -20,8 +20,8 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 1024;     // of a CTA, or
+constexpr int kFewThreads = 256;   // where sequences and rows are no more
 constexpr unsigned kFull = 0xffffffffu;
 
 enum : int { kNoBlocks = 1, kOutOfRange = 2 };
@@ -32,9 +32,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   extern __shared__ int smem[];
   int* before = smem;                 // [S] new blocks of the sequences before
   int* starts = smem + a.num_seqs;    // [S + 1]
-  __shared__ long long warp_sum[kWarps];
+  __shared__ long long warp_sum[kThreads / 32];
   __shared__ int wrong;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  if (!COMMIT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int S = a.num_seqs, shift = a.block_shift, mask = (1 << shift) - 1;
   const long long most = static_cast<long long>(a.max_blocks_per_seq) << shift;
   auto held = [&](long long n) { return static_cast<int>((n + mask) >> shift); };
@@ -43,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
 
   const int avail = *a.num_free;
   // a run of sequences for each thread; sums of a run, of a warp's runs, of all
-  const int per = (S + kThreads - 1) / kThreads, s0 = min(tid * per, S), s1 = min(s0 + per, S);
+  const int per = (S + threads - 1) / threads, s0 = min(tid * per, S), s1 = min(s0 + per, S);
   long long mine = 0;
   bool bad = avail < 0 || avail > a.free_capacity;
   for (int s = s0; s < s1; ++s) {
@@ -68,8 +69,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
   long long base = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < threads >> 5; ++w) {
     if (w < warp) base += warp_sum[w];
     total += warp_sum[w];
   }
@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
 
   if constexpr (ROWS) {
     const int first = S > 0 ? starts[0] : 0, end = S > 0 ? starts[S] : 0;
-    for (long long row = static_cast<long long>(blockIdx.x) * kThreads + tid; row < a.rows;
-         row += static_cast<long long>(gridDim.x) * kThreads) {
+    for (long long row = static_cast<long long>(blockIdx.x) * threads + tid; row < a.rows;
+         row += static_cast<long long>(gridDim.x) * threads) {
       long long slot = -1, position = 0;
       if (code == 0 && row >= first && row < end) {
         int s = 0, n = S;  // the last sequence that starts at or before the row
@@ -115,8 +115,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     }
   }
   if constexpr (COMMIT) {
-    __syncthreads();  // lengths may be written over those that were read
-    for (int s = tid; s < S; s += kThreads)
+    // lengths may be written over those that were read, by this CTA or by the launch before
+    if (ROWS) __syncthreads();
+    else asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int s = tid; s < S; s += threads)
       a.new_lens[s] = a.seq_lens[s] + (code == 0 ? starts[s + 1] - starts[s] : 0);
     if (tid == 0) {
       *a.new_free = code == 0 ? avail - static_cast<int>(total) : avail;
@@ -127,7 +129,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
 
 template <bool ROWS, bool COMMIT>
 cudaError_t launch(const AppendArgs& a, int ctas, cudaStream_t stream) {
-  const int smem = (2 * a.num_seqs + 1) * static_cast<int>(sizeof(int));
   auto kern = append_kernel<ROWS, COMMIT>;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = once_per_context(done, [&] {
@@ -135,8 +136,17 @@ cudaError_t launch(const AppendArgs& a, int ctas, cudaStream_t stream) {
                                 (2 * kAppendMaxSeqs + 1) * static_cast<int>(sizeof(int)));
   });
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(a.num_seqs <= kFewThreads && a.rows <= kFewThreads ? kFewThreads : kThreads);
+  cfg.dynamicSmemBytes = (2 * a.num_seqs + 1) * sizeof(int);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];  // the second launch takes its sums while the first writes rows
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = COMMIT && !ROWS ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace

@@ -29,8 +29,9 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 8;  // of a token
+constexpr long long kManyWarps = 152 * 6;
+constexpr int kBatch = 6;     // rounds of rows whose loads are under way together
 constexpr unsigned kFull = 0xffffffffu;
 
 template <typename Ty>
@@ -49,17 +50,13 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 }
 
 template <typename Ty, int D, bool INTERLEAVED, bool NORM, bool CACHE>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs a, int warps_per_token) {
+__global__ void __launch_bounds__(kMaxWarps * 32) rotate_kernel(const RotateArgs a) {
   using T = typename Ty::T;
   constexpr int kLanes = D / 16;        // of a row
   constexpr int kRows = 32 / kLanes;    // of a warp at a time
-  __shared__ float2 turns[kWarps][D / 2];  // [token of the CTA][pair]: cos, sin
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tokens = kWarps / warps_per_token;  // of the CTA
-  const long long t0 = static_cast<long long>(blockIdx.x) * tokens;
-  const int mine = warp / warps_per_token;
-  const long long t = t0 + mine;
-  const bool here = t < a.num_tokens;
+  __shared__ float2 turns[D / 2];  // of the pairs: cos, sin
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const long long t = blockIdx.x;
   const int n = a.rotary_dim / 2, Hq = a.num_q_heads, Hkv = a.num_kv_heads;
 
   // this lane's vectors of a row, and whether they are rotated
@@ -80,15 +77,15 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs a, in
 
   long long slot = -1;
   if constexpr (CACHE) {
-    if (here) slot = a.slot_mapping[t];
+    slot = a.slot_mapping[t];
     if (slot >= a.num_slots) {
-      if (lane == 0 && warp % warps_per_token == 0) atomicAdd(a.bad, 1ull);
+      if (threadIdx.x == 0) atomicAdd(a.bad, 1ull);
       slot = -1;
     }
   }
-  const int rows = here ? Hq + (CACHE ? (slot >= 0 ? 2 * Hkv : 0) : Hkv) : 0;
-  const int step = warps_per_token * kRows;
-  int row = (warp % warps_per_token) * kRows + lane / kLanes;
+  const int rows = Hq + (CACHE ? (slot >= 0 ? 2 * Hkv : 0) : Hkv);
+  const int step = warps * kRows;
+  int row = warp * kRows + lane / kLanes;
   auto from = [&](int r) {
     if (r < Hq) return static_cast<const T*>(a.query) + t * a.query_stride + static_cast<long long>(r) * D;
     if (r < Hq + Hkv) return static_cast<const T*>(a.key) + t * a.key_stride + static_cast<long long>(r - Hq) * D;
@@ -102,94 +99,99 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs a, in
                    : static_cast<T*>(a.value_cache) + (slot * Hkv + h - Hkv) * D;
   };
   // plain loads: the rows may be written in place
-  uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va;
-  auto load = [&](int r) {
-    if (r >= rows) return;
-    const T* p = from(r);
-    va = *reinterpret_cast<const uint4*>(p + oa);
-    vb = *reinterpret_cast<const uint4*>(p + ob);
+  uint4 va[kBatch] = {}, vb[kBatch] = {};
+  auto load = [&]() {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (row + k * step >= rows) return;
+      const T* p = from(row + k * step);
+      va[k] = *reinterpret_cast<const uint4*>(p + oa);
+      vb[k] = *reinterpret_cast<const uint4*>(p + ob);
+    }
   };
-  load(row);
+  load();
 
-  for (int i = threadIdx.x; i < tokens * n; i += kThreads) {
-    const int at = i / n, pair = i % n;
-    if (t0 + at >= a.num_tokens) break;
-    const unsigned long long phase = static_cast<unsigned long long>(a.positions[t0 + at]) * a.frequencies[pair];
+  for (int pair = threadIdx.x; pair < n; pair += blockDim.x) {
+    const unsigned long long phase = static_cast<unsigned long long>(a.positions[t]) * a.frequencies[pair];
     float s, c;
     sincospif(__ll2float_rn(static_cast<long long>(phase)) * 0x1p-63f, &s, &c);
-    turns[at][pair] = make_float2(c * a.factor, s * a.factor);
+    turns[pair] = make_float2(c * a.factor, s * a.factor);
   }
   __syncthreads();
   float2 cs[8];  // of the lane's pairs
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int pair = INTERLEAVED ? (i < 4 ? oa : ob) / 2 + (i & 3) : 8 * j + i;
-    cs[i] = (i < 4 || !INTERLEAVED ? rot_a : rot_b) ? turns[mine][pair] : make_float2(1.f, 0.f);
+    cs[i] = (i < 4 || !INTERLEAVED ? rot_a : rot_b) ? turns[pair] : make_float2(1.f, 0.f);
   }
 
   // rows of all lanes of the warp: they meet in shuffles
-  const int rounds = (rows - (warp % warps_per_token) * kRows + step - 1) / step;
-  for (int k = 0; k < rounds; ++k, row += step) {
-    uint4 wa = va, wb = vb;
-    load(row + step);
-    const bool live = row < rows;
-    if (!CACHE || row < Hq + Hkv || NORM) {  // with norms all lanes meet
-      float x[16];
-      unpack8<Ty>(wa, x);
-      unpack8<Ty>(wb, x + 8);
-      if constexpr (NORM) {
-        auto squares = [&](float f) {
-          float ss = 0.f;
+  const int rounds = (rows - warp * kRows + step - 1) / step;
+  for (int k0 = 0; k0 < rounds; k0 += kBatch) {
+    if (k0 > 0) load();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) ss = fmaf(x[i] * f, x[i] * f, ss);
+    for (int k = 0; k < kBatch; ++k, row += step) {
+      if (k0 + k >= rounds) break;
+      uint4 wa = va[k], wb = vb[k];
+      const bool live = row < rows;
+      if (!CACHE || row < Hq + Hkv || NORM) {  // with norms all lanes meet
+        float x[16];
+        unpack8<Ty>(wa, x);
+        unpack8<Ty>(wb, x + 8);
+        if constexpr (NORM) {
+          auto squares = [&](float f) {
+            float ss = 0.f;
 #pragma unroll
-          for (int off = 1; off < kLanes; off <<= 1) ss += __shfl_xor_sync(kFull, ss, off);
-          return ss;
-        };
-        const float ss = squares(1.f);
-        float inv = rsqrtf(ss * (1.f / D) + a.eps);
-        if (__any_sync(kFull, ss == INFINITY)) {  // squares out of range: the norm of x 2^-80, where eps is nothing
-          const float small = rsqrtf(squares(0x1p-80f) * (1.f / D));
-          if (ss == INFINITY) {
-            inv = small;
+            for (int i = 0; i < 16; ++i) ss = fmaf(x[i] * f, x[i] * f, ss);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= 0x1p-80f;
+            for (int off = 1; off < kLanes; off <<= 1) ss += __shfl_xor_sync(kFull, ss, off);
+            return ss;
+          };
+          const float ss = squares(1.f);
+          float inv = rsqrtf(ss * (1.f / D) + a.eps);
+          if (__any_sync(kFull, ss == INFINITY)) {  // squares out of range: the norm of x 2^-80, where eps is nothing
+            const float small = rsqrtf(squares(0x1p-80f) * (1.f / D));
+            if (ss == INFINITY) {
+              inv = small;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] *= 0x1p-80f;
+            }
+          }
+          if (row < Hq + Hkv) {
+            const T* w = static_cast<const T*>(row < Hq ? a.query_weight : a.key_weight);
+            float f[16];
+            unpack8<Ty>(__ldg(reinterpret_cast<const uint4*>(w + oa)), f);
+            unpack8<Ty>(__ldg(reinterpret_cast<const uint4*>(w + ob)), f + 8);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * f[i];
           }
         }
-        if (row < Hq + Hkv) {
-          const T* w = static_cast<const T*>(row < Hq ? a.query_weight : a.key_weight);
-          float f[16];
-          unpack8<Ty>(__ldg(reinterpret_cast<const uint4*>(w + oa)), f);
-          unpack8<Ty>(__ldg(reinterpret_cast<const uint4*>(w + ob)), f + 8);
+        auto turn = [&](float& p, float& q, const float2& z) {
+          const float u = p * z.x - q * z.y;
+          q = q * z.x + p * z.y;
+          p = u;
+        };
+        if constexpr (INTERLEAVED) {
+          if (rot_a)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * f[i];
+            for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], cs[i]);
+          if (rot_b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) turn(x[8 + 2 * i], x[9 + 2 * i], cs[4 + i]);
+        } else if (rot_a) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], cs[i]);
+        }
+        if (!CACHE || row < Hq + Hkv) {  // V's rows stay as they are
+          wa = pack8<Ty>(x);
+          wb = pack8<Ty>(x + 8);
         }
       }
-      auto turn = [&](float& p, float& q, const float2& z) {
-        const float u = p * z.x - q * z.y;
-        q = q * z.x + p * z.y;
-        p = u;
-      };
-      if constexpr (INTERLEAVED) {
-        if (rot_a)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], cs[i]);
-        if (rot_b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) turn(x[8 + 2 * i], x[9 + 2 * i], cs[4 + i]);
-      } else if (rot_a) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], cs[i]);
+      if (live) {
+        T* p = into(row);
+        *reinterpret_cast<uint4*>(p + oa) = wa;
+        *reinterpret_cast<uint4*>(p + ob) = wb;
       }
-      if (!CACHE || row < Hq + Hkv) {  // V's rows stay as they are
-        wa = pack8<Ty>(x);
-        wb = pack8<Ty>(x + 8);
-      }
-    }
-    if (live) {
-      T* p = into(row);
-      *reinterpret_cast<uint4*>(p + oa) = wa;
-      *reinterpret_cast<uint4*>(p + ob) = wb;
     }
   }
 }
@@ -198,12 +200,12 @@ template <typename Ty, int D, bool INTERLEAVED>
 cudaError_t launch(const RotateArgs& a, cudaStream_t stream) {
   const bool cache = a.key_out == nullptr, norm = a.query_weight != nullptr;
   const int rows = a.num_q_heads + (cache ? 2 : 1) * a.num_kv_heads, at_a_time = 32 / (D / 16);
-  // as many warps as leave each of them three rounds of rows
+  // One warp for a token, which goes its way without waiting for others, where there are tokens
+  // enough to fill the SMs; otherwise as many as leave each of them a round of rows.
   int warps = 1;
-  while (warps < kWarps && (rows + warps * at_a_time - 1) / (warps * at_a_time) > 3) warps *= 2;
-  const long long tokens = kWarps / warps, ctas = (a.num_tokens + tokens - 1) / tokens;
+  while (static_cast<long long>(a.num_tokens) * warps < kManyWarps && warps < kMaxWarps && warps * at_a_time < rows) warps *= 2;
   auto go = [&](auto kern) {
-    kern<<<static_cast<unsigned>(ctas), kThreads, 0, stream>>>(a, warps);
+    kern<<<static_cast<unsigned>(a.num_tokens), 32 * warps, 0, stream>>>(a);
     return cudaGetLastError();
   };
   if (norm) return cache ? go(rotate_kernel<Ty, D, INTERLEAVED, true, true>) : go(rotate_kernel<Ty, D, INTERLEAVED, true, false>);

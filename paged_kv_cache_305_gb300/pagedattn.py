@@ -189,52 +189,61 @@ def reshape_and_cache(key: torch.Tensor, value: torch.Tensor, key_cache: torch.T
                                       B, NB, _dtype_code(key), _stream(key, stream)))
 
 
-def _need_rows(t: torch.Tensor, name: str, tokens: int, heads: int, head_dim: int, dtype, device: int) -> int:
-    """Checks [tokens, heads, head_dim] rows whose tokens may lie apart; returns the stride of a token."""
-    _need(t.shape == (tokens, heads, head_dim) and t.dtype == dtype, f"{name} dtype or shape mismatch")
-    _need(t.get_device() == device, "tensors must be on one device")
+def _token_stride(t: torch.Tensor, name: str, shape: torch.Size, dtype, device: int) -> int:
+    """The stride of a token of rows [tokens, heads, head_dim], whose tokens may lie apart."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} dtype or shape mismatch")
+    if t.get_device() != device:
+        raise ValueError("tensors must be on one device")
     far, head, one = t.stride()
-    _need((one == 1 or head_dim == 1) and (head == head_dim or heads == 1),
-          f"the heads of a token of {name} must be contiguous")
-    return far if tokens > 1 else max(far, heads * head_dim)
+    _, heads, head_dim = shape
+    if one != 1 or (head != head_dim and heads != 1):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return far if far >= heads * head_dim or shape[0] > 1 else heads * head_dim
 
 
 def _rotate(cache, query_out, key_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
             frequencies, interleaved, factor, query_weight, key_weight, eps, stream):
-    _need(query.dim() == 3 and key.dim() == 3, "query and key must be [num_tokens, heads, head_dim]")
-    T, Hq, d = query.shape
-    Hkv = key.shape[1]
-    _need((query_weight is None) == (key_weight is None), "query_weight and key_weight: both or neither")
-    others = [positions, frequencies]
-    if query_weight is not None:
-        _need(query_weight.shape == key_weight.shape == (d,) and query_weight.dtype == key_weight.dtype == query.dtype,
-              "query_weight and key_weight must be [head_dim] of query's dtype")
-        others += [query_weight, key_weight]
-    _need(positions.dtype == torch.int64 and positions.shape == (T,), "positions must be int64 [num_tokens]")
-    _need(frequencies.dtype == torch.int64 and frequencies.dim() == 1, "frequencies must be int64 [rotary_dim / 2]")
-    if cache:
-        others += [key_cache, value_cache, slot_mapping]
-    device = _device_of(*others)
-    q_far = _need_rows(query, "query", T, Hq, d, query.dtype, device)
-    qo_far = _need_rows(query_out, "query_out", T, Hq, d, query.dtype, device)
-    k_far = _need_rows(key, "key", T, Hkv, d, query.dtype, device)
-    weights = (query_weight.data_ptr(), key_weight.data_ptr()) if query_weight is not None else (0, 0)
-    turn = 2 * frequencies.shape[0], int(bool(interleaved)), float(factor), float(eps)
+    q_shape, k_shape, dtype = query.shape, key.shape, query.dtype
+    if len(q_shape) != 3 or len(k_shape) != 3 or k_shape[0] != q_shape[0] or k_shape[2] != q_shape[2]:
+        raise ValueError("query and key must be [num_tokens, heads, head_dim]")
+    T, Hq, d = q_shape
+    Hkv = k_shape[1]
+    if positions.dtype != torch.int64 or positions.shape != (T,):
+        raise ValueError("positions must be int64 [num_tokens]")
+    n = frequencies.shape
+    if frequencies.dtype != torch.int64 or len(n) != 1:
+        raise ValueError("frequencies must be int64 [rotary_dim / 2]")
+    others = (key_cache, value_cache, slot_mapping) if cache else ()
+    weights = (0, 0)
+    if query_weight is not None or key_weight is not None:
+        if query_weight is None or key_weight is None:
+            raise ValueError("query_weight and key_weight: both or neither")
+        if not (query_weight.shape == key_weight.shape == (d,) and query_weight.dtype == key_weight.dtype == dtype):
+            raise ValueError("query_weight and key_weight must be [head_dim] of query's dtype")
+        weights = query_weight.data_ptr(), key_weight.data_ptr()
+        others += query_weight, key_weight
+    device = _device_of(positions, frequencies, *others)
+    q_far = _token_stride(query, "query", q_shape, dtype, device)
+    qo_far = _token_stride(query_out, "query_out", q_shape, dtype, device)
+    k_far = _token_stride(key, "key", k_shape, dtype, device)
     code = _dtype_code(query)
     if not cache:
-        ko_far = _need_rows(key_out, "key_out", T, Hkv, d, query.dtype, device)
+        ko_far = _token_stride(key_out, "key_out", k_shape, dtype, device)
         _enqueue(load_library().pa_rotate, device, stream, query_out.data_ptr(), key_out.data_ptr(),
                  query.data_ptr(), key.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), *weights,
-                 T, Hq, Hkv, d, *turn, qo_far, ko_far, q_far, k_far, code)
+                 T, Hq, Hkv, d, 2 * n[0], 1 if interleaved else 0, factor, eps, qo_far, ko_far, q_far, k_far, code)
         return
-    v_far = _need_rows(value, "value", T, Hkv, d, query.dtype, device)
-    _need(key_cache.dim() == 4 and key_cache.shape[2:] == (Hkv, d) and value_cache.shape == key_cache.shape
-          and key_cache.dtype == value_cache.dtype == query.dtype, "cache dtype or shape mismatch")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,), "slot_mapping must be int64 [num_tokens]")
+    v_far = _token_stride(value, "value", k_shape, dtype, device)
+    NB, B, *row = key_cache.shape
+    if row != [Hkv, d] or value_cache.shape != key_cache.shape or not key_cache.dtype == value_cache.dtype == dtype:
+        raise ValueError("cache dtype or shape mismatch")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
     _enqueue(load_library().pa_rotate_and_cache, device, stream, query_out.data_ptr(), query.data_ptr(),
              key.data_ptr(), value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
              slot_mapping.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), *weights, T, Hq, Hkv, d,
-             key_cache.shape[1], key_cache.shape[0], *turn, qo_far, q_far, k_far, v_far, code)
+             B, NB, 2 * n[0], 1 if interleaved else 0, factor, eps, qo_far, q_far, k_far, v_far, code)
 
 
 def rotate(query_out: torch.Tensor, key_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -278,22 +287,30 @@ def append_tokens(new_lens: torch.Tensor, new_free: torch.Tensor, slot_mapping: 
     what is there afterwards. Where the step does not fit nothing changes, all slots are -1 and
     ``status`` (int32 [1]) is raised to 1 (too few blocks) or 2 (lengths or starts out of range).
     """
-    S = seq_lens.shape[0]
-    for name, t, shape in (("new_lens", new_lens, (S,)), ("seq_lens", seq_lens, (S,)), ("new_free", new_free, (1,)),
-                           ("num_free", num_free, (1,)), ("status", status, (1,)),
-                           ("query_start", query_start, (S + 1,))):
-        _need(t.dtype == torch.int32 and t.shape == shape, f"{name} must be int32 {list(shape)}")
-    _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == S,
-          "block_tables must be int32 [num_seqs, max_blocks_per_seq]")
-    _need(free_blocks.dtype == torch.int32 and free_blocks.dim() == 1, "free_blocks must be 1-D int32")
-    _need(slot_mapping.dtype == positions.dtype == torch.int64 and slot_mapping.dim() == 1
-          and slot_mapping.shape == positions.shape, "slot_mapping and positions must be int64 [rows]")
+    lens, tables, rows = seq_lens.shape, block_tables.shape, slot_mapping.shape
+    i32, i64 = torch.int32, torch.int64
+    if len(lens) != 1 or new_lens.shape != lens or not seq_lens.dtype == new_lens.dtype == i32:
+        raise ValueError("seq_lens and new_lens must be int32 [num_seqs]")
+    S = lens[0]
+    if query_start.shape != (S + 1,) or query_start.dtype != i32:
+        raise ValueError("query_start must be int32 [num_seqs + 1]")
+    if len(tables) != 2 or tables[0] != S or block_tables.dtype != i32:
+        raise ValueError("block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    one = (1,)
+    if not (num_free.shape == new_free.shape == status.shape == one
+            and num_free.dtype == new_free.dtype == status.dtype == i32):
+        raise ValueError("num_free, new_free and status must be int32 [1]")
+    capacity = free_blocks.shape
+    if len(capacity) != 1 or free_blocks.dtype != i32:
+        raise ValueError("free_blocks must be 1-D int32")
+    if len(rows) != 1 or positions.shape != rows or not slot_mapping.dtype == positions.dtype == i64:
+        raise ValueError("slot_mapping and positions must be int64 [rows]")
     device = _device_of(new_lens, new_free, slot_mapping, positions, block_tables, seq_lens, query_start,
                         free_blocks, num_free, status)
     _enqueue(load_library().pa_append_tokens, device, stream, new_lens.data_ptr(), new_free.data_ptr(),
              slot_mapping.data_ptr(), positions.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
              query_start.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(), status.data_ptr(), S,
-             slot_mapping.shape[0], free_blocks.shape[0], int(block_size), block_tables.shape[1], int(num_blocks))
+             rows[0], capacity[0], block_size, tables[1], num_blocks)
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int,
