@@ -12,12 +12,16 @@
 // fraction of a turn, off by position 2^-65 and no more, and sincospi of it needs no further
 // reduction. No table of cosines is read, however long the context.
 //
-// Work. A token's rows (Q, K and V heads) are shared by 1, 2, 4 or 8 warps; a lane holds 16
+// Work. A CTA is a token, whose rows (Q, K and V heads) are shared by 1, 2, 4 or 8 warps; a lane holds 16
 // elements of a row in two 16-byte vectors, chosen so that both elements of its pairs are
 // its own and neighbouring lanes' vectors touch: (8 j, n + 8 j) of the rotated part, or
 // (8 j, d / 2 + 8 j) interleaved. Cosines and sines are computed once for a token, while the
 // first rows are under way, and kept in registers for all of its rows. Bound by memory: each
-// row is read once and written once.
+// row is read once and written once. 32768 tokens of 32, 8 and 8 heads of 128, with the cache
+// write: 118 us (6.8 TB/s) with one warp a token and six rounds of rows (4 rows each) under way
+// together, 127 us with two warps; CTAs of 8 warps, 4 for a token: 163 us with the next round
+// under way, 185 us with three. 128 tokens: 2.8 us with 8 warps a token, 5.0 us with one; the
+// two meet at about 1000 tokens (5.6 us).
 #include <cuda_runtime.h>
 #include <math.h>
 

@@ -28,7 +28,7 @@ struct AppendArgs {
 };
 
 // A call of up to this many rows is one CTA's, with the new lengths written at its end.
-// Above, CTAs find their rows' sequences each for itself and a second launch writes them.
+// Above, CTAs find their rows' sequences each for itself and a second launch writes the lengths.
 constexpr int kAppendOneCta = 4096;
 constexpr int kAppendMaxSeqs = 16384;  // 8 bytes of shared memory each
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
