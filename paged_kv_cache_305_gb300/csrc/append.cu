@@ -155,7 +155,7 @@ cudaError_t launch(const AppendArgs& a, int ctas, cudaStream_t stream) {
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   if (a.rows <= kAppendOneCta) return launch<true, true>(a, 1, stream);
-  const cudaError_t e = launch<true, false>(a, std::min((a.rows + kThreads - 1) / kThreads, 152), stream);
+  const cudaError_t e = launch<true, false>(a, std::min((a.rows - 1) / kThreads + 1, 152), stream);
   return e != cudaSuccess ? e : launch<false, true>(a, 1, stream);
 }
 

@@ -447,7 +447,10 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
   const int lane = threadIdx.x & 31, r8 = lane >> 2, t = lane & 3;
   const int rr = lane & 7;
   const bool edge = hi < kTokens;
-  if (edge && lane >= hi) ev = static_cast<uint32_t>(st.r) * 0x01010101u;
+  if (edge && lane >= hi) {  // whatever a slot behind the sequence holds
+    ek = 0;
+    ev = static_cast<uint32_t>(st.r) * 0x01010101u;
+  }
 
   // V's factors over 2^(r - 1) as fp16, two to a register. One vote says that all lie in
   // [r - 15, r], and K's below 2^65, where no sum of a row's products overflows before it meets

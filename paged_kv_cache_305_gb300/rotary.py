@@ -13,8 +13,8 @@ from typing import List, Optional, Sequence, Tuple
 
 import torch
 
-# 2 pi as a fraction, beyond the 64 bits that are asked for
-_TWO_PI = 2 * Fraction(3141592653589793238462643383279502884197, 10 ** 39)
+# 2**192 / (2 pi), from more digits of pi than the 64 bits that are asked for need
+_UNIT = round(2 ** 191 / Fraction(3141592653589793238462643383279502884197, 10 ** 39))
 
 
 def rotary_inverse_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
@@ -74,6 +74,7 @@ def rotary_frequencies(inverse: Sequence[float], device="cuda") -> torch.Tensor:
         f = float(f)
         if not math.isfinite(f):
             raise ValueError("a frequency is not finite")
-        t = round(Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64
+        n, d = f.as_integer_ratio()
+        t = ((n * _UNIT * 2 // (d << 128)) + 1 >> 1) % 2 ** 64  # nearest
         turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
     return torch.tensor(turns, dtype=torch.int64, device=device)

@@ -147,6 +147,50 @@ def test_decode_never_reads_past_the_length(d, B):
     check_decode(query, kc, vc, sc, bt, lens, B, 0.3 / np.sqrt(d), "bf16", max(32, B))
 
 
+# every token counts: equal scores and whole values, so that one left out, taken twice or taken
+# from another place shifts the sum by about 1 or more
+EVERY = [
+    # dtype, d, Hq, Hkv, B, lengths, table tokens, partition_tokens
+    ("bf16", 128, 8, 2, 16, [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 257, 0, 500], 512, 0),
+    ("fp16", 64, 4, 4, 16, [5000, 1, 2047, 2048, 2049, 777], 8192, 64),
+    ("bf16", 128, 32, 8, 16, [900, 33, 0, 1, 257, 64, 3000], 19456, 0),
+    ("fp16", 64, 6, 6, 8, [31, 700, 5, 64, 65], 16384, 0),
+    ("bf16", 64, 42, 6, 64, [1500, 1, 129, 0, 63, 64, 300], 11264, 0),
+    ("fp16", 128, 16, 1, 32, [40, 1030, 96, 513], 2048, 0),
+    ("bf16", 128, 16, 4, 4, [333, 20, 0, 129, 77, 3, 64, 65, 4000], 29184, 0),
+    ("fp16", 64, 4, 2, 1, [50, 260, 31, 33, 1025], 58880, 0),
+    ("bf16", 64, 5, 1, 2, [511, 513, 2, 1, 66], 1024, 0),
+    ("bf16", 128, 4, 1, 16, [60000, 1], 65536, 0),
+]
+
+
+@pytest.mark.parametrize("idx", range(len(EVERY)))
+def test_decode_takes_every_token_once(idx):
+    dtype, d, Hq, Hkv, B, lens, width, pt = EVERY[idx]
+    rng = np.random.default_rng(200 + idx)
+    NB = sum(-(-n // B) for n in lens) + 3
+    kc, _, sc = random_pool(rng, NB, B, Hkv, d)
+    codes = rng.choice([2, 4, 5, 6, 7, 10, 12, 13, 14, 15], size=(NB, B, Hkv, d))  # +-1, 2, 3, 4, 6
+    vc = fp4.pack(codes.astype(np.uint8))
+    kc[:], sc[:, :, 0], sc[:, :, 1] = 0x22, 120, 127  # keys all alike
+    bt = tables_for(rng, lens, B, NB, MB=width // B)
+    query = W.normal_bits((len(lens), Hq, d), dtype, 200 + idx, 2)
+    q, btd = dev_bits(query, dtype), up(bt)
+    kd = up(kc)
+    out = torch.full(query.shape, float("nan"), dtype=torch.float32, device="cuda")
+    pa.decode_fp4(out, q, kd, up(vc), up(sc), btd, up(np.array(lens, np.int32)), 0.05, pt, pa.alloc_workspace(q, kd, btd))
+    got, V = out.double().cpu().numpy(), fp4.pool_values(vc, sc, 1)
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert not got[s].any()
+            continue
+        total = oracle.gather_kv(V, bt[s], n, B).sum(0)  # whole numbers below 2^24
+        off = np.abs(got[s] * n - np.repeat(total, Hq // Hkv, axis=0))
+        # equal weights are exact and so are sums of whole numbers; joins and the quotient round: a few
+        # times 2^-23 of the result, times n: 60000 * 6 * 2^-21 = 0.17
+        assert np.max(off) <= 0.3, f"{EVERY[idx]} sequence {s}: {np.max(off)}"
+
+
 def one_sequence(rng, n, d, Hkv=1, B=16, spread=2):
     NB = -(-n // B) + 2
     kc, vc, sc = random_pool(rng, NB, B, Hkv, d, spread)
@@ -260,6 +304,23 @@ def test_decode_bf16_queries_of_any_size(size):
     K, V = (oracle.gather_kv(fp4.pool_values(c, sc, i), bt[0], n, 8) for i, c in enumerate((kc, vc)))
     got = run(query, kc, vc, sc, bt, n, 0.05, "bf16")
     check_rows(got[0], query[0], K, V, 0.05, "bf16", weight_error(n, 2), f"{size}")
+
+
+@pytest.mark.parametrize("B", [16, 4])
+def test_decode_slots_behind_a_sequence_do_not_reach_its_scores(B):
+    # small keys with large queries, and the largest factors in the slots behind the last token
+    rng = np.random.default_rng(17)
+    n, d = 37, 64
+    kc, vc, sc, bt = one_sequence(rng, n, d, 1, B)
+    sc[:, :, 0] = 40
+    last = bt[0, (n - 1) // B]
+    sc[last, :, :, (n - 1) % B + 1:] = 250
+    kc[last, (n - 1) % B + 1:] = 0x77
+    q = rng.uniform(1, 2, (1, 4, d)) * rng.choice([-1, 1], (1, 4, d)) * 2.0 ** 85
+    query = W.f32_to_bits(q.astype(np.float32), "bf16")
+    K, V = (oracle.gather_kv(fp4.pool_values(c, sc, i), bt[0], n, B) for i, c in enumerate((kc, vc)))
+    got = run(query, kc, vc, sc, bt, n, 0.05, "bf16")
+    check_rows(got[0], query[0], K, V, 0.05, "bf16", weight_error(n, 2))
 
 
 def test_decode_queries_of_heads_far_apart():
