@@ -606,7 +606,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         __syncwarp();
         if (lane == 0 && a.stall_for_test == 0) tc::mbar_arrive(empty(stage));
       };
-      if (BITS != 4 || !(note.flags & kLast)) release();
+      const bool alone = BITS == 4 && Wh == 1;  // this warp has the whole segment of its head
+      if (BITS != 4 || alone || !(note.flags & kLast)) release();
       if (!(note.flags & kLast)) continue;
 
       // ---- segment end: join the states of the head's warps ---------------
@@ -626,6 +627,40 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       const int r8 = lane >> 2, tq = 2 * (lane & 3);
       const size_t row0 = static_cast<size_t>(note.s) * a.num_q_heads +
                           static_cast<size_t>(note.hg * Hc + hsub) * G;
+      // O times 2^(top - 127), as two factors apart: one, or the product with 1 / l, may be subnormal
+      auto order_factors = [](float top) {
+        const int n = static_cast<int>(fminf(fmaxf(top - 127.f, -252.f), 252.f));
+        return make_float2(exponent_factor(127 + n / 2), exponent_factor(127 + n - n / 2));
+      };
+      if constexpr (BITS == 4) {
+        if (alone) {  // straight from its registers: a join of one would take 1000 instructions
+          const float2 ff = order_factors(static_cast<float>(st.r - 1));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int head = nt * 8 + tq + c;
+              if (head >= G) continue;
+              const float l = st.l[nt][c];
+              float iv = l > 0.f ? 1.f / l : 0.f;
+              if (l != l) iv = l;  // NaN scores give NaN
+              const size_t row = row0 + head, piece = (static_cast<size_t>(max(note.slot, 0)) * Hc + hsub) * G + head;
+              if (note.slot >= 0 && r8 == 0) a.seg_stat[piece] = make_float2(st.fresh ? -INFINITY : st.m[nt][c], l);
+#pragma unroll
+              for (int mt = 0; mt < D / 16; ++mt) {
+                const int dim = Geo::dim_of(mt, 0, r8);
+                const float2 v = make_float2(st.o[mt][nt][c] * iv * ff.x * ff.y, st.o[mt][nt][c + 2] * iv * ff.x * ff.y);
+                if (note.slot >= 0)
+                  *reinterpret_cast<float2*>(a.seg_out + piece * D + dim) = v;
+                else if (a.out_f32)
+                  *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row * D + dim) = v;
+                else
+                  *reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D + dim) = Ty::pack(v.x, v.y);
+              }
+            }
+          continue;
+        }
+      }
       // Where warp w leaves row `at` of a round. 4-bit: in its own rows of the stage, which nobody
       // reads any more, 8 of them (as many bytes as a row of O) for each head: all heads at once.
       constexpr int kRound = BITS == 4 ? kMaxGroup : kJoinHeads;
@@ -698,10 +733,8 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if constexpr (!kCodes) iv *= 1.f / kWeightScale<Ty>;
           acc = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
           if constexpr (kCodes) {
-            // times 2^(top - 127), as two factors apart: one, or the product with iv, may be subnormal
-            const int n = static_cast<int>(fminf(fmaxf(top - 127.f, -252.f), 252.f));
-            const float f0 = exponent_factor(127 + n / 2), f1 = exponent_factor(127 + n - n / 2);
-            acc = make_float4(acc.x * f0 * f1, acc.y * f0 * f1, acc.z * f0 * f1, acc.w * f0 * f1);
+            const float2 ff = order_factors(top);
+            acc = make_float4(acc.x * ff.x * ff.y, acc.y * ff.x * ff.y, acc.z * ff.x * ff.y, acc.w * ff.x * ff.y);
           }
           const size_t row = row0 + head;
           if (note.slot >= 0) {
