@@ -434,6 +434,89 @@ struct Factors4 {
 constexpr int kTame = 15;  // binary orders below r within which factors multiply fp16 weights
 constexpr float kShift4 = 6.f;
 
+// V's codes of a group of 32 dims as A operands of its two m-tiles: [tokens 0-15, 16-31][m-tile].
+template <int D>
+__device__ __forceinline__ void value_4(uint32_t sv, int g, uint32_t (&a)[2][2][4]) {
+  uint32_t v[4];
+  ldmatrix_x4_trans(v, sv + Tile<D, 4>::in_group(threadIdx.x & 7, g));
+  constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    // codes of the even tokens, and of the odd ones
+    const uint32_t u = __byte_perm(v[2 * hf], v[2 * hf + 1], 0x5410);
+    const uint32_t w = __byte_perm(v[2 * hf], v[2 * hf + 1], 0x7632);
+    uint32_t e[4], o[4];  // dims 0, 2 and 1, 3 of tokens 0-7, then of 8-15
+    e2m1x8_to_f16x2((u & kLow) | (w << 4 & ~kLow), e);
+    e2m1x8_to_f16x2((u >> 4 & kLow) | (w & ~kLow), o);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a[hf][h][0] = e[h];
+      a[hf][h][1] = o[h];
+      a[hf][h][2] = e[2 + h];
+      a[hf][h][3] = o[2 + h];
+    }
+  }
+}
+
+// The weighted sum of a 4-bit tile whose factors are too far apart for fp16, through bf16: o
+// [m-tile][nt][4] += .., p the weights.
+template <int D, int NT, bool SPLIT>
+__device__ __forceinline__ void add_wild_4(float (&o)[D / 16][NT][4], const float (&p)[NT][4][2], uint32_t sv, uint32_t ev,
+                                        int r) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31, r8 = lane >> 2;
+  const uint32_t rest = (lane & 2) != 0 ? kAll : 0u;  // SPLIT: columns 4-7
+  uint32_t evs[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) evs[i] = __shfl_sync(kAll, ev, r8 + 8 * i);
+#pragma unroll
+  for (int g = 0; g < D / kFp4Group; ++g) {
+    uint32_t a[2][2][4], bh[4][NT], bl[4][NT];
+    value_4<D>(sv, g, a);
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 c = F16::unpack(a[hf][h][k]);
+          a[hf][h][k] = BF16::pack(c.x, c.y);
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = static_cast<int>(evs[i] >> (8 * g) & 255u);
+      const float f = exponent_factor(e == 255 ? 255 : e == 0 ? 0 : max(e - r + 128, 0));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        weight_parts<BF16, SPLIT>(p[nt][i][0] * f, p[nt][i][1] * f, rest, bh[i][nt], bl[i][nt]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float t[NT][4] = {};
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          BF16::mma(t[nt], a[hf][h], bh[2 * hf][nt], bh[2 * hf + 1][nt]);
+          if constexpr (!SPLIT) BF16::mma(t[nt], a[hf][h], bl[2 * hf][nt], bl[2 * hf + 1][nt]);
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[2 * g + h][nt][e] += t[nt][e];
+    }
+  }
+}
+
+// The same as a function apart, on copies: with more than 4 query heads the ordinary path needs
+// the registers (64 sequences of 1K to 8K tokens, 16 heads a kv head: 142 us with the code in place,
+// 134 us; 8 heads: 87.5 and 85.3; 1 head: 67.0 and 69.2 us).
+template <int D, int NT>
+__device__ __noinline__ void add_wild_apart_4(float (&o)[D / 16][NT][4], const float (&p)[NT][4][2], uint32_t sv,
+                                              uint32_t ev, int r) {
+  add_wild_4<D, NT, false>(o, p, sv, ev, r);
+}
+
 // 4-bit tile. sk, sv: the groups of K and V rows that this lane's addresses for ldmatrix lie in
 // (tokens 0-7, 8-15, 16-23 or 24-31 of the tile: lane & 24); ek, ev: exponent bytes of token
 // `lane`; tokens 0 .. hi - 1 count (the others' V rows are zero).
@@ -598,29 +681,28 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
   }
 
   const uint32_t rest = (lane & 2) != 0 ? kAll : 0u;  // SPLIT: columns 4-7
-  // V's codes of a group as A operands of its two m-tiles: [tokens 0-15, 16-31][m-tile]
-  auto value = [&](int g, uint32_t (&a)[2][2][4]) {
-    uint32_t v[4];
-    ldmatrix_x4_trans(v, sv + Geo::in_group(rr, g));
-    constexpr uint32_t kLow = 0x0f0f0f0fu;
+  if (wild) {
+    if constexpr (SPLIT) {
+      add_wild_4<D, NT, true>(st.o, x, sv, ev, st.r);
+    } else {
+      State<D, NT> copy = st;
+      float p[NT][4][2];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      // codes of the even tokens, and of the odd ones
-      const uint32_t u = __byte_perm(v[2 * hf], v[2 * hf + 1], 0x5410);
-      const uint32_t w = __byte_perm(v[2 * hf], v[2 * hf + 1], 0x7632);
-      uint32_t e[4], o[4];  // dims 0, 2 and 1, 3 of tokens 0-7, then of 8-15
-      e2m1x8_to_f16x2((u & kLow) | (w << 4 & ~kLow), e);
-      e2m1x8_to_f16x2((u >> 4 & kLow) | (w & ~kLow), o);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        a[hf][h][0] = e[h];
-        a[hf][h][1] = o[h];
-        a[hf][h][2] = e[2 + h];
-        a[hf][h][3] = o[2 + h];
-      }
+        for (int i = 0; i < 4; ++i) {
+          p[nt][i][0] = x[nt][i][0];
+          p[nt][i][1] = x[nt][i][1];
+        }
+      add_wild_apart_4<D, NT>(copy.o, p, sv, ev, st.r);
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st.o[mt][nt][e] = copy.o[mt][nt][e];
     }
-  };
-  if (!wild) {
+  } else {
     uint32_t ph[4][NT], pl[4][NT];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -631,7 +713,7 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       uint32_t a[2][2][4];
-      value(g, a);
+      value_4<D>(sv, g, a);
       const uint4 fv = *reinterpret_cast<const uint4*>(&fac.v[t][g * 4]);
       const uint32_t fg[4] = {fv.x, fv.y, fv.z, fv.w};
 #pragma unroll
@@ -655,44 +737,6 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) st.add(2 * kG - 2 + h, o[(kG - 1) & 1][h]);
-    return;
-  }
-  uint32_t evs[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) evs[i] = __shfl_sync(kAll, ev, r8 + 8 * i);
-#pragma unroll
-  for (int g = 0; g < kG; ++g) {
-    uint32_t a[2][2][4], bh[4][NT], bl[4][NT];
-    value(g, a);
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 c = F16::unpack(a[hf][h][k]);
-          a[hf][h][k] = BF16::pack(c.x, c.y);
-        }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = static_cast<int>(evs[i] >> (8 * g) & 255u);
-      const float f = exponent_factor(e == 255 ? 255 : e == 0 ? 0 : max(e - st.r + 128, 0));
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        weight_parts<BF16, SPLIT>(x[nt][i][0] * f, x[nt][i][1] * f, rest, bh[i][nt], bl[i][nt]);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float o[NT][4] = {};
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          BF16::mma(o[nt], a[hf][h], bh[2 * hf][nt], bh[2 * hf + 1][nt]);
-          if constexpr (!SPLIT) BF16::mma(o[nt], a[hf][h], bl[2 * hf][nt], bl[2 * hf + 1][nt]);
-        }
-      st.add(2 * g + h, o);
-    }
   }
 }
 
