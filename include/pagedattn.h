@@ -526,9 +526,10 @@ int pa_gather_cache_fp4(void* key_out, void* value_out,
  * codes, as in pa_decode_fp8 (a bf16 query too); the factors of K's groups enter between
  * the products of one group and the next. Softmax weights, times the factor of V's group,
  * enter as the sum of two 16-bit parts. Where all factors of V in 32 neighbouring tokens
- * of a kv head lie within 2^12 of the largest so far (zero groups apart), the parts are
- * fp16, off by 2^-20 of themselves or 2^-32 of the largest weight times the largest factor
- * so far, where that is more; otherwise they are bf16, off by 2^-17 of themselves.
+ * of a kv head lie within 2^15 of the largest so far (zero groups apart), the parts are
+ * fp16, off by 2^-22 of themselves, or by 2^-31 of the largest weight, or (times their
+ * factor) by 2^-32 of the largest weight times the largest factor so far, whichever is
+ * most; otherwise they are bf16, off by 2^-17 of themselves.
  * (Where one sequence's V factors lie more than 2^100 apart, the smaller ones may lose
  * more.) A group that reads as NaN makes NaN of its 32 outputs (V), or of its head's (K).
  * workspace: pa_decode_fp4_workspace_bytes(...) bytes. Other arguments, the cut of the

@@ -11,8 +11,8 @@
 // call's kernels, replayed from a graph). A row is one (sequence, head
 // group); its tokens (those behind the shared prefix, where a pass of its own
 // computes that; otherwise the prefix's first, through the group's table) are
-// taken in stages of 32 KB (at d = 128: K and V of 32 8-bit or 16 16-bit tokens
-// for each computing warp), cut at multiples of the stage's tokens. All stages, in
+// taken in stages of 32 KB (at d = 128: K and V of 64 4-bit, 32 8-bit or 16 16-bit
+// tokens for each computing warp), cut at multiples of the stage's tokens. All stages, in
 // (head group, sequence, stage) order, form one line, which is cut into equal
 // shares, one for each CTA of the persistent grid, inside rows as it comes. The
 // cuts depend on the lengths and the grid alone. (Shares of 80 to 90 % with the
@@ -23,8 +23,10 @@
 // Pieces. The part of a row inside a share is a segment. A row that is one
 // segment is finished at once; otherwise each segment leaves a piece (fp32
 // normalised output, reference and sum of its weights), and a merge kernel behind
-// this one joins them, in order. A piece is stored and forgotten: a merge by the last
-// one to arrive would fence, count and read the others back while its CTA waits
+// this one joins them, in order. (4-bit: warps of a head join in the stage that the
+// segment ends in; where one warp has a head it writes what it holds, 136 us for 128
+// sequences and 143 through the join.) A piece is stored and forgotten: a merge by the
+// last one to arrive would fence, count and read the others back while its CTA waits
 // (that cost 10 % of the 128-sequence case). Segment (row R, share u) has the
 // slot R + u: every row and every share begins one boundary, so slots rise along
 // the line, those of a row follow each other, and there are as many as rows and
@@ -32,8 +34,8 @@
 //
 // Streaming. Four warps compute, a fifth feeds them: it finds the rows
 // of the CTA's share, reads the block table and fills the stages of a ring in shared
-// memory, 32 KB each at d = 128: one tile for every computing warp, the tiles of the
-// CTA's heads side by side. A lane issues a tensor copy per block for K and for
+// memory, 32 KB each at d = 128: one tile for every computing warp (4-bit: two), the
+// tiles of the CTA's heads side by side. A lane issues a tensor copy per block for K and for
 // V, straight from the block table and for all heads at once, and a bulk copy
 // for the block's exponent bytes. Blocks under 8 tokens, and pools beyond a
 // tensor map's reach, are copied row by row: the feeding warp hands out the slots
@@ -644,12 +646,15 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               const float l = st.l[nt][c];
               float iv = l > 0.f ? 1.f / l : 0.f;
               if (l != l) iv = l;  // NaN scores give NaN
-              const size_t row = row0 + head, piece = (static_cast<size_t>(max(note.slot, 0)) * Hc + hsub) * G + head;
-              if (note.slot >= 0 && r8 == 0) a.seg_stat[piece] = make_float2(st.fresh ? -INFINITY : st.m[nt][c], l);
+              const size_t row = row0 + head;
+              const size_t piece = (static_cast<size_t>(max(note.slot, 0)) * Hc + hsub) * G + head;
+              if (note.slot >= 0 && r8 == 0)
+                a.seg_stat[piece] = make_float2(st.fresh ? -INFINITY : st.m[nt][c], l);
 #pragma unroll
               for (int mt = 0; mt < D / 16; ++mt) {
                 const int dim = Geo::dim_of(mt, 0, r8);
-                const float2 v = make_float2(st.o[mt][nt][c] * iv * ff.x * ff.y, st.o[mt][nt][c + 2] * iv * ff.x * ff.y);
+                const float2 v = make_float2(st.o[mt][nt][c] * iv * ff.x * ff.y,
+                                             st.o[mt][nt][c + 2] * iv * ff.x * ff.y);
                 if (note.slot >= 0)
                   *reinterpret_cast<float2*>(a.seg_out + piece * D + dim) = v;
                 else if (a.out_f32)
