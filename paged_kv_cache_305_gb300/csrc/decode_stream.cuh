@@ -457,7 +457,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     auto row_at = [&](int x) {
       return static_cast<uint32_t>((x / lb * Hc + hsub) * lb * kRB + (x % lb >> 3) * 8 * kRB);
     };
-    // the same for rows 8 i, by shifts: lb, Hc and Wh are powers of two
+    // the same for rows 8 i, by shifts: lb is a power of two
     const int lb8 = 31 - __clz(lb >> 3);
     auto eight_at = [&](int i) {
       return (((((i >> lb8) * Hc + hsub) << lb8) + (i & ((1 << lb8) - 1))) * 8) * kRB;
@@ -710,7 +710,7 @@ paged_stream_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           float M = -INFINITY;
           for (int w = w0; w < w0 + Wh; ++w) M = fmaxf(M, stat(w, 0));
           // the order of a warp's O, and the largest of them. 8-bit: with the reference of its
-          // weights, a whole number; 4-bit: r alone, the reference is none
+          // weights, a whole number as well; 4-bit: of r alone, f carries the reference
           auto order = [&](int w) {
             if (BITS == 4) return stat(w, 0) == -INFINITY ? kLowest : stat(w, 2);
             return stat(w, 2) + (stat(w, 0) - M);

@@ -424,15 +424,15 @@ __device__ __forceinline__ void tile_8(uint32_t sk, uint32_t k_next, uint32_t sv
 }
 
 // Factors of a tile of 4-bit rows, from the lanes that own its tokens to those that use
-// them: K's of each token as fp32, V's over r as fp16 pairs of tokens 8 i + 2 t, + 1.
+// them: K's of each token as fp32, V's over 2^(r - 1) as fp16 pairs of tokens 8 i + 2 t, + 1.
 template <int D>
 struct Factors4 {
   static constexpr int kG = D / kFp4Group;
   float k[32][kG];
   uint32_t v[4][kG * 4 + 4];  // [t][g * 4 + i]; padded so that the writes of two t fall in other banks
 };
-constexpr int kTame = 15;  // binary orders below r within which factors multiply fp16 weights
-constexpr float kShift4 = 6.f;
+constexpr int kTame = 15;     // binary orders below r within which factors multiply fp16 weights
+constexpr float kShift4 = 6.f;  // binary orders from the reference m to the largest score when it is set
 
 // V's codes of a group of 32 dims as A operands of its two m-tiles: [tokens 0-15, 16-31][m-tile].
 template <int D>
@@ -461,8 +461,8 @@ __device__ __forceinline__ void value_4(uint32_t sv, int g, uint32_t (&a)[2][2][
 // The weighted sum of a 4-bit tile whose factors are too far apart for fp16, through bf16: o
 // [m-tile][nt][4] += .., p the weights.
 template <int D, int NT, bool SPLIT>
-__device__ __forceinline__ void add_wild_4(float (&o)[D / 16][NT][4], const float (&p)[NT][4][2], uint32_t sv, uint32_t ev,
-                                        int r) {
+__device__ __forceinline__ void add_wild_4(float (&o)[D / 16][NT][4], const float (&p)[NT][4][2],
+                                           uint32_t sv, uint32_t ev, int r) {
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31, r8 = lane >> 2;
   const uint32_t rest = (lane & 2) != 0 ? kAll : 0u;  // SPLIT: columns 4-7
