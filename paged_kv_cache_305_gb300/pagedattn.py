@@ -232,7 +232,8 @@ def _rotate(cache, query_out, key_out, query, key, value, key_cache, value_cache
         ko_far = _token_stride(key_out, "key_out", k_shape, dtype, device)
         _enqueue(load_library().pa_rotate, device, stream, query_out.data_ptr(), key_out.data_ptr(),
                  query.data_ptr(), key.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), *weights,
-                 T, Hq, Hkv, d, 2 * n[0], 1 if interleaved else 0, factor, eps, qo_far, ko_far, q_far, k_far, code)
+                 T, Hq, Hkv, d, 2 * n[0], 1 if interleaved else 0, float(factor), float(eps), qo_far, ko_far,
+                 q_far, k_far, code)
         return
     v_far = _token_stride(value, "value", k_shape, dtype, device)
     NB, B, *row = key_cache.shape
@@ -243,7 +244,7 @@ def _rotate(cache, query_out, key_out, query, key, value, key_cache, value_cache
     _enqueue(load_library().pa_rotate_and_cache, device, stream, query_out.data_ptr(), query.data_ptr(),
              key.data_ptr(), value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
              slot_mapping.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), *weights, T, Hq, Hkv, d,
-             B, NB, 2 * n[0], 1 if interleaved else 0, factor, eps, qo_far, q_far, k_far, v_far, code)
+             B, NB, 2 * n[0], 1 if interleaved else 0, float(factor), float(eps), qo_far, q_far, k_far, v_far, code)
 
 
 def rotate(query_out: torch.Tensor, key_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -305,12 +306,14 @@ def append_tokens(new_lens: torch.Tensor, new_free: torch.Tensor, slot_mapping: 
         raise ValueError("free_blocks must be 1-D int32")
     if len(rows) != 1 or positions.shape != rows or not slot_mapping.dtype == positions.dtype == i64:
         raise ValueError("slot_mapping and positions must be int64 [rows]")
+    if max(rows[0], capacity[0], tables[1]) > 0x7fffffff:
+        raise ValueError("2^31 or more rows, free blocks or blocks of a sequence")
     device = _device_of(new_lens, new_free, slot_mapping, positions, block_tables, seq_lens, query_start,
                         free_blocks, num_free, status)
     _enqueue(load_library().pa_append_tokens, device, stream, new_lens.data_ptr(), new_free.data_ptr(),
              slot_mapping.data_ptr(), positions.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
              query_start.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(), status.data_ptr(), S,
-             rows[0], capacity[0], block_size, tables[1], num_blocks)
+             rows[0], capacity[0], int(block_size), tables[1], int(num_blocks))
 
 
 def decode_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int,

@@ -189,3 +189,13 @@ def test_binding_refuses():
         pa.append_tokens(lens, n, slots, slots[:4], bt, lens, st, lens, n, n, 16, 8)
     with pytest.raises(ValueError, match="block_tables"):
         pa.append_tokens(lens, n, slots, slots, bt[:1], lens, st, lens, n, n, 16, 8)
+
+
+def test_append_refuses_counts_beyond_32_bits():
+    i32, i64 = dict(dtype=torch.int32, device="meta"), dict(dtype=torch.int64, device="meta")
+    n, far = torch.zeros(1, **i32), 2 ** 32 + 4
+    for rows, capacity, MB in ((far, 4, 4), (4, far, 4), (4, 4, far)):
+        lens, slots = torch.empty(2, **i32), torch.empty(rows, **i64)
+        with pytest.raises(ValueError, match="2\\^31"):
+            pa.append_tokens(lens, n, slots, slots, torch.empty(2, MB, **i32), lens, torch.empty(3, **i32),
+                             torch.empty(capacity, **i32), n, n, 16, 8)
