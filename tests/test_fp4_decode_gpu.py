@@ -430,6 +430,52 @@ def test_decode_bit_identical_however_placed_and_repeated():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("B", [64, 4])
+def test_blocks_behind_32_bit_offsets(B):
+    """The last blocks of a pool whose codes and exponent bytes both pass 2^32 bytes: written, copied, read
+    back and attended as in a small pool, and nothing where their offsets would fall in 32 bits."""
+    Hkv, d, dtype = 8, 128, "bf16"
+    codes, exps = B * Hkv * d // 2, B * Hkv * d // 16  # bytes a block
+    NB = 2 ** 32 // exps + 200
+    if torch.cuda.mem_get_info()[0] < NB * (2 * codes + exps) + 2 ** 32:
+        pytest.skip("too little free memory")
+    big = (*(torch.empty(NB, B, Hkv, d // 2, dtype=torch.uint8, device="cuda") for _ in range(2)),
+           torch.empty(NB, Hkv, 2, B, d // 32, dtype=torch.uint8, device="cuda"))
+    few = 100
+    small = pa.alloc_fp4_cache(few, B, Hkv, d)
+    for x in small:
+        x.fill_(0x77)
+    last = NB - few  # block i of the small pool is block last + i of the large one
+    wrapped = [(last * n % 2 ** 32) // n for n in (codes, codes, exps)]
+    for x, at in zip(big, wrapped):
+        x[last:].fill_(0x77)
+        assert at + few < last
+        x[at:at + few + 1].fill_(0x5A)
+
+    lens = [B * 30 + 3, B * 25 + 1]
+    rng = np.random.default_rng(B)
+    bt = tables_for(rng, lens, B, few - 20)
+    slots = np.concatenate([bt[s, np.arange(n) // B].astype(np.int64) * B + np.arange(n) % B for s, n in enumerate(lens)])
+    T = len(slots)
+    key, value = (dev_bits(W.normal_bits((T, Hkv, d), dtype, 51, i), dtype) for i in range(2))
+    query = dev_bits(W.normal_bits((2, 32, d), dtype, 52, 0), dtype)
+    src, dst = (np.arange(20) + x for x in (0, few - 20))
+    lens_d, starts = up(np.array(lens, np.int32)), up(np.array([0, lens[0]], np.int64))
+    seen = []
+    for pool, first in ((small, 0), (big, last)):
+        pa.reshape_and_cache_fp4(key, value, *pool, up(slots + first * B))
+        pa.copy_blocks_fp4(*pool, up((src + first).astype(np.int32)), up((dst + first).astype(np.int32)))
+        table = up((bt + first).astype(np.int32))
+        rows = [torch.empty_like(key) for _ in range(2)]
+        pa.gather_cache_fp4(*rows, *pool, table, lens_d, starts)
+        out = torch.empty(query.shape, dtype=torch.float32, device="cuda")
+        pa.decode_fp4(out, query, *pool, table, lens_d, 0.1, workspace=pa.alloc_workspace(query, pool[0], table))
+        seen.append((out, *rows, *(x[first:first + few] for x in pool)))
+    assert all(torch.equal(a, b) for a, b in zip(*seen)) and not seen[0][0].isnan().any()
+    for x, at in zip(big, wrapped):
+        assert (x[at:at + few + 1] == 0x5A).all()
+
+
 def test_workspace_may_hold_anything_and_is_shared():
     rng = np.random.default_rng(21)
     lens, B, Hkv, d = [2000, 1, 0, 513, 1024], 16, 2, 128

@@ -429,6 +429,38 @@ def test_a_captured_step_goes_on_by_itself(pool, dtype, Hq, Hkv, d, B, rot, inte
     assert int(height) == NB - len(used)
 
 
+def test_a_large_append_captured_and_replayed():
+    """Lengths and the stack's height written over those read, by the second of its two launches; the
+    table is read by what follows in the graph."""
+    rng = np.random.default_rng(12)
+    S, B, MB, new, rounds = 40, 16, 60, 150, 5
+    NB = S * MB
+    lens, starts = rng.integers(0, 90, S).astype(np.int32), np.arange(S + 1, dtype=np.int32) * new
+    want = (rng.integers(0, NB, (S, MB)), lens, NB)
+    free = rng.permutation(NB)
+    t, ln, height = up(want[0].astype(np.int32)), up(lens), up(np.array([NB], np.int32))
+    status, free_d, starts_d = torch.zeros_like(height), up(free.astype(np.int32)), up(starts)
+    slots, positions = (torch.zeros(S * new, dtype=torch.int64, device="cuda") for _ in range(2))
+    state = [x.clone() for x in (t, ln, height)]
+
+    def call():
+        pa.append_tokens(ln, height, slots, positions, t, ln, starts_d, free_d, height, status, B, NB)
+        return t.clone(), slots + 0, positions + 0
+
+    call()  # before the capture: first calls look up the device
+    for x, was in zip((t, ln, height), state):
+        x.copy_(was)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = call()
+    for k in range(rounds):
+        g.replay()
+        *want, w_slots, w_positions, w_status, _ = step.append_tokens(want[0], want[1], starts, free, want[2], S * new, B, NB)
+        assert np.array_equal(got[0].cpu().numpy(), want[0]) and np.array_equal(ln.cpu().numpy(), want[1])
+        assert int(height) == want[2] and int(status) == w_status == 0
+        assert np.array_equal(got[1].cpu().numpy(), w_slots) and np.array_equal(got[2].cpu().numpy(), w_positions)
+
+
 def test_on_other_streams_at_once():
     rng = np.random.default_rng(9)
     T, Hq, Hkv, d = 300, 8, 2, 128
