@@ -537,7 +537,8 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
 
   // V's factors over 2^(r - 1) as fp16, two to a register. One vote says that all lie in
   // [r - 15, r], and K's below 2^65, where no sum of a row's products overflows before it meets
-  // the query's factor; otherwise the bytes are looked at one by one.
+  // the query's factor; otherwise, and while r is so small that byte 0, a factor of zero, would be
+  // among them (a row's first tile, as a rule), the bytes are looked at one by one.
   bool wild = false;
   float unit = 1.f;  // of K's factors
   uint32_t f[kG / 2], out_of_range = 0;
@@ -547,7 +548,7 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
     out_of_range |= e + static_cast<uint32_t>((15 - st.r) * 65537);
     f[k] = e * 1024u + static_cast<uint32_t>((16 - st.r) * 65537) * 1024u;
   }
-  if (__any_sync(kAll, (out_of_range & 0xfff0fff0u) != 0 || (ek & ek << 1 & 0x80808080u) != 0)) {
+  if (__any_sync(kAll, (out_of_range & 0xfff0fff0u) != 0 || (ek & ek << 1 & 0x80808080u) != 0) || st.r <= kTame) {
     if (__any_sync(kAll, (ek & ek << 1 & 0x80808080u) != 0)) unit = 0x1p64f;
     int top = 0;
     unsigned low = ~0u;

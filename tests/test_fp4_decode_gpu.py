@@ -561,6 +561,41 @@ def test_stalled_ring_winds_down():
     assert torch.equal(out, want) and pa.wait_timeout_count() == 0
 
 
+@pytest.mark.parametrize("dtype,d,Hq,Hkv,B", [("bf16", 128, 8, 2, 16), ("fp16", 64, 4, 4, 16), ("bf16", 64, 11, 1, 8),
+                                              ("fp16", 128, 6, 1, 4)])
+def test_decode_values_under_exponent_zero_are_zeros(dtype, d, Hq, Hkv, B):
+    # codes of every kind whose exponents alone were cleared
+    rng = np.random.default_rng(30)
+    lens = [1, 31, 64, 65, 700]
+    NB = sum(-(-n // B) for n in lens)
+    kc, vc, sc = random_pool(rng, NB, B, Hkv, d)
+    sc[:, :, 1] = 0
+    bt = tables_for(rng, lens, B, NB)
+    o32 = check_decode(W.normal_bits((5, Hq, d), dtype, 30, 2), kc, vc, sc, bt, lens, B, 0.05, dtype)
+    assert not o32.any()
+
+
+@pytest.mark.parametrize("d,Hq,B", [(128, 4, 16), (64, 8, 16), (128, 12, 4)])
+@pytest.mark.parametrize("top", [1, 5, 10, 15, 16, 17])
+def test_decode_exponents_next_to_zero(d, Hq, B, top):
+    # V's bytes 0 .. top with the largest code under every byte 0; equal weights, so that a factor of 2^-127 in the
+    # place of zero shows: half of 6 2^-127 against a bound of about 2^-17 of 6 2^(top - 127)
+    rng = np.random.default_rng(31)
+    n = 40
+    kc, vc, sc, bt = one_sequence(rng, n, d, 1, B)
+    e = rng.integers(0, top + 1, sc[:, :, 1].shape).astype(np.uint8)
+    sc[:, :, 1] = np.where(rng.random(e.shape) < 0.5, 0, e)
+    codes = fp4.unpack(vc).reshape(*vc.shape[:-1], d // 32, 32)
+    codes[sc[:, :, 1].transpose(0, 2, 1, 3) == 0] = 7
+    codes[bt[0, 0], 0], sc[bt[0, 0], :, 1, 0] = 7, top  # the largest value, in every group
+    vc = fp4.pack(codes.reshape(*vc.shape[:-1], d))
+    query = W.f32_to_bits(np.zeros((1, Hq, d), np.float32), "bf16")
+    K, V = (oracle.gather_kv(fp4.pool_values(c, sc, i), bt[0], n, B) for i, c in enumerate((kc, vc)))
+    # every group of V holds the largest factor: errors of 2^-31 and 2^-32 a token, of the largest value
+    got = run(query, kc, vc, sc, bt, n, 0.1, "bf16")
+    check_rows(got[0], query[0], K, V, 0.1, "bf16", weight_error(n, 0), f"{top}")
+
+
 # ------------------------------------------------------------ all together --
 @pytest.mark.parametrize("dtype,B,Hq,Hkv,d", [("bf16", 16, 8, 2, 128), ("fp16", 8, 4, 4, 64), ("bf16", 2, 6, 3, 64)])
 def test_serving_loop_on_a_4_bit_pool(dtype, B, Hq, Hkv, d):
