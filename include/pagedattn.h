@@ -478,7 +478,9 @@ size_t pa_decode_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_h
  *   cache_scales            [NB, Hkv, 2, B, d / 32]  uint8; K's at index 0, V's at 1
  * Element i of the row of (slot, kv head) is code_i * 2^(e - 127), e the byte of
  * its group of 32; e = 0 reads as a factor of zero (a zero-filled pool holds
- * zeros), e = 255 as one of infinity. e2m1 is the format with a sign, two exponent
+ * zeros). e = 255 marks a group that is not finite: the read-back takes the factor as
+ * infinity (NaN for codes of zero, and the write makes no others), decode takes all 32
+ * elements as NaN. e2m1 is the format with a sign, two exponent
  * bits and one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0 to 7; 8 to 15 are
  * their negatives). A pool takes d / 2 + d / 32 bytes a row (68 for d = 128) where a
  * 16-bit cache takes 2 d. Tables, slots, lengths and the block manager are those of
@@ -531,7 +533,7 @@ int pa_gather_cache_fp4(void* key_out, void* value_out,
  * factor) by 2^-32 of the largest weight times the largest factor so far, whichever is
  * most; otherwise they are bf16, off by 2^-17 of themselves.
  * (Where one sequence's V factors lie more than 2^100 apart, the smaller ones may lose
- * more.) A group that reads as NaN makes NaN of its 32 outputs (V), or of its head's (K).
+ * more.) A group with byte 255 makes NaN of its 32 outputs (V), or of its head's (K).
  * workspace: pa_decode_fp4_workspace_bytes(...) bytes. Other arguments, the cut of the
  * work, sharing of workspaces, limits and errors as for pa_decode_fp8.
  */

@@ -6,8 +6,9 @@
 // 2, 3, 4, 6 and their negatives. The factor is a power of two, so scaling is exact:
 // a code is the nearest e2m1 value of the scaled element (one rounding, ties to even).
 //   e = 0    a group of zeros: the factor reads as 0
-//   e = 255  the factor reads as infinity; a group that held a NaN or an infinity is
-//            written with codes of zero, and 0 * inf is NaN: all 32 read as NaN
+//   e = 255  the group is not finite. One that held a NaN or an infinity is written with
+//            codes of zero. The read-back takes the factor as infinity, and 0 * inf is
+//            NaN; decode takes all 32 as NaN whatever their codes
 // Smallest factor. 6 is the largest code and the codes next to it are 2 apart, so up to
 // 7 times the factor no element is off by more than elements between 4 and 6 may be; with
 // the factor twice as large it would be off as much, and all others more. So e is the

@@ -549,7 +549,12 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
     f[k] = e * 1024u + static_cast<uint32_t>((16 - st.r) * 65537) * 1024u;
   }
   if (__any_sync(kAll, (out_of_range & 0xfff0fff0u) != 0 || (ek & ek << 1 & 0x80808080u) != 0) || st.r <= kTame) {
-    if (__any_sync(kAll, (ek & ek << 1 & 0x80808080u) != 0)) unit = 0x1p64f;
+    if (__any_sync(kAll, (ek & ek << 1 & 0x80808080u) != 0)) {
+      bool nan = false;
+#pragma unroll
+      for (int g = 0; g < kG; ++g) nan |= (ek >> (8 * g) & 255u) == 255u;
+      unit = __any_sync(kAll, nan) ? NAN : 0x1p64f;  // one such token makes all of a head's outputs NaN
+    }
     int top = 0;
     unsigned low = ~0u;
 #pragma unroll

@@ -596,6 +596,26 @@ def test_decode_exponents_next_to_zero(d, Hq, B, top):
     check_rows(got[0], query[0], K, V, 0.1, "bf16", weight_error(n, 0), f"{top}")
 
 
+@pytest.mark.parametrize("Hq,B", [(4, 16), (8, 16), (11, 4)])
+def test_decode_exponent_255_is_nan_whatever_its_codes(Hq, B):
+    rng = np.random.default_rng(32)
+    n, d, at = 100, 128, 37
+    kc, vc, sc, bt = one_sequence(rng, n, d, 1, B)
+    query = np.abs(oracle.to_float64(W.normal_bits((1, Hq, d), "bf16", 32, 2), "bf16"))
+    query = W.f32_to_bits(query.astype(np.float32), "bf16")
+    blk, off = bt[0, at // B], at % B
+    hit = np.zeros((1, Hq, d), bool)
+    hit[..., 64:96] = True
+    random = rng.integers(0, 256, 16).astype(np.uint8)
+    for codes in (random, 0x77, 0xFF, 0):
+        v2, s2 = vc.copy(), sc.copy()
+        v2[blk, off, 0, 32:48], s2[blk, 0, 1, off, 2] = codes, 255
+        assert np.array_equal(np.isnan(run(query, kc, v2, s2, bt, n, 0.09, "bf16")), hit)
+        k2, s2 = kc.copy(), sc.copy()
+        k2[blk, off, 0, 32:48], s2[blk, 0, 0, off, 2] = codes, 255
+        assert np.isnan(run(query, k2, vc, s2, bt, n, 0.09, "bf16")).all()
+
+
 # ------------------------------------------------------------ all together --
 @pytest.mark.parametrize("dtype,B,Hq,Hkv,d", [("bf16", 16, 8, 2, 128), ("fp16", 8, 4, 4, 64), ("bf16", 2, 6, 3, 64)])
 def test_serving_loop_on_a_4_bit_pool(dtype, B, Hq, Hkv, d):
