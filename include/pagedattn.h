@@ -533,7 +533,9 @@ int pa_gather_cache_fp4(void* key_out, void* value_out,
  * factor) by 2^-32 of the largest weight times the largest factor so far, whichever is
  * most; otherwise they are bf16, off by 2^-17 of themselves.
  * (Where one sequence's V factors lie more than 2^100 apart, the smaller ones may lose
- * more.) A group with byte 255 makes NaN of its 32 outputs (V), or of its head's (K).
+ * more, and so may scores of keys with factors below 2^-100 in the 32 tokens around a key
+ * with one of 2^65 or more.) A group with byte 255 makes NaN of its 32 outputs (V), or of
+ * its head's (K).
  * workspace: pa_decode_fp4_workspace_bytes(...) bytes. Other arguments, the cut of the
  * work, sharing of workspaces, limits and errors as for pa_decode_fp8.
  */

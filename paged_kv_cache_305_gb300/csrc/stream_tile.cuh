@@ -537,8 +537,9 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
 
   // V's factors over 2^(r - 1) as fp16, two to a register. One vote says that all lie in
   // [r - 15, r], and K's below 2^65, where no sum of a row's products overflows before it meets
-  // the query's factor; otherwise, and while r is so small that byte 0, a factor of zero, would be
-  // among them (a row's first tile, as a rule), the bytes are looked at one by one.
+  // the query's factor (with a larger one all of the tile's go 2^32 lower until it has been met);
+  // otherwise, and while r is so small that byte 0, a factor of zero, would be among them (a row's
+  // first tile, as a rule), the bytes are looked at one by one.
   bool wild = false;
   float unit = 1.f;  // of K's factors
   uint32_t f[kG / 2], out_of_range = 0;
@@ -553,7 +554,7 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
       bool nan = false;
 #pragma unroll
       for (int g = 0; g < kG; ++g) nan |= (ek >> (8 * g) & 255u) == 255u;
-      unit = __any_sync(kAll, nan) ? NAN : 0x1p64f;  // one such token makes all of a head's outputs NaN
+      unit = __any_sync(kAll, nan) ? NAN : 0x1p32f;  // one such token makes all of a head's outputs NaN
     }
     int top = 0;
     unsigned low = ~0u;
@@ -587,7 +588,7 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
     for (int g = 0; g < kG; ++g) fk[g] = exponent_factor(static_cast<int>(ek >> (8 * g) & 255u));
     if (unit != 1.f) {
 #pragma unroll
-      for (int g = 0; g < kG; ++g) fk[g] *= 0x1p-64f;
+      for (int g = 0; g < kG; ++g) fk[g] *= 0x1p-32f;
     }
     if constexpr (kG == 4)
       *reinterpret_cast<float4*>(fac.k[lane]) = make_float4(fk[0], fk[1], fk[2], fk[3]);
@@ -649,7 +650,15 @@ __device__ __forceinline__ void tile_4(uint32_t sk, uint32_t sv, uint32_t ek, ui
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) x[nt][i][c] = __fmul_rn(x[nt][i][c], q.sl2[nt][c] * unit);
+      for (int c = 0; c < 2; ++c) x[nt][i][c] = __fmul_rn(x[nt][i][c], q.sl2[nt][c]);
+  if (unit != 1.f) {  // apart: with the query's factor it may pass fp32's range
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) x[nt][i][c] *= unit;
+  }
 
   if (edge) {
 #pragma unroll

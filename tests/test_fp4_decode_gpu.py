@@ -616,6 +616,30 @@ def test_decode_exponent_255_is_nan_whatever_its_codes(Hq, B):
         assert np.isnan(run(query, k2, vc, s2, bt, n, 0.09, "bf16")).all()
 
 
+@pytest.mark.parametrize("order", [30, 80, 95, 115])
+@pytest.mark.parametrize("Hq,at", [(4, 5), (8, 33), (12, 63)])
+def test_decode_a_huge_key_leaves_the_others_their_scores(Hq, at, order):
+    # bf16 queries of about 2^order and keys that make scores of ordinary size with them, beside one key
+    # whose score is far below any that counts, and one whose huge group meets zeros of the query
+    rng = np.random.default_rng(33)
+    n, d, B, far = 64, 128, 16, 20
+    kc, vc, sc, bt = one_sequence(rng, n, d)
+    sc[:, :, 0] = 125 - order
+    q = rng.uniform(1, 2, (1, Hq, d)) * 2.0 ** order
+    q[..., 96:] = 0
+    query = W.f32_to_bits(q.astype(np.float32), "bf16")
+    blk, off = bt[0, at // B], at % B
+    kc[blk, off], sc[blk, 0, 0, off] = 0xFF, 200   # -6 2^73 in every element
+    sc[bt[0, far // B], 0, 0, far % B, 3] = 230
+    K, V = (oracle.gather_kv(fp4.pool_values(c, sc, i), bt[0], n, B) for i, c in enumerate((kc, vc)))
+    got = run(query, kc, vc, sc, bt, n, 0.05, "bf16")
+    ref, _ = oracle.single_query_attention(q := oracle.to_float64(query[0], "bf16"), K[:, 0], V[:, 0], 0.05)
+    rest = np.delete(K, at, 0)
+    rest[..., 96:] = 0  # their products are zeros
+    tol = fp8.decode_bound(q, rest, np.delete(V, at, 0), 0.05, weight_error(n, 2))
+    assert np.max(np.abs(got[0] - ref)) <= tol
+
+
 # ------------------------------------------------------------ all together --
 @pytest.mark.parametrize("dtype,B,Hq,Hkv,d", [("bf16", 16, 8, 2, 128), ("fp16", 8, 4, 4, 64), ("bf16", 2, 6, 3, 64)])
 def test_serving_loop_on_a_4_bit_pool(dtype, B, Hq, Hkv, d):
