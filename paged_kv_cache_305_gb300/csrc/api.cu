@@ -984,7 +984,7 @@ int stream_impl(void* out, const void* query, const void* key_cache, const void*
   a.groups = groups;
   a.cut = wl.cut ? 1 : 0;
   const int tile = bits == 4 ? 64 : bits == 8 ? 32 : 16;  // tokens of a warp in a stage
-  a.least_tiles = std::max(partition_tokens / tile, bits == 4 ? pa::kLeastTiles / 2 : pa::kLeastTiles);
+  a.least_tiles = std::max((partition_tokens + tile - 1) / tile, bits == 4 ? pa::kLeastTiles / 2 : pa::kLeastTiles);
   if (wl.total > 0) {
     a.ws_rows = reinterpret_cast<int2*>(ws);
     a.pre_stat = reinterpret_cast<float2*>(ws + wl.pre_stat);

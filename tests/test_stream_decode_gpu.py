@@ -466,3 +466,21 @@ def test_pieces_inside_a_chunk_of_a_shared_prefix():
         got = out.double().cpu().numpy()
         for s in range(S):
             check_means(got[s], oracle.gather_kv(V, bt[s], int(lens[s]), B), 16, (bound, s))
+
+
+# ------------------------------------------------------------------ shares --
+@pytest.mark.parametrize("bits,pt", [(4, 160), (4, 1008), (4, 64), (8, 144), (8, 1008)])
+def test_shares_are_not_under_partition_tokens(bits, pt):
+    # four kv heads at a time (a wide table), so that a share is counted in tiles of one warp; all shares
+    # but a row's last have at least pt tokens
+    Hq, Hkv, d, B, width, n = 4, 4, 64, 16, 1 << 18, 10 * pt
+    alloc, decode = (pa.alloc_fp4_cache, pa.decode_fp4) if bits == 4 else (pa.alloc_fp8_cache, pa.decode_fp8)
+    pool = alloc(8, B, Hkv, d)
+    q = dev_bits(W.normal_bits((1, Hq, d), "bf16", pt, 2), "bf16")
+    bt = torch.zeros(1, width // B, dtype=torch.int32, device="cuda")
+    ws = pa.alloc_workspace(q, pool[0], bt)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    decode(out, q, *pool, bt, torch.tensor([n], dtype=torch.int32, device="cuda"), 0.1, pt, ws)
+    pieces = ws[:8 * Hkv].view(torch.int32).view(Hkv, 2)[:, 1].tolist()
+    assert pieces == [pieces[0]] * Hkv and 2 <= pieces[0] <= 10
+    assert not out.any()
