@@ -18,8 +18,8 @@ _UNIT = round(2 ** 191 / Fraction(3141592653589793238462643383279502884197, 10 *
 
 
 def rotary_inverse_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
-                               factor: float = 1.0, original_length: int = 8192, low: float = 1.0,
-                               high: float = 4.0) -> Tuple[List[float], float]:
+                               factor: float = 1.0, original_length: int = 8192, low: Optional[float] = None,
+                               high: Optional[float] = None) -> Tuple[List[float], float]:
     """Radians a position for the pairs i < rotary_dim / 2, and the factor of rotated elements.
 
     Plain: w_i = base ** (-2 i / rotary_dim), factor 1. Scaled for contexts ``factor`` times
@@ -28,11 +28,11 @@ def rotary_inverse_frequencies(rotary_dim: int, base: float = 10000.0, scaling: 
     * ``"linear"``  every frequency is divided by ``factor`` (positions are interpolated);
     * ``"base"``    the base is multiplied by factor ** (d / (d - 2)), d = rotary_dim: the highest
       frequency stays, the lowest is divided by ``factor``;
-    * ``"parts"``   by the turns that a pair makes over ``original_length`` tokens: above ``high`` it
-      stays, below ``low`` it is divided by ``factor``, in between the two are mixed in proportion to
-      the turns;
+    * ``"parts"``   by the turns that a pair makes over ``original_length`` tokens: above ``high`` (4
+      unless given) it stays, below ``low`` (1) it is divided by ``factor``, in between the two are
+      mixed in proportion to the turns;
     * ``"yarn"``    the same ends, mixed in proportion to the pair's index between the indexes (rounded
-      outwards) at which a pair makes ``high`` and ``low`` turns (usually 32 and 1), and rotated
+      outwards) at which a pair makes ``high`` and ``low`` turns (32 and 1 unless given), and rotated
       elements are multiplied by 1 + 0.1 ln(factor).
     """
     if rotary_dim < 2 or rotary_dim % 2:
@@ -43,6 +43,9 @@ def rotary_inverse_frequencies(rotary_dim: int, base: float = 10000.0, scaling: 
         raise ValueError(f"scaling {scaling!r} is none of linear, base, parts, yarn")
     if scaling is not None and not (factor >= 1.0 and math.isfinite(factor)):
         raise ValueError(f"factor {factor} must be at least 1")
+    low = 1.0 if low is None else low
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
     if scaling in ("parts", "yarn") and not (0.0 < low < high and original_length > 0):
         raise ValueError(f"low {low} and high {high} must be positive and rise, original_length {original_length} positive")
     n = rotary_dim // 2

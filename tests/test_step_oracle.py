@@ -47,6 +47,26 @@ def test_scaling_by_parts(scaling, low, high):
     assert np.allclose(same, w, rtol=1e-14) and f == 1.0
 
 
+def test_defaults_of_scaling_by_parts():
+    # the usual ones, against plain restatements: "parts" mixes by the turns between 1 and 4, "yarn" by the
+    # index between those that make 32 and 1
+    d, base, s, L = 128, 10000.0, 4.0, 4096
+    w = base ** (-np.arange(64) / 64)
+    keep = np.clip((L * w / (2 * math.pi) - 1.0) / 3.0, 0, 1)
+    got, f = pa.rotary_inverse_frequencies(d, base, "parts", s, L)
+    assert f == 1.0 and np.allclose(got, w * keep + w / s * (1 - keep), rtol=1e-12)
+    first, last = (64 * math.log(L / (2 * math.pi * t)) / math.log(base) for t in (32, 1))
+    first, last = math.floor(first), math.ceil(last)
+    keep = 1 - np.clip((np.arange(64) - first) / (last - first), 0, 1)
+    got, f = pa.rotary_inverse_frequencies(d, base, "yarn", s, L)
+    assert f == 1.0 + 0.1 * math.log(s) and np.allclose(got, w * keep + w / s * (1 - keep), rtol=1e-12)
+    # either may be given alone
+    assert pa.rotary_inverse_frequencies(d, base, "yarn", s, L, low=2.0) == \
+        pa.rotary_inverse_frequencies(d, base, "yarn", s, L, 2.0, 32.0)
+    assert pa.rotary_inverse_frequencies(d, base, "parts", s, L, high=8.0) == \
+        pa.rotary_inverse_frequencies(d, base, "parts", s, L, 1.0, 8.0)
+
+
 def test_frequencies_are_turns_in_64_bits():
     w, _ = pa.rotary_inverse_frequencies(128, 10000.0, "linear", 3.7)
     t = pa.rotary_frequencies(w + [0.0, -w[3], 2 * math.pi + 1e-3, 3.5], device="cpu")
