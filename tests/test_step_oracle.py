@@ -219,3 +219,42 @@ def test_append_refuses_counts_beyond_32_bits():
         with pytest.raises(ValueError, match="2\\^31"):
             pa.append_tokens(lens, n, slots, slots, torch.empty(2, MB, **i32), lens, torch.empty(3, **i32),
                              torch.empty(capacity, **i32), n, n, 16, 8)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    # ctypes would cut each of them to a small one that the call takes
+    i32, i64, u8, bf16 = (dict(dtype=t, device="meta") for t in (torch.int32, torch.int64, torch.uint8, torch.bfloat16))
+    far = 2 ** 32 + 16
+    lens, n, slots = torch.empty(2, **i32), torch.zeros(1, **i32), torch.empty(2, **i64)
+    for sizes in ((far, 8), (16, far), (16 - 2 ** 32, 8)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            pa.append_tokens(lens, n, slots, slots, torch.empty(2, 4, **i32), lens, torch.empty(3, **i32),
+                             torch.empty(4, **i32), n, n, *sizes)
+    q, k = torch.empty(2, 4, 64, **bf16), torch.empty(2, 2, 64, **bf16)
+    with pytest.raises(ValueError, match="2\\^31"):
+        pa.rotate(q, k, q, k, slots, torch.empty(2 ** 31 + 16, **i64))
+    pool4 = *(torch.empty(8, 16, 2, 32, **u8) for _ in range(2)), torch.empty(8, 2, 2, 16, 2, **u8)
+    pool8 = *(torch.empty(8, 16, 2, 64, dtype=torch.float8_e4m3fn, device="meta") for _ in range(2)), \
+        torch.empty(8, 2, 2, 16, **u8)
+    bt, wide = torch.empty(2, 4, **i32), torch.empty(2, far, **i32)
+    many = torch.empty(far, **i32)
+    for pool, decode, gather, copy in ((pool4, pa.decode_fp4, pa.gather_cache_fp4, pa.copy_blocks_fp4),
+                                       (pool8, pa.decode_fp8, pa.gather_cache_fp8, pa.copy_blocks_fp8)):
+        for table, pt in ((wide, 0), (bt, far)):
+            with pytest.raises(ValueError, match="2\\^31"):
+                decode(q, q, *pool, table, lens, 0.1, pt)
+        with pytest.raises(ValueError, match="2\\^31"):
+            gather(k, k, *pool, wide, lens, slots)
+        with pytest.raises(ValueError, match="2\\^31"):
+            copy(*pool, many, many)
+    caches = [torch.empty(8, 16, 2, 64, **bf16) for _ in range(2)]
+    start = torch.empty(3, **i32)
+    for bounds in ((far, 4), (4, far)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            pa.decode_shared_prefix(q, q, *caches, bt, lens, start, lens, *bounds, 0.1)
+    for table, pt in ((wide, 0), (bt, far)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            pa.decode(q, q, *caches, table, lens, 0.1, pt)
+    for table, length in ((wide, 1), (bt, far)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            pa.prefill(q, q, *caches, table, lens, start, length, 0.1)
