@@ -136,6 +136,65 @@ def test_norms_of_rows_of_any_size(dtype):
     assert torch.equal(qo, ko)
 
 
+MANY = [
+    # dtype, T, Hq, Hkv, d, rotary_dim, interleaved, norm: rows that take a warp more rounds than it has under way
+    # together. 912 tokens or more: one warp a token; just below: two; few: eight
+    ("bf16", 913, 32, 8, 128, 128, False, False),
+    ("bf16", 913, 32, 8, 128, 128, False, True),
+    ("fp16", 913, 29, 3, 128, 64, True, True),
+    ("fp16", 912, 29, 3, 128, 128, False, False),
+    ("bf16", 1000, 64, 8, 64, 64, False, True),
+    ("fp16", 913, 64, 8, 64, 32, True, False),
+    ("bf16", 911, 64, 8, 128, 96, False, True),
+    ("fp16", 911, 61, 7, 128, 128, True, False),
+    ("bf16", 3, 200, 10, 128, 128, False, True),
+    ("fp16", 2, 431, 5, 64, 64, False, False),
+]
+
+
+@pytest.mark.parametrize("idx", range(len(MANY)))
+def test_rotate_rows_of_many_rounds(idx):
+    dtype, T, Hq, Hkv, d, rot, inter, norm = MANY[idx]
+    rng = np.random.default_rng(40 + idx)
+    bits = W.normal_bits((T, Hq + 2 * Hkv, d), dtype, 40 + idx, 1)
+    # rows of a NaN or an infinity among the first: nothing of them may reach rows behind
+    odd = rng.choice(T, min(T, 40), replace=False)
+    bits[odd[0::2], 1, 3::40] = {"bf16": 0x7FC0, "fp16": 0x7E00}[dtype]
+    bits[odd[1::2], 2, 5] = {"bf16": 0xFF80, "fp16": 0xFC00}[dtype]
+    qkv = dev_bits(bits, dtype)
+    q, k, v = qkv.split((Hq, Hkv, Hkv), 1)
+    pos, freq = rng.integers(0, 200000, T), random_frequencies(rng, rot // 2)
+    w = [dev_bits(W.normal_bits((d,), dtype, 41 + idx, 2 + i), dtype) if norm else None for i in range(2)]
+    kw = dict(interleaved=inter, query_weight=w[0], key_weight=w[1])
+    qo, ko = torch.empty(T, Hq, d, dtype=q.dtype, device="cuda"), torch.empty(T, Hkv, d, dtype=q.dtype, device="cuda")
+    pa.rotate(qo, ko, q, k, up(pos), freq, **kw)
+    angle = step.angles(pos, [int(f) for f in freq])
+    for got, x, weight in ((qo, q, w[0]), (ko, k, w[1])):
+        x, weight = values(x, dtype), None if weight is None else values(weight, dtype)
+        ref, got = step.rotate(x, angle, inter, 1.0, weight), values(got, dtype)
+        fine = np.isfinite(ref)
+        with np.errstate(invalid="ignore"):
+            tol = step.rotate_bound(x, rot // 2, inter, 1.0, weight, 1e-6, ref, dtype)
+        assert np.all(np.abs(got[fine] - ref[fine]) <= tol[fine])
+        assert np.array_equal(got[~fine], ref[~fine], equal_nan=True)
+    B, NB = 16, T // 16 + 3
+    kc, vc = (torch.full((NB, B, Hkv, d), 7.0 + i, dtype=q.dtype, device="cuda") for i in range(2))
+    slots = rng.permutation(NB * B)[:T]
+    slots[2::5] = -1  # a padded batch
+    qo2 = torch.empty_like(qo)
+    pa.rotate_and_cache(qo2, q, k, v, kc, vc, up(slots), up(pos), freq, **kw)
+    wk, wv = torch.full_like(kc, 7.0), torch.full_like(vc, 8.0)
+    keep = up(np.flatnonzero(slots >= 0))
+    wk.view(-1, Hkv, d)[up(slots)[keep]] = ko[keep]
+    wv.view(-1, Hkv, d)[up(slots)[keep]] = v[keep]
+    assert np.array_equal(host_bits(qo2), host_bits(qo))
+    assert torch.equal(kc, wk) and torch.equal(vc, wv)
+    # in place, in the projection's output
+    pa.rotate(q, k, q, k, up(pos), freq, **kw)
+    assert np.array_equal(host_bits(q), host_bits(qo)) and np.array_equal(host_bits(k), host_bits(ko))
+    assert torch.equal(v, dev_bits(bits, dtype)[:, Hq + Hkv:])
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("norm", [False, True])
 def test_nan_and_infinity_stay_in_their_pairs(interleaved, norm):
