@@ -169,9 +169,10 @@ def _need(cond: bool, msg: str) -> None:
         raise ValueError(msg)
 
 
-def _need_32_bits(*sizes: int) -> None:
-    """Sizes that the library takes as 32-bit integers, which ctypes would cut without a word."""
-    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+def _need_32_bits(sizes: int) -> None:
+    """`sizes`, the sizes of a call ORed together: those that the library takes as 32-bit integers and
+    ctypes would cut without a word."""
+    if sizes >> 31 not in (0, -1):
         raise ValueError("a size is 2^31 or more, or below -2^31")
 
 
@@ -188,7 +189,7 @@ def reshape_and_cache(key: torch.Tensor, value: torch.Tensor, key_cache: torch.T
     T = key.shape[0]
     _need(key.shape == (T, Hkv, d) and value.shape == (T, Hkv, d), "key/value shape mismatch")
     _need(slot_mapping.shape == (T,), "slot_mapping shape mismatch")
-    _need_32_bits(T, NB)
+    _need_32_bits(T | NB)
     L = load_library()
     with torch.cuda.device(key.device):
         _check(L.pa_reshape_and_cache(key.data_ptr(), value.data_ptr(), key_cache.data_ptr(),
@@ -221,7 +222,7 @@ def _rotate(cache, query_out, key_out, query, key, value, key_cache, value_cache
     n = frequencies.shape
     if frequencies.dtype != torch.int64 or len(n) != 1:
         raise ValueError("frequencies must be int64 [rotary_dim / 2]")
-    _need_32_bits(T, 2 * n[0])
+    _need_32_bits(T | 2 * n[0])
     others = (key_cache, value_cache, slot_mapping) if cache else ()
     weights = (0, 0)
     if query_weight is not None or key_weight is not None:
@@ -315,7 +316,7 @@ def append_tokens(new_lens: torch.Tensor, new_free: torch.Tensor, slot_mapping: 
     if len(rows) != 1 or positions.shape != rows or not slot_mapping.dtype == positions.dtype == i64:
         raise ValueError("slot_mapping and positions must be int64 [rows]")
     block_size, num_blocks = int(block_size), int(num_blocks)
-    _need_32_bits(rows[0], capacity[0], tables[1], block_size, num_blocks)
+    _need_32_bits(rows[0] | capacity[0] | tables[1] | block_size | num_blocks)
     device = _device_of(new_lens, new_free, slot_mapping, positions, block_tables, seq_lens, query_start,
                         free_blocks, num_free, status)
     _enqueue(load_library().pa_append_tokens, device, stream, new_lens.data_ptr(), new_free.data_ptr(),
@@ -394,7 +395,7 @@ def decode(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
           "block_tables and seq_lens must be int32")
     _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
           "block_tables/seq_lens shape mismatch")
-    _need_32_bits(S, block_tables.shape[1], NB, partition_tokens)
+    _need_32_bits(S | block_tables.shape[1] | NB | partition_tokens)
     for t in (out, query, key_cache, value_cache, block_tables, seq_lens):
         _need(t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors")
     ws_ptr, ws_bytes = 0, 0
@@ -433,7 +434,7 @@ def decode_append(out: torch.Tensor, query: torch.Tensor, new_key: torch.Tensor,
           "block_tables and seq_lens must be int32")
     _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
           "block_tables/seq_lens shape mismatch")
-    _need_32_bits(S, block_tables.shape[1], NB, partition_tokens)
+    _need_32_bits(S | block_tables.shape[1] | NB | partition_tokens)
     for t in (out, query, key_cache, value_cache, block_tables, seq_lens):
         _need(t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors")
     ws_ptr, ws_bytes = 0, 0
@@ -486,7 +487,7 @@ def _prefill(entry, out: torch.Tensor, query: torch.Tensor, key_cache: torch.Ten
           and query_start.dtype == torch.int32, "block_tables, seq_lens, query_start must be int32")
     _need(block_tables.shape[0] == S and query_start.shape == (S + 1,), "shape mismatch")
     max_query_len = int(max_query_len)
-    _need_32_bits(S, block_tables.shape[1], NB, max_query_len)
+    _need_32_bits(S | block_tables.shape[1] | NB | max_query_len)
     for t in (out, query, key_cache, value_cache, block_tables, seq_lens, query_start):
         _need(t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors")
     ws_ptr, ws_bytes = 0, 0
@@ -567,7 +568,7 @@ def decode_no_alloc(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Ten
           "block_tables and seq_lens must be int32")
     _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
           "block_tables/seq_lens shape mismatch")
-    _need_32_bits(S, block_tables.shape[1], NB, partition_tokens)
+    _need_32_bits(S | block_tables.shape[1] | NB | partition_tokens)
     for t in (out, query, key_cache, value_cache, block_tables, seq_lens):
         _need(t.is_cuda and t.is_contiguous(), "tensors must be contiguous CUDA tensors")
     L = load_library()
@@ -595,7 +596,7 @@ def copy_blocks(key_cache: torch.Tensor, value_cache: torch.Tensor, src: torch.T
     _need(src.dtype == torch.int32 and dst.dtype == torch.int32 and src.shape == dst.shape
           and src.dim() == 1 and src.is_cuda and dst.is_cuda, "src/dst must be 1-D int32 CUDA tensors")
     NB, B, Hkv, d = key_cache.shape
-    _need_32_bits(src.shape[0], NB)
+    _need_32_bits(src.shape[0] | NB)
     L = load_library()
     with torch.cuda.device(key_cache.device):
         _check(L.pa_copy_blocks(key_cache.data_ptr(), value_cache.data_ptr(), src.data_ptr(),
@@ -740,7 +741,7 @@ def gather_cache_fp4(key_out: torch.Tensor, value_out: torch.Tensor, key_cache: 
 def _write_scaled(entry, need_pool, key, value, key_cache, value_cache, cache_scales, slot_mapping, stream):
     NB, B, Hkv, d = need_pool(key_cache, value_cache, cache_scales)
     T = key.shape[0]
-    _need_32_bits(T, NB)
+    _need_32_bits(T | NB)
     device = _device_of(key, value, key_cache, value_cache, cache_scales, slot_mapping)
     _need(key.shape == (T, Hkv, d) and value.shape == (T, Hkv, d), "key/value shape mismatch")
     _need(key.dtype == value.dtype, "dtype mismatch")
@@ -755,7 +756,7 @@ def _copy_scaled(entry, need_pool, key_cache, value_cache, cache_scales, src, ds
     NB, B, Hkv, d = need_pool(key_cache, value_cache, cache_scales)
     _need(src.dtype == torch.int32 and dst.dtype == torch.int32 and src.shape == dst.shape
           and src.dim() == 1, "src/dst must be 1-D int32 tensors")
-    _need_32_bits(src.shape[0], NB)
+    _need_32_bits(src.shape[0] | NB)
     device = _device_of(key_cache, value_cache, cache_scales, src, dst)
     _enqueue(entry, device, stream, key_cache.data_ptr(),
              value_cache.data_ptr(), cache_scales.data_ptr(), src.data_ptr(), dst.data_ptr(),
@@ -773,7 +774,7 @@ def _gather_scaled(entry, need_pool, key_out, value_out, key_cache, value_cache,
     _need(block_tables.dim() == 2 and block_tables.shape[0] == S and seq_lens.shape == (S,),
           "block_tables/seq_lens shape mismatch")
     _need(out_start.dtype == torch.int64 and out_start.shape == (S,), "out_start must be int64 [num_seqs]")
-    _need_32_bits(S, block_tables.shape[1], NB)
+    _need_32_bits(S | block_tables.shape[1] | NB)
     device = _device_of(key_out, value_out, key_cache, value_cache, cache_scales, block_tables,
                         seq_lens, out_start)
     _enqueue(entry, device, stream, key_out.data_ptr(),
@@ -797,7 +798,7 @@ def _need_decode(out: torch.Tensor, query: torch.Tensor, head_dim: int, block_ta
     code = _dtype_code(query)
     types = code, PA_FLOAT32 if out.dtype == torch.float32 else code
     sizes = shape[0], shape[1], tables[1]
-    _need_32_bits(*sizes)
+    _need_32_bits(shape[0] | shape[1] | tables[1])
     if workspace is None:
         return _device_of(query, out, block_tables, seq_lens, *others), sizes, (*types, 0, 0)
     device = _device_of(query, out, block_tables, seq_lens, workspace, *others)
@@ -857,7 +858,7 @@ def _decode_scaled(entry, need_pool, out, query, key_cache, value_cache, cache_s
                    scale, partition_tokens, workspace, stream):
     NB, B, Hkv, d = need_pool(key_cache, value_cache, cache_scales)
     partition_tokens = int(partition_tokens)
-    _need_32_bits(NB, partition_tokens)
+    _need_32_bits(NB | partition_tokens)
     device, (S, Hq, MB), rest = _need_decode(out, query, d, block_tables, seq_lens, workspace,
                                              key_cache, value_cache, cache_scales)
     _enqueue(entry, device, stream, out.data_ptr(), query.data_ptr(),
@@ -926,7 +927,7 @@ def _decode_shared_prefix(entry, out, query, key_cache, value_cache, block_table
     _need(value_cache.shape == key_cache.shape, "cache shape mismatch")
     _need(query.dtype == key_cache.dtype == value_cache.dtype, "query/cache dtype mismatch")
     max_prefix_len, max_group_size = int(max_prefix_len), int(max_group_size)
-    _need_32_bits(NB, max_prefix_len, max_group_size)
+    _need_32_bits(NB | max_prefix_len | max_group_size)
     _need(group_start.dtype == torch.int32 and prefix_lens.dtype == torch.int32,
           "group_start and prefix_lens must be int32")
     _need(prefix_lens.dim() == 1 and group_start.shape == (prefix_lens.shape[0] + 1,),
