@@ -778,9 +778,9 @@ template <bool TOGETHER>
 constexpr int kMergeWarps = TOGETHER ? 8 : 4;
 constexpr long long kTogetherRows = 152 * 8;
 
-// out = sum_k f_k o_k / sum_k f_k, f_k = l_k / Lm 2^(m_k - M), M and Lm the largest m
-// and l (weights of at most 1: sums of large V must not overflow), over a query row's pieces,
-// the prefix pass's first, in order. A row without segments was finished by the
+// out = sum_k f_k o_k / sum_k f_k, f_k = l_k / L 2^(m_k - M), M the largest m and L the sum
+// of the l (so that all weights are at most 1 together: sums of large V must not overflow), over a
+// query row's pieces, the prefix pass's first, in order. A row without segments was finished by the
 // streaming kernel. TOGETHER: a CTA takes a row, each warp a
 // share of its pieces (few rows, of many pieces); otherwise each warp takes one.
 template <typename Ty, int D, bool TOGETHER>
@@ -818,18 +818,18 @@ __global__ void __launch_bounds__(kMergeWarps<TOGETHER> * 32) decode_merge_kerne
     };
     const int share = TOGETHER ? (n + W - 1) / W : n;
     const int k_lo = TOGETHER ? min(warp * share, n) : 0, k_hi = min(k_lo + share, n);
-    float M = -INFINITY, Lm = 0.f;
+    float M = -INFINITY, L = 0.f;
     for (int k = k_lo + lane; k < k_hi; k += 32) {
       const float2 x = stat_at(k);
       M = fmaxf(M, x.x);
-      Lm = fmaxf(Lm, x.y);
+      L += x.y;
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
       M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
-      Lm = fmaxf(Lm, __shfl_xor_sync(kFull, Lm, off));
+      L += __shfl_xor_sync(kFull, L, off);
     }
-    const float unit = 1.f / Lm;  // not used where all sums are 0
+    const float unit = 1.f / L;  // not used where all sums are 0
     float acc[E], den = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.f;
@@ -854,28 +854,28 @@ __global__ void __launch_bounds__(kMergeWarps<TOGETHER> * 32) decode_merge_kerne
       }
     }
     if constexpr (TOGETHER) {
-      __shared__ float sM[W], sLm[W], sDen[W], sAcc[W][D];
+      __shared__ float sM[W], sL[W], sDen[W], sAcc[W][D];
       if (lane == 0) {
         sM[warp] = M;
-        sLm[warp] = Lm;
+        sL[warp] = L;
         sDen[warp] = den;
       }
 #pragma unroll
       for (int i = 0; i < E; ++i) sAcc[warp][lane * E + i] = acc[i];
       __syncthreads();
       if (warp != 0) return;
-      float top = -INFINITY, top_l = 0.f;
+      float top = -INFINITY, all_l = 0.f;
       for (int w = 0; w < W; ++w) {
         top = fmaxf(top, sM[w]);
-        top_l = fmaxf(top_l, sLm[w]);
+        all_l += sL[w];
       }
-      const float one = 1.f / top_l;
+      const float one = 1.f / all_l;
       den = 0.f;
 #pragma unroll
       for (int i = 0; i < E; ++i) acc[i] = 0.f;
       for (int w = 0; w < W; ++w) {
         // a share without a sum holds zeros, or NaN
-        const float f = sLm[w] == 0.f ? 1.f : sLm[w] * one * ex2(sM[w] - top);
+        const float f = sL[w] == 0.f ? 1.f : sL[w] * one * ex2(sM[w] - top);
         den += f * sDen[w];
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] += f * sAcc[w][lane * E + i];

@@ -484,3 +484,30 @@ def test_shares_are_not_under_partition_tokens(bits, pt):
     pieces = ws[:8 * Hkv].view(torch.int32).view(Hkv, 2)[:, 1].tolist()
     assert pieces == [pieces[0]] * Hkv and 2 <= pieces[0] <= 10
     assert not out.any()
+
+
+# ------------------------------------------------------- the end of the range --
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("S,Hq", [(1, 4), (2, 40), (60, 32)])
+def test_pieces_of_the_largest_values_are_joined_in_range(bits, S, Hq):
+    # V 6 2^125 (4-bit) or 448 2^119 in every element, equal scores: any sum of two pieces with weights of about one
+    # is out of range, their mean is not. Few rows (a CTA merges each) and many (a warp each)
+    rng = np.random.default_rng(S)
+    Hkv, d, B, NB = 4, 64, 16, 64
+    code, byte = ((0x77, 252) if bits == 4 else (0x7E, 246))
+    pool = (pa.alloc_fp4_cache if bits == 4 else pa.alloc_fp8_cache)(NB, B, Hkv, d)
+    pool[1].view(torch.uint8).fill_(code)
+    pool[2][:, :, 1] = byte
+    pool[2][:, :, 1, 3, ...] = byte - 5
+    lens = rng.integers(3000, 9000, S)
+    bt = torch.randint(0, NB, (S, 600), dtype=torch.int32, device="cuda")
+    q = dev_bits(W.normal_bits((S, Hq, d), "bf16", S, 2), "bf16")
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    (pa.decode_fp4 if bits == 4 else pa.decode_fp8)(out, q, *pool, bt, up(lens.astype(np.int32)), 0.1,
+                                                    workspace=pa.alloc_workspace(q, pool[0], bt))
+    top = (6.0 if bits == 4 else 448.0) * 2.0 ** (byte - 127)
+    small = (lens + 12) // 16  # one token of 16 is 2^-5 as large
+    want = top * (1 - small / lens * (1 - 2.0 ** -5))
+    # sums of n positive terms in fp32, twice, and a handful of roundings
+    rel = np.abs(out.double().cpu().numpy() / want[:, None, None] - 1)
+    assert np.all(rel <= (2 * lens[:, None, None] + 32) * 2.0 ** -24)
