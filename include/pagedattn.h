@@ -328,7 +328,7 @@ int pa_rotate(void* query_out, void* key_out, const void* query, const void* key
  * rows of value go to their slots of the caches (16-bit, of dtype). Slots as there: K and
  * V of a token with a negative slot are not written, nor are those of one above the pool,
  * which is counted; its query is rotated all the same. (For an 8-bit or 4-bit pool:
- * pa_rotate, then that pool's write.)
+ * pa_rotate, then that pool's write, which takes contiguous rows of K and of V.)
  */
 int pa_rotate_and_cache(void* query_out, const void* query, const void* key, const void* value,
                         void* key_cache, void* value_cache, const int64_t* slot_mapping,

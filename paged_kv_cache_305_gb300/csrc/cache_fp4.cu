@@ -24,8 +24,8 @@ constexpr int kThreads = 128;
 // slot is known; a group is two neighbouring threads, whose largest magnitudes meet in
 // one shuffle. Magnitudes are compared as integers (the fp32 bits without the sign), so
 // that infinities and NaN come out on top and mark the group. Bound by memory: 4 bytes
-// read and 17/16 written per pair of K and V elements. 32768 tokens of 8 heads of 128: 27.2
-// us (6.2 TB/s) with loads that say that the rows are read once, 30.5 us with ordinary ones.
+// read and 17/16 written per pair of K and V elements. 32768 tokens of 8 heads of 128: 28.1
+// us (6.0 TB/s) with loads that say that the rows are read once, 30.2 us with ordinary ones.
 // ---------------------------------------------------------------------------
 template <typename Ty, int D>
 __global__ void __launch_bounds__(kThreads)

@@ -509,8 +509,10 @@ __device__ __forceinline__ void add_wild_4(float (&o)[D / 16][NT][4], const floa
 }
 
 // The same as a function apart, on copies: with more than 4 query heads the ordinary path needs
-// the registers (64 sequences of 1K to 8K tokens, 16 heads a kv head: 142 us with the code in place,
-// 134 us; 8 heads: 87.5 and 85.3; 1 head: 67.0 and 69.2 us).
+// the registers (64 sequences of 1K to 8K tokens, 16 heads a kv head: 140 us with the code in place,
+// 133 us; 8 heads: 87.3 and 84.3; 1 head: 74.9 us both). What a tile costs that comes here: 128
+// sequences of 4 heads a kv head, all tiles, 224 us (136 the other way); 64 of 8 heads 173 (84), of 16
+// heads 307 (133).
 template <int D, int NT>
 __device__ __noinline__ void add_wild_apart_4(float (&o)[D / 16][NT][4], const float (&p)[NT][4][2], uint32_t sv,
                                               uint32_t ev, int r) {
